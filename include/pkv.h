@@ -74,6 +74,10 @@ typedef int32_t pkv_status;
                                        >= 65536 (or inf / NaN), beyond the fp16 range its
                                        P.V product uses; that request's outputs are
                                        unspecified */
+#define PKV_DEV_BAD_POSITION 32     /* a negative rotary position */
+#define PKV_DEV_BAD_ROW 64          /* weight_rows entry outside [0, num_rows) */
+#define PKV_DEV_BAD_KEPT 128        /* a kept index that the request's source table does not
+                                       cover */
 
 /*
  * pkv_kv_cache_write -- scatter the step's new K/V rows into the paged pool.
@@ -365,6 +369,188 @@ pkv_status pkv_cascade_decode(float *out, float *out_lse, const void *q, const v
 
 /*
  * ---------------------------------------------------------------------------
+ * Rotary positions on the way into the cache.
+ * ---------------------------------------------------------------------------
+ * pkv_rope_frequencies -- host: the angle per position, in radians, of each
+ * rotated pair p < rotary_dim / 2 (r = rotary_dim), with the usual ways of
+ * stretching a model's context by the factor `stretch` >= 1:
+ *
+ *   PKV_ROPE_PLAIN   f_p = base^(-2p / r)            (stretch etc. unused)
+ *   PKV_ROPE_LINEAR  f_p / stretch: positions are interpolated
+ *   PKV_ROPE_BASE    f_p with base * stretch^(r / (r - 2)): the slowest pair
+ *                    is stretched in full, the fastest not at all (r > 2)
+ *   PKV_ROPE_BANDS   by the turns a pair makes over the original context,
+ *                    n_p = original_len * f_p / 2 pi: with
+ *                    w = clamp((n_p - low) / (high - low), 0, 1),
+ *                    f_p * (w + (1 - w) / stretch)
+ *   PKV_ROPE_RAMP    by the pair's index: with d(n) = r ln(original_len /
+ *                    (2 pi n)) / (2 ln base) (the index of the pair that makes
+ *                    n turns), a = max(0, floor(d(high))), b = min(r - 1,
+ *                    ceil(d(low))), w = clamp((p - a) / max(b - a, 0.001), 0, 1),
+ *                    f_p * ((1 - w) + w / stretch), and the rotated values
+ *                    are scaled by factor = 0.1 ln(stretch) + 1
+ *
+ *   inv_freq [rotary_dim / 2] double (HOST memory), written; *factor (host)
+ *   receives the scale of the rotated values (1 except for PKV_ROPE_RAMP).
+ * Errors: PKV_ERR_INVALID_ARG for an odd or non-positive rotary_dim, base <= 1,
+ * an unknown kind, stretch < 1, or (BANDS, RAMP) original_len <= 0 or not
+ * 0 < low < high.
+ */
+#define PKV_ROPE_PLAIN 0
+#define PKV_ROPE_LINEAR 1
+#define PKV_ROPE_BASE 2
+#define PKV_ROPE_BANDS 3
+#define PKV_ROPE_RAMP 4
+pkv_status pkv_rope_frequencies(double *inv_freq, float *factor, int32_t rotary_dim, double base,
+                                int32_t kind, double stretch, double original_len, double low,
+                                double high);
+
+/*
+ * pkv_rope_kv_cache_write -- rotate a step's queries and keys by their
+ * positions, write the keys and values into the paged pool: one pass in place
+ * of rotating q and k and then pkv_kv_cache_write.
+ *
+ *   q_out        [num_tokens][num_heads][head_dim] bf16, dense, written; may be
+ *                q itself when q is dense (q_stride = num_heads * head_dim)
+ *   kv_pool      as pkv_kv_cache_write
+ *   q            num_tokens rows of [num_heads][head_dim] bf16, q_stride
+ *                elements apart
+ *   k_new, v_new num_tokens rows of [num_kv_heads][head_dim] bf16, k_stride and
+ *                v_stride elements apart (q, k_new and v_new may be column
+ *                ranges of one projection output)
+ *   positions    [num_tokens] int32 >= 0: each token's position, independent
+ *                of its slot (after an eviction the slots are compact, the
+ *                positions go on)
+ *   slot_mapping as pkv_kv_cache_write (-1: q is rotated, nothing is written)
+ *   inv_freq     [rotary_dim / 2] double (device), radians per position;
+ *                angles are formed modulo a full turn before they are rounded,
+ *                so far positions lose nothing
+ *   factor       scale of the rotated values
+ *   interleaved  0: pair p is dimensions (p, p + rotary_dim / 2);
+ *                1: dimensions (2p, 2p + 1)
+ *
+ * With t = positions[i] * inv_freq[p], a pair (a, b) becomes
+ *   factor * (a cos t - b sin t,  b cos t + a sin t),
+ * computed in fp32 and rounded once to bf16. Dimensions >= rotary_dim, and
+ * v_new, are bit copies. Slots must be distinct, as in pkv_kv_cache_write.
+ * head_dim: a multiple of 8 up to 512; rotary_dim: even, 2 .. head_dim. All
+ * tensor pointers 16-byte aligned, strides multiples of 8 elements.
+ * Errors: PKV_ERR_INVALID_ARG also when q_out overlaps k_new or v_new, or q
+ * in any other way than the one allowed; PKV_DEV_BAD_POSITION (the token is
+ * skipped, q_out's row included); PKV_DEV_BAD_SLOT (q_out's row is written).
+ */
+pkv_status pkv_rope_kv_cache_write(void *q_out, void *kv_pool, const void *q, const void *k_new,
+                                   const void *v_new, int64_t q_stride, int64_t k_stride,
+                                   int64_t v_stride, const int32_t *positions,
+                                   const int32_t *slot_mapping, const double *inv_freq,
+                                   float factor, int32_t interleaved, int32_t num_tokens,
+                                   int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                                   int32_t rotary_dim, int32_t num_blocks, int32_t block_size,
+                                   int32_t *dev_status, void *stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Holding a request inside a cache budget: the attention weight that each
+ * cached key has received is accumulated step by step, and when a request's
+ * context is cut back, each KV head keeps the keys with the most of it. The
+ * kept rows move, in order, to fresh blocks (pkv_bm_evict_step hands them out);
+ * the sources may therefore be shared with other sequences.
+ *
+ * The accumulated weights are the caller's, [num_rows][num_kv_heads][row_len]
+ * fp32: key p of request i (position p of its block table) is entry
+ * [weight_rows[i]][h][p]. weight_rows (device, [num_seqs] int32) may be NULL:
+ * row i is request i. The rows of one call must be distinct.
+ * ---------------------------------------------------------------------------
+ * pkv_attention_key_weights -- add the softmax weights of a step's attention,
+ * summed over its queries and over the query heads that share a KV head, to
+ * each key's running sum. Arguments as pkv_paged_attention_varlen, plus
+ *
+ *   weights_out  written: entries p < seq_lens[i] of the requests with at least
+ *                one query; every other entry stays as it was
+ *   weights_in   read: the sums so far; may be weights_out itself
+ *   lse          [num_tokens][num_heads] fp32, the attention call's out_lse
+ *   prior_lens   [num_seqs] int32 or NULL: keys p < prior_lens[i] have a sum so
+ *                far, later ones start from zero (NULL: seq_len - query_len, the
+ *                step's own tokens are new)
+ *   decay        factor on the sums so far (finite, >= 0; 0 drops them unread)
+ *
+ *   weights_out[r][h][p] = (p < prior ? decay * weights_in[r][h][p] : 0)
+ *     + sum over queries j with pos_j >= p, heads a of KV head h, of
+ *       exp(scale * q[j][a] . K[p][h] - lse[j][a]),
+ *   pos_j = seq_len - query_len + j. An lse of -inf (a row without keys)
+ *   contributes nothing. Sums are fp32 in a fixed order: the same call gives
+ *   the same bits.
+ * head_dim 64 or 128; block_size a multiple of 16 up to 256; row_len >=
+ * max_seq_len; weights_in equal to weights_out or disjoint from it.
+ * Errors: as the attention call (PKV_DEV_BAD_BLOCK: that page's keys keep their
+ * old entries); PKV_DEV_BAD_ROW (the request is skipped).
+ */
+pkv_status pkv_attention_key_weights(float *weights_out, const float *weights_in, const void *q,
+                                     const void *kv_pool, const float *lse,
+                                     const int32_t *block_table, int32_t max_blocks_per_seq,
+                                     const int32_t *cu_seqlens_q, const int32_t *seq_lens,
+                                     const int32_t *prior_lens, const int32_t *weight_rows,
+                                     int32_t num_rows, int32_t row_len, int32_t num_seqs,
+                                     int32_t num_tokens, int32_t max_query_len,
+                                     int32_t max_seq_len, int32_t num_heads,
+                                     int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                     int32_t num_blocks, float scale, float decay,
+                                     int32_t *dev_status, void *stream);
+
+/*
+ * pkv_evict_select -- choose the keys that a request keeps, per KV head.
+ *
+ *   kept         [num_seqs][num_kv_heads][max_keep_len] int32, written:
+ *                entries j < keep_lens[i] are the kept keys' indexes, ascending;
+ *                later entries stay as they were
+ *   weights_out  as weights, or NULL: entry [row][h][j] = the weight of the
+ *                j-th kept key (the running sums of the shortened context);
+ *                must not overlap weights
+ *   weights      the accumulated weights
+ *   seq_lens     [num_seqs] int32 >= 0, at most max_seq_len
+ *   keep_lens    [num_seqs] int32, 0 <= keep_lens[i] <= seq_lens[i], at most
+ *                max_keep_len
+ *   num_sink, num_recent >= 0: keys kept whatever their weight: the last
+ *                r = min(num_recent, keep) of the context and its first
+ *                min(num_sink, keep - r)
+ * The rest of keep_lens[i] goes to the heaviest of the other keys; of equal
+ * weights the lowest index is kept; a NaN counts as heavier than any number.
+ * row_len >= max_seq_len (with weights_out, max_keep_len as well).
+ * Errors: PKV_DEV_BAD_LENGTHS, PKV_DEV_BAD_ROW (the request is skipped).
+ */
+pkv_status pkv_evict_select(int32_t *kept, float *weights_out, const float *weights,
+                            const int32_t *seq_lens, const int32_t *keep_lens,
+                            const int32_t *weight_rows, int32_t num_rows, int32_t row_len,
+                            int32_t num_seqs, int32_t num_kv_heads, int32_t max_seq_len,
+                            int32_t max_keep_len, int32_t num_sink, int32_t num_recent,
+                            int32_t *dev_status, void *stream);
+
+/*
+ * pkv_evict_compact -- move the kept keys' K and V rows to fresh blocks:
+ * for every request i, KV head h and j < keep_lens[i], with s = kept[i][h][j],
+ *   pool[K|V][dst_table[i][j / bs]][j % bs][h] =
+ *       pool[K|V][src_table[i][s / bs]][s % bs][h]          (bit copies).
+ *
+ *   src_table    [num_seqs][max_src_blocks] int32
+ *   dst_table    [num_seqs][max_dst_blocks] int32: blocks that no src_table
+ *                entry read by the call names, each named once
+ *   kept         as pkv_evict_select wrote it (any order, repeats allowed)
+ *   keep_lens    [num_seqs] int32, 0 .. min(max_keep_len, max_dst_blocks *
+ *                block_size)
+ * num_kv_heads * head_dim and head_dim as pkv_rope_kv_cache_write.
+ * Errors: PKV_DEV_BAD_LENGTHS (the request is skipped), PKV_DEV_BAD_KEPT (an
+ * index outside [0, max_src_blocks * block_size)) and PKV_DEV_BAD_BLOCK (a
+ * block id outside the pool): that row is not copied.
+ */
+pkv_status pkv_evict_compact(void *kv_pool, const int32_t *src_table, int32_t max_src_blocks,
+                             const int32_t *dst_table, int32_t max_dst_blocks,
+                             const int32_t *kept, int32_t max_keep_len, const int32_t *keep_lens,
+                             int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim,
+                             int32_t block_size, int32_t num_blocks, int32_t *dev_status,
+                             void *stream);
+
+/*
+ * ---------------------------------------------------------------------------
  * Host block manager and block copies -- the allocator side of the paged
  * cache ([page 2] PagedAttention deep-dive: the physical block pool carved up
  * at start-up; a block table per sequence mapping logical to physical blocks;
@@ -436,6 +622,25 @@ pkv_status pkv_bm_build_step(pkv_block_manager *bm, const int64_t *seq_ids, cons
                              int32_t *seq_lens, int32_t *cu_seqlens, int32_t *slot_mapping,
                              int32_t *copy_src, int32_t *copy_dst, int32_t max_copies,
                              int32_t *num_copies);
+
+/* Cut a batch of sequences back to keep_lens[i] tokens each, in fresh blocks
+ * (host arrays; the outputs are the tables of pkv_evict_compact):
+ *   seq_ids   [num_seqs] int64, distinct existing sequences
+ *   keep_lens [num_seqs] int32, 0 .. the sequence's length
+ *   src_table [num_seqs][max_src_blocks] int32, out: the sequence's blocks so
+ *             far, padded with -1
+ *   dst_table [num_seqs][max_dst_blocks] int32, out: its new blocks, padded
+ *             with -1
+ * The fresh blocks of the whole batch are taken from the free pool before any
+ * old block goes back to it, so no destination is a source; old blocks that
+ * other sequences share stay with those. Old blocks may be handed out again by
+ * the next call: enqueue the copies before the next step's writes, on the same
+ * stream. All or nothing: PKV_ERR_NO_BLOCKS if the pool cannot hold the new
+ * blocks beside the old, PKV_ERR_INVALID_ARG for an unknown or repeated
+ * sequence, a bad keep length, or a table row too short. */
+pkv_status pkv_bm_evict_step(pkv_block_manager *bm, const int64_t *seq_ids,
+                             const int32_t *keep_lens, int32_t num_seqs, int32_t max_src_blocks,
+                             int32_t *src_table, int32_t max_dst_blocks, int32_t *dst_table);
 
 /* Views: free blocks; a sequence's length (-1 if unknown); a block's
  * reference count (-1 if out of range); a sequence's block table into

@@ -49,6 +49,17 @@ _SIGNATURES = {
         _i32, [_vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _i32, _vp, _i32]
         + [_i32] * 6 + [ctypes.c_float, _vp, ctypes.c_size_t, _vp, _vp]),
     "pkv_copy_blocks": (_i32, [_vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp]),
+    "pkv_rope_frequencies": (
+        _i32, [_vp, _vp, _i32, ctypes.c_double, _i32] + [ctypes.c_double] * 4),
+    "pkv_rope_kv_cache_write": (
+        _i32, [_vp] * 5 + [ctypes.c_int64] * 3 + [_vp] * 3 + [ctypes.c_float] + [_i32] * 8
+        + [_vp, _vp]),
+    "pkv_attention_key_weights": (
+        _i32, [_vp] * 6 + [_i32] + [_vp] * 4 + [_i32] * 11
+        + [ctypes.c_float, ctypes.c_float, _vp, _vp]),
+    "pkv_evict_select": (_i32, [_vp] * 6 + [_i32] * 8 + [_vp, _vp]),
+    "pkv_evict_compact": (
+        _i32, [_vp, _vp, _i32, _vp, _i32, _vp, _i32, _vp] + [_i32] * 5 + [_vp, _vp]),
     "pkv_bm_create": (_i32, [_i32, _i32, _vp, ctypes.POINTER(_vp)]),
     "pkv_bm_destroy": (None, [_vp]),
     "pkv_bm_add_seq": (_i32, [_vp, ctypes.c_int64]),
@@ -57,6 +68,7 @@ _SIGNATURES = {
     "pkv_bm_append": (_i32, [_vp, ctypes.c_int64, _i32, _vp, _vp, _vp, _i32, _vp]),
     "pkv_bm_build_step": (_i32, [_vp, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i32,
                                  _vp]),
+    "pkv_bm_evict_step": (_i32, [_vp, _vp, _vp, _i32, _i32, _vp, _i32, _vp]),
     "pkv_bm_num_free": (_i32, [_vp]),
     "pkv_bm_seq_len": (ctypes.c_int64, [_vp, ctypes.c_int64]),
     "pkv_bm_refcount": (_i32, [_vp, _i32]),
@@ -70,6 +82,9 @@ DEV_BAD_BLOCK = 2
 DEV_BAD_LENGTHS = 4
 DEV_TIMEOUT = 8
 DEV_V_RANGE = 16
+DEV_BAD_POSITION = 32
+DEV_BAD_ROW = 64
+DEV_BAD_KEPT = 128
 
 
 class PkvError(RuntimeError):
@@ -493,6 +508,26 @@ class BlockManager:
         _check(st, "bm_build_step")
         return (table[:b], lens[:b], cu, slots[:int(nn.sum())], src[:n.value], dst[:n.value])
 
+    def evict_step(self, seq_ids, keep_lens, max_src_blocks: int, max_dst_blocks: int):
+        """Cut each sequence back to ``keep_lens`` tokens in fresh blocks.
+
+        Returns ``(src_table, dst_table)`` as numpy int32 arrays, the tables of
+        :func:`evict_compact`. Enqueue that copy before the next step's
+        writes, on the same stream: the old blocks may be handed out again."""
+        np = self._np
+        ids = np.ascontiguousarray(seq_ids, dtype=np.int64)
+        keep = np.ascontiguousarray(keep_lens, dtype=np.int32)
+        if ids.ndim != 1 or keep.shape != ids.shape:
+            raise ValueError("seq_ids and keep_lens must be one-dimensional, of one length")
+        b = ids.shape[0]
+        src = np.full((b, max_src_blocks), -1, dtype=np.int32)
+        dst = np.full((b, max_dst_blocks), -1, dtype=np.int32)
+        st = self._lib.pkv_bm_evict_step(self._h, ids.ctypes.data, keep.ctypes.data, b,
+                                         max_src_blocks, src.ctypes.data, max_dst_blocks,
+                                         dst.ctypes.data)
+        _check(st, "bm_evict_step")
+        return src, dst
+
     def num_free(self) -> int:
         return int(self._lib.pkv_bm_num_free(self._h))
 
@@ -564,3 +599,265 @@ def cascade_decode(q: torch.Tensor, kv_pool: torch.Tensor, group_starts: torch.T
         _stream(stream, q.device))
     _check(st, "cascade_decode")
     return out, out_lse
+
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "bands": 3, "ramp": 4}
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str = "none",
+                     stretch: float = 1.0, original_len: float = 0.0, low: float = 1.0,
+                     high: float | None = None):
+    """Rotary frequencies ``(inv_freq, factor)``: a float64 CPU tensor
+    [rotary_dim / 2] in radians per position (move it to the device once) and
+    the scale of the rotated values.
+
+    ``scaling`` stretches the context by ``stretch``: "none", "linear"
+    (positions interpolated), "base" (a larger base), "bands" (pairs that make
+    fewer than ``low`` turns over ``original_len`` positions are stretched,
+    those above ``high``, default 4, are not) or "ramp" (the same between pair
+    indexes, ``high`` 32 by default, with a scale on the rotated values). The
+    formulas stand with ``pkv_rope_frequencies`` in ``include/pkv.h``."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {', '.join(ROPE_SCALINGS)}, got {scaling!r}")
+    if high is None:
+        high = 32.0 if scaling == "ramp" else 4.0
+    inv_freq = torch.empty(max(int(rotary_dim) // 2, 1), dtype=torch.float64)
+    factor = ctypes.c_float(0.0)
+    st = load_library().pkv_rope_frequencies(
+        inv_freq.data_ptr(), ctypes.addressof(factor), int(rotary_dim), float(base),
+        ROPE_SCALINGS[scaling], float(stretch), float(original_len), float(low), float(high))
+    _check(st, "rope_frequencies")
+    return inv_freq, float(factor.value)
+
+
+def _need_rows(t: torch.Tensor, heads: int, head_dim: int, tokens: int, name: str) -> int:
+    """Check a [T,heads,D] bf16 tensor whose tokens may be any distance apart
+    (a column range of a projection's output); returns that distance."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if tuple(t.shape) != (tokens, heads, head_dim):
+        raise ValueError(f"{name} must be [{tokens}, {heads}, {head_dim}], got {tuple(t.shape)}")
+    st = t.stride()
+    if (head_dim > 1 and st[2] != 1) or (heads > 1 and st[1] != head_dim):
+        raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {st}")
+    return st[0] if tokens > 1 else heads * head_dim
+
+
+def _same_device(device, *tensors) -> None:
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"all tensors must be on one device, got {t.device} and {device}")
+
+
+def _on_stream(stream, device):
+    """The stream as torch sees it, for allocations that the call's work uses."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return torch.cuda.stream(stream)
+    return torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=device))
+
+
+def _run(what: str, device, stream, *args) -> None:
+    """Call ``pkv_<what>`` with ``device`` current and the stream last."""
+    fn = getattr(load_library(), "pkv_" + what)
+    raw = _stream(stream, device)
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, raw)
+    _check(st, what)
+
+
+def rope_kv_cache_write(q: torch.Tensor, kv_pool: torch.Tensor, k_new: torch.Tensor,
+                        v_new: torch.Tensor, positions: torch.Tensor, slot_mapping: torch.Tensor,
+                        inv_freq: torch.Tensor, *, interleaved: bool = False, factor: float = 1.0,
+                        q_out: torch.Tensor | None = None,
+                        dev_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Rotate q and k_new by ``positions`` and write k_new/v_new into the pool.
+
+    q [T,H,D], k_new/v_new [T,Hkv,D] bf16; a token's heads contiguous, tokens
+    any distance apart (slices of one projection output do). ``inv_freq`` is
+    the float64 device tensor of ``rope_frequencies``; the first
+    ``2 * len(inv_freq)`` dimensions rotate. ``positions`` are independent of
+    ``slot_mapping`` (-1: nothing is written). Returns ``q_out`` [T,H,D],
+    which may be a dense q itself."""
+    _need(kv_pool, torch.bfloat16, 5, "kv_pool")
+    _need(positions, torch.int32, 1, "positions")
+    _need(slot_mapping, torch.int32, 1, "slot_mapping")
+    _need(inv_freq, torch.float64, 1, "inv_freq")
+    _, nb, bs, hkv, d = kv_pool.shape
+    t = slot_mapping.shape[0]
+    if positions.shape[0] != t:
+        raise ValueError("positions and slot_mapping differ in length")
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a [num_tokens, num_heads, head_dim] tensor")
+    h = q.shape[1]
+    qs = _need_rows(q, h, d, t, "q")
+    ks = _need_rows(k_new, hkv, d, t, "k_new")
+    vs = _need_rows(v_new, hkv, d, t, "v_new")
+    device = kv_pool.device
+    if q_out is None:
+        with _on_stream(stream, device):
+            q_out = torch.empty((t, h, d), dtype=torch.bfloat16, device=device)
+    else:
+        _need(q_out, torch.bfloat16, 3, "q_out")
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have the shape of q")
+    if dev_status is not None:
+        _need(dev_status, torch.int32, 1, "dev_status")
+    _same_device(device, q, k_new, v_new, positions, slot_mapping, inv_freq, q_out, dev_status)
+    if debug_checks.enabled():
+        debug_checks.check_slot_mapping(slot_mapping, num_blocks=nb, block_size=bs)
+        debug_checks.check_positions(positions)
+    _run("rope_kv_cache_write", device, stream, _ptr(q_out), _ptr(kv_pool), _ptr(q), _ptr(k_new),
+         _ptr(v_new), qs, ks, vs, _ptr(positions), _ptr(slot_mapping), _ptr(inv_freq),
+         float(factor), int(bool(interleaved)), t, h, hkv, d, 2 * inv_freq.shape[0], nb, bs,
+         _ptr(dev_status))
+    return q_out
+
+
+def attention_key_weights(q: torch.Tensor, kv_pool: torch.Tensor, lse: torch.Tensor,
+                          block_table: torch.Tensor, cu_seqlens: torch.Tensor,
+                          seq_lens: torch.Tensor, max_query_len: int, max_seq_len: int,
+                          weights: torch.Tensor, *, out: torch.Tensor | None = None,
+                          weight_rows: torch.Tensor | None = None,
+                          prior_lens: torch.Tensor | None = None, decay: float = 1.0,
+                          scale: float | None = None, dev_status: torch.Tensor | None = None,
+                          stream=None) -> torch.Tensor:
+    """Add a step's softmax weights to each cached key's running sum.
+
+    ``lse`` [T,H] is the attention call's ``out_lse``; ``weights``
+    [rows,Hkv,row_len] fp32 the sums so far, request i's in row
+    ``weight_rows[i]`` (default i). Keys at or behind ``prior_lens[i]``
+    (default: the step's own tokens) start from zero; ``decay`` scales the
+    others' old sums. Writes and returns ``out`` (default: ``weights``, in place)."""
+    _need(q, torch.bfloat16, 3, "q")
+    _need(kv_pool, torch.bfloat16, 5, "kv_pool")
+    _need(lse, torch.float32, 2, "lse")
+    _need(block_table, torch.int32, 2, "block_table")
+    _need(cu_seqlens, torch.int32, 1, "cu_seqlens")
+    _need(seq_lens, torch.int32, 1, "seq_lens")
+    _need(weights, torch.float32, 3, "weights")
+    t, h, d = q.shape
+    _, nb, bs, hkv, d2 = kv_pool.shape
+    if d2 != d:
+        raise ValueError("q and kv_pool head_dim differ")
+    if tuple(lse.shape) != (t, h):
+        raise ValueError("lse must be [num_tokens, num_heads]")
+    b = seq_lens.shape[0]
+    if cu_seqlens.shape[0] != b + 1 or block_table.shape[0] != b:
+        raise ValueError("cu_seqlens must be [B+1] and block_table [B, max_blocks]")
+    rows, wh, row_len = weights.shape
+    if wh != hkv:
+        raise ValueError("weights must be [rows, num_kv_heads, row_len]")
+    if out is None:
+        out = weights
+    else:
+        _need(out, torch.float32, 3, "out")
+        if out.shape != weights.shape:
+            raise ValueError("out must have the shape of weights")
+    for x, name in ((weight_rows, "weight_rows"), (prior_lens, "prior_lens")):
+        if x is not None:
+            _need(x, torch.int32, 1, name)
+            if x.shape[0] != b:
+                raise ValueError(f"{name} must have one entry per request")
+    if dev_status is not None:
+        _need(dev_status, torch.int32, 1, "dev_status")
+    device = kv_pool.device
+    _same_device(device, q, lse, block_table, cu_seqlens, seq_lens, weights, out, weight_rows,
+                 prior_lens, dev_status)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if debug_checks.enabled():
+        debug_checks.check_attention_tables(
+            cu_seqlens, seq_lens, block_table, num_tokens=t, max_query_len=int(max_query_len),
+            max_seq_len=int(max_seq_len), num_blocks=nb, block_size=bs)
+        debug_checks.check_weight_rows(weight_rows, num_seqs=b, num_rows=rows)
+    _run("attention_key_weights", device, stream, _ptr(out), _ptr(weights), _ptr(q),
+         _ptr(kv_pool), _ptr(lse), _ptr(block_table), block_table.shape[1], _ptr(cu_seqlens),
+         _ptr(seq_lens), _ptr(prior_lens), _ptr(weight_rows), rows, row_len, b, t,
+         int(max_query_len), int(max_seq_len), h, hkv, d, bs, nb, float(scale), float(decay),
+         _ptr(dev_status))
+    return out
+
+
+def evict_select(weights: torch.Tensor, seq_lens: torch.Tensor, keep_lens: torch.Tensor,
+                 max_seq_len: int, max_keep_len: int, *, num_sink: int = 0, num_recent: int = 0,
+                 weight_rows: torch.Tensor | None = None, kept: torch.Tensor | None = None,
+                 weights_out: torch.Tensor | None = None,
+                 dev_status: torch.Tensor | None = None, stream=None):
+    """Choose the ``keep_lens[i]`` keys that each KV head of request i keeps.
+
+    The last ``num_recent`` and first ``num_sink`` keys stay whatever their
+    weight, the rest of the budget goes to the heaviest (ties: the lowest
+    index). Returns ``(kept, weights_out)``: kept [B,Hkv,max_keep_len] int32,
+    ascending, filled up to ``keep_lens[i]`` (a tensor made here holds -1
+    behind that); ``weights_out``, when given, receives the kept keys' weights
+    at the front of the same rows."""
+    _need(weights, torch.float32, 3, "weights")
+    _need(seq_lens, torch.int32, 1, "seq_lens")
+    _need(keep_lens, torch.int32, 1, "keep_lens")
+    rows, hkv, row_len = weights.shape
+    b = seq_lens.shape[0]
+    if keep_lens.shape[0] != b:
+        raise ValueError("seq_lens and keep_lens differ in length")
+    device = weights.device
+    if kept is None:
+        with _on_stream(stream, device):
+            kept = torch.full((b, hkv, int(max_keep_len)), -1, dtype=torch.int32, device=device)
+    else:
+        _need(kept, torch.int32, 3, "kept")
+        if tuple(kept.shape) != (b, hkv, int(max_keep_len)):
+            raise ValueError("kept must be [num_seqs, num_kv_heads, max_keep_len]")
+    if weights_out is not None:
+        _need(weights_out, torch.float32, 3, "weights_out")
+        if weights_out.shape != weights.shape:
+            raise ValueError("weights_out must have the shape of weights")
+    if weight_rows is not None:
+        _need(weight_rows, torch.int32, 1, "weight_rows")
+        if weight_rows.shape[0] != b:
+            raise ValueError("weight_rows must have one entry per request")
+    if dev_status is not None:
+        _need(dev_status, torch.int32, 1, "dev_status")
+    _same_device(device, seq_lens, keep_lens, kept, weights_out, weight_rows, dev_status)
+    if debug_checks.enabled():
+        debug_checks.check_weight_rows(weight_rows, num_seqs=b, num_rows=rows)
+        debug_checks.check_keep_lens(seq_lens, keep_lens, max_seq_len=int(max_seq_len),
+                                     max_keep_len=int(max_keep_len))
+    _run("evict_select", device, stream, _ptr(kept), _ptr(weights_out), _ptr(weights),
+         _ptr(seq_lens), _ptr(keep_lens), _ptr(weight_rows), rows, row_len, b, hkv,
+         int(max_seq_len), int(max_keep_len), int(num_sink), int(num_recent), _ptr(dev_status))
+    return kept, weights_out
+
+
+def evict_compact(kv_pool: torch.Tensor, src_table: torch.Tensor, dst_table: torch.Tensor,
+                  kept: torch.Tensor, keep_lens: torch.Tensor, *,
+                  dev_status: torch.Tensor | None = None, stream=None) -> None:
+    """Copy the kept keys' K and V rows (``kept`` of :func:`evict_select`) from
+    the blocks of ``src_table`` to the front of those of ``dst_table``, which
+    must be other blocks (``BlockManager.evict_step`` hands both out)."""
+    _need(kv_pool, torch.bfloat16, 5, "kv_pool")
+    _need(src_table, torch.int32, 2, "src_table")
+    _need(dst_table, torch.int32, 2, "dst_table")
+    _need(kept, torch.int32, 3, "kept")
+    _need(keep_lens, torch.int32, 1, "keep_lens")
+    _, nb, bs, hkv, d = kv_pool.shape
+    b = keep_lens.shape[0]
+    if kept.shape[:2] != (b, hkv):
+        raise ValueError("kept must be [num_seqs, num_kv_heads, max_keep_len]")
+    if src_table.shape[0] != b or dst_table.shape[0] != b:
+        raise ValueError("src_table and dst_table must have one row per request")
+    if dev_status is not None:
+        _need(dev_status, torch.int32, 1, "dev_status")
+    device = kv_pool.device
+    _same_device(device, src_table, dst_table, kept, keep_lens, dev_status)
+    if debug_checks.enabled():
+        debug_checks.check_compaction(src_table, dst_table, kept, keep_lens, num_blocks=nb,
+                                      block_size=bs)
+    _run("evict_compact", device, stream, _ptr(kv_pool), _ptr(src_table), src_table.shape[1],
+         _ptr(dst_table), dst_table.shape[1], _ptr(kept), kept.shape[2], _ptr(keep_lens), b, hkv,
+         d, bs, nb, _ptr(dev_status))

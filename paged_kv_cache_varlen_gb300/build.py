@@ -17,7 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIBRARY = os.path.join(PKG, "libpkv.so")
 SOURCES = ["kv_write.cu", "decode_mma.cu", "merge.cu", "prefill_tc.cu", "copy_blocks.cu",
-           "api.cpp",
+           "rope_write.cu", "key_weights.cu", "evict.cu", "api.cpp", "budget_api.cpp",
            "api_noalloc.cu", "block_manager.cpp"]
 HEADERS = [os.path.join(CSRC, "common.cuh"), os.path.join(CSRC, "launch.h"),
            os.path.join(ROOT, "include", "pkv.h")]

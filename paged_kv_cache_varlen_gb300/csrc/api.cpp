@@ -275,6 +275,10 @@ pkv_status plan_attention(AttnPlan* a, float* out, float* out_lse, const void* q
   return PKV_OK;
 }
 
+}  // namespace
+
+namespace pkv {
+
 // The pool [2][NB][BS][Hkv][D] viewed as [D/64][Hkv][2*NB*BS rows][64]
 // (strides 128 B, D*2, Hkv*D*2; the V half starts at row NB*BS), 128-byte
 // swizzle, with a box of 16 rows of one KV head and `chunks` 64-column
@@ -292,7 +296,8 @@ bool encode_kv_view(CUtensorMap* map, const void* kv_pool, int32_t num_blocks, i
   return encode_4d(map, kv_pool, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// q [T][H][D] with a box of {64, G, 128/G} (one 128-row Q tile per chunk).
+// q [T][H][D] with a box of {64, G, 128/G} (one Q tile of up to 128 rows per
+// chunk).
 bool encode_q_tiles(CUtensorMap* map, const void* q, int32_t num_tokens, int32_t num_heads,
                     int32_t num_kv_heads, int32_t head_dim) {
   const uint64_t D = (uint64_t)head_dim;
@@ -300,6 +305,13 @@ bool encode_q_tiles(CUtensorMap* map, const void* q, int32_t num_tokens, int32_t
   return encode_3d(map, q, D, num_heads, num_tokens, D * 2, (uint64_t)num_heads * D * 2, 64,
                    (uint32_t)group, (uint32_t)(128 / group), CU_TENSOR_MAP_SWIZZLE_128B);
 }
+
+}  // namespace pkv
+
+namespace {
+
+using pkv::encode_kv_view;
+using pkv::encode_q_tiles;
 
 // Encode the plan's TMA tensor maps (needs the driver; still enqueues nothing).
 pkv_status encode_plan(AttnPlan* a) {

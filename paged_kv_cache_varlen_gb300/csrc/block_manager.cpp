@@ -22,8 +22,10 @@
 #include <stdint.h>
 
 #include <deque>
+#include <exception>
 #include <new>
 #include <unordered_map>
+#include <unordered_set>
 #include <vector>
 
 #include "../../include/pkv.h"
@@ -235,6 +237,60 @@ pkv_status pkv_bm_build_step(pkv_block_manager* bm, const int64_t* seq_ids, cons
       row[b] = b < (int32_t)s.table.size() ? s.table[b] : -1;
   }
   return emit_copies(src, dst, copy_src, copy_dst, max_copies, num_copies);
+}
+
+pkv_status pkv_bm_evict_step(pkv_block_manager* bm, const int64_t* seq_ids,
+                             const int32_t* keep_lens, int32_t num_seqs, int32_t max_src_blocks,
+                             int32_t* src_table, int32_t max_dst_blocks, int32_t* dst_table) {
+  if (!bm || num_seqs < 0 || max_src_blocks < 0 || max_dst_blocks < 0) return PKV_ERR_INVALID_ARG;
+  if (num_seqs == 0) return PKV_OK;
+  if (!seq_ids || !keep_lens || (max_src_blocks > 0 && !src_table) ||
+      (max_dst_blocks > 0 && !dst_table))
+    return PKV_ERR_INVALID_ARG;
+  try {
+    std::vector<pkv_block_manager::Seq*> seqs(num_seqs);
+    std::vector<std::vector<int32_t>> fresh(num_seqs);
+    std::unordered_set<int64_t> seen;
+    const int64_t bs = bm->block_size;
+    int64_t need = 0;
+    for (int32_t i = 0; i < num_seqs; ++i) {
+      seqs[i] = find(bm, seq_ids[i]);
+      if (!seqs[i] || !seen.insert(seq_ids[i]).second) return PKV_ERR_INVALID_ARG;
+      if (keep_lens[i] < 0 || keep_lens[i] > seqs[i]->len) return PKV_ERR_INVALID_ARG;
+      const int64_t n = (keep_lens[i] + bs - 1) / bs;
+      if ((int64_t)seqs[i]->table.size() > max_src_blocks || n > max_dst_blocks)
+        return PKV_ERR_INVALID_ARG;
+      fresh[i].reserve(n);
+      need += n;
+    }
+    if (need > (int64_t)bm->free_pool.size()) return PKV_ERR_NO_BLOCKS;
+    // all fresh blocks first: no block released here is a destination of
+    // this batch
+    for (int32_t i = 0; i < num_seqs; ++i) {
+      const int64_t n = (keep_lens[i] + bs - 1) / bs;
+      for (int64_t b = 0; b < n; ++b) {
+        fresh[i].push_back(bm->free_pool.front());
+        bm->free_pool.pop_front();
+        bm->refs[fresh[i].back()] = 1;
+      }
+    }
+    for (int32_t i = 0; i < num_seqs; ++i) {
+      pkv_block_manager::Seq& s = *seqs[i];
+      int32_t* src = src_table + (int64_t)i * max_src_blocks;
+      int32_t* dst = dst_table + (int64_t)i * max_dst_blocks;
+      for (int32_t b = 0; b < max_src_blocks; ++b)
+        src[b] = b < (int32_t)s.table.size() ? s.table[b] : -1;
+      for (int32_t b = 0; b < max_dst_blocks; ++b)
+        dst[b] = b < (int32_t)fresh[i].size() ? fresh[i][b] : -1;
+      for (int32_t b : s.table)
+        if (--bm->refs[b] == 0) bm->free_pool.push_back(b);
+      s.table.swap(fresh[i]);
+      s.len = keep_lens[i];
+    }
+  } catch (const std::exception&) {  // out of host memory
+    return PKV_ERR_NO_BLOCKS;
+  }
+  return PKV_OK;
 }
 
 int32_t pkv_bm_num_free(const pkv_block_manager* bm) {

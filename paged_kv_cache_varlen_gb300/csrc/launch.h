@@ -188,5 +188,76 @@ cudaError_t launch_lse_merge(float* out, float* out_lse, const float* part_out,
                              const float* part_lse, int32_t num_parts, int64_t num_rows,
                              int32_t head_dim, cudaStream_t stream);
 
+// The encoded TMA views that several calls use (api.cpp); false when the
+// driver's encoder is missing or refuses.
+// Pool as [D/64][Hkv][2*NB*BS rows][64], boxes of 16 rows of one KV head and
+// `chunks` 64-column chunks.
+bool encode_kv_view(CUtensorMap* map, const void* kv_pool, int32_t num_blocks, int32_t block_size,
+                    int32_t num_kv_heads, int32_t head_dim, uint32_t chunks);
+// q [T][H][D] in boxes of {64 columns, G heads, 128/G tokens}.
+bool encode_q_tiles(CUtensorMap* map, const void* q, int32_t num_tokens, int32_t num_heads,
+                    int32_t num_kv_heads, int32_t head_dim);
+
+struct RopeWriteParams {
+  uint16_t* q_out;            // [T][H][D] bf16
+  void* pool;                 // [2][NB][BS][Hkv][D] bf16
+  const uint16_t* q;          // rows of [H][D], q_stride elements apart
+  const uint16_t* k;          // rows of [Hkv][D]
+  const uint16_t* v;
+  int64_t q_stride, k_stride, v_stride;
+  const int32_t* positions;   // [T]
+  const int32_t* slots;       // [T]
+  const double* inv_freq;     // [rotary_dim / 2] radians per position
+  float factor;
+  int32_t interleaved;
+  int32_t num_tokens, num_heads, num_kv_heads, head_dim, rotary_dim;
+  int64_t num_slots;          // NB * BS
+  int32_t* status;
+};
+cudaError_t launch_rope_write(const RopeWriteParams& p, cudaStream_t stream);
+
+struct KeyWeightsParams {
+  float* out;                 // [rows][Hkv][row_len]
+  const float* in;            // the same shape; may be out
+  const uint16_t* q;          // [T][H][D] bf16
+  const uint16_t* pool;       // [2][NB][BS][Hkv][D] bf16
+  const float* lse;           // [T][H]
+  const int32_t* block_table; // [B][max_blocks]
+  const int32_t* cu_seqlens;  // [B+1]
+  const int32_t* seq_lens;    // [B]
+  const int32_t* prior_lens;  // [B] or null: seq_len - query_len
+  const int32_t* rows;        // [B] or null: row i
+  int32_t num_rows, row_len, max_blocks;
+  int32_t num_seqs, num_tokens, max_query_len, max_seq_len;
+  int32_t num_heads, num_kv_heads, head_dim, block_size, num_blocks;
+  float scale_log2;           // scale * log2(e)
+  float decay;
+  int32_t* status;
+};
+cudaError_t launch_key_weights(const KeyWeightsParams& p, cudaStream_t stream);
+
+struct EvictSelectParams {
+  int32_t* kept;              // [B][Hkv][max_keep]
+  float* out;                 // [rows][Hkv][row_len] or null
+  const float* weights;       // [rows][Hkv][row_len]
+  const int32_t* seq_lens;    // [B]
+  const int32_t* keep_lens;   // [B]
+  const int32_t* rows;        // [B] or null
+  int32_t num_rows, row_len, num_seqs, num_kv_heads, max_seq_len, max_keep;
+  int32_t num_sink, num_recent;
+  int32_t* status;
+};
+cudaError_t launch_evict_select(const EvictSelectParams& p, cudaStream_t stream);
+
+struct EvictCompactParams {
+  uint4* pool;                // [2][NB][BS][Hkv][D] bf16
+  const int32_t* src_table;   // [B][max_src]
+  const int32_t* dst_table;   // [B][max_dst]
+  const int32_t* kept;        // [B][Hkv][max_keep]
+  const int32_t* keep_lens;   // [B]
+  int32_t max_src, max_dst, max_keep, num_seqs, num_kv_heads, head_vecs, block_size, num_blocks;
+  int32_t* status;
+};
+cudaError_t launch_evict_compact(const EvictCompactParams& p, cudaStream_t stream);
 
 }  // namespace pkv

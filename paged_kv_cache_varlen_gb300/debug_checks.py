@@ -16,7 +16,10 @@ key ranges, at least 1 with non-negative positions), at most max_seq_len and
 within its table row; every block id a request's context covers inside the
 pool; every slot of the KV write inside the pool (or -1, skipped); and, for
 the combined KV write and attention call, every slot the one block_table gives
-to its token's query position.
+to its token's query position; no negative rotary position; distinct weight
+rows inside the weights; keep lengths within the context; and, for the move of
+kept rows, indexes and block ids inside their tables and the pool, and
+destination blocks that are distinct and no sources.
 """
 from __future__ import annotations
 
@@ -122,3 +125,80 @@ def check_slot_mapping(slot_mapping, *, num_blocks: int, block_size: int) -> Non
         t = int(bad[0])
         raise ValueError(f"slot_mapping[{t}] = {slots[t]} outside the pool "
                          f"[0, {num_blocks * block_size}) and not -1")
+
+
+def check_positions(positions) -> None:
+    """Raise ValueError on the first negative rotary position."""
+    pos = _host(positions).astype(np.int64)
+    bad = np.nonzero(pos < 0)[0]
+    if bad.size:
+        raise ValueError(f"positions[{int(bad[0])}] = {pos[bad[0]]} is negative")
+
+
+def check_weight_rows(weight_rows, *, num_seqs: int, num_rows: int) -> None:
+    """Raise ValueError unless the requests' weight rows are distinct rows."""
+    if weight_rows is None:
+        return
+    rows = _host(weight_rows).astype(np.int64)
+    bad = np.nonzero((rows < 0) | (rows >= num_rows))[0]
+    if bad.size:
+        i = int(bad[0])
+        raise ValueError(f"weight_rows[{i}] = {rows[i]} outside [0, {num_rows})")
+    first: dict[int, int] = {}
+    for i, row in enumerate(rows.tolist()):
+        if row in first:
+            raise ValueError(f"weight_rows[{i}] = weight_rows[{first[row]}] = {row}")
+        first[row] = i
+
+
+def check_keep_lens(seq_lens, keep_lens, *, max_seq_len: int, max_keep_len: int) -> None:
+    """Raise ValueError on the first length the selection would reject."""
+    lens = _host(seq_lens).astype(np.int64)
+    keep = _host(keep_lens).astype(np.int64)
+    bad = np.nonzero((lens < 0) | (lens > max_seq_len))[0]
+    if bad.size:
+        i = int(bad[0])
+        raise ValueError(f"request {i}: seq_len {lens[i]} outside [0, {max_seq_len}]")
+    bad = np.nonzero((keep < 0) | (keep > lens) | (keep > max_keep_len))[0]
+    if bad.size:
+        i = int(bad[0])
+        raise ValueError(f"request {i}: keep_len {keep[i]} of {lens[i]} keys (at most "
+                         f"{max_keep_len})")
+
+
+def check_compaction(src_table, dst_table, kept, keep_lens, *, num_blocks: int,
+                     block_size: int) -> None:
+    """Raise ValueError on the first row the move would reject, and when a
+    destination block is named twice or is a source."""
+    src = _host(src_table).astype(np.int64)
+    dst = _host(dst_table).astype(np.int64)
+    idx = _host(kept).astype(np.int64)
+    keep = _host(keep_lens).astype(np.int64)
+    sources: set[int] = set()
+    taken: dict[int, int] = {}
+    for i in range(keep.shape[0]):
+        n = int(keep[i])
+        if n < 0 or n > idx.shape[2] or n > dst.shape[1] * block_size:
+            raise ValueError(f"request {i}: keep_len {n} outside its kept row or its table")
+        if n == 0:
+            continue
+        bad = np.argwhere((idx[i, :, :n] < 0) | (idx[i, :, :n] >= src.shape[1] * block_size))
+        if bad.size:
+            h, j = (int(x) for x in bad[0])
+            raise ValueError(f"kept[{i}][{h}][{j}] = {idx[i, h, j]} outside the table row")
+        used = np.unique(idx[i, :, :n] // block_size)
+        for b in used.tolist():
+            if not 0 <= src[i, b] < num_blocks:
+                raise ValueError(f"src_table[{i}][{b}] = {src[i, b]} outside the pool "
+                                 f"[0, {num_blocks})")
+        sources.update(src[i, used].tolist())
+        for b in range(-(-n // block_size)):
+            d = int(dst[i, b])
+            if not 0 <= d < num_blocks:
+                raise ValueError(f"dst_table[{i}][{b}] = {d} outside the pool [0, {num_blocks})")
+            if d in taken:
+                raise ValueError(f"dst_table[{i}][{b}] = {d} is request {taken[d]}'s block too")
+            taken[d] = i
+    both = sources & taken.keys()
+    if both:
+        raise ValueError(f"block {min(both)} is both a source and a destination")
