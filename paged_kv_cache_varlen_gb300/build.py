@@ -17,9 +17,10 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIBRARY = os.path.join(PKG, "libpkv.so")
 SOURCES = ["kv_write.cu", "decode_mma.cu", "merge.cu", "prefill_tc.cu", "copy_blocks.cu",
-           "rope_write.cu", "key_weights.cu", "evict.cu", "api.cpp", "budget_api.cpp",
-           "api_noalloc.cu", "block_manager.cpp"]
+           "rope_write.cu", "key_weights.cu", "key_weights_tc.cu", "evict.cu", "api.cpp",
+           "budget_api.cpp", "api_noalloc.cu", "block_manager.cpp"]
 HEADERS = [os.path.join(CSRC, "common.cuh"), os.path.join(CSRC, "launch.h"),
+           os.path.join(CSRC, "key_weights.cuh"),
            os.path.join(ROOT, "include", "pkv.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",

@@ -18,8 +18,7 @@
 // that read.
 #include <math.h>
 
-#include "common.cuh"
-#include "launch.h"
+#include "key_weights.cuh"
 
 namespace pkv {
 namespace {
@@ -36,32 +35,6 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// A request's lengths, checked; false when it has no work here (no queries,
-// or inconsistent lengths, flagged by the thread `flag`).
-struct Request {
-  int t0, qlen, L, prior, row;
-};
-__device__ __forceinline__ bool load_request(const KeyWeightsParams& p, int i, bool flag,
-                                             Request* r) {
-  const int32_t t0 = __ldg(p.cu_seqlens + i), t1 = __ldg(p.cu_seqlens + i + 1);
-  const int32_t L = __ldg(p.seq_lens + i);
-  const int32_t row = p.rows ? __ldg(p.rows + i) : i;
-  const int32_t qlen = t1 - t0;
-  const int32_t prior = p.prior_lens ? __ldg(p.prior_lens + i) : L - qlen;
-  if (t0 < 0 || t1 < t0 || t1 > p.num_tokens || (qlen > 0 && (qlen > p.max_query_len || L < qlen ||
-      L > p.max_seq_len || (int64_t)L > (int64_t)p.max_blocks * p.block_size))) {
-    if (flag) set_status(p.status, PKV_DEV_BAD_LENGTHS);
-    return false;
-  }
-  if (qlen == 0) return false;
-  if (row < 0 || row >= p.num_rows) {
-    if (flag) set_status(p.status, PKV_DEV_BAD_ROW);
-    return false;
-  }
-  *r = Request{t0, qlen, L, prior, row};
-  return true;
-}
-
 // NT: 8-column tiles held in registers at a time; ONE: every column of a
 // request fits in them (single tokens and short steps), so Q is loaded once.
 template <int D, int NT, bool ONE>
@@ -73,11 +46,12 @@ __global__ void __launch_bounds__(kWarps * 32) key_weights_kernel(const KeyWeigh
   const int h = unit % p.num_kv_heads;
   const int key0 = (unit / p.num_kv_heads) * kChunk;
   const int i = blockIdx.y;
-  Request r;
-  if (!load_request(p, i, unit == 0 && lane == 0, &r)) return;
+  KeyRequest r;
+  if (!key_request(p, i, unit == 0 && lane == 0, &r)) return;
   if (key0 >= r.L) return;
   const int G = p.num_heads / p.num_kv_heads;
   const int cols = r.qlen * G;
+  if (ONE && cols > NT * 8) return;  // a longer step: the tcgen05 grid takes it
   const int qpos0 = r.L - r.qlen;
   const int row = lane >> 2, quad = lane & 3;
   constexpr int KB = D / 32;  // 32-dimension blocks of a row: one vector a lane
@@ -193,8 +167,7 @@ cudaError_t launch(const KeyWeightsParams& p, cudaStream_t stream) {
 }
 
 template <int D>
-cudaError_t pick(const KeyWeightsParams& p, cudaStream_t stream) {
-  const int64_t cols = (int64_t)p.max_query_len * (p.num_heads / p.num_kv_heads);
+cudaError_t launch_d(const KeyWeightsParams& p, int64_t cols, cudaStream_t stream) {
   if (cols <= 8) return launch<D, 1, true>(p, stream);
   if (cols <= 16) return launch<D, 2, true>(p, stream);
   if (cols <= 32) return launch<D, 4, true>(p, stream);
@@ -204,7 +177,11 @@ cudaError_t pick(const KeyWeightsParams& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_key_weights(const KeyWeightsParams& p, cudaStream_t stream) {
-  return p.head_dim == 64 ? pick<64>(p, stream) : pick<128>(p, stream);
+  // columns of the longest request that this grid takes
+  const int G = p.num_heads / p.num_kv_heads;
+  int64_t cols = (int64_t)p.max_query_len * G;
+  if (p.short_max_q > 0 && p.short_max_q < p.max_query_len) cols = (int64_t)p.short_max_q * G;
+  return p.head_dim == 64 ? launch_d<64>(p, cols, stream) : launch_d<128>(p, cols, stream);
 }
 
 }  // namespace pkv

@@ -232,9 +232,19 @@ struct KeyWeightsParams {
   int32_t num_heads, num_kv_heads, head_dim, block_size, num_blocks;
   float scale_log2;           // scale * log2(e)
   float decay;
+  // requests of up to short_max_q queries run on the mma.sync grid, longer
+  // ones on the tcgen05 grid; 0: all on the former. no_short: the former is
+  // not launched, the latter flags a short request as PKV_DEV_BAD_LENGTHS
+  int32_t short_max_q;
+  int32_t no_short;
   int32_t* status;
 };
 cudaError_t launch_key_weights(const KeyWeightsParams& p, cudaStream_t stream);
+// Requests longer than short_max_q; `q_map` as for the prefill kernel (boxes
+// of 128 / G queries), `k_map` the pool in boxes of 16 keys and one
+// 64-column chunk.
+cudaError_t launch_key_weights_tc(const KeyWeightsParams& p, const CUtensorMap& q_map,
+                                  const CUtensorMap& k_map, cudaStream_t stream);
 
 struct EvictSelectParams {
   int32_t* kept;              // [B][Hkv][max_keep]
