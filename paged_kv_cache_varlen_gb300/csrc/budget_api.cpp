@@ -21,7 +21,7 @@ bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
 
 pkv_status launched(cudaError_t e) { return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA; }
 
-// Grid y and z dimensions: one slice per request (or KV head).
+// Grid y dimension: one slice per request.
 constexpr int32_t kMaxSeqs = 65535;
 
 }  // namespace
@@ -138,7 +138,7 @@ pkv_status pkv_attention_key_weights(float* weights_out, const float* weights_in
   if (num_seqs < 0 || num_tokens < 0) return PKV_ERR_INVALID_ARG;
   if (num_tokens == 0) return PKV_OK;
   if (num_seqs == 0) return PKV_ERR_INVALID_ARG;
-  if (num_seqs > kMaxSeqs || num_kv_heads > kMaxSeqs) return PKV_ERR_UNSUPPORTED;
+  if (num_seqs > kMaxSeqs) return PKV_ERR_UNSUPPORTED;
   if (!weights_out || !weights_in || !q || !kv_pool || !lse || !block_table || !cu_seqlens_q ||
       !seq_lens)
     return PKV_ERR_INVALID_ARG;
@@ -205,12 +205,11 @@ pkv_status pkv_attention_key_weights(float* weights_out, const float* weights_in
   const bool any_short = short_q > 0 && (int64_t)num_seqs * max_query_len - num_tokens >=
                                             (int64_t)max_query_len - short_q;
   p.no_short = !any_short;
-  CUtensorMap q_map{}, k_map{};
-  if (!pkv::encode_q_tiles(&q_map, q, num_tokens, num_heads, num_kv_heads, head_dim) ||
-      !pkv::encode_kv_view(&k_map, kv_pool, num_blocks, block_size, num_kv_heads, head_dim, 1))
+  CUtensorMap q_map{};
+  if (!pkv::encode_q_tiles(&q_map, q, num_tokens, num_heads, num_kv_heads, head_dim))
     return PKV_ERR_CUDA;
   if (any_short && pkv::launch_key_weights(p, st) != cudaSuccess) return PKV_ERR_CUDA;
-  return launched(pkv::launch_key_weights_tc(p, q_map, k_map, st));
+  return launched(pkv::launch_key_weights_tc(p, q_map, st));
 }
 
 pkv_status pkv_evict_select(int32_t* kept, float* weights_out, const float* weights,
