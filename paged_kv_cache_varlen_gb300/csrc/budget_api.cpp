@@ -205,11 +205,12 @@ pkv_status pkv_attention_key_weights(float* weights_out, const float* weights_in
   const bool any_short = short_q > 0 && (int64_t)num_seqs * max_query_len - num_tokens >=
                                             (int64_t)max_query_len - short_q;
   p.no_short = !any_short;
-  CUtensorMap q_map{};
-  if (!pkv::encode_q_tiles(&q_map, q, num_tokens, num_heads, num_kv_heads, head_dim))
+  CUtensorMap q_map{}, k_map{};
+  if (!pkv::encode_q_tiles(&q_map, q, num_tokens, num_heads, num_kv_heads, head_dim) ||
+      !pkv::encode_kv_view(&k_map, kv_pool, num_blocks, block_size, num_kv_heads, head_dim, 1))
     return PKV_ERR_CUDA;
   if (any_short && pkv::launch_key_weights(p, st) != cudaSuccess) return PKV_ERR_CUDA;
-  return launched(pkv::launch_key_weights_tc(p, q_map, st));
+  return launched(pkv::launch_key_weights_tc(p, q_map, k_map, st));
 }
 
 pkv_status pkv_evict_select(int32_t* kept, float* weights_out, const float* weights,

@@ -52,7 +52,8 @@ constexpr uint32_t kKCol = kKT * kAcc * kHalf; // then the K tiles: bf16 pairs, 
 static_assert(kKCol + kKT * 64 <= kTmemCols, "accumulators and K tiles fit in TMEM");
 
 struct Bars {
-  uint64_t k_full[kKT];
+  uint64_t k_land, k_read;     // K in shared memory; read by the epilogue warps
+  uint64_t k_full[kKT];        // K in tensor memory
   uint64_t q_full[kStages], q_empty[kStages];
   uint64_t l_full[kStages], l_empty[kStages];
   uint64_t s_full[kKT][kAcc], s_free[kKT][kAcc];
@@ -179,7 +180,8 @@ __device__ __forceinline__ int lse_slot(int col) {
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     key_weights_tc_kernel(const __grid_constant__ CUtensorMap q_map,
-                          const KeyWeightsParams p, const int clusters) {
+                          const __grid_constant__ CUtensorMap k_map, const KeyWeightsParams p,
+                          const int clusters) {
   using Lay = Layout<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -201,8 +203,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   // lengths are known, so that the two loads overlap
   const int my_key = key0 + ((warp >> 2) & 1) * kTM + (warp & 3) * 32 + lane;
   int32_t my_page = -1;
-  if (warp < kEpiWarps && my_key / p.block_size < p.max_blocks)
-    my_page = __ldg(table + my_key / p.block_size);
+  const int box_key = key0 + (lane & 15) * 16;  // (the copying warp: its lane's 16 keys)
+  const int look = warp == kTmaWarp ? box_key : my_key;
+  if (warp <= kTmaWarp && look / p.block_size < p.max_blocks)
+    my_page = __ldg(table + look / p.block_size);
   // the CTAs of a cluster share (request, head, keys): these exits are uniform
   KeyRequest r;
   if (!key_request(p, i, threadIdx.x == 0 && blockIdx.x == 0, &r)) return;
@@ -220,6 +224,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n = (all_tiles - rank + clusters - 1) / clusters;  // tiles rank, rank + clusters, ...
 
   if (warp == kTmaWarp && lane == 0) {
+    prefetch_tmap(&k_map);
+    prefetch_tmap(&q_map);
+    mbar_init(smem_addr(&bars->k_land), 1);
+    mbar_init(smem_addr(&bars->k_read), 8 * nk);
     for (int x = 0; x < kKT; ++x) mbar_init(smem_addr(&bars->k_full[x]), 8);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_addr(&bars->q_full[s]), 1);
@@ -251,12 +259,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   float total = 0.f;  // of one key, in an epilogue thread
 
   if (warp == kTmaWarp) {
+    // ---- K: 16-key boxes into the last Q stages (K tile x: stage 2 + x),
+    // which are free until the epilogue warps have moved K to tensor memory.
+    // Bad pages and keys past the context stay unloaded: their rows meet
+    // nothing else and are never written out
+    const bool in = lane < kKT * kTM / 16 && box_key < r.L && n > 0;
+    const bool good = in && my_page >= 0 && my_page < p.num_blocks;
+    const uint32_t load = __ballot_sync(kFull, good);
+    if (__any_sync(kFull, in && !good) && lane == 0 && rank == 0)
+      set_status(p.status, PKV_DEV_BAD_BLOCK);
+    if (lane == 0)
+      mbar_arrive_expect_tx(smem_addr(&bars->k_land), __popc(load) * Lay::NCH * 16 * 128);
+    __syncwarp();
+    if (good)
+      for (int c = 0; c < Lay::NCH; ++c)
+        tma_load_4d(q_s + (2 + (lane >> 3)) * Lay::TILE_BYTES + c * Lay::CH_BYTES +
+                        (lane & 7) * 16 * 128,
+                    &k_map, smem_addr(&bars->k_land), 0,
+                    my_page * p.block_size + box_key % p.block_size, h, c);
     if (lane == 0) {
-      prefetch_tmap(&q_map);
       const uint32_t bytes = (uint32_t)(Lay::NCH * QT * G * 128);
       int t = 0;
       for (; t < n; ++t) {
         const int s = t % kStages;
+        if (t == 2 && !mbar_wait(smem_addr(&bars->k_read), 0, p.status, abort)) break;
         if (t >= kStages &&
             !mbar_wait(smem_addr(&bars->q_empty[s]), (t / kStages - 1) & 1, p.status, abort))
           break;
@@ -269,6 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // copies in flight land before the CTA can exit
       for (int g = max(0, t - kStages); g < t; ++g)
         mbar_wait(smem_addr(&bars->q_full[g % kStages]), (g / kStages) & 1, nullptr);
+      mbar_wait(smem_addr(&bars->k_land), 0, nullptr);
     }
   } else if (warp >= kMmaWarp) {
     // ---- the products of K tile x. (A lane's next operands wait for the
@@ -365,23 +392,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int x = (warp >> 2) & 1, half = warp >> 3;
     const int wkey = key0 + x * kTM + (warp & 3) * 32;  // the warp's first key
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    if (n > 0) {
-      // half of the key's row to tensor memory, the A operand; rows past the
-      // context or in a bad page are zeros, and never written out
-      const bool good = my_key < r.L && my_page >= 0 && my_page < p.num_blocks;
-      if (my_key < r.L && !good && rank == 0) set_status(p.status, PKV_DEV_BAD_BLOCK);
-      const uint4* src = reinterpret_cast<const uint4*>(
-          p.pool + (((int64_t)(good ? my_page : 0) * p.block_size +
-                     (good ? my_key % p.block_size : 0)) *
-                        p.num_kv_heads + h) * D + half * (D / 2));
+    bool ok = n > 0 && warp_wait(smem_addr(&bars->k_land), 0, p.status, abort);
+    if (ok) {
+      // half of the key's row to tensor memory, the A operand
+      constexpr int U = D / 16;  // 16-byte units of half a row
+      const uint32_t row = (warp & 3) * 32 + lane;
       uint32_t w[D / 4];
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
-        const uint4 v = good ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-        w[4 * c] = v.x;
-        w[4 * c + 1] = v.y;
-        w[4 * c + 2] = v.z;
-        w[4 * c + 3] = v.w;
+      for (uint32_t c = 0; c < U; ++c) {
+        const uint32_t unit = half * U + c;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[4 * c]), "=r"(w[4 * c + 1]), "=r"(w[4 * c + 2]), "=r"(w[4 * c + 3])
+                     : "r"(q_s + (2 + x) * Lay::TILE_BYTES + (unit >> 3) * Lay::CH_BYTES +
+                           row * 128 + (((unit & 7) ^ (row & 7)) << 4))
+                     : "memory");
       }
       const uint32_t at = tmem + lanes + kKCol + (uint32_t)(x * (D / 2) + half * (D / 4));
       if constexpr (D == 128)
@@ -391,7 +415,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&bars->k_full[x]));
+      arrive_if(smem_addr(&bars->k_read), lane == 0);
+      arrive_if(smem_addr(&bars->k_full[x]), lane == 0);
     }
     const float2 sc = make_float2(p.scale_log2, p.scale_log2);
     const uint32_t nl = smem_addr(lse_s + half * kHalf + 4 * (lane & 3));
@@ -404,14 +429,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     float sum4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < 4; ++k) a[k] = make_float2(0.f, 0.f);
-    bool ok = true;
     uint32_t b = half, turn = 0;  // the accumulator, and how often it has been used
     // the first column of this half that sees the warp's first key, and the
     // columns there are from this half's first one on
     int first = (wkey - qpos0 - j0 - rank * QT) * G - half * kHalf;
     int left = (r.qlen - j0 - rank * QT) * G - half * kHalf;
     const int step = clusters * QT * G;
-    for (int t = 0; t < n; ++t, first -= step, left -= step) {
+    for (int t = 0; ok && t < n; ++t, first -= step, left -= step) {
       const uint32_t s = (uint32_t)t % kStages;
       // even lanes: the tile's scores, odd lanes: its lse
       ok = warp_wait((lane & 1) ? l_full0 + s * 8 : s_full0 + b * 8,
@@ -533,7 +557,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D>
-cudaError_t launch(const KeyWeightsParams& p, const CUtensorMap& q_map, cudaStream_t stream) {
+cudaError_t launch(const KeyWeightsParams& p, const CUtensorMap& q_map, const CUtensorMap& k_map,
+                   cudaStream_t stream) {
   auto kernel = key_weights_tc_kernel<D>;
   static SmemLimit limit;
   cudaError_t e = limit.ensure(reinterpret_cast<const void*>(kernel), Layout<D>::BYTES);
@@ -568,14 +593,15 @@ cudaError_t launch(const KeyWeightsParams& p, const CUtensorMap& q_map, cudaStre
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, q_map, p, clusters);
+  return cudaLaunchKernelEx(&cfg, kernel, q_map, k_map, p, clusters);
 }
 
 }  // namespace
 
 cudaError_t launch_key_weights_tc(const KeyWeightsParams& p, const CUtensorMap& q_map,
-                                  cudaStream_t stream) {
-  return p.head_dim == 64 ? launch<64>(p, q_map, stream) : launch<128>(p, q_map, stream);
+                                  const CUtensorMap& k_map, cudaStream_t stream) {
+  return p.head_dim == 64 ? launch<64>(p, q_map, k_map, stream)
+                          : launch<128>(p, q_map, k_map, stream);
 }
 
 }  // namespace pkv

@@ -241,9 +241,10 @@ struct KeyWeightsParams {
 };
 cudaError_t launch_key_weights(const KeyWeightsParams& p, cudaStream_t stream);
 // Requests longer than short_max_q; `q_map` as for the prefill kernel (boxes
-// of 128 / G queries).
+// of 128 / G queries), `k_map` the pool in boxes of 16 keys and one 64-column
+// chunk.
 cudaError_t launch_key_weights_tc(const KeyWeightsParams& p, const CUtensorMap& q_map,
-                                  cudaStream_t stream);
+                                  const CUtensorMap& k_map, cudaStream_t stream);
 
 struct EvictSelectParams {
   int32_t* kept;              // [B][Hkv][max_keep]
