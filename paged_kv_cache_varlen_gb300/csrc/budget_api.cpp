@@ -21,8 +21,8 @@ bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
 
 pkv_status launched(cudaError_t e) { return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA; }
 
-// Grid y dimension: one slice per request.
-constexpr int32_t kMaxSeqs = 65535;
+// Grid y dimension: one slice per request, and one more.
+constexpr int32_t kMaxSeqs = 65534;
 
 }  // namespace
 
@@ -192,6 +192,7 @@ pkv_status pkv_attention_key_weights(float* weights_out, const float* weights_in
   p.decay = decay;
   p.short_max_q = 0;
   p.no_short = 0;
+  p.after_tc = 0;
   p.status = dev_status;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // Requests of up to 32 (query, head) columns keep their queries in a
@@ -209,8 +210,10 @@ pkv_status pkv_attention_key_weights(float* weights_out, const float* weights_in
   if (!pkv::encode_q_tiles(&q_map, q, num_tokens, num_heads, num_kv_heads, head_dim) ||
       !pkv::encode_kv_view(&k_map, kv_pool, num_blocks, block_size, num_kv_heads, head_dim, 1))
     return PKV_ERR_CUDA;
-  if (any_short && pkv::launch_key_weights(p, st) != cudaSuccess) return PKV_ERR_CUDA;
-  return launched(pkv::launch_key_weights_tc(p, q_map, k_map, st));
+  if (pkv::launch_key_weights_tc(p, q_map, k_map, st) != cudaSuccess) return PKV_ERR_CUDA;
+  if (!any_short) return PKV_OK;
+  p.after_tc = 1;
+  return launched(pkv::launch_key_weights(p, st));
 }
 
 pkv_status pkv_evict_select(int32_t* kept, float* weights_out, const float* weights,

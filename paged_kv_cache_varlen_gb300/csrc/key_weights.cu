@@ -9,13 +9,14 @@
 // sum needs nothing from other keys: keys are the rows of S^T = K Q^T, the
 // (query, head) pairs its columns, and a key's sum runs along its own row.
 //
-// A warp takes 16-key tiles of one (request, KV head): the tile's K rows are
-// the A operand of mma.m16n8k16, straight from global memory into registers.
-// The order of the dimensions inside a dot product is free as long as both
-// operands agree, so a lane's 16-byte vector (8 consecutive dimensions of a
-// row) serves as the A fragments of two MMAs and no shared memory or
-// transposition is needed. K is read once; single-token steps are bound by
-// that read.
+// A warp takes a run of 16-key tiles of one (request, KV head): the tile's K
+// rows are the A operand of mma.m16n8k16, straight from global memory into
+// registers. The order of the dimensions inside a dot product is free as long
+// as both operands agree, so a lane's 16-byte vector (8 consecutive
+// dimensions of a row) serves as the A fragments of two MMAs and no shared
+// memory or transposition is needed. The next tile's loads go out as soon as
+// the MMAs have taken this one's registers, before its exponentials. K is read
+// once; single-token steps are bound by that read.
 #include <math.h>
 
 #include "key_weights.cuh"
@@ -25,8 +26,6 @@ namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kWarps = 4;
-constexpr int kChunk = 128;  // keys of one warp's unit of work
-
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
@@ -35,16 +34,30 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// 16 bytes that no other warp reads again.
+__device__ __forceinline__ uint4 ld_once(const uint16_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
 // NT: 8-column tiles held in registers at a time; ONE: every column of a
 // request fits in them (single tokens and short steps), so Q is loaded once.
 template <int D, int NT, bool ONE>
-__global__ void __launch_bounds__(kWarps * 32) key_weights_kernel(const KeyWeightsParams p) {
-  griddep_wait();
+__global__ void __launch_bounds__(kWarps * 32)
+    key_weights_kernel(const KeyWeightsParams p, const int chunk) {
+  // Behind the tcgen05 grid of the same call (which started once everything
+  // before it had finished) the CTAs do not wait for it, so that they fill the
+  // SMs it leaves; one extra CTA does, and with it this grid's completion.
+  if (!p.after_tc || blockIdx.y == p.num_seqs) griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (blockIdx.y == p.num_seqs) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int unit = blockIdx.x * kWarps + warp;
   const int h = unit % p.num_kv_heads;
-  const int key0 = (unit / p.num_kv_heads) * kChunk;
+  const int key0 = (unit / p.num_kv_heads) * chunk;
   const int i = blockIdx.y;
   KeyRequest r;
   if (!key_request(p, i, unit == 0 && lane == 0, &r)) return;
@@ -85,77 +98,103 @@ __global__ void __launch_bounds__(kWarps * 32) key_weights_kernel(const KeyWeigh
       }
     }
   };
-  if (ONE) load_columns(0);
-
   // block ids of the chunk's 16-key tiles, one a lane
   const int32_t* table = p.block_table + (int64_t)i * p.max_blocks;
+  const int tiles = (min(chunk, r.L - key0) + 15) / 16;
   int32_t ids = -1;
-  if (lane < kChunk / 16 && key0 + lane * 16 < r.L)
-    ids = __ldg(table + (key0 + lane * 16) / p.block_size);
+  if (lane < tiles) ids = __ldg(table + (key0 + lane * 16) / p.block_size);
+  const bool lost = lane < tiles && (ids < 0 || ids >= p.num_blocks);
+  if (lost) ids = -1;
+  if (__any_sync(kFull, lost) && lane == 0) set_status(p.status, PKV_DEV_BAD_BLOCK);
   float* out = p.out + ((int64_t)r.row * p.num_kv_heads + h) * p.row_len;
   const float* in = p.in + ((int64_t)r.row * p.num_kv_heads + h) * p.row_len;
-  bool bad = false;
-  for (int t = 0; t < kChunk / 16; ++t) {
-    const int k0 = key0 + t * 16;
-    if (k0 >= r.L) break;
+
+  uint4 ka[KB], kb[KB];  // rows row and row + 8 of a tile
+  auto fetch = [&](int t) {
     const int32_t id = __shfl_sync(kFull, ids, t);
-    if (id < 0 || id >= p.num_blocks) {
-      bad = true;
-      continue;
-    }
-    const uint16_t* k = p.pool + (((int64_t)id * p.block_size + k0 % p.block_size + row) *
-                                      p.num_kv_heads + h) * D;
-    uint4 ka[KB], kb[KB];
+    if (id < 0) return;  // not in the pool: computed on what is there, not stored
+    const uint16_t* src =
+        p.pool + (((int64_t)id * p.block_size + (key0 + t * 16) % p.block_size + row) *
+                      p.num_kv_heads + h) * D + quad * 8;
 #pragma unroll
     for (int b = 0; b < KB; ++b) {
-      ka[b] = *reinterpret_cast<const uint4*>(k + b * 32 + quad * 8);
-      kb[b] = *reinterpret_cast<const uint4*>(k + (int64_t)8 * p.num_kv_heads * D + b * 32 +
-                                              quad * 8);
+      ka[b] = ld_once(src + b * 32);
+      kb[b] = ld_once(src + (int64_t)8 * p.num_kv_heads * D + b * 32);
     }
+  };
+  // c += K (16 keys) Q^T (8 columns of tile n)
+  auto scores = [&](int n, float (&c)[4]) {
+#pragma unroll
+    for (int b = 0; b < KB; ++b) {
+      mma_bf16(c, ka[b].x, kb[b].x, ka[b].y, kb[b].y, qf[n][b].x, qf[n][b].y);
+      mma_bf16(c, ka[b].z, kb[b].z, ka[b].w, kb[b].w, qf[n][b].z, qf[n][b].w);
+    }
+  };
+  auto weights = [&](int n, const float (&c)[4], int k0, float& s0, float& s1) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float w0 = fast_exp2(fmaf(c[e], p.scale_log2, -lse2[n][e]));
+      const float w1 = fast_exp2(fmaf(c[2 + e], p.scale_log2, -lse2[n][e]));
+      s0 += k0 + row <= last[n][e] ? w0 : 0.f;
+      s1 += k0 + row + 8 <= last[n][e] ? w1 : 0.f;
+    }
+  };
+#pragma unroll
+  for (int b = 0; b < KB; ++b) ka[b] = kb[b] = make_uint4(0, 0, 0, 0);
+  fetch(0);
+  if (ONE) load_columns(0);
+  for (int t = 0; t < tiles; ++t) {
+    const int k0 = key0 + t * 16;
+    const bool there = __shfl_sync(kFull, ids, t) >= 0;
+    const int key = k0 + row + quad * 8;
+    const bool mine = there && quad < 2 && key < r.L;
+    float before = 0.f;
+    if (mine && key < r.prior && p.decay != 0.f) before = p.decay * in[key];
     float s0 = 0.f, s1 = 0.f;  // keys k0 + row, k0 + row + 8
-    // the first column group that sees the tile's first key
-    const int c_first = ONE ? 0 : max(0, k0 - qpos0) * G / (NT * 8) * (NT * 8);
-    for (int c0 = c_first; c0 < cols; c0 += NT * 8) {
-      if (!ONE) load_columns(c0);
+    if (ONE) {
+      float c[NT][4];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
+        c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
+        scores(n, c[n]);
+      }
+      if (t + 1 < tiles) fetch(t + 1);
 #pragma unroll
-        for (int b = 0; b < KB; ++b) {
-          mma_bf16(c, ka[b].x, kb[b].x, ka[b].y, kb[b].y, qf[n][b].x, qf[n][b].y);
-          mma_bf16(c, ka[b].z, kb[b].z, ka[b].w, kb[b].w, qf[n][b].z, qf[n][b].w);
-        }
+      for (int n = 0; n < NT; ++n) weights(n, c[n], k0, s0, s1);
+    } else {
+      // from the first column group that sees the tile's first key
+      for (int c0 = max(0, k0 - qpos0) * G / (NT * 8) * (NT * 8); c0 < cols; c0 += NT * 8) {
+        load_columns(c0);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float w0 = fast_exp2(fmaf(c[e], p.scale_log2, -lse2[n][e]));
-          const float w1 = fast_exp2(fmaf(c[2 + e], p.scale_log2, -lse2[n][e]));
-          s0 += k0 + row <= last[n][e] ? w0 : 0.f;
-          s1 += k0 + row + 8 <= last[n][e] ? w1 : 0.f;
+        for (int n = 0; n < NT; ++n) {
+          float c[4] = {0.f, 0.f, 0.f, 0.f};
+          scores(n, c);
+          weights(n, c, k0, s0, s1);
         }
       }
-      if (ONE) break;
+      if (t + 1 < tiles) fetch(t + 1);
     }
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
       s0 += __shfl_xor_sync(kFull, s0, o);
       s1 += __shfl_xor_sync(kFull, s1, o);
     }
-    if (quad < 2) {
-      const int key = k0 + row + quad * 8;
-      if (key < r.L) {
-        const float s = quad ? s1 : s0;
-        out[key] = key < r.prior && p.decay != 0.f ? fmaf(p.decay, in[key], s) : s;
-      }
-    }
+    if (mine) out[key] = before + (quad ? s1 : s0);
   }
-  if (bad && lane == 0) set_status(p.status, PKV_DEV_BAD_BLOCK);
 }
 
 template <int D, int NT, bool ONE>
 cudaError_t launch(const KeyWeightsParams& p, cudaStream_t stream) {
-  const int64_t units = ((int64_t)p.max_seq_len + kChunk - 1) / kChunk * p.num_kv_heads;
+  // Keys of a warp's unit: 128 amortise its start (64 x 512-4096 keys, 8 KV
+  // heads: 49.5 us; 64 keys 50.3, 256 54.2); fewer while that leaves less
+  // than about two units for each of the GPU's resident warps (13 requests of
+  // up to 5000 keys, 4 KV heads, beside chunks: 66.0 us with 64, 69.4 with 128).
+  int chunk = 128;
+  auto units_of = [&](int c) { return ((int64_t)p.max_seq_len + c - 1) / c * p.num_kv_heads; };
+  while (chunk > 16 && units_of(chunk) * p.num_seqs < 8192) chunk /= 2;
+  const int64_t units = units_of(chunk);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((units + kWarps - 1) / kWarps), (unsigned)p.num_seqs);
+  cfg.gridDim = dim3((unsigned)((units + kWarps - 1) / kWarps), (unsigned)p.num_seqs + (p.after_tc ? 1u : 0u));
   cfg.blockDim = dim3(kWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -163,7 +202,7 @@ cudaError_t launch(const KeyWeightsParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, key_weights_kernel<D, NT, ONE>, p);
+  return cudaLaunchKernelEx(&cfg, key_weights_kernel<D, NT, ONE>, p, chunk);
 }
 
 template <int D>

@@ -237,6 +237,7 @@ struct KeyWeightsParams {
   // not launched, the latter flags a short request as PKV_DEV_BAD_LENGTHS
   int32_t short_max_q;
   int32_t no_short;
+  int32_t after_tc;           // mma.sync grid: launched right behind the tcgen05 grid
   int32_t* status;
 };
 cudaError_t launch_key_weights(const KeyWeightsParams& p, cudaStream_t stream);

@@ -130,7 +130,7 @@ def _weights(lib, **over):
 
 
 @pytest.mark.parametrize("over,status", [
-    ({"tokens": -1}, 1), ({"seqs": 0}, 1), ({"seqs": 65536, "num_rows": 65536}, 2),
+    ({"tokens": -1}, 1), ({"seqs": 0}, 1), ({"seqs": 65535, "num_rows": 65535}, 2),
     ({"out": None}, 1), ({"inp": None}, 1), ({"q": None}, 1), ({"pool": None}, 1),
     ({"lse": None}, 1), ({"table": None}, 1), ({"cu": None}, 1), ({"lens": None}, 1),
     ({"heads": 5}, 1), ({"max_blocks": 0}, 1), ({"num_rows": 0}, 1), ({"num_rows": 1}, 1),
@@ -159,7 +159,7 @@ def _select(lib, **over):
 
 @pytest.mark.parametrize("over,status", [
     ({"seqs": -1}, 1), ({"kv_heads": 0}, 1), ({"sink": -1}, 1), ({"recent": -1}, 1),
-    ({"max_len": -1}, 1), ({"max_keep": -1}, 1), ({"seqs": 65536, "num_rows": 65536}, 2),
+    ({"max_len": -1}, 1), ({"max_keep": -1}, 1), ({"seqs": 65535, "num_rows": 65535}, 2),
     ({"kept": None}, 1), ({"weights": None}, 1), ({"lens": None}, 1), ({"keep": None}, 1),
     ({"row_len": 63}, 1), ({"num_rows": 1}, 1), ({"out": 2 * A}, 1), ({"out": 2 * A + 1020}, 1),
     ({"out": 5 * A, "max_keep": 65}, 1), ({"weights": 2 * A + 2}, 1),
@@ -183,7 +183,7 @@ def _compact(lib, **over):
 
 @pytest.mark.parametrize("over,status", [
     ({"seqs": -1}, 1), ({"kv_heads": 0}, 1), ({"bs": 0}, 1), ({"blocks": 0}, 1),
-    ({"max_src": -1}, 1), ({"max_keep": -1}, 1), ({"seqs": 65536}, 2),
+    ({"max_src": -1}, 1), ({"max_keep": -1}, 1), ({"seqs": 65535}, 2),
     ({"pool": None}, 1), ({"src": None}, 1), ({"dst": None}, 1), ({"kept": None}, 1),
     ({"keep": None}, 1), ({"pool": A + 8}, 1), ({"head_dim": 100}, 2), ({"head_dim": 1024}, 2),
     ({"max_src": 1 << 28}, 2),
