@@ -226,7 +226,8 @@ pkv_status pkv_evict_select(int32_t* kept, float* weights_out, const float* weig
       num_sink < 0 || num_recent < 0)
     return PKV_ERR_INVALID_ARG;
   if (num_seqs == 0 || max_keep_len == 0) return PKV_OK;
-  if (num_seqs > kMaxSeqs) return PKV_ERR_UNSUPPORTED;
+  if (num_seqs > kMaxSeqs || num_kv_heads > INT32_MAX / 8) return PKV_ERR_UNSUPPORTED;
+  if (max_seq_len > INT32_MAX / 2) return PKV_ERR_UNSUPPORTED;  // indexes of a padded row
   if (!kept || !weights || !seq_lens || !keep_lens) return PKV_ERR_INVALID_ARG;
   if (row_len < max_seq_len || (weights_out && row_len < max_keep_len)) return PKV_ERR_INVALID_ARG;
   if (!weight_rows && num_rows < num_seqs) return PKV_ERR_INVALID_ARG;
@@ -269,6 +270,8 @@ pkv_status pkv_evict_compact(void* kv_pool, const int32_t* src_table, int32_t ma
   if ((int64_t)max_src_blocks * block_size > INT32_MAX ||
       (int64_t)max_dst_blocks * block_size > INT32_MAX)
     return PKV_ERR_UNSUPPORTED;
+  // rows of a request are counted in 32 bits
+  if ((int64_t)max_keep_len * num_kv_heads > INT32_MAX / 2) return PKV_ERR_UNSUPPORTED;
   pkv::EvictCompactParams p;
   p.pool = static_cast<uint4*>(kv_pool);
   p.src_table = src_table;
