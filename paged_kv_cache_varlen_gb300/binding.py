@@ -130,8 +130,14 @@ def _ptr(t: torch.Tensor | None) -> int | None:
     return None if t is None else t.data_ptr()
 
 
+# the current stream's handle without the Stream object around it (2 us less)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream, device) -> int:
     if stream is None:
+        if _raw_stream is not None and device.index is not None:
+            return _raw_stream(device.index)
         stream = torch.cuda.current_stream(device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -630,46 +636,57 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str = "
     return inv_freq, float(factor.value)
 
 
-def _need_rows(t: torch.Tensor, heads: int, head_dim: int, tokens: int, name: str) -> int:
+# The calls below are made once a layer and step, on a handful of small tensors:
+# their checks are written to cost little when everything is in order.
+
+
+def _need_on(t, dtype, ndim: int, device, name: str) -> None:
+    """:func:`_need`, and on ``device``."""
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.dim() == ndim and t.is_contiguous()
+            and t.device == device):
+        return
+    _need(t, dtype, ndim, name)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device} as the others")
+
+
+def _need_rows(t, shape, device, name: str) -> int:
     """Check a [T,heads,D] bf16 tensor whose tokens may be any distance apart
     (a column range of a projection's output); returns that distance."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
+    if t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}, got {t.device}")
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if tuple(t.shape) != (tokens, heads, head_dim):
-        raise ValueError(f"{name} must be [{tokens}, {heads}, {head_dim}], got {tuple(t.shape)}")
-    st = t.stride()
-    if (head_dim > 1 and st[2] != 1) or (heads > 1 and st[1] != head_dim):
-        raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {st}")
-    return st[0] if tokens > 1 else heads * head_dim
-
-
-def _same_device(device, *tensors) -> None:
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"all tensors must be on one device, got {t.device} and {device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    tokens, heads, head_dim = shape
+    far, near, one = t.stride()
+    if (head_dim > 1 and one != 1) or (heads > 1 and near != head_dim):
+        raise ValueError(f"{name}: the heads of a token must be contiguous, got strides "
+                         f"{t.stride()}")
+    return far if tokens > 1 else heads * head_dim
 
 
 def _on_stream(stream, device):
     """The stream as torch sees it, for allocations that the call's work uses."""
-    if stream is None or isinstance(stream, torch.cuda.Stream):
-        return torch.cuda.stream(stream)
-    return torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=device))
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
 
 
 def _run(what: str, device, stream, *args) -> None:
     """Call ``pkv_<what>`` with ``device`` current and the stream last."""
-    fn = getattr(load_library(), "pkv_" + what)
+    fn = getattr(_handle or load_library(), "pkv_" + what)
     raw = _stream(stream, device)
     if torch.cuda.current_device() == device.index:
         st = fn(*args, raw)
     else:
         with torch.cuda.device(device):
             st = fn(*args, raw)
-    _check(st, what)
+    if st:
+        _check(st, what)
 
 
 def rope_kv_cache_write(q: torch.Tensor, kv_pool: torch.Tensor, k_new: torch.Tensor,
@@ -686,9 +703,10 @@ def rope_kv_cache_write(q: torch.Tensor, kv_pool: torch.Tensor, k_new: torch.Ten
     ``slot_mapping`` (-1: nothing is written). Returns ``q_out`` [T,H,D],
     which may be a dense q itself."""
     _need(kv_pool, torch.bfloat16, 5, "kv_pool")
-    _need(positions, torch.int32, 1, "positions")
-    _need(slot_mapping, torch.int32, 1, "slot_mapping")
-    _need(inv_freq, torch.float64, 1, "inv_freq")
+    device = kv_pool.device
+    _need_on(positions, torch.int32, 1, device, "positions")
+    _need_on(slot_mapping, torch.int32, 1, device, "slot_mapping")
+    _need_on(inv_freq, torch.float64, 1, device, "inv_freq")
     _, nb, bs, hkv, d = kv_pool.shape
     t = slot_mapping.shape[0]
     if positions.shape[0] != t:
@@ -696,27 +714,27 @@ def rope_kv_cache_write(q: torch.Tensor, kv_pool: torch.Tensor, k_new: torch.Ten
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a [num_tokens, num_heads, head_dim] tensor")
     h = q.shape[1]
-    qs = _need_rows(q, h, d, t, "q")
-    ks = _need_rows(k_new, hkv, d, t, "k_new")
-    vs = _need_rows(v_new, hkv, d, t, "v_new")
-    device = kv_pool.device
-    if q_out is None:
-        with _on_stream(stream, device):
-            q_out = torch.empty((t, h, d), dtype=torch.bfloat16, device=device)
-    else:
-        _need(q_out, torch.bfloat16, 3, "q_out")
+    qs = _need_rows(q, (t, h, d), device, "q")
+    ks = _need_rows(k_new, (t, hkv, d), device, "k_new")
+    vs = _need_rows(v_new, (t, hkv, d), device, "v_new")
+    if q_out is not None:
+        _need_on(q_out, torch.bfloat16, 3, device, "q_out")
         if q_out.shape != q.shape:
             raise ValueError("q_out must have the shape of q")
+    elif stream is None:
+        q_out = torch.empty((t, h, d), dtype=torch.bfloat16, device=device)
+    else:
+        with _on_stream(stream, device):
+            q_out = torch.empty((t, h, d), dtype=torch.bfloat16, device=device)
     if dev_status is not None:
-        _need(dev_status, torch.int32, 1, "dev_status")
-    _same_device(device, q, k_new, v_new, positions, slot_mapping, inv_freq, q_out, dev_status)
+        _need_on(dev_status, torch.int32, 1, device, "dev_status")
     if debug_checks.enabled():
         debug_checks.check_slot_mapping(slot_mapping, num_blocks=nb, block_size=bs)
         debug_checks.check_positions(positions)
-    _run("rope_kv_cache_write", device, stream, _ptr(q_out), _ptr(kv_pool), _ptr(q), _ptr(k_new),
-         _ptr(v_new), qs, ks, vs, _ptr(positions), _ptr(slot_mapping), _ptr(inv_freq),
-         float(factor), int(bool(interleaved)), t, h, hkv, d, 2 * inv_freq.shape[0], nb, bs,
-         _ptr(dev_status))
+    _run("rope_kv_cache_write", device, stream, q_out.data_ptr(), kv_pool.data_ptr(),
+         q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), qs, ks, vs, positions.data_ptr(),
+         slot_mapping.data_ptr(), inv_freq.data_ptr(), factor, bool(interleaved), t, h, hkv, d,
+         2 * inv_freq.shape[0], nb, bs, _ptr(dev_status))
     return q_out
 
 
@@ -735,18 +753,19 @@ def attention_key_weights(q: torch.Tensor, kv_pool: torch.Tensor, lse: torch.Ten
     ``weight_rows[i]`` (default i). Keys at or behind ``prior_lens[i]``
     (default: the step's own tokens) start from zero; ``decay`` scales the
     others' old sums. Writes and returns ``out`` (default: ``weights``, in place)."""
-    _need(q, torch.bfloat16, 3, "q")
     _need(kv_pool, torch.bfloat16, 5, "kv_pool")
-    _need(lse, torch.float32, 2, "lse")
-    _need(block_table, torch.int32, 2, "block_table")
-    _need(cu_seqlens, torch.int32, 1, "cu_seqlens")
-    _need(seq_lens, torch.int32, 1, "seq_lens")
-    _need(weights, torch.float32, 3, "weights")
+    device = kv_pool.device
+    _need_on(q, torch.bfloat16, 3, device, "q")
+    _need_on(lse, torch.float32, 2, device, "lse")
+    _need_on(block_table, torch.int32, 2, device, "block_table")
+    _need_on(cu_seqlens, torch.int32, 1, device, "cu_seqlens")
+    _need_on(seq_lens, torch.int32, 1, device, "seq_lens")
+    _need_on(weights, torch.float32, 3, device, "weights")
     t, h, d = q.shape
     _, nb, bs, hkv, d2 = kv_pool.shape
     if d2 != d:
         raise ValueError("q and kv_pool head_dim differ")
-    if tuple(lse.shape) != (t, h):
+    if lse.shape != (t, h):
         raise ValueError("lse must be [num_tokens, num_heads]")
     b = seq_lens.shape[0]
     if cu_seqlens.shape[0] != b + 1 or block_table.shape[0] != b:
@@ -757,19 +776,16 @@ def attention_key_weights(q: torch.Tensor, kv_pool: torch.Tensor, lse: torch.Ten
     if out is None:
         out = weights
     else:
-        _need(out, torch.float32, 3, "out")
+        _need_on(out, torch.float32, 3, device, "out")
         if out.shape != weights.shape:
             raise ValueError("out must have the shape of weights")
     for x, name in ((weight_rows, "weight_rows"), (prior_lens, "prior_lens")):
         if x is not None:
-            _need(x, torch.int32, 1, name)
+            _need_on(x, torch.int32, 1, device, name)
             if x.shape[0] != b:
                 raise ValueError(f"{name} must have one entry per request")
     if dev_status is not None:
-        _need(dev_status, torch.int32, 1, "dev_status")
-    device = kv_pool.device
-    _same_device(device, q, lse, block_table, cu_seqlens, seq_lens, weights, out, weight_rows,
-                 prior_lens, dev_status)
+        _need_on(dev_status, torch.int32, 1, device, "dev_status")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if debug_checks.enabled():
@@ -777,11 +793,11 @@ def attention_key_weights(q: torch.Tensor, kv_pool: torch.Tensor, lse: torch.Ten
             cu_seqlens, seq_lens, block_table, num_tokens=t, max_query_len=int(max_query_len),
             max_seq_len=int(max_seq_len), num_blocks=nb, block_size=bs)
         debug_checks.check_weight_rows(weight_rows, num_seqs=b, num_rows=rows)
-    _run("attention_key_weights", device, stream, _ptr(out), _ptr(weights), _ptr(q),
-         _ptr(kv_pool), _ptr(lse), _ptr(block_table), block_table.shape[1], _ptr(cu_seqlens),
-         _ptr(seq_lens), _ptr(prior_lens), _ptr(weight_rows), rows, row_len, b, t,
-         int(max_query_len), int(max_seq_len), h, hkv, d, bs, nb, float(scale), float(decay),
-         _ptr(dev_status))
+    _run("attention_key_weights", device, stream, out.data_ptr(), weights.data_ptr(),
+         q.data_ptr(), kv_pool.data_ptr(), lse.data_ptr(), block_table.data_ptr(),
+         block_table.shape[1], cu_seqlens.data_ptr(), seq_lens.data_ptr(), _ptr(prior_lens),
+         _ptr(weight_rows), rows, row_len, b, t, int(max_query_len), int(max_seq_len), h, hkv, d,
+         bs, nb, scale, decay, _ptr(dev_status))
     return out
 
 
@@ -799,37 +815,39 @@ def evict_select(weights: torch.Tensor, seq_lens: torch.Tensor, keep_lens: torch
     behind that); ``weights_out``, when given, receives the kept keys' weights
     at the front of the same rows."""
     _need(weights, torch.float32, 3, "weights")
-    _need(seq_lens, torch.int32, 1, "seq_lens")
-    _need(keep_lens, torch.int32, 1, "keep_lens")
+    device = weights.device
+    _need_on(seq_lens, torch.int32, 1, device, "seq_lens")
+    _need_on(keep_lens, torch.int32, 1, device, "keep_lens")
     rows, hkv, row_len = weights.shape
     b = seq_lens.shape[0]
     if keep_lens.shape[0] != b:
         raise ValueError("seq_lens and keep_lens differ in length")
-    device = weights.device
-    if kept is None:
-        with _on_stream(stream, device):
-            kept = torch.full((b, hkv, int(max_keep_len)), -1, dtype=torch.int32, device=device)
-    else:
-        _need(kept, torch.int32, 3, "kept")
-        if tuple(kept.shape) != (b, hkv, int(max_keep_len)):
+    shape = (b, hkv, int(max_keep_len))
+    if kept is not None:
+        _need_on(kept, torch.int32, 3, device, "kept")
+        if kept.shape != shape:
             raise ValueError("kept must be [num_seqs, num_kv_heads, max_keep_len]")
+    elif stream is None:
+        kept = torch.full(shape, -1, dtype=torch.int32, device=device)
+    else:
+        with _on_stream(stream, device):
+            kept = torch.full(shape, -1, dtype=torch.int32, device=device)
     if weights_out is not None:
-        _need(weights_out, torch.float32, 3, "weights_out")
+        _need_on(weights_out, torch.float32, 3, device, "weights_out")
         if weights_out.shape != weights.shape:
             raise ValueError("weights_out must have the shape of weights")
     if weight_rows is not None:
-        _need(weight_rows, torch.int32, 1, "weight_rows")
+        _need_on(weight_rows, torch.int32, 1, device, "weight_rows")
         if weight_rows.shape[0] != b:
             raise ValueError("weight_rows must have one entry per request")
     if dev_status is not None:
-        _need(dev_status, torch.int32, 1, "dev_status")
-    _same_device(device, seq_lens, keep_lens, kept, weights_out, weight_rows, dev_status)
+        _need_on(dev_status, torch.int32, 1, device, "dev_status")
     if debug_checks.enabled():
         debug_checks.check_weight_rows(weight_rows, num_seqs=b, num_rows=rows)
         debug_checks.check_keep_lens(seq_lens, keep_lens, max_seq_len=int(max_seq_len),
                                      max_keep_len=int(max_keep_len))
-    _run("evict_select", device, stream, _ptr(kept), _ptr(weights_out), _ptr(weights),
-         _ptr(seq_lens), _ptr(keep_lens), _ptr(weight_rows), rows, row_len, b, hkv,
+    _run("evict_select", device, stream, kept.data_ptr(), _ptr(weights_out), weights.data_ptr(),
+         seq_lens.data_ptr(), keep_lens.data_ptr(), _ptr(weight_rows), rows, row_len, b, hkv,
          int(max_seq_len), int(max_keep_len), int(num_sink), int(num_recent), _ptr(dev_status))
     return kept, weights_out
 
@@ -841,23 +859,22 @@ def evict_compact(kv_pool: torch.Tensor, src_table: torch.Tensor, dst_table: tor
     the blocks of ``src_table`` to the front of those of ``dst_table``, which
     must be other blocks (``BlockManager.evict_step`` hands both out)."""
     _need(kv_pool, torch.bfloat16, 5, "kv_pool")
-    _need(src_table, torch.int32, 2, "src_table")
-    _need(dst_table, torch.int32, 2, "dst_table")
-    _need(kept, torch.int32, 3, "kept")
-    _need(keep_lens, torch.int32, 1, "keep_lens")
+    device = kv_pool.device
+    _need_on(src_table, torch.int32, 2, device, "src_table")
+    _need_on(dst_table, torch.int32, 2, device, "dst_table")
+    _need_on(kept, torch.int32, 3, device, "kept")
+    _need_on(keep_lens, torch.int32, 1, device, "keep_lens")
     _, nb, bs, hkv, d = kv_pool.shape
-    b = keep_lens.shape[0]
-    if kept.shape[:2] != (b, hkv):
+    b, heads, max_keep = kept.shape
+    if b != keep_lens.shape[0] or heads != hkv:
         raise ValueError("kept must be [num_seqs, num_kv_heads, max_keep_len]")
     if src_table.shape[0] != b or dst_table.shape[0] != b:
         raise ValueError("src_table and dst_table must have one row per request")
     if dev_status is not None:
-        _need(dev_status, torch.int32, 1, "dev_status")
-    device = kv_pool.device
-    _same_device(device, src_table, dst_table, kept, keep_lens, dev_status)
+        _need_on(dev_status, torch.int32, 1, device, "dev_status")
     if debug_checks.enabled():
         debug_checks.check_compaction(src_table, dst_table, kept, keep_lens, num_blocks=nb,
                                       block_size=bs)
-    _run("evict_compact", device, stream, _ptr(kv_pool), _ptr(src_table), src_table.shape[1],
-         _ptr(dst_table), dst_table.shape[1], _ptr(kept), kept.shape[2], _ptr(keep_lens), b, hkv,
-         d, bs, nb, _ptr(dev_status))
+    _run("evict_compact", device, stream, kv_pool.data_ptr(), src_table.data_ptr(),
+         src_table.shape[1], dst_table.data_ptr(), dst_table.shape[1], kept.data_ptr(), max_keep,
+         keep_lens.data_ptr(), b, hkv, d, bs, nb, _ptr(dev_status))

@@ -15,22 +15,29 @@ constexpr uint32_t kFull = 0xffffffffu;
 // when a digit's bin is taken whole), then one pass that writes the keys above
 // it and the first of those equal to it, in index order.
 //
-// A row (request, KV head) is read once: its keys stay in the registers of the
-// 512 threads of one CTA, or of a cluster of 2, 4 or 8 when it is long or the
-// rows are few; the CTAs' histograms are added up over distributed shared
-// memory. Rows past 131072 keys are read again for each digit (from L2). The
-// row's 4 bytes a key are little: the passes' barriers and the histograms'
-// atomics bound it.
+// A row (request, KV head) is read once into the shared memory of one CTA, or
+// of a cluster of 2, 4 or 8 when it is long or the rows are few; the CTAs'
+// histograms are added up in the first one's. Rows of more than kStaged keys a
+// CTA are read again in each pass (from L2). The row's 4 bytes a key are
+// little: the passes' barriers and the histograms' atomics bound it.
 // ---------------------------------------------------------------------------
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kScanThreads = 512;  // four bins each
 constexpr int kMaxCluster = 8;
+constexpr int kStaged = 40960;     // keys of a CTA's share that shared memory holds
+// Copies of the histogram, one for each lane modulo kCopies: attention weights
+// crowd into a few dozen bins of the first digit. Each starts 8 banks on, so
+// that a bin's copies lie in different banks.
+constexpr int kCopies = 2;
+constexpr int kCopyStride = kBins + 8;
 
 // Order-preserving key of a weight: larger weights have larger keys, -0 and
-// +0 the same one, a NaN the largest.
+// +0 the same one, a NaN the largest but kProtected, which stands for the keys
+// that are kept whatever their weight (and so need no care of their own: the
+// selection is the `keep` largest keys of the row).
+constexpr uint32_t kProtected = 0xffffffffu;
 __device__ __forceinline__ uint32_t weight_key(float w) {
-  if (w != w) return 0xffffffffu;
+  if (w != w) return 0xfffffffeu;
   const uint32_t b = __float_as_uint(w + 0.f);
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
@@ -41,29 +48,41 @@ __device__ __forceinline__ void cluster_arrive() {
 __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// The int at the same shared-memory offset of cluster CTA `rank`.
-__device__ __forceinline__ int ld_cluster(const int* p, int rank) {
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  cluster_arrive();
+  cluster_wait();
+}
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, int rank) {
   uint32_t remote;
-  int v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_addr(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
-  return v;
+  return remote;
+}
+// To the same shared-memory offset of cluster CTA `rank`.
+__device__ __forceinline__ void st_cluster(const int* p, int rank, int v) {
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(cluster_addr(p, rank)), "r"(v) : "memory");
+}
+__device__ __forceinline__ void add_cluster(const int* p, int rank, int v) {
+  asm volatile("red.shared::cluster.add.s32 [%0], %1;" ::"r"(cluster_addr(p, rank)), "r"(v)
+               : "memory");
 }
 
-// K: 32-key steps of a warp's share held in registers; 0: the row is read
-// from memory in every pass.
-template <int K>
-__global__ void __launch_bounds__(kSelThreads)
+// Staged: the CTA's share of the row is kept in shared memory.
+template <bool Staged>
+__global__ void __launch_bounds__(1024, 2)
     evict_select_kernel(const EvictSelectParams p, const int clusters) {
-  __shared__ int hist[kBins];
-  __shared__ int warp_sum[kSelWarps];
-  __shared__ int found_bin, found_left, found_whole;
-  __shared__ int warp_gt[kSelWarps], warp_eq[kSelWarps];
-  __shared__ int cta_count[2];
+  extern __shared__ __align__(16) uint32_t smem[];
+  int* acc = reinterpret_cast<int*>(smem);  // [kBins] of the cluster, in rank 0 (none without)
+  uint32_t* staged = smem + (clusters > 1 ? kBins : 0);
+  __shared__ __align__(16) int hist[kCopies * kCopyStride];
+  __shared__ int warp_sum[kScanThreads / 32];
+  __shared__ int found[3];  // bin, places left in it, whether it is taken whole
+  __shared__ int warp_gt[32], warp_eq[32];
+  __shared__ int cta_gt[kMaxCluster], cta_eq[kMaxCluster];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   griddep_wait();
   griddep_launch_dependents();
   const int rank = blockIdx.x % clusters, h = blockIdx.x / clusters, i = blockIdx.y;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int L = __ldg(p.seq_lens + i), keep = __ldg(p.keep_lens + i);
   const int row = p.rows ? __ldg(p.rows + i) : i;
   // the CTAs of a cluster share the row: these exits are uniform
@@ -80,173 +99,179 @@ __global__ void __launch_bounds__(kSelThreads)
   const float* w = p.weights + at;
   const int recent = min(p.num_recent, keep);
   const int sink = min(p.num_sink, keep - recent);
-  const int lo = sink, hi = L - recent;  // keys [lo, hi) compete for `left` places
-  int left = keep - sink - recent;
-  const bool any = left > 0;
+  int left = keep;  // places for the keys that match the digits found so far
 
   // the warp's share of the row: `steps` times 32 keys, in index order
-  const int per_step = clusters * kSelThreads;
+  const int per_step = clusters * (int)blockDim.x;
   const int steps = (int)(((int64_t)L + per_step - 1) / per_step);
-  const int64_t first = (int64_t)(rank * kSelWarps + warp) * steps * 32;
+  const int64_t first = (int64_t)(rank * warps + warp) * steps * 32;
   const int base = (int)min((int64_t)L, first) + lane;
   const int end = (int)min((int64_t)L, first + (int64_t)steps * 32);
-  float v[K > 0 ? K : 1];
-  if (K > 0) {
-#pragma unroll
-    for (int j = 0; j < K; ++j) v[j] = base + j * 32 < end ? __ldg(w + base + j * 32) : 0.f;
-  }
-  // f(index, weight) of the lane's keys, in step with the whole warp
-  auto for_keys = [&](auto f) {
-    if (K > 0) {
-#pragma unroll
-      for (int j = 0; j < K; ++j)
-        if (j < steps) f(base + j * 32, v[j]);
-    } else {
-      for (int j = 0; j < steps; ++j)
-        f(base + j * 32, base + j * 32 < end ? __ldg(w + base + j * 32) : 0.f);
-    }
+  auto key_of = [&](int k, float x) {
+    return k < sink || k >= L - recent ? kProtected : weight_key(x);
   };
-  auto sync_cluster = [&] {
-    __syncwarp();
-    if (clusters > 1) {
-      cluster_arrive();
-      cluster_wait();
-    } else {
-      __syncthreads();
-    }
+  auto count = [&](uint32_t bin) {
+    atomicAdd(&hist[(lane % kCopies) * kCopyStride + bin], 1);
+  };
+  auto clear = [&] {
+    for (int b = threadIdx.x; b < kCopies * kCopyStride / 4; b += blockDim.x)
+      reinterpret_cast<int4*>(hist)[b] = make_int4(0, 0, 0, 0);
+  };
+  clear();
+  if (clusters > 1)
+    for (int b = threadIdx.x; b < kBins; b += blockDim.x) acc[b] = 0;
+  __syncthreads();
+  // the keys, and the histogram of their first digit, in one pass
+  uint32_t* mine = staged + warp * steps * 32 + lane;
+  constexpr int kBatch = 8;  // loads in flight
+  for (int k = base, j = 0; k < end; k += kBatch * 32, j += kBatch * 32) {
+    float x[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) x[b] = k + b * 32 < end ? __ldg(w + k + b * 32) : 0.f;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+      if (k + b * 32 < end) {
+        const uint32_t key = key_of(k + b * 32, x[b]);
+        if (Staged) mine[j + b * 32] = key;
+        count(key >> 21);
+      }
+  }
+  if (clusters > 1) cluster_sync();  // every CTA's acc is clear
+  // f(index, key) of the lane's keys (each lane reads what it wrote)
+  auto for_keys = [&](auto f) {
+#pragma unroll 4
+    for (int k = base, j = 0; k < end; k += 32, j += 32) f(k, Staged ? mine[j] : key_of(k, __ldg(w + k)));
   };
 
-  // the left-th largest key among [lo, hi): its digits from the top
+  // the keep-th largest key: its digits from the top
   uint32_t prefix = 0, known = 0;  // the digits found, and their bits
-  for (int digit = 0; digit < 3 && any; ++digit) {
+  for (int digit = 0; digit < 3; ++digit) {
     const int shift = digit == 0 ? 21 : (digit == 1 ? 10 : 0);
     const uint32_t mask = digit == 2 ? 1023u : 2047u;
-    for (int b = threadIdx.x; b < kBins; b += kSelThreads) hist[b] = 0;
+    if (digit > 0) {
+      clear();
+      __syncthreads();
+      for_keys([&](int, uint32_t key) {
+        if ((key & known) == prefix) count((key >> shift) & mask);
+      });
+    }
     __syncthreads();
-    for_keys([&](int k, float x) {
-      const uint32_t key = weight_key(x);
-      if (k >= lo && k < hi && k < end && (key & known) == prefix)
-        atomicAdd(&hist[(key >> shift) & mask], 1);
-    });
-    sync_cluster();
-    // a thread has 4 bins, counted from the largest; a scan over the threads
-    constexpr int kPer = kBins / kSelThreads;
-    const int top = kBins - 1 - threadIdx.x * kPer;
-    int n[kPer], mine = 0;
+    // a thread has 4 bins, counted from the largest
+    const int top = kBins - 1 - threadIdx.x * 4;
+    int n[4] = {0, 0, 0, 0};
+    if (threadIdx.x < kScanThreads) {
 #pragma unroll
-    for (int b = 0; b < kPer; ++b) {
-      n[b] = hist[top - b];
-      if (clusters > 1) {
-        n[b] = 0;
-        for (int c = 0; c < clusters; ++c) n[b] += ld_cluster(hist + top - b, c);
+      for (int c = 0; c < kCopies; ++c) {
+        const int4 x = *reinterpret_cast<const int4*>(hist + c * kCopyStride + top - 3);
+        n[0] += x.w;
+        n[1] += x.z;
+        n[2] += x.y;
+        n[3] += x.x;
       }
-      mine += n[b];
     }
-    __syncwarp();
-    if (clusters > 1) cluster_arrive();  // done with the others' histograms
-    int incl = mine;
+    if (clusters > 1) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(kFull, incl, o);
-      if (lane >= o) incl += x;
+      for (int b = 0; b < 4; ++b)
+        if (n[b] != 0) add_cluster(acc + top - b, 0, n[b]);
+      cluster_sync();
+      if (rank == 0 && threadIdx.x < kScanThreads) {
+        int4* own = reinterpret_cast<int4*>(acc + top - 3);
+        const int4 x = *own;
+        n[0] = x.w;
+        n[1] = x.z;
+        n[2] = x.y;
+        n[3] = x.x;
+        *own = make_int4(0, 0, 0, 0);  // for the next digit
+      }
     }
-    if (lane == 31) warp_sum[warp] = incl;
-    __syncthreads();
-    int before = incl - mine;
-    for (int x = 0; x < warp; ++x) before += warp_sum[x];
-    if (before < left && before + mine >= left) {  // exactly one thread
-      int places = left - before, b = 0;
+    if (rank == 0) {
+      // the bin of the left-th key: a scan over the threads
+      const int sum = n[0] + n[1] + n[2] + n[3];
+      int incl = sum;
 #pragma unroll
-      for (int c = 0; c < kPer - 1; ++c)
-        if (b == c && places > n[c]) {
-          places -= n[c];
-          b = c + 1;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += x;
+      }
+      if (lane == 31 && warp < kScanThreads / 32) warp_sum[warp] = incl;
+      __syncthreads();
+      int before = incl - sum;
+      for (int x = 0; x < min(warp, kScanThreads / 32); ++x) before += warp_sum[x];
+      if (sum > 0 && before < left && before + sum >= left) {  // exactly one thread
+        int places = left - before, b = 0, size = n[0];
+#pragma unroll
+        for (int c = 0; c < 3; ++c)
+          if (b == c && places > n[c]) {
+            places -= n[c];
+            b = c + 1;
+            size = n[c + 1];
+          }
+        for (int c = 0; c < clusters; ++c) {
+          if (clusters > 1) {
+            st_cluster(found + 0, c, top - b);
+            st_cluster(found + 1, c, places);
+            st_cluster(found + 2, c, size == places);
+          } else {
+            found[0] = top - b;
+            found[1] = places;
+            found[2] = size == places;
+          }
         }
-      found_bin = top - b;
-      found_left = places;
-      int size = n[0];
-#pragma unroll
-      for (int c = 1; c < kPer; ++c)
-        if (b == c) size = n[c];
-      found_whole = size == places;
+      }
     }
-    __syncwarp();
-    if (clusters > 1) cluster_wait();
-    __syncthreads();
-    prefix |= (uint32_t)found_bin << shift;
+    if (clusters > 1)
+      cluster_sync();
+    else
+      __syncthreads();
+    prefix |= (uint32_t)found[0] << shift;
     known |= mask << shift;
-    left = found_left;
-    if (found_whole) break;  // every key with this prefix is kept
+    left = found[1];
+    if (found[2]) break;  // every key with this prefix is kept
+    // (`found` is written again only behind the next digit's barriers)
   }
 
-  // kept: the protected keys, the keys above the prefix, and the first `left`
-  // of those that match it
-  auto classify = [&](int k, float x, bool* take, bool* tie) {
-    const uint32_t key = weight_key(x) & known;
-    const bool inside = k >= lo && k < hi;
-    *take = k < end && (!inside || (any && key > prefix));
-    *tie = k < end && inside && any && key == prefix;
-  };
+  // kept: the keys above the prefix, and the first `left` of those that match it
   int gt = 0, eq = 0;
-  for_keys([&](int k, float x) {
-    bool take, tie;
-    classify(k, x, &take, &tie);
-    gt += take;
-    eq += tie;
+  for_keys([&](int, uint32_t key) {
+    gt += (key & known) > prefix;
+    eq += (key & known) == prefix;
   });
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    gt += __shfl_xor_sync(kFull, gt, o);
-    eq += __shfl_xor_sync(kFull, eq, o);
-  }
+  gt = __reduce_add_sync(kFull, gt);
+  eq = __reduce_add_sync(kFull, eq);
   if (lane == 0) {
     warp_gt[warp] = gt;
     warp_eq[warp] = eq;
   }
   __syncthreads();
-  int ngt = 0, neq = 0;  // kept outright / matching, before this warp's share
+  // kept outright / matching, before this warp's share
+  int ngt = __reduce_add_sync(kFull, lane < warp ? warp_gt[lane] : 0);
+  int neq = __reduce_add_sync(kFull, lane < warp ? warp_eq[lane] : 0);
   if (clusters > 1) {
-    if (threadIdx.x == 0) {
-      int a = 0, b = 0;
-      for (int x = 0; x < kSelWarps; ++x) {
-        a += warp_gt[x];
-        b += warp_eq[x];
-      }
-      cta_count[0] = a;
-      cta_count[1] = b;
+    if (warp == warps - 1 && lane < clusters) {
+      st_cluster(cta_gt + rank, lane, ngt + gt);
+      st_cluster(cta_eq + rank, lane, neq + eq);
     }
-    __syncwarp();
-    cluster_arrive();
-    cluster_wait();
+    cluster_sync();
     for (int c = 0; c < rank; ++c) {
-      ngt += ld_cluster(&cta_count[0], c);
-      neq += ld_cluster(&cta_count[1], c);
+      ngt += cta_gt[c];
+      neq += cta_eq[c];
     }
-    cluster_arrive();  // waited for before the CTA exits
-  }
-  for (int x = 0; x < warp; ++x) {
-    ngt += warp_gt[x];
-    neq += warp_eq[x];
   }
   int32_t* kept = p.kept + ((int64_t)i * p.num_kv_heads + h) * p.max_keep;
   float* out = p.out ? p.out + at : nullptr;
   const uint32_t below = (1u << lane) - 1;
-  for_keys([&](int k, float x) {
-    bool take, tie;
-    classify(k, x, &take, &tie);
+  for (int k = base, j = 0; k - lane < end; k += 32, j += 32) {  // in step with the whole warp
+    const uint32_t key = k < end ? (Staged ? mine[j] : key_of(k, __ldg(w + k))) & known : 0;
+    const bool take = k < end && key > prefix, tie = k < end && key == prefix;
     const uint32_t mt = __ballot_sync(kFull, take), me = __ballot_sync(kFull, tie);
     const int eq_before = neq + __popc(me & below);
     if (take || (tie && eq_before < left)) {
       const int o = ngt + __popc(mt & below) + min(eq_before, left);
       kept[o] = k;
-      if (out) out[o] = x;
+      if (out) out[o] = __ldg(w + k);
     }
     ngt += __popc(mt);
     neq += __popc(me);
-  });
-  if (clusters > 1) {
-    __syncwarp();
-    cluster_wait();
   }
 }
 
@@ -334,38 +359,44 @@ cudaLaunchConfig_t config(dim3 grid, int threads, cudaStream_t stream, cudaLaunc
 
 namespace {
 
-template <int K>
-cudaError_t launch_select(const EvictSelectParams& p, int clusters, cudaStream_t stream) {
+template <bool Staged>
+cudaError_t launch_select(const EvictSelectParams& p, int clusters, int threads, int staged,
+                          cudaStream_t stream) {
+  auto kernel = evict_select_kernel<Staged>;
+  static SmemLimit limit;
+  if (Staged) {
+    cudaError_t e =
+        limit.ensure(reinterpret_cast<const void*>(kernel), (kStaged + kBins) * 4);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg =
-      config(dim3((unsigned)(p.num_kv_heads * clusters), (unsigned)p.num_seqs), kSelThreads,
-             stream, attr);
+      config(dim3((unsigned)(p.num_kv_heads * clusters), (unsigned)p.num_seqs), threads, stream,
+             attr);
+  cfg.dynamicSmemBytes = ((size_t)staged + (clusters > 1 ? kBins : 0)) * 4;
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = (unsigned)clusters;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, evict_select_kernel<K>, p, clusters);
+  return cudaLaunchKernelEx(&cfg, kernel, p, clusters);
 }
 
 }  // namespace
 
 cudaError_t launch_evict_select(const EvictSelectParams& p, cudaStream_t stream) {
-  const int64_t rows = (int64_t)p.num_seqs * p.num_kv_heads;
-  // 16 keys a thread at most, in as few CTAs as hold the row; more CTAs while
-  // the rows leave SMs without one and a thread has more than 4 keys
-  const int64_t L = p.max_seq_len;
+  const int64_t rows = (int64_t)p.num_seqs * p.num_kv_heads, L = p.max_seq_len;
+  // as few CTAs as keep a share at 8192 keys (four CTAs an SM), twice as many
+  // while the rows leave SMs without one and a share has over 2048 keys
   int clusters = 1;
-  while (clusters < kMaxCluster && L > (int64_t)clusters * kSelThreads * 16) clusters *= 2;
-  while (clusters < kMaxCluster && rows * clusters * 2 <= 152 &&
-         L > (int64_t)clusters * kSelThreads * 4)
+  while (clusters < kMaxCluster && L > (int64_t)clusters * 8192) clusters *= 2;
+  while (clusters < kMaxCluster && rows * clusters * 2 <= 152 && L > (int64_t)clusters * 2048)
     clusters *= 2;
-  const int64_t steps = (L + clusters * kSelThreads - 1) / (clusters * kSelThreads);
-  if (steps <= 4) return launch_select<4>(p, clusters, stream);
-  if (steps <= 8) return launch_select<8>(p, clusters, stream);
-  if (steps <= 16) return launch_select<16>(p, clusters, stream);
-  if (steps <= 32) return launch_select<32>(p, clusters, stream);
-  return launch_select<0>(p, clusters, stream);
+  const int threads = L > (int64_t)clusters * 8192 ? 1024 : 512;
+  const int64_t per_step = (int64_t)clusters * threads;
+  const int64_t share = (L + per_step - 1) / per_step * threads;
+  if (share <= kStaged) return launch_select<true>(p, clusters, threads, (int)share, stream);
+  return launch_select<false>(p, clusters, threads, 0, stream);
 }
 
 cudaError_t launch_evict_compact(const EvictCompactParams& p, cudaStream_t stream) {
