@@ -637,36 +637,31 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str = "
 
 
 # The calls below are made once a layer and step, on a handful of small tensors:
-# their checks are written to cost little when everything is in order.
+# the module `_marshal` checks their tensors as `_need` does and calls libpkv.
+_native = None
 
 
-def _need_on(t, dtype, ndim: int, device, name: str) -> None:
-    """:func:`_need`, and on ``device``."""
-    if (type(t) is torch.Tensor and t.dtype is dtype and t.dim() == ndim and t.is_contiguous()
-            and t.device == device):
-        return
-    _need(t, dtype, ndim, name)
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device} as the others")
+def _marshal():
+    global _native
+    if _native is None:
+        load_library()  # a missing library is reported the same way
+        import importlib
+
+        try:
+            module = importlib.import_module("._marshal", __package__)
+        except ImportError as e:
+            raise PkvError(f"{_HERE}/_marshal.so cannot be loaded ({e}): build it first (python -c "
+                           "'import __graft_entry__ as g; g.build()')") from e
+        module.set_error(PkvError)
+        _native = module
+    return _native
 
 
-def _need_rows(t, shape, device, name: str) -> int:
-    """Check a [T,heads,D] bf16 tensor whose tokens may be any distance apart
-    (a column range of a projection's output); returns that distance."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != device:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}, got {t.device}")
-    if t.dtype is not torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    tokens, heads, head_dim = shape
-    far, near, one = t.stride()
-    if (head_dim > 1 and one != 1) or (heads > 1 and near != head_dim):
-        raise ValueError(f"{name}: the heads of a token must be contiguous, got strides "
-                         f"{t.stride()}")
-    return far if tokens > 1 else heads * head_dim
+def _handle_of(stream):
+    """None, or the stream's integer handle."""
+    if stream is None:
+        return None
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _on_stream(stream, device):
@@ -674,19 +669,6 @@ def _on_stream(stream, device):
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     return torch.cuda.stream(stream)
-
-
-def _run(what: str, device, stream, *args) -> None:
-    """Call ``pkv_<what>`` with ``device`` current and the stream last."""
-    fn = getattr(_handle or load_library(), "pkv_" + what)
-    raw = _stream(stream, device)
-    if torch.cuda.current_device() == device.index:
-        st = fn(*args, raw)
-    else:
-        with torch.cuda.device(device):
-            st = fn(*args, raw)
-    if st:
-        _check(st, what)
 
 
 def rope_kv_cache_write(q: torch.Tensor, kv_pool: torch.Tensor, k_new: torch.Tensor,
@@ -702,40 +684,16 @@ def rope_kv_cache_write(q: torch.Tensor, kv_pool: torch.Tensor, k_new: torch.Ten
     ``2 * len(inv_freq)`` dimensions rotate. ``positions`` are independent of
     ``slot_mapping`` (-1: nothing is written). Returns ``q_out`` [T,H,D],
     which may be a dense q itself."""
-    _need(kv_pool, torch.bfloat16, 5, "kv_pool")
-    device = kv_pool.device
-    _need_on(positions, torch.int32, 1, device, "positions")
-    _need_on(slot_mapping, torch.int32, 1, device, "slot_mapping")
-    _need_on(inv_freq, torch.float64, 1, device, "inv_freq")
-    _, nb, bs, hkv, d = kv_pool.shape
-    t = slot_mapping.shape[0]
-    if positions.shape[0] != t:
-        raise ValueError("positions and slot_mapping differ in length")
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("q must be a [num_tokens, num_heads, head_dim] tensor")
-    h = q.shape[1]
-    qs = _need_rows(q, (t, h, d), device, "q")
-    ks = _need_rows(k_new, (t, hkv, d), device, "k_new")
-    vs = _need_rows(v_new, (t, hkv, d), device, "v_new")
-    if q_out is not None:
-        _need_on(q_out, torch.bfloat16, 3, device, "q_out")
-        if q_out.shape != q.shape:
-            raise ValueError("q_out must have the shape of q")
-    elif stream is None:
-        q_out = torch.empty((t, h, d), dtype=torch.bfloat16, device=device)
-    else:
-        with _on_stream(stream, device):
-            q_out = torch.empty((t, h, d), dtype=torch.bfloat16, device=device)
-    if dev_status is not None:
-        _need_on(dev_status, torch.int32, 1, device, "dev_status")
     if debug_checks.enabled():
-        debug_checks.check_slot_mapping(slot_mapping, num_blocks=nb, block_size=bs)
+        debug_checks.check_slot_mapping(slot_mapping, num_blocks=kv_pool.shape[1],
+                                        block_size=kv_pool.shape[2])
         debug_checks.check_positions(positions)
-    _run("rope_kv_cache_write", device, stream, q_out.data_ptr(), kv_pool.data_ptr(),
-         q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), qs, ks, vs, positions.data_ptr(),
-         slot_mapping.data_ptr(), inv_freq.data_ptr(), factor, bool(interleaved), t, h, hkv, d,
-         2 * inv_freq.shape[0], nb, bs, _ptr(dev_status))
-    return q_out
+    if q_out is None and stream is not None:
+        with _on_stream(stream, q.device):
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    return (_native or _marshal()).rope_kv_cache_write(
+        q, kv_pool, k_new, v_new, positions, slot_mapping, inv_freq, interleaved, factor, q_out,
+        dev_status, _handle_of(stream))
 
 
 def attention_key_weights(q: torch.Tensor, kv_pool: torch.Tensor, lse: torch.Tensor,
@@ -753,52 +711,16 @@ def attention_key_weights(q: torch.Tensor, kv_pool: torch.Tensor, lse: torch.Ten
     ``weight_rows[i]`` (default i). Keys at or behind ``prior_lens[i]``
     (default: the step's own tokens) start from zero; ``decay`` scales the
     others' old sums. Writes and returns ``out`` (default: ``weights``, in place)."""
-    _need(kv_pool, torch.bfloat16, 5, "kv_pool")
-    device = kv_pool.device
-    _need_on(q, torch.bfloat16, 3, device, "q")
-    _need_on(lse, torch.float32, 2, device, "lse")
-    _need_on(block_table, torch.int32, 2, device, "block_table")
-    _need_on(cu_seqlens, torch.int32, 1, device, "cu_seqlens")
-    _need_on(seq_lens, torch.int32, 1, device, "seq_lens")
-    _need_on(weights, torch.float32, 3, device, "weights")
-    t, h, d = q.shape
-    _, nb, bs, hkv, d2 = kv_pool.shape
-    if d2 != d:
-        raise ValueError("q and kv_pool head_dim differ")
-    if lse.shape != (t, h):
-        raise ValueError("lse must be [num_tokens, num_heads]")
-    b = seq_lens.shape[0]
-    if cu_seqlens.shape[0] != b + 1 or block_table.shape[0] != b:
-        raise ValueError("cu_seqlens must be [B+1] and block_table [B, max_blocks]")
-    rows, wh, row_len = weights.shape
-    if wh != hkv:
-        raise ValueError("weights must be [rows, num_kv_heads, row_len]")
-    if out is None:
-        out = weights
-    else:
-        _need_on(out, torch.float32, 3, device, "out")
-        if out.shape != weights.shape:
-            raise ValueError("out must have the shape of weights")
-    for x, name in ((weight_rows, "weight_rows"), (prior_lens, "prior_lens")):
-        if x is not None:
-            _need_on(x, torch.int32, 1, device, name)
-            if x.shape[0] != b:
-                raise ValueError(f"{name} must have one entry per request")
-    if dev_status is not None:
-        _need_on(dev_status, torch.int32, 1, device, "dev_status")
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
     if debug_checks.enabled():
         debug_checks.check_attention_tables(
-            cu_seqlens, seq_lens, block_table, num_tokens=t, max_query_len=int(max_query_len),
-            max_seq_len=int(max_seq_len), num_blocks=nb, block_size=bs)
-        debug_checks.check_weight_rows(weight_rows, num_seqs=b, num_rows=rows)
-    _run("attention_key_weights", device, stream, out.data_ptr(), weights.data_ptr(),
-         q.data_ptr(), kv_pool.data_ptr(), lse.data_ptr(), block_table.data_ptr(),
-         block_table.shape[1], cu_seqlens.data_ptr(), seq_lens.data_ptr(), _ptr(prior_lens),
-         _ptr(weight_rows), rows, row_len, b, t, int(max_query_len), int(max_seq_len), h, hkv, d,
-         bs, nb, scale, decay, _ptr(dev_status))
-    return out
+            cu_seqlens, seq_lens, block_table, num_tokens=q.shape[0],
+            max_query_len=int(max_query_len), max_seq_len=int(max_seq_len),
+            num_blocks=kv_pool.shape[1], block_size=kv_pool.shape[2])
+        debug_checks.check_weight_rows(weight_rows, num_seqs=seq_lens.shape[0],
+                                       num_rows=weights.shape[0])
+    return (_native or _marshal()).attention_key_weights(
+        q, kv_pool, lse, block_table, cu_seqlens, seq_lens, max_query_len, max_seq_len, weights,
+        out, weight_rows, prior_lens, decay, scale, dev_status, _handle_of(stream))
 
 
 def evict_select(weights: torch.Tensor, seq_lens: torch.Tensor, keep_lens: torch.Tensor,
@@ -814,41 +736,22 @@ def evict_select(weights: torch.Tensor, seq_lens: torch.Tensor, keep_lens: torch
     ascending, filled up to ``keep_lens[i]`` (a tensor made here holds -1
     behind that); ``weights_out``, when given, receives the kept keys' weights
     at the front of the same rows."""
-    _need(weights, torch.float32, 3, "weights")
-    device = weights.device
-    _need_on(seq_lens, torch.int32, 1, device, "seq_lens")
-    _need_on(keep_lens, torch.int32, 1, device, "keep_lens")
-    rows, hkv, row_len = weights.shape
-    b = seq_lens.shape[0]
-    if keep_lens.shape[0] != b:
-        raise ValueError("seq_lens and keep_lens differ in length")
-    shape = (b, hkv, int(max_keep_len))
-    if kept is not None:
-        _need_on(kept, torch.int32, 3, device, "kept")
-        if kept.shape != shape:
-            raise ValueError("kept must be [num_seqs, num_kv_heads, max_keep_len]")
-    elif stream is None:
-        kept = torch.full(shape, -1, dtype=torch.int32, device=device)
-    else:
-        with _on_stream(stream, device):
-            kept = torch.full(shape, -1, dtype=torch.int32, device=device)
-    if weights_out is not None:
-        _need_on(weights_out, torch.float32, 3, device, "weights_out")
-        if weights_out.shape != weights.shape:
-            raise ValueError("weights_out must have the shape of weights")
-    if weight_rows is not None:
-        _need_on(weight_rows, torch.int32, 1, device, "weight_rows")
-        if weight_rows.shape[0] != b:
-            raise ValueError("weight_rows must have one entry per request")
-    if dev_status is not None:
-        _need_on(dev_status, torch.int32, 1, device, "dev_status")
     if debug_checks.enabled():
-        debug_checks.check_weight_rows(weight_rows, num_seqs=b, num_rows=rows)
+        debug_checks.check_weight_rows(weight_rows, num_seqs=seq_lens.shape[0],
+                                       num_rows=weights.shape[0])
         debug_checks.check_keep_lens(seq_lens, keep_lens, max_seq_len=int(max_seq_len),
                                      max_keep_len=int(max_keep_len))
-    _run("evict_select", device, stream, kept.data_ptr(), _ptr(weights_out), weights.data_ptr(),
-         seq_lens.data_ptr(), keep_lens.data_ptr(), _ptr(weight_rows), rows, row_len, b, hkv,
-         int(max_seq_len), int(max_keep_len), int(num_sink), int(num_recent), _ptr(dev_status))
+    if kept is None:
+        _need(weights, torch.float32, 3, "weights")
+        shape, device = (seq_lens.shape[0], weights.shape[1], int(max_keep_len)), weights.device
+        if stream is None:
+            kept = torch.full(shape, -1, dtype=torch.int32, device=device)
+        else:
+            with _on_stream(stream, device):
+                kept = torch.full(shape, -1, dtype=torch.int32, device=device)
+    (_native or _marshal()).evict_select(
+        weights, seq_lens, keep_lens, max_seq_len, max_keep_len, num_sink, num_recent, weight_rows,
+        kept, weights_out, dev_status, _handle_of(stream))
     return kept, weights_out
 
 
@@ -858,23 +761,8 @@ def evict_compact(kv_pool: torch.Tensor, src_table: torch.Tensor, dst_table: tor
     """Copy the kept keys' K and V rows (``kept`` of :func:`evict_select`) from
     the blocks of ``src_table`` to the front of those of ``dst_table``, which
     must be other blocks (``BlockManager.evict_step`` hands both out)."""
-    _need(kv_pool, torch.bfloat16, 5, "kv_pool")
-    device = kv_pool.device
-    _need_on(src_table, torch.int32, 2, device, "src_table")
-    _need_on(dst_table, torch.int32, 2, device, "dst_table")
-    _need_on(kept, torch.int32, 3, device, "kept")
-    _need_on(keep_lens, torch.int32, 1, device, "keep_lens")
-    _, nb, bs, hkv, d = kv_pool.shape
-    b, heads, max_keep = kept.shape
-    if b != keep_lens.shape[0] or heads != hkv:
-        raise ValueError("kept must be [num_seqs, num_kv_heads, max_keep_len]")
-    if src_table.shape[0] != b or dst_table.shape[0] != b:
-        raise ValueError("src_table and dst_table must have one row per request")
-    if dev_status is not None:
-        _need_on(dev_status, torch.int32, 1, device, "dev_status")
     if debug_checks.enabled():
-        debug_checks.check_compaction(src_table, dst_table, kept, keep_lens, num_blocks=nb,
-                                      block_size=bs)
-    _run("evict_compact", device, stream, kv_pool.data_ptr(), src_table.data_ptr(),
-         src_table.shape[1], dst_table.data_ptr(), dst_table.shape[1], kept.data_ptr(), max_keep,
-         keep_lens.data_ptr(), b, hkv, d, bs, nb, _ptr(dev_status))
+        debug_checks.check_compaction(src_table, dst_table, kept, keep_lens,
+                                      num_blocks=kv_pool.shape[1], block_size=kv_pool.shape[2])
+    (_native or _marshal()).evict_compact(kv_pool, src_table, dst_table, kept, keep_lens,
+                                          dev_status, _handle_of(stream))

@@ -3,12 +3,16 @@
 Each translation unit compiles in parallel into ``_build/``; the objects are
 linked into ``paged_kv_cache_varlen_gb300/libpkv.so`` (static cudart, no
 driver-library link: the tensor-map encoder is looked up at run time).
+``_marshal.so`` beside it is the Python module that marshals the arguments of
+the per-step calls (host code against torch's and Python's headers; it calls
+libpkv.so).
 """
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -16,6 +20,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIBRARY = os.path.join(PKG, "libpkv.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
+MARSHAL_SOURCE = "marshal.cpp"
 SOURCES = ["kv_write.cu", "decode_mma.cu", "merge.cu", "prefill_tc.cu", "copy_blocks.cu",
            "rope_write.cu", "key_weights.cu", "key_weights_tc.cu", "evict.cu", "api.cpp",
            "budget_api.cpp", "api_noalloc.cu", "block_manager.cpp"]
@@ -35,12 +41,27 @@ def nvcc() -> str:
 
 
 def _newest_input() -> float:
-    files = [os.path.join(CSRC, s) for s in SOURCES] + HEADERS + [os.path.abspath(__file__)]
+    files = ([os.path.join(CSRC, s) for s in SOURCES + [MARSHAL_SOURCE]] + HEADERS
+             + [os.path.abspath(__file__)])
     return max(os.path.getmtime(f) for f in files)
 
 
 def up_to_date() -> bool:
-    return os.path.exists(LIBRARY) and os.path.getmtime(LIBRARY) >= _newest_input()
+    newest = _newest_input()
+    return all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in (LIBRARY, MARSHAL))
+
+
+def _torch_paths() -> tuple[list[str], str]:
+    """Include flags of torch, Python and CUDA, and torch's library folder."""
+    import torch
+
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    include = os.path.join(root, "include")
+    dirs = [include, os.path.join(include, "torch", "csrc", "api", "include"),
+            sysconfig.get_paths()["include"]]
+    flags = [f"-I{d}" for d in dirs]
+    flags.append(f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}")
+    return flags, os.path.join(root, "lib")
 
 
 def _compile(src: str, verbose: bool) -> str:
@@ -48,6 +69,8 @@ def _compile(src: str, verbose: bool) -> str:
     cmd = [nvcc(), *NVCC_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
     if verbose and src.endswith(".cu"):
         cmd += ["-Xptxas", "-v"]
+    if src == MARSHAL_SOURCE:
+        cmd += _torch_paths()[0]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"nvcc failed on {src}:\n{res.stderr}")
@@ -61,15 +84,23 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIBRARY
     os.makedirs(BUILD_DIR, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as pool:
-        objs = list(pool.map(lambda s: _compile(s, verbose), SOURCES))
-    tmp = LIBRARY + ".tmp"
-    cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as pool:
+        objs = list(pool.map(lambda s: _compile(s, verbose), [MARSHAL_SOURCE] + SOURCES))
+    _link(LIBRARY, objs[1:], [])
+    torch_lib = _torch_paths()[1]
+    _link(MARSHAL, objs[:1],
+          [f"-L{PKG}", "-l:libpkv.so", f"-L{torch_lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch_python", "-Xlinker", "-rpath,$ORIGIN", "-Xlinker", f"-rpath,{torch_lib}"])
+    return LIBRARY
+
+
+def _link(target: str, objs: list[str], extra: list[str]) -> None:
+    tmp = target + ".tmp"
+    cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs, *extra, "-cudart", "static"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stderr}")
-    os.replace(tmp, LIBRARY)
-    return LIBRARY
+    os.replace(tmp, target)
 
 
 if __name__ == "__main__":
