@@ -11,9 +11,11 @@ constexpr uint32_t kFull = 0xffffffffu;
 
 // ---------------------------------------------------------------------------
 // Selection: the n heaviest of a row's keys by a radix search for the n-th
-// largest value (digits of 11, 11 and 10 bits, a histogram each; it ends early
-// when a digit's bin is taken whole), then one pass that writes the keys above
-// it and the first of those equal to it, in index order.
+// largest value (digits of 11, 11 and 10 bits, a histogram each), then one pass
+// that writes the keys above it and the first of those equal to it, in index
+// order. The search ends early when a digit's bin is taken whole, or when it
+// is so small that its keys can be ranked against one another (the usual case
+// after one digit of some thousand keys).
 //
 // A row (request, KV head) is read once into the shared memory of one CTA, or
 // of a cluster of 2, 4 or 8 when it is long or the rows are few; the CTAs'
@@ -30,6 +32,7 @@ constexpr int kStaged = 40960;     // keys of a CTA's share that shared memory h
 // that a bin's copies lie in different banks.
 constexpr int kCopies = 2;
 constexpr int kCopyStride = kBins + 8;
+constexpr int kRanked = 384;  // keys at most that are ranked against one another
 
 // Order-preserving key of a weight: larger weights have larger keys, -0 and
 // +0 the same one, a NaN the largest but kProtected, which stands for the keys
@@ -40,6 +43,11 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   if (w != w) return 0xfffffffeu;
   const uint32_t b = __float_as_uint(w + 0.f);
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+// The weight of a key, where it tells it; not finite for kProtected and NaN.
+__device__ __forceinline__ float key_weight(uint32_t key) {
+  return __uint_as_float((key & 0x80000000u) ? key & 0x7fffffffu : ~key);
 }
 
 __device__ __forceinline__ void cluster_arrive() {
@@ -62,6 +70,12 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, int rank) {
 __device__ __forceinline__ void st_cluster(const int* p, int rank, int v) {
   asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(cluster_addr(p, rank)), "r"(v) : "memory");
 }
+__device__ __forceinline__ int take_cluster(const int* p, int rank) {  // fetch and add 1
+  int v;
+  asm volatile("atom.shared::cluster.add.s32 %0, [%1], 1;" : "=r"(v) : "r"(cluster_addr(p, rank))
+               : "memory");
+  return v;
+}
 __device__ __forceinline__ void add_cluster(const int* p, int rank, int v) {
   asm volatile("red.shared::cluster.add.s32 [%0], %1;" ::"r"(cluster_addr(p, rank)), "r"(v)
                : "memory");
@@ -76,7 +90,9 @@ __global__ void __launch_bounds__(1024, 2)
   uint32_t* staged = smem + (clusters > 1 ? kBins : 0);
   __shared__ __align__(16) int hist[kCopies * kCopyStride];
   __shared__ int warp_sum[kScanThreads / 32];
-  __shared__ int found[3];  // bin, places left in it, whether it is taken whole
+  __shared__ int found[3];  // bin (or key), places left in it, its size
+  __shared__ __align__(16) int list[kRanked];  // of the cluster, in rank 0
+  __shared__ int list_n;
   __shared__ int warp_gt[32], warp_eq[32];
   __shared__ int cta_gt[kMaxCluster], cta_eq[kMaxCluster];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
@@ -101,14 +117,16 @@ __global__ void __launch_bounds__(1024, 2)
   const int sink = min(p.num_sink, keep - recent);
   int left = keep;  // places for the keys that match the digits found so far
 
-  // the warp's share of the row: `steps` times 32 keys, in index order
-  const int per_step = clusters * (int)blockDim.x;
-  const int steps = (int)(((int64_t)L + per_step - 1) / per_step);
-  const int64_t first = (int64_t)(rank * warps + warp) * steps * 32;
+  // the warp's share of the row: `groups` times 4 steps of 32 keys, in index
+  // order; key 32 j + lane of group g is component j of the lane's vector g
+  const int per_group = clusters * (int)blockDim.x * 4;
+  const int groups = (int)(((int64_t)L + per_group - 1) / per_group);
+  const int64_t first = (int64_t)(rank * warps + warp) * groups * 128;
   const int base = (int)min((int64_t)L, first) + lane;
-  const int end = (int)min((int64_t)L, first + (int64_t)steps * 32);
+  const int end = (int)min((int64_t)L, first + (int64_t)groups * 128);
+  // (no weight has key 0: it stands behind the share's end)
   auto key_of = [&](int k, float x) {
-    return k < sink || k >= L - recent ? kProtected : weight_key(x);
+    return k >= end ? 0u : k < sink || k >= L - recent ? kProtected : weight_key(x);
   };
   auto count = [&](uint32_t bin) {
     atomicAdd(&hist[(lane % kCopies) * kCopyStride + bin], 1);
@@ -118,29 +136,39 @@ __global__ void __launch_bounds__(1024, 2)
       reinterpret_cast<int4*>(hist)[b] = make_int4(0, 0, 0, 0);
   };
   clear();
+  if (threadIdx.x == 0) list_n = 0;
   if (clusters > 1)
     for (int b = threadIdx.x; b < kBins; b += blockDim.x) acc[b] = 0;
   __syncthreads();
+  uint4* mine = reinterpret_cast<uint4*>(staged) + warp * groups * 32 + lane;
+  auto load_keys = [&](int k) {
+    float x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = k + j * 32 < end ? __ldg(w + k + j * 32) : 0.f;
+    return make_uint4(key_of(k, x[0]), key_of(k + 32, x[1]), key_of(k + 64, x[2]),
+                      key_of(k + 96, x[3]));
+  };
   // the keys, and the histogram of their first digit, in one pass
-  uint32_t* mine = staged + warp * steps * 32 + lane;
-  constexpr int kBatch = 8;  // loads in flight
-  for (int k = base, j = 0; k < end; k += kBatch * 32, j += kBatch * 32) {
-    float x[kBatch];
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) x[b] = k + b * 32 < end ? __ldg(w + k + b * 32) : 0.f;
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b)
-      if (k + b * 32 < end) {
-        const uint32_t key = key_of(k + b * 32, x[b]);
-        if (Staged) mine[j + b * 32] = key;
-        count(key >> 21);
-      }
+#pragma unroll 2
+  for (int g = 0; g < groups; ++g) {
+    const uint4 key = load_keys(base + g * 128);
+    if (Staged) mine[g * 32] = key;
+    count(key.x >> 21);
+    count(key.y >> 21);
+    count(key.z >> 21);
+    count(key.w >> 21);
   }
   if (clusters > 1) cluster_sync();  // every CTA's acc is clear
-  // f(index, key) of the lane's keys (each lane reads what it wrote)
+  // f(key) of the lane's keys (each lane reads what it wrote)
   auto for_keys = [&](auto f) {
-#pragma unroll 4
-    for (int k = base, j = 0; k < end; k += 32, j += 32) f(k, Staged ? mine[j] : key_of(k, __ldg(w + k)));
+#pragma unroll 2
+    for (int g = 0; g < groups; ++g) {
+      const uint4 key = Staged ? mine[g * 32] : load_keys(base + g * 128);
+      f(key.x);
+      f(key.y);
+      f(key.z);
+      f(key.w);
+    }
   };
 
   // the keep-th largest key: its digits from the top
@@ -151,7 +179,7 @@ __global__ void __launch_bounds__(1024, 2)
     if (digit > 0) {
       clear();
       __syncthreads();
-      for_keys([&](int, uint32_t key) {
+      for_keys([&](uint32_t key) {
         if ((key & known) == prefix) count((key >> shift) & mask);
       });
     }
@@ -195,8 +223,8 @@ __global__ void __launch_bounds__(1024, 2)
       }
       if (lane == 31 && warp < kScanThreads / 32) warp_sum[warp] = incl;
       __syncthreads();
-      int before = incl - sum;
-      for (int x = 0; x < min(warp, kScanThreads / 32); ++x) before += warp_sum[x];
+      const int before =
+          incl - sum + __reduce_add_sync(kFull, lane < min(warp, kScanThreads / 32) ? warp_sum[lane] : 0);
       if (sum > 0 && before < left && before + sum >= left) {  // exactly one thread
         int places = left - before, b = 0, size = n[0];
 #pragma unroll
@@ -210,11 +238,11 @@ __global__ void __launch_bounds__(1024, 2)
           if (clusters > 1) {
             st_cluster(found + 0, c, top - b);
             st_cluster(found + 1, c, places);
-            st_cluster(found + 2, c, size == places);
+            st_cluster(found + 2, c, size);
           } else {
             found[0] = top - b;
             found[1] = places;
-            found[2] = size == places;
+            found[2] = size;
           }
         }
       }
@@ -226,13 +254,60 @@ __global__ void __launch_bounds__(1024, 2)
     prefix |= (uint32_t)found[0] << shift;
     known |= mask << shift;
     left = found[1];
-    if (found[2]) break;  // every key with this prefix is kept
-    // (`found` is written again only behind the next digit's barriers)
+    const int size = found[2];
+    if (size == left || known == 0xffffffffu) break;  // every key with this prefix is kept
+    if (size > kRanked) continue;  // (`found` is written again only behind the next barriers)
+    // the bin's keys, in any order, to rank 0
+    for_keys([&](uint32_t key) {
+      if ((key & known) != prefix) return;
+      if (clusters > 1)
+        st_cluster(list + take_cluster(&list_n, 0), 0, (int)key);
+      else
+        list[atomicAdd(&list_n, 1)] = (int)key;
+    });
+    if (clusters > 1)
+      cluster_sync();
+    else
+      __syncthreads();
+    if (rank == 0 && threadIdx.x < size) {
+      const uint32_t own = (uint32_t)list[threadIdx.x];
+      int above = 0, same = 0;
+      auto meet = [&](int key, int j) {
+        above += j < size && (uint32_t)key > own;
+        same += j < size && (uint32_t)key == own;
+      };
+#pragma unroll 4
+      for (int j = 0; j < size; j += 4) {
+        const int4 four = *reinterpret_cast<const int4*>(list + j);
+        meet(four.x, j);
+        meet(four.y, j + 1);
+        meet(four.z, j + 2);
+        meet(four.w, j + 3);
+      }
+      if (above < left && left <= above + same)  // (equal keys write the same)
+        for (int c = 0; c < clusters; ++c) {
+          if (clusters > 1) {
+            st_cluster(found + 0, c, (int)own);
+            st_cluster(found + 1, c, left - above);
+          } else {
+            found[0] = (int)own;
+            found[1] = left - above;
+          }
+        }
+    }
+    if (clusters > 1)
+      cluster_sync();
+    else
+      __syncthreads();
+    prefix = (uint32_t)found[0];
+    known = 0xffffffffu;
+    left = found[1];
+    break;
   }
 
   // kept: the keys above the prefix, and the first `left` of those that match it
   int gt = 0, eq = 0;
-  for_keys([&](int, uint32_t key) {
+  for_keys([&](uint32_t key) {
     gt += (key & known) > prefix;
     eq += (key & known) == prefix;
   });
@@ -260,18 +335,29 @@ __global__ void __launch_bounds__(1024, 2)
   int32_t* kept = p.kept + ((int64_t)i * p.num_kv_heads + h) * p.max_keep;
   float* out = p.out ? p.out + at : nullptr;
   const uint32_t below = (1u << lane) - 1;
-  for (int k = base, j = 0; k - lane < end; k += 32, j += 32) {  // in step with the whole warp
-    const uint32_t key = k < end ? (Staged ? mine[j] : key_of(k, __ldg(w + k))) & known : 0;
-    const bool take = k < end && key > prefix, tie = k < end && key == prefix;
-    const uint32_t mt = __ballot_sync(kFull, take), me = __ballot_sync(kFull, tie);
-    const int eq_before = neq + __popc(me & below);
-    if (take || (tie && eq_before < left)) {
-      const int o = ngt + __popc(mt & below) + min(eq_before, left);
-      kept[o] = k;
-      if (out) out[o] = __ldg(w + k);
+  for (int g = 0; g < groups; ++g) {
+    const uint4 four = Staged ? mine[g * 32] : load_keys(base + g * 128);
+    const uint32_t key[4] = {four.x, four.y, four.z, four.w};
+    int o[4];  // where the key goes, -1: nowhere
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {  // in step with the whole warp
+      const bool take = (key[j] & known) > prefix, tie = (key[j] & known) == prefix;
+      const uint32_t mt = __ballot_sync(kFull, take), me = __ballot_sync(kFull, tie);
+      const int eq_before = neq + __popc(me & below);
+      o[j] = take || (tie && eq_before < left)
+                 ? ngt + __popc(mt & below) + min(eq_before, left) : -1;
+      ngt += __popc(mt);
+      neq += __popc(me);
     }
-    ngt += __popc(mt);
-    neq += __popc(me);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (o[j] >= 0) {
+        const int k = base + g * 128 + j * 32;
+        const float x = key_weight(key[j]);
+        kept[o[j]] = k;
+        // (a key does not tell a zero's sign, a NaN's bits, a protected weight)
+        if (out) out[o[j]] = isfinite(x) && x != 0.f ? x : __ldg(w + k);
+      }
   }
 }
 
@@ -393,8 +479,8 @@ cudaError_t launch_evict_select(const EvictSelectParams& p, cudaStream_t stream)
   while (clusters < kMaxCluster && rows * clusters * 2 <= 152 && L > (int64_t)clusters * 2048)
     clusters *= 2;
   const int threads = L > (int64_t)clusters * 8192 ? 1024 : 512;
-  const int64_t per_step = (int64_t)clusters * threads;
-  const int64_t share = (L + per_step - 1) / per_step * threads;
+  const int64_t per_group = (int64_t)clusters * threads * 4;
+  const int64_t share = (L + per_group - 1) / per_group * threads * 4;
   if (share <= kStaged) return launch_select<true>(p, clusters, threads, (int)share, stream);
   return launch_select<false>(p, clusters, threads, 0, stream);
 }
