@@ -40,9 +40,8 @@ constexpr int kRanked = 384;  // keys at most that are ranked against one anothe
 // selection is the `keep` largest keys of the row).
 constexpr uint32_t kProtected = 0xffffffffu;
 __device__ __forceinline__ uint32_t weight_key(float w) {
-  if (w != w) return 0xfffffffeu;
-  const uint32_t b = __float_as_uint(w + 0.f);
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  const int32_t b = __float_as_int(w + 0.f);
+  return w != w ? 0xfffffffeu : (uint32_t)b ^ ((uint32_t)(b >> 31) | 0x80000000u);
 }
 
 // The weight of a key, where it tells it; not finite for kProtected and NaN.
@@ -70,9 +69,11 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, int rank) {
 __device__ __forceinline__ void st_cluster(const int* p, int rank, int v) {
   asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(cluster_addr(p, rank)), "r"(v) : "memory");
 }
-__device__ __forceinline__ int take_cluster(const int* p, int rank) {  // fetch and add 1
+__device__ __forceinline__ int take_cluster(const int* p, int rank, int add) {  // fetch and add
   int v;
-  asm volatile("atom.shared::cluster.add.s32 %0, [%1], 1;" : "=r"(v) : "r"(cluster_addr(p, rank))
+  asm volatile("atom.shared::cluster.add.s32 %0, [%1], %2;"
+               : "=r"(v)
+               : "r"(cluster_addr(p, rank)), "r"(add)
                : "memory");
   return v;
 }
@@ -131,20 +132,31 @@ __global__ void __launch_bounds__(1024, 2)
   auto count = [&](uint32_t bin) {
     atomicAdd(&hist[(lane % kCopies) * kCopyStride + bin], 1);
   };
+  // (the protected keys are hundreds in one bin: added as a number, below)
+  auto count_first = [&](uint32_t key) {
+    if (key != kProtected && key != 0) count(key >> 21);
+  };
   auto clear = [&] {
     for (int b = threadIdx.x; b < kCopies * kCopyStride / 4; b += blockDim.x)
       reinterpret_cast<int4*>(hist)[b] = make_int4(0, 0, 0, 0);
   };
   clear();
   if (threadIdx.x == 0) list_n = 0;
+  for (int b = threadIdx.x; b < kRanked; b += blockDim.x) list[b] = 0;
   if (clusters > 1)
     for (int b = threadIdx.x; b < kBins; b += blockDim.x) acc[b] = 0;
   __syncthreads();
   uint4* mine = reinterpret_cast<uint4*>(staged) + warp * groups * 32 + lane;
+  // groups whose keys are all there and compete: nothing to check key by key
+  const int plain_lo = sink + lane, plain_hi = min(end, L - recent) - 128 + lane;
   auto load_keys = [&](int k) {
+    const float* at_k = w + k;
+    if (k >= plain_lo && k <= plain_hi)  // (the same for the whole warp)
+      return make_uint4(weight_key(__ldg(at_k)), weight_key(__ldg(at_k + 32)),
+                        weight_key(__ldg(at_k + 64)), weight_key(__ldg(at_k + 96)));
     float x[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = k + j * 32 < end ? __ldg(w + k + j * 32) : 0.f;
+    for (int j = 0; j < 4; ++j) x[j] = k + j * 32 < end ? __ldg(at_k + j * 32) : 0.f;
     return make_uint4(key_of(k, x[0]), key_of(k + 32, x[1]), key_of(k + 64, x[2]),
                       key_of(k + 96, x[3]));
   };
@@ -153,10 +165,10 @@ __global__ void __launch_bounds__(1024, 2)
   for (int g = 0; g < groups; ++g) {
     const uint4 key = load_keys(base + g * 128);
     if (Staged) mine[g * 32] = key;
-    count(key.x >> 21);
-    count(key.y >> 21);
-    count(key.z >> 21);
-    count(key.w >> 21);
+    count_first(key.x);
+    count_first(key.y);
+    count_first(key.z);
+    count_first(key.w);
   }
   if (clusters > 1) cluster_sync();  // every CTA's acc is clear
   // f(key) of the lane's keys (each lane reads what it wrote)
@@ -173,6 +185,8 @@ __global__ void __launch_bounds__(1024, 2)
 
   // the keep-th largest key: its digits from the top
   uint32_t prefix = 0, known = 0;  // the digits found, and their bits
+  bool whole = false;              // whether every key that matches them is kept
+  int gt = -1, eq = 0;  // the lane's keys above the prefix and matching it, once counted
   for (int digit = 0; digit < 3; ++digit) {
     const int shift = digit == 0 ? 21 : (digit == 1 ? 10 : 0);
     const uint32_t mask = digit == 2 ? 1023u : 2047u;
@@ -196,6 +210,7 @@ __global__ void __launch_bounds__(1024, 2)
         n[2] += x.y;
         n[3] += x.x;
       }
+      if (digit == 0 && threadIdx.x == 0 && rank == 0) n[0] += sink + recent;
     }
     if (clusters > 1) {
 #pragma unroll
@@ -255,43 +270,71 @@ __global__ void __launch_bounds__(1024, 2)
     known |= mask << shift;
     left = found[1];
     const int size = found[2];
-    if (size == left || known == 0xffffffffu) break;  // every key with this prefix is kept
+    whole = size == left;  // every key with this prefix is kept
+    if (whole || known == 0xffffffffu) break;
     if (size > kRanked) continue;  // (`found` is written again only behind the next barriers)
-    // the bin's keys, in any order, to rank 0
+    // the bin's keys, in any order, to rank 0: the lane's one or none from a
+    // register, several by another pass
+    int matches = 0;
+    uint32_t match = 0;
+    gt = 0;
     for_keys([&](uint32_t key) {
-      if ((key & known) != prefix) return;
-      if (clusters > 1)
-        st_cluster(list + take_cluster(&list_n, 0), 0, (int)key);
-      else
-        list[atomicAdd(&list_n, 1)] = (int)key;
+      gt += (key & known) > prefix;
+      if ((key & known) == prefix) {
+        ++matches;
+        match = key;
+      }
     });
+    int place = matches;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(kFull, place, o);
+      if (lane >= o) place += x;
+    }
+    int start = 0;
+    if (lane == 31 && place > 0)
+      start = clusters > 1 ? take_cluster(&list_n, 0, place) : atomicAdd(&list_n, place);
+    place += __shfl_sync(kFull, start, 31) - matches;
+    auto put = [&](uint32_t key) {
+      if (clusters > 1)
+        st_cluster(list + place++, 0, (int)key);
+      else
+        list[place++] = (int)key;
+    };
+    if (matches == 1) put(match);
+    if (matches > 1)
+      for_keys([&](uint32_t key) {
+        if ((key & known) == prefix) put(key);
+      });
     if (clusters > 1)
       cluster_sync();
     else
       __syncthreads();
     if (rank == 0 && threadIdx.x < size) {
       const uint32_t own = (uint32_t)list[threadIdx.x];
-      int above = 0, same = 0;
-      auto meet = [&](int key, int j) {
-        above += j < size && (uint32_t)key > own;
-        same += j < size && (uint32_t)key == own;
+      int above = 0, same = 0;  // (the list's last vector is padded with 0)
+      auto meet = [&](int key) {
+        above += (uint32_t)key > own;
+        same += (uint32_t)key == own;
       };
 #pragma unroll 4
       for (int j = 0; j < size; j += 4) {
         const int4 four = *reinterpret_cast<const int4*>(list + j);
-        meet(four.x, j);
-        meet(four.y, j + 1);
-        meet(four.z, j + 2);
-        meet(four.w, j + 3);
+        meet(four.x);
+        meet(four.y);
+        meet(four.z);
+        meet(four.w);
       }
       if (above < left && left <= above + same)  // (equal keys write the same)
         for (int c = 0; c < clusters; ++c) {
           if (clusters > 1) {
             st_cluster(found + 0, c, (int)own);
             st_cluster(found + 1, c, left - above);
+            st_cluster(found + 2, c, same);
           } else {
             found[0] = (int)own;
             found[1] = left - above;
+            found[2] = same;
           }
         }
     }
@@ -299,18 +342,32 @@ __global__ void __launch_bounds__(1024, 2)
       cluster_sync();
     else
       __syncthreads();
-    prefix = (uint32_t)found[0];
+    const uint32_t key_found = (uint32_t)found[0];
+    if (matches == 1) {
+      gt += match > key_found;
+      eq = match == key_found;
+    } else if (matches > 1) {
+      for_keys([&](uint32_t key) {
+        if ((key & known) != prefix) return;
+        gt += key > key_found;
+        eq += key == key_found;
+      });
+    }
+    prefix = key_found;
     known = 0xffffffffu;
     left = found[1];
+    whole = found[2] == left;
     break;
   }
 
   // kept: the keys above the prefix, and the first `left` of those that match it
-  int gt = 0, eq = 0;
-  for_keys([&](uint32_t key) {
-    gt += (key & known) > prefix;
-    eq += (key & known) == prefix;
-  });
+  if (gt < 0) {
+    gt = 0;
+    for_keys([&](uint32_t key) {
+      gt += (key & known) > prefix;
+      eq += (key & known) == prefix;
+    });
+  }
   gt = __reduce_add_sync(kFull, gt);
   eq = __reduce_add_sync(kFull, eq);
   if (lane == 0) {
@@ -335,29 +392,31 @@ __global__ void __launch_bounds__(1024, 2)
   int32_t* kept = p.kept + ((int64_t)i * p.num_kv_heads + h) * p.max_keep;
   float* out = p.out ? p.out + at : nullptr;
   const uint32_t below = (1u << lane) - 1;
+  ngt += whole ? neq : min(neq, left);  // the keys kept before this warp's share
   for (int g = 0; g < groups; ++g) {
     const uint4 four = Staged ? mine[g * 32] : load_keys(base + g * 128);
     const uint32_t key[4] = {four.x, four.y, four.z, four.w};
-    int o[4];  // where the key goes, -1: nowhere
 #pragma unroll
     for (int j = 0; j < 4; ++j) {  // in step with the whole warp
-      const bool take = (key[j] & known) > prefix, tie = (key[j] & known) == prefix;
-      const uint32_t mt = __ballot_sync(kFull, take), me = __ballot_sync(kFull, tie);
-      const int eq_before = neq + __popc(me & below);
-      o[j] = take || (tie && eq_before < left)
-                 ? ngt + __popc(mt & below) + min(eq_before, left) : -1;
-      ngt += __popc(mt);
-      neq += __popc(me);
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (o[j] >= 0) {
-        const int k = base + g * 128 + j * 32;
-        const float x = key_weight(key[j]);
-        kept[o[j]] = k;
-        // (a key does not tell a zero's sign, a NaN's bits, a protected weight)
-        if (out) out[o[j]] = isfinite(x) && x != 0.f ? x : __ldg(w + k);
+      const uint32_t digits = key[j] & known;
+      bool keep_it = digits >= prefix;
+      if (!whole) {
+        const uint32_t me = __ballot_sync(kFull, digits == prefix);
+        if (digits == prefix && neq + __popc(me & below) >= left) keep_it = false;
+        neq += __popc(me);
       }
+      const uint32_t m = __ballot_sync(kFull, keep_it);
+      if (keep_it) {
+        const int o = ngt + __popc(m & below), k = base + g * 128 + j * 32;
+        kept[o] = k;
+        if (out) {
+          // (a key does not tell a zero's sign, a NaN's bits, a protected weight)
+          const float x = key_weight(key[j]);
+          out[o] = isfinite(x) && x != 0.f ? x : __ldg(w + k);
+        }
+      }
+      ngt += __popc(m);
+    }
   }
 }
 
