@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(1024, 2)
 // are contiguous; the sources are runs of head_dim * 2 bytes. Every byte moves
 // once: HBM-bound, and a thread has its four rows' loads in flight together.
 // ---------------------------------------------------------------------------
-constexpr int kMoveThreads = 256;
+constexpr int kMoveThreads = 128;
 constexpr int kMoveRows = 4;  // rows of a thread
 
 __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const EvictCompactParams p) {
