@@ -191,7 +191,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_wait();
   griddep_launch_dependents();
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (the shuffle tells the compiler that the warp's number is uniform)
+  const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   // the first keys, which the most queries see, of every head come first
   const int i = blockIdx.y;
   const int rank = blockIdx.x % clusters;
@@ -569,7 +570,9 @@ cudaError_t launch(const KeyWeightsParams& p, const CUtensorMap& q_map, const CU
   if (e != cudaSuccess) return e;
   const int G = p.num_heads / p.num_kv_heads;
   const int64_t key_tiles = ((int64_t)p.max_seq_len + kKT * kTM - 1) / (kKT * kTM);
-  const int64_t items = key_tiles * p.num_kv_heads * p.num_seqs;
+  // (the work is that of about num_tokens / max_query_len requests of full length)
+  const int64_t items =
+      key_tiles * p.num_kv_heads * ((p.num_tokens + p.max_query_len - 1) / p.max_query_len);
   const int q_tiles = (p.max_query_len + kTN / G - 1) / (kTN / G);
   // Split an item's Q tiles while there are fewer than 3 CTAs an SM to even
   // the load out and a CTA keeps at least 8 tiles for its K tiles. (One
