@@ -574,13 +574,15 @@ cudaError_t launch(const KeyWeightsParams& p, const CUtensorMap& q_map, const CU
   const int64_t items =
       key_tiles * p.num_kv_heads * ((p.num_tokens + p.max_query_len - 1) / p.max_query_len);
   const int q_tiles = (p.max_query_len + kTN / G - 1) / (kTN / G);
-  // Split an item's Q tiles while there are fewer than 3 CTAs an SM to even
-  // the load out and a CTA keeps at least 8 tiles for its K tiles. (One
-  // 8192-token prompt, 256 items of 8 to 256 tiles: 217 us whole, 214 in two,
-  // 255 in four: clusters wait until all their SMs are free, and every
-  // CTA pays about 4 us before its first and after its last product.)
+  // Split an item's Q tiles while there are fewer than two items an SM and a
+  // CTA keeps at least 8 tiles for its K tiles. (One 8192-token prompt, 256
+  // items of 8 to 256 tiles: 217 us whole, 212 in two, 255 in four; a mixed
+  // batch with some 480 items of about 12 tiles: 60 us whole, 85 in two: a
+  // cluster waits until all its SMs are free, and every CTA pays about 4 us
+  // before its first and after its last product. CTAs that went through a list
+  // of items, one after the other, paid as much between them.)
   int clusters = 1;
-  while (clusters < kMaxCluster && items * clusters < 3 * sms && q_tiles / clusters >= 16)
+  while (clusters < kMaxCluster && items * clusters < 2 * sms && q_tiles / clusters >= 16)
     clusters *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(key_tiles * p.num_kv_heads * clusters), (unsigned)p.num_seqs);
