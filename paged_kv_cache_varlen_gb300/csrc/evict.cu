@@ -21,7 +21,9 @@ constexpr uint32_t kFull = 0xffffffffu;
 // of a cluster of 2, 4 or 8 when it is long or the rows are few; the CTAs'
 // histograms are added up in the first one's. Rows of more than kStaged keys a
 // CTA are read again in each pass (from L2). The row's 4 bytes a key are
-// little: the passes' barriers and the histograms' atomics bound it.
+// little: the instructions of the passes bound it (73 % of the issue slots),
+// or their barriers when the rows are few. Measured: 64 x 8 rows of 1500 to
+// 8192 keys, 1024 kept: 21.4 us; 2 x 8 rows of 128K, 8192 kept: 24 us.
 // ---------------------------------------------------------------------------
 constexpr int kBins = 2048;
 constexpr int kScanThreads = 512;  // four bins each
@@ -426,6 +428,9 @@ __global__ void __launch_bounds__(1024, 2)
 // groups take the KV heads of one destination token, so a CTA's destinations
 // are contiguous; the sources are runs of head_dim * 2 bytes. Every byte moves
 // once: HBM-bound, and a thread has its four rows' loads in flight together.
+// Measured: 64 requests, 1024 tokens of 8 heads of 128 each: 88.5 us, 6.1 TB/s
+// (90 % of the measured copy rate); with 2 or 8 rows a thread 94.7 and 106 us,
+// with 256 or 512 threads 91.7 and 96.8 us.
 // ---------------------------------------------------------------------------
 constexpr int kMoveThreads = 128;
 constexpr int kMoveRows = 4;  // rows of a thread

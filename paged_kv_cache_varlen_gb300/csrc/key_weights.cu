@@ -17,6 +17,11 @@
 // memory or transposition is needed. The next tile's loads go out as soon as
 // the MMAs have taken this one's registers, before its exponentials. K is read
 // once; single-token steps are bound by that read.
+// Measured (32 query and 8 KV heads of 128): 64 contexts of 512 to 4096 keys
+// 49.5 us, 6.3 TB/s (92 % of the measured copy rate); 8 contexts of 32K to 128K
+// 236 us, 6.7 TB/s (98 %). The same with the tile staged by TMA, four 4 KB
+// slots a warp: 66.7 and 280 us (a third of the warps fit); with the next tile
+// in a second set of registers: 57.4 and 257 us.
 #include <math.h>
 
 #include "key_weights.cuh"

@@ -27,7 +27,12 @@
 //     few dozen additions keep a sum over 10^5 columns within 2^-21.
 //
 // Bound: one ex2 a score (32 a cycle and SM) and 2 D flops a score
-// (8192 a cycle and SM dense): 512 cycles each for 128 x 128 at D = 128.
+// (8192 a cycle and SM dense): 512 cycles each for 128 x 128 at D = 128, so
+// 1024 a Q tile against 256 keys; the epilogue's warps alone take 1240 with
+// their other instructions, and about 1600 beside the issuing and copying
+// warps that wait. Measured: one 8192-token prompt, 32 query and 8 KV heads of
+// 128: 209 to 225 us, 1.24 to 1.33 PFLOP/s (65 to 70 % of the measured bf16
+// rate); 512 queries over 32K keys 131 us.
 #include <math.h>
 
 #include "key_weights.cuh"
@@ -438,9 +443,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int step = clusters * QT * G;
     for (int t = 0; ok && t < n; ++t, first -= step, left -= step) {
       const uint32_t s = (uint32_t)t % kStages;
-      // even lanes: the tile's scores, odd lanes: its lse
-      ok = warp_wait((lane & 1) ? l_full0 + s * 8 : s_full0 + b * 8,
-                     (lane & 1) ? (uint32_t)t / kStages : turn, p.status, abort);
+      ok = warp_wait(s_full0 + b * 8, turn, p.status, abort) &&
+           warp_wait(l_full0 + s * 8, (uint32_t)t / kStages, p.status, abort);
       if (!ok) break;
       tc_fence_after();
       const uint32_t acc = tmem + lanes + (x * kAcc + b) * kHalf;
