@@ -49,8 +49,10 @@ __device__ __forceinline__ uint4 ld_once(const uint16_t* p) {
 }
 
 // NT: 8-column tiles held in registers at a time; ONE: every column of a
-// request fits in them (single tokens and short steps), so Q is loaded once.
-template <int D, int NT, bool ONE>
+// request fits in them (single tokens and short steps), so Q is loaded once;
+// LOOP: a warp goes on to further units of its head (without, it has one: 13
+// registers fewer, 49.5 us for 56.3 on the first batch above).
+template <int D, int NT, bool ONE, bool LOOP>
 __global__ void __launch_bounds__(kWarps * 32)
     key_weights_kernel(const KeyWeightsParams p, const int chunk) {
   // Behind the tcgen05 grid of the same call (which started once everything
@@ -60,9 +62,11 @@ __global__ void __launch_bounds__(kWarps * 32)
   griddep_launch_dependents();
   if (blockIdx.y == p.num_seqs) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int unit = blockIdx.x * kWarps + warp;
+  // a warp's units are the same head's: the stride is a multiple of the heads
+  const int unit = blockIdx.x * kWarps + warp, stride = gridDim.x * kWarps;
   const int h = unit % p.num_kv_heads;
-  const int key0 = (unit / p.num_kv_heads) * chunk;
+  int key0 = (unit / p.num_kv_heads) * chunk;
+  const int step = stride / p.num_kv_heads * chunk;
   const int i = blockIdx.y;
   KeyRequest r;
   if (!key_request(p, i, unit == 0 && lane == 0, &r)) return;
@@ -103,17 +107,11 @@ __global__ void __launch_bounds__(kWarps * 32)
       }
     }
   };
-  // block ids of the chunk's 16-key tiles, one a lane
   const int32_t* table = p.block_table + (int64_t)i * p.max_blocks;
-  const int tiles = (min(chunk, r.L - key0) + 15) / 16;
-  int32_t ids = -1;
-  if (lane < tiles) ids = __ldg(table + (key0 + lane * 16) / p.block_size);
-  const bool lost = lane < tiles && (ids < 0 || ids >= p.num_blocks);
-  if (lost) ids = -1;
-  if (__any_sync(kFull, lost) && lane == 0) set_status(p.status, PKV_DEV_BAD_BLOCK);
   float* out = p.out + ((int64_t)r.row * p.num_kv_heads + h) * p.row_len;
   const float* in = p.in + ((int64_t)r.row * p.num_kv_heads + h) * p.row_len;
 
+  int32_t ids = -1;  // block ids of the chunk's 16-key tiles, one a lane
   uint4 ka[KB], kb[KB];  // rows row and row + 8 of a tile
   auto fetch = [&](int t) {
     const int32_t id = __shfl_sync(kFull, ids, t);
@@ -146,49 +144,58 @@ __global__ void __launch_bounds__(kWarps * 32)
   };
 #pragma unroll
   for (int b = 0; b < KB; ++b) ka[b] = kb[b] = make_uint4(0, 0, 0, 0);
-  fetch(0);
-  if (ONE) load_columns(0);
-  for (int t = 0; t < tiles; ++t) {
-    const int k0 = key0 + t * 16;
-    const bool there = __shfl_sync(kFull, ids, t) >= 0;
-    const int key = k0 + row + quad * 8;
-    const bool mine = there && quad < 2 && key < r.L;
-    float before = 0.f;
-    if (mine && key < r.prior && p.decay != 0.f) before = p.decay * in[key];
-    float s0 = 0.f, s1 = 0.f;  // keys k0 + row, k0 + row + 8
-    if (ONE) {
-      float c[NT][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
-        scores(n, c[n]);
-      }
-      if (t + 1 < tiles) fetch(t + 1);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) weights(n, c[n], k0, s0, s1);
-    } else {
-      // from the first column group that sees the tile's first key
-      for (int c0 = max(0, k0 - qpos0) * G / (NT * 8) * (NT * 8); c0 < cols; c0 += NT * 8) {
-        load_columns(c0);
+  if (ONE && LOOP) load_columns(0);
+  do {
+    const int tiles = (min(chunk, r.L - key0) + 15) / 16;
+    ids = lane < tiles ? __ldg(table + (key0 + lane * 16) / p.block_size) : -1;
+    const bool lost = lane < tiles && (ids < 0 || ids >= p.num_blocks);
+    if (lost) ids = -1;
+    if (__any_sync(kFull, lost) && lane == 0) set_status(p.status, PKV_DEV_BAD_BLOCK);
+    fetch(0);
+    if (ONE && !LOOP) load_columns(0);
+    for (int t = 0; t < tiles; ++t) {
+      const int k0 = key0 + t * 16;
+      const bool there = __shfl_sync(kFull, ids, t) >= 0;
+      const int key = k0 + row + quad * 8;
+      const bool mine = there && quad < 2 && key < r.L;
+      float before = 0.f;
+      if (mine && key < r.prior && p.decay != 0.f) before = p.decay * in[key];
+      float s0 = 0.f, s1 = 0.f;  // keys k0 + row, k0 + row + 8
+      if (ONE) {
+        float c[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          float c[4] = {0.f, 0.f, 0.f, 0.f};
-          scores(n, c);
-          weights(n, c, k0, s0, s1);
+          c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
+          scores(n, c[n]);
         }
-      }
-      if (t + 1 < tiles) fetch(t + 1);
-    }
+        if (t + 1 < tiles) fetch(t + 1);
 #pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      s0 += __shfl_xor_sync(kFull, s0, o);
-      s1 += __shfl_xor_sync(kFull, s1, o);
+        for (int n = 0; n < NT; ++n) weights(n, c[n], k0, s0, s1);
+      } else {
+        // from the first column group that sees the tile's first key
+        for (int c0 = max(0, k0 - qpos0) * G / (NT * 8) * (NT * 8); c0 < cols; c0 += NT * 8) {
+          load_columns(c0);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
+            scores(n, c);
+            weights(n, c, k0, s0, s1);
+          }
+        }
+        if (t + 1 < tiles) fetch(t + 1);
+      }
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) {
+        s0 += __shfl_xor_sync(kFull, s0, o);
+        s1 += __shfl_xor_sync(kFull, s1, o);
+      }
+      if (mine) out[key] = before + (quad ? s1 : s0);
     }
-    if (mine) out[key] = before + (quad ? s1 : s0);
-  }
+    key0 += step;
+  } while (LOOP && key0 < r.L);
 }
 
-template <int D, int NT, bool ONE>
+template <int D, int NT, bool ONE, bool LOOP = false>
 cudaError_t launch(const KeyWeightsParams& p, cudaStream_t stream) {
   // Keys of a warp's unit: 128 amortise its start (64 x 512-4096 keys, 8 KV
   // heads: 49.5 us; 64 keys 50.3, 256 54.2); fewer while that leaves less
@@ -198,8 +205,20 @@ cudaError_t launch(const KeyWeightsParams& p, cudaStream_t stream) {
   auto units_of = [&](int c) { return ((int64_t)p.max_seq_len + c - 1) / c * p.num_kv_heads; };
   while (chunk > 16 && units_of(chunk) * p.num_seqs < 8192) chunk /= 2;
   const int64_t units = units_of(chunk);
+  int64_t ctas = (units + kWarps - 1) / kWarps;
+  if constexpr (ONE && !LOOP) {
+    // max_seq_len may be far above the requests' lengths: past so many CTAs,
+    // fewer of them go on to further units (64 x 512-4096 keys under a bound
+    // of 131072: 57 us, 141 with a warp for each unit in bounds)
+    if (ctas * p.num_seqs > 32768) return launch<D, NT, ONE, true>(p, stream);
+  }
+  if (LOOP) {
+    const int64_t hkv = p.num_kv_heads;
+    ctas = 8192 / p.num_seqs > 0 ? 8192 / p.num_seqs : 1;
+    ctas = (ctas + hkv - 1) / hkv * hkv;  // a warp's stride is a multiple of the heads
+  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((units + kWarps - 1) / kWarps), (unsigned)p.num_seqs + (p.after_tc ? 1u : 0u));
+  cfg.gridDim = dim3((unsigned)ctas, (unsigned)p.num_seqs + (p.after_tc ? 1u : 0u));
   cfg.blockDim = dim3(kWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -207,7 +226,7 @@ cudaError_t launch(const KeyWeightsParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, key_weights_kernel<D, NT, ONE>, p, chunk);
+  return cudaLaunchKernelEx(&cfg, key_weights_kernel<D, NT, ONE, LOOP>, p, chunk);
 }
 
 template <int D>

@@ -34,8 +34,18 @@
 // 128: 209 to 225 us, 1.24 to 1.33 PFLOP/s (65 to 70 % of the measured bf16
 // rate); 512 queries over 32K keys 131 us.
 #include <math.h>
+#include <stddef.h>
 
 #include "key_weights.cuh"
+
+#ifdef PKV_TEST_HOLD_ARRIVAL
+// Test builds only: while set, epilogue warp 0 of CTA 0 withholds its release
+// of its first accumulator, so that an issuing warp's bounded wait runs out.
+__device__ int g_pkv_test_hold_key_weights;
+extern "C" int pkv_test_hold_key_weights(int on) {
+  return (int)cudaMemcpyToSymbol(g_pkv_test_hold_key_weights, &on, sizeof(int));
+}
+#endif
 
 namespace pkv {
 namespace {
@@ -56,7 +66,7 @@ constexpr int kAcc = 3;                  // accumulators of kHalf columns per K 
 constexpr uint32_t kKCol = kKT * kAcc * kHalf; // then the K tiles: bf16 pairs, D / 2 columns each
 static_assert(kKCol + kKT * 64 <= kTmemCols, "accumulators and K tiles fit in TMEM");
 
-struct Bars {
+struct Bars {  // kNumBars barriers, then the rest
   uint64_t k_land, k_read;     // K in shared memory; read by the epilogue warps
   uint64_t k_full[kKT];        // K in tensor memory
   uint64_t q_full[kStages], q_empty[kStages];
@@ -68,6 +78,9 @@ struct Bars {
   uint32_t masked[kStages];  // bit g: some column of the tile's group g of 32 adds nothing
 };
 
+constexpr uint32_t kNumBars = offsetof(Bars, tmem_base) / 8;
+constexpr int kListed = 256;  // requests at most whose items a CTA lists
+
 template <int D>
 struct Layout {
   static constexpr int NCH = D / 64;               // 128-byte column chunks of a row
@@ -77,12 +90,16 @@ struct Layout {
   static constexpr int LSE_OFF = Q_OFF + kStages * TILE_BYTES;     // [kStages][kTN] float
   static constexpr int RED_OFF = LSE_OFF + kStages * kTN * 4;      // [kMaxCluster][2][256] float
   static constexpr int BAR_OFF = RED_OFF + kMaxCluster * 2 * kKT * kTM * 4;
-  static constexpr int NEED = 1024 + BAR_OFF + (int)sizeof(Bars);
+  static constexpr int LIST_OFF = BAR_OFF + ((int)sizeof(Bars) + 15) / 16 * 16;  // [kListed + 1]
+  static constexpr int NEED = 1024 + LIST_OFF + (kListed + 1) * 4;
   // one CTA per SM: each allocates all 512 TMEM columns
   static constexpr int BYTES = NEED > 120 * 1024 ? NEED : 120 * 1024;
 };
 static_assert(Layout<128>::BYTES <= 227 * 1024, "the stages fit a CTA");
 
+__device__ __forceinline__ void mbar_inval(uint32_t bar) {
+  asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
@@ -182,27 +199,22 @@ __device__ __forceinline__ int lse_slot(int col) {
   return ((col >> 4) << 4) | ((col & 6) << 1) | ((col >> 2) & 2) | (col & 1);
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
-    key_weights_tc_kernel(const __grid_constant__ CUtensorMap q_map,
-                          const __grid_constant__ CUtensorMap k_map, const KeyWeightsParams p,
-                          const int clusters) {
+// One item: request i, KV head and keys by its place `local` among the
+// request's items (every head's first keys, which the most queries see, come
+// first), split over `ctas` CTAs of a cluster. Whole CTA. `again`: more items
+// may follow; `started`: the CTA has had one before (its tensor memory and
+// barriers are there). False when a wait gave up.
+template <int D, bool again>
+__device__ __forceinline__ bool key_item(const CUtensorMap& q_map, const CUtensorMap& k_map,
+                                         const KeyWeightsParams& p, uint8_t* smem, int i,
+                                         int local, int rank, int ctas, bool flag,
+                                         bool* started) {
   using Lay = Layout<D>;
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   Bars* bars = reinterpret_cast<Bars*>(smem + Lay::BAR_OFF);
-
-  griddep_wait();
-  griddep_launch_dependents();
-
   // (the shuffle tells the compiler that the warp's number is uniform)
   const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  // the first keys, which the most queries see, of every head come first
-  const int i = blockIdx.y;
-  const int rank = blockIdx.x % clusters;
-  const int h = (blockIdx.x / clusters) % p.num_kv_heads;
-  const int key0 = (int)(blockIdx.x / clusters) / p.num_kv_heads * (kKT * kTM);
+  const int h = local % p.num_kv_heads;
+  const int key0 = local / p.num_kv_heads * (kKT * kTM);
   const int G = p.num_heads / p.num_kv_heads;
   const int32_t* table = p.block_table + (int64_t)i * p.max_blocks;
   // an epilogue thread's key, and its page: looked up before the request's
@@ -213,25 +225,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int look = warp == kTmaWarp ? box_key : my_key;
   if (warp <= kTmaWarp && look / p.block_size < p.max_blocks)
     my_page = __ldg(table + look / p.block_size);
-  // the CTAs of a cluster share (request, head, keys): these exits are uniform
+  // these exits are uniform, for a cluster too
   KeyRequest r;
-  if (!key_request(p, i, threadIdx.x == 0 && blockIdx.x == 0, &r)) return;
+  if (!key_request(p, i, flag, &r)) return true;
   if (r.qlen <= p.short_max_q) {  // on the mma.sync grid
-    if (p.no_short && threadIdx.x == 0 && blockIdx.x == 0)
-      set_status(p.status, PKV_DEV_BAD_LENGTHS);
-    return;
+    if (p.no_short && flag) set_status(p.status, PKV_DEV_BAD_LENGTHS);
+    return true;
   }
-  if (key0 >= r.L) return;
+  if (key0 >= r.L) return true;
   const int nk = min(kKT, (r.L - key0 + kTM - 1) / kTM);  // K tiles with keys
   const int QT = kTN / G;                                 // queries per Q tile
   const int qpos0 = r.L - r.qlen;
   const int j0 = max(0, key0 - qpos0);                    // the first query that sees key0
   const int all_tiles = (r.qlen - j0 + QT - 1) / QT;
-  const int n = (all_tiles - rank + clusters - 1) / clusters;  // tiles rank, rank + clusters, ...
+  const int n = (all_tiles - rank + ctas - 1) / ctas;  // tiles rank, rank + ctas, ...
 
   if (warp == kTmaWarp && lane == 0) {
-    prefetch_tmap(&k_map);
-    prefetch_tmap(&q_map);
+    if (!*started) {
+      prefetch_tmap(&k_map);
+      prefetch_tmap(&q_map);
+      bars->abort = 0;
+    } else {  // (every arrival on them has been waited for)
+      for (uint32_t b = 0; b < kNumBars; ++b) mbar_inval(smem_addr(bars) + b * 8);
+    }
     mbar_init(smem_addr(&bars->k_land), 1);
     mbar_init(smem_addr(&bars->k_read), 8 * nk);
     for (int x = 0; x < kKT; ++x) mbar_init(smem_addr(&bars->k_full[x]), 8);
@@ -247,17 +263,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_addr(&bars->s_free[x][b]), 4);
       }
     mbar_init(smem_addr(&bars->mma_done), nk);
-    bars->abort = 0;
     fence_barrier_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == kMmaWarp && !*started) {
     tmem_alloc(smem_addr(&bars->tmem_base), kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (clusters > 1) cluster_arrive();  // waited for before the first remote store
+  *started = true;
+  if (ctas > 1) cluster_arrive();  // waited for before the first remote store
   const uint32_t tmem = bars->tmem_base;
   volatile int32_t* abort = &bars->abort;
   const uint32_t q_s = smem_addr(smem + Lay::Q_OFF);
@@ -293,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             !mbar_wait(smem_addr(&bars->q_empty[s]), (t / kStages - 1) & 1, p.status, abort))
           break;
         mbar_arrive_expect_tx(smem_addr(&bars->q_full[s]), bytes);
-        const int j = r.t0 + j0 + (rank + t * clusters) * QT;
+        const int j = r.t0 + j0 + (rank + t * ctas) * QT;
         for (int c = 0; c < Lay::NCH; ++c)
           tma_load_3d(q_s + s * Lay::TILE_BYTES + c * Lay::CH_BYTES, &q_map,
                       smem_addr(&bars->q_full[s]), c * 64, h * G, j);
@@ -302,6 +318,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int g = max(0, t - kStages); g < t; ++g)
         mbar_wait(smem_addr(&bars->q_full[g % kStages]), (g / kStages) & 1, nullptr);
       mbar_wait(smem_addr(&bars->k_land), 0, nullptr);
+      // and, where the barriers will be set up again, so do the issuing warps'
+      // last releases of the stages
+      if (again && t == n)
+        for (int g = max(0, n - kStages); g < n; ++g)
+          mbar_wait(smem_addr(&bars->q_empty[g % kStages]), (g / kStages) & 1, p.status, abort);
     }
   } else if (warp >= kMmaWarp) {
     // ---- the products of K tile x. (A lane's next operands wait for the
@@ -360,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       src[e] = p.lse + (int64_t)r.t0 * p.num_heads + h * G + c % G;
     }
     auto fetch = [&](int t, float (&v)[E]) {
-      const int j = j0 + (rank + t * clusters) * QT;
+      const int j = j0 + (rank + t * ctas) * QT;
 #pragma unroll
       for (int e = 0; e < E; ++e)
         v[e] = t < n && dj[e] < r.qlen - j
@@ -440,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // columns there are from this half's first one on
     int first = (wkey - qpos0 - j0 - rank * QT) * G - half * kHalf;
     int left = (r.qlen - j0 - rank * QT) * G - half * kHalf;
-    const int step = clusters * QT * G;
+    const int step = ctas * QT * G;
     for (int t = 0; ok && t < n; ++t, first -= step, left -= step) {
       const uint32_t s = (uint32_t)t % kStages;
       ok = warp_wait(s_full0 + b * 8, turn, p.status, abort) &&
@@ -463,7 +484,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (g == 1) {  // the tile is in registers, and its lse
           tc_fence_before();
           __syncwarp();
-          arrive_if(s_free0 + b * 8, lane == 0);
+#ifdef PKV_TEST_HOLD_ARRIVAL
+          if (!(g_pkv_test_hold_key_weights && blockIdx.x == 0 && blockIdx.y == 0 && warp == 0 &&
+                t == 0))
+#endif
+            arrive_if(s_free0 + b * 8, lane == 0);
           arrive_if(l_empty0 + s * 8, lane == 0);
         }
         if (plain) {
@@ -533,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int slot = warp < kEpiWarps ? (rank * 2 + (warp >> 3)) * kKeys + (warp & 7) * 32 +
                                           (lane >> 2) + 8 * (lane & 3)
                                     : -1;
-  if (clusters > 1) {
+  if (ctas > 1) {
     __syncwarp();
     cluster_wait();  // every CTA of the cluster has started
     if (slot >= 0) st_cluster(smem_addr(red + slot), 0, total);
@@ -547,26 +572,96 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (rank == 0 && threadIdx.x < kKeys) {
     if (my_key < r.L && my_page >= 0 && my_page < p.num_blocks) {
       total = red[threadIdx.x];
-      for (int c = 1; c < 2 * clusters; ++c) total += red[c * kKeys + threadIdx.x];
+      for (int c = 1; c < 2 * ctas; ++c) total += red[c * kKeys + threadIdx.x];
       const int64_t at = ((int64_t)r.row * p.num_kv_heads + h) * p.row_len + my_key;
       p.out[at] = my_key < r.prior && p.decay != 0.f ? fmaf(p.decay, p.in[at], total) : total;
     }
   }
+  // all of the item's work is complete
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
-    __syncwarp();
-    tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+  tc_fence_after();
+  return *const_cast<volatile int32_t*>(&bars->abort) == 0;
+}
+
+// Not Listed: a cluster of `ctas` CTAs for each item (blockIdx.y the request,
+// blockIdx.x / ctas its item). Listed: each CTA goes through a share of all
+// requests' items, listed in shared memory; every other turn goes backwards
+// through the CTAs, so that a CTA's items are of mixed sizes.
+template <int D, bool Listed>
+__global__ void __launch_bounds__(kThreads, 1)
+    key_weights_tc_kernel(const __grid_constant__ CUtensorMap q_map,
+                          const __grid_constant__ CUtensorMap k_map, const KeyWeightsParams p,
+                          const int ctas) {
+  using Lay = Layout<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+
+  griddep_wait();
+  griddep_launch_dependents();
+
+  bool started = false;
+  if constexpr (!Listed) {
+    key_item<D, false>(q_map, k_map, p, smem, blockIdx.y, blockIdx.x / ctas, blockIdx.x % ctas,
+                       ctas, threadIdx.x == 0 && blockIdx.x == 0, &started);
+  } else {
+    int* before = reinterpret_cast<int*>(smem + Lay::LIST_OFF);  // items before each request
+    for (int i = threadIdx.x; i < p.num_seqs; i += kThreads) {
+      KeyRequest r;
+      const bool any = key_request(p, i, blockIdx.x == 0, &r);
+      const bool here = any && r.qlen > p.short_max_q;
+      if (any && !here && p.no_short && blockIdx.x == 0) set_status(p.status, PKV_DEV_BAD_LENGTHS);
+      before[i + 1] = here ? (r.L + kKT * kTM - 1) / (kKT * kTM) * p.num_kv_heads : 0;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      const int lane = threadIdx.x;
+      int sum = 0;
+      for (int i0 = 0; i0 < p.num_seqs; i0 += 32) {
+        const bool in = i0 + lane < p.num_seqs;
+        int v = in ? before[i0 + lane + 1] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int x = __shfl_up_sync(kFull, v, o);
+          if (lane >= o) v += x;
+        }
+        if (in) before[i0 + lane + 1] = sum + v;
+        sum += __shfl_sync(kFull, v, 31);
+      }
+      if (lane == 0) before[0] = 0;
+    }
+    __syncthreads();
+    for (int turn = 0;; ++turn) {
+      const int64_t at = (int64_t)turn * gridDim.x +
+                         ((turn & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      if (at >= before[p.num_seqs]) break;
+      int lo = 0, hi = p.num_seqs;  // the last request with before[lo] <= at
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (before[mid] <= at)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      if (!key_item<D, true>(q_map, k_map, p, smem, lo, (int)at - before[lo], 0, 1, false,
+                             &started))
+        break;
+    }
   }
+  if (started && __shfl_sync(kFull, threadIdx.x >> 5, 0) == kMmaWarp)
+    tmem_dealloc(reinterpret_cast<Bars*>(smem + Lay::BAR_OFF)->tmem_base, kTmemCols);
 }
 
 template <int D>
 cudaError_t launch(const KeyWeightsParams& p, const CUtensorMap& q_map, const CUtensorMap& k_map,
                    cudaStream_t stream) {
-  auto kernel = key_weights_tc_kernel<D>;
-  static SmemLimit limit;
-  cudaError_t e = limit.ensure(reinterpret_cast<const void*>(kernel), Layout<D>::BYTES);
+  static SmemLimit limit, limit_listed;
+  cudaError_t e = limit.ensure(reinterpret_cast<const void*>(key_weights_tc_kernel<D, false>),
+                               Layout<D>::BYTES);
+  if (e == cudaSuccess)
+    e = limit_listed.ensure(reinterpret_cast<const void*>(key_weights_tc_kernel<D, true>),
+                            Layout<D>::BYTES);
   if (e != cudaSuccess) return e;
   int dev = 0, sms = 0;
   e = cudaGetDevice(&dev);
@@ -583,13 +678,25 @@ cudaError_t launch(const KeyWeightsParams& p, const CUtensorMap& q_map, const CU
   // items of 8 to 256 tiles: 217 us whole, 212 in two, 255 in four; a mixed
   // batch with some 480 items of about 12 tiles: 60 us whole, 85 in two: a
   // cluster waits until all its SMs are free, and every CTA pays about 4 us
-  // before its first and after its last product. CTAs that went through a list
-  // of items, one after the other, paid as much between them.)
+  // before its first and after its last product.)
   int clusters = 1;
   while (clusters < kMaxCluster && items * clusters < 2 * sms && q_tiles / clusters >= 16)
     clusters *= 2;
+  // Many items: max_seq_len may be far above the requests' lengths, and a CTA
+  // that finds no keys takes a turn on an SM like any other (one CTA an SM).
+  // CTAs that list the items first skip the empty ones. (32 chunks of 20 to
+  // 100 queries, 2560 items in bounds and about half of them there: 59.5 us,
+  // 69 with a CTA for each; 512 queries over 32K keys, 1024 items, all there:
+  // 136 us, 131 with a CTA for each, which the hardware hands out as SMs fall
+  // free; 13 requests, 1040 items in bounds, 484 there: 83 and 59 us, the
+  // difference being the single tokens' grid, which then waits to the end.)
+  const int64_t bound = key_tiles * p.num_kv_heads * p.num_seqs;
+  const bool listed =
+      clusters == 1 && p.num_seqs <= kListed && bound > 12 * sms && bound < (1 << 30);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(key_tiles * p.num_kv_heads * clusters), (unsigned)p.num_seqs);
+  cfg.gridDim = listed ? dim3((unsigned)sms)
+                       : dim3((unsigned)(key_tiles * p.num_kv_heads * clusters),
+                              (unsigned)p.num_seqs);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = Layout<D>::BYTES;
   cfg.stream = stream;
@@ -602,7 +709,9 @@ cudaError_t launch(const KeyWeightsParams& p, const CUtensorMap& q_map, const CU
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, q_map, k_map, p, clusters);
+  return listed ? cudaLaunchKernelEx(&cfg, key_weights_tc_kernel<D, true>, q_map, k_map, p, 1)
+                : cudaLaunchKernelEx(&cfg, key_weights_tc_kernel<D, false>, q_map, k_map, p,
+                                     clusters);
 }
 
 }  // namespace

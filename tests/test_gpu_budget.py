@@ -717,3 +717,131 @@ def test_offsets_past_32_bits():
     # 4 terms of about 1, each within a few fp32 steps
     np.testing.assert_allclose(f64(w[0]), want, rtol=2.0 ** -19)
     assert st.item() == 0
+
+
+# ------------------------------------------ bounds far above what is there, and
+# more work than CTAs
+@pytest.mark.parametrize("qlens,name", [
+    ([1] * 9, "single tokens"), ([1, 40, 300, 2, 90, 64, 1, 33, 257], "a mixed batch"),
+    ([60, 40, 300, 33, 90, 64, 70, 34, 257], "chunks"),
+])
+def test_key_weights_under_a_loose_bound(qlens, name):
+    # max_seq_len only bounds the lengths: a million of them changes how the
+    # work is handed out, not a bit of the result
+    lens = [max(x) for x in zip([1, 700, 1300, 257, 90, 64, 2049, 333, 512], qlens)]
+    b = Batch(lens, qlens, 8, 2, 128, seed=21, poison=False)
+    tight = b.call(torch.zeros((9, 2, 2049), device="cuda"))
+    w = torch.full((9, 2, 1 << 20), 3.0, device="cuda")
+    b.max_len = 1 << 20
+    st = status_word()
+    got = b.call(w, prior=[0] * 9, st=st)
+    assert st.item() == 0
+    for i, L in enumerate(lens):
+        assert torch.equal(got[i, :, :L], tight[i, :, :L])
+        assert (got[i, :, L:] == 3.0).all()
+
+
+def test_key_weights_of_many_requests_under_a_loose_bound():
+    # more requests than a CTA lists
+    n = 300
+    r = np.random.RandomState(5)
+    qlens = r.randint(30, 50, n)
+    lens = qlens + r.randint(0, 200, n)
+    b = Batch(list(lens), list(qlens), 4, 2, 64, seed=22, poison=False)
+    tight = b.call(torch.zeros((n, 2, int(lens.max())), device="cuda"))
+    b.max_len = 20000
+    got = b.call(torch.zeros((n, 2, 20000), device="cuda"), prior=[0] * n)
+    assert torch.equal(got[:, :, :int(lens.max())], tight)
+    assert (got[:, :, int(lens.max()):] == 0).all()
+
+
+def test_evict_select_under_a_loose_bound():
+    w = weight_rows_of("special", (3, 2, 150000), 8)
+    lens, keep = [700, 90, 3000], [100, 90, 1]
+    kept, _ = pkv.evict_select(w, i32(lens), i32(keep), 150000, 120, num_sink=2, num_recent=9)
+    check_select(w, lens, keep, [0, 1, 2], 2, 9, kept, None, torch.full_like(kept, -1), None)
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_rope_of_more_tokens_than_resident_warps(inter):
+    t = 10007
+    q, k, v, pool, pos, slots = rope_inputs(t, 3, 1, 64, 77, max_pos=1 << 20)
+    inv = pkv.rope_frequencies(64, 500000.0)[0].cuda()
+    pool0 = pool.clone()
+    out = pkv.rope_kv_cache_write(q, pool, k, v, i32(pos), i32(slots), inv, interleaved=inter)
+    check_rope(q, k, v, pool0, pos, slots, inv, 1.0, inter, out, pool)
+
+
+def test_two_streams_at_once():
+    # no call keeps anything that another one on another stream could share
+    batches = [Batch([900, 70], [300, 1], 8, 2, 64, seed=s, poison=False) for s in (31, 32)]
+    want = [b.call(torch.zeros((2, 2, 900), device="cuda")) for b in batches]
+    sel = [pkv.evict_select(w, i32([900, 70]), i32([200, 10]), 900, 200)[0] for w in want]
+    streams = [torch.cuda.Stream() for _ in batches]
+    outs = [torch.zeros((2, 2, 900), device="cuda") for _ in batches]
+    kept = [torch.full((2, 2, 200), -1, dtype=torch.int32, device="cuda") for _ in batches]
+    lens, keep = i32([900, 70]), i32([200, 10])
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for b, s, o, kk in zip(batches, streams, outs, kept):
+            b.call(o, decay=0.0, stream=s)
+            pkv.evict_select(o, lens, keep, 900, 200, kept=kk, stream=s)
+    torch.cuda.synchronize()
+    for w, o, s, kk in zip(want, outs, sel, kept):
+        assert torch.equal(w, o) and torch.equal(s, kk)
+
+
+def test_budget_binding_refusals():
+    b = Batch([40, 20], [1, 1], 8, 2, 64, seed=3)
+    w = torch.zeros((2, 2, 40), device="cuda")
+    with pytest.raises(TypeError):
+        b.call(w.double())
+    with pytest.raises(ValueError):
+        b.call(w[:, :, ::2])                       # not contiguous
+    with pytest.raises(ValueError):
+        b.call(torch.zeros((2, 3, 40), device="cuda"))
+    with pytest.raises(ValueError):
+        b.call(w, out=torch.zeros((3, 2, 40), device="cuda"))
+    with pytest.raises(ValueError):
+        b.call(w, rows=[0, 1, 2])
+    with pytest.raises(ValueError):
+        b.call(w.cpu())
+    with pytest.raises(binding.PkvError) as e:     # rows shorter than the contexts
+        b.call(torch.zeros((2, 2, 39), device="cuda"))
+    assert e.value.status == 1
+    lens, keep = i32([40, 20]), i32([5, 5])
+    with pytest.raises(ValueError):
+        pkv.evict_select(w, lens, keep[:1], 40, 5)
+    with pytest.raises(ValueError):
+        pkv.evict_select(w, lens, keep, 40, 5, kept=torch.zeros((2, 2, 6), dtype=torch.int32,
+                                                                device="cuda"))
+    with pytest.raises(TypeError):
+        pkv.evict_select(w, lens.long(), keep, 40, 5)
+    with pytest.raises(binding.PkvError):          # the weights would overwrite their source
+        pkv.evict_select(w, lens, keep, 40, 5, weights_out=w)
+    src, dst, kept, pool = compaction([40, 20], [5, 5], 2, 64, 16, 1)
+    with pytest.raises(ValueError):
+        pkv.evict_compact(pool, i32(src), i32(dst), i32(kept[:, :1]), keep)
+    with pytest.raises(ValueError):
+        pkv.evict_compact(pool, i32(src[:1]), i32(dst), i32(kept), keep)
+    with pytest.raises(TypeError):
+        pkv.evict_compact(pool.float(), i32(src), i32(dst), i32(kept), keep)
+
+
+def test_debug_checks_name_the_bad_entry_of_budget_calls(monkeypatch):
+    monkeypatch.setenv("PKV_DEBUG_CHECKS", "1")
+    b = Batch([40, 20], [1, 1], 8, 2, 64, seed=3)
+    w = torch.zeros((2, 2, 40), device="cuda")
+    with pytest.raises(ValueError, match="weight_rows"):
+        b.call(w, rows=[1, 1])
+    with pytest.raises(ValueError, match="keep_len"):
+        pkv.evict_select(w, i32([40, 20]), i32([5, 21]), 40, 30)
+    src, dst, kept, pool = compaction([40, 20], [5, 5], 2, 64, 16, 1)
+    dst[1, 0] = src[0, kept[0, 0, 0] // 16]
+    with pytest.raises(ValueError, match="both a source and a destination"):
+        pkv.evict_compact(pool, i32(src), i32(dst), i32(kept), i32([5, 5]))
+    q, k, v, pool, pos, slots = rope_inputs(3, 4, 2, 64, 3)
+    pos[1] = -4
+    with pytest.raises(ValueError, match="positions"):
+        pkv.rope_kv_cache_write(q, pool, k, v, i32(pos), i32(slots),
+                                pkv.rope_frequencies(64)[0].cuda())
