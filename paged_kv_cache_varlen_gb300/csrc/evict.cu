@@ -11,30 +11,29 @@ constexpr uint32_t kFull = 0xffffffffu;
 
 // ---------------------------------------------------------------------------
 // Selection: the n heaviest of a row's keys by a radix search for the n-th
-// largest value (digits of 11, 11 and 10 bits, a histogram each), then one pass
-// that writes the keys above it and the first of those equal to it, in index
-// order. The search ends early when a digit's bin is taken whole, or when it
-// is so small that its keys can be ranked against one another (the usual case
-// after one digit of some thousand keys).
+// largest value, then one pass that writes the keys above it and the first of
+// those equal to it, in index order. The search counts the keys in 2048 bins,
+// finds the n-th one's bin, counts that bin's keys by their next 11 bits, and so
+// on; it ends when a bin is taken whole, or is so small that its keys can be
+// ranked against one another. The first bins are 1/32 of an octave each, so the
+// latter is the usual case after one pass of 100K keys.
 //
-// A row (request, KV head) is read once into the shared memory of one CTA, or
-// of a cluster of 2, 4 or 8 when it is long or the rows are few; the CTAs'
-// histograms are added up in the first one's. Rows of more than kStaged keys a
-// CTA are read again in each pass (from L2). The row's 4 bytes a key are
-// little: the instructions of the passes bound it (73 % of the issue slots),
-// or their barriers when the rows are few. Measured: 64 x 8 rows of 1500 to
-// 8192 keys, 1024 kept: 21.4 us; 2 x 8 rows of 128K, 8192 kept: 24 us.
+// A row (request, KV head) is read once into the shared memory of one CTA, or,
+// when the rows are few, of a cluster, as long as each of its CTAs has an SM
+// (launch_evict_select). The CTAs add up one another's bins by groups of 32,
+// then the 32 of one group, so that each finds the same bin for itself with one
+// barrier a pass. Rows of more than kStaged keys a CTA are read again in each
+// pass (from L2). The row's 4 bytes a key are little: the instructions bound it
+// (69 % of the issue slots of the SMs at work; the SMs that get a fourth row
+// end last), or barriers and latency when the rows are few. Measured: 64 x 8
+// rows of 1500 to 8192 keys, 1024 kept: 14.1 us; 2 x 8 rows of 128K, 8192 kept:
+// 18.3 us.
 // ---------------------------------------------------------------------------
 constexpr int kBins = 2048;
-constexpr int kScanThreads = 512;  // four bins each
+constexpr int kGroups = kBins / 32;  // sums of 32 bins, one bin a lane
 constexpr int kMaxCluster = 8;
 constexpr int kStaged = 40960;     // keys of a CTA's share that shared memory holds
-// Copies of the histogram, one for each lane modulo kCopies: attention weights
-// crowd into a few dozen bins of the first digit. Each starts 8 banks on, so
-// that a bin's copies lie in different banks.
-constexpr int kCopies = 2;
-constexpr int kCopyStride = kBins + 8;
-constexpr int kRanked = 384;  // keys at most that are ranked against one another
+constexpr int kRanked = 384;       // keys at most that are ranked against one another
 
 // Order-preserving key of a weight: larger weights have larger keys, -0 and
 // +0 the same one, a NaN the largest but kProtected, which stands for the keys
@@ -44,6 +43,16 @@ constexpr uint32_t kProtected = 0xffffffffu;
 __device__ __forceinline__ uint32_t weight_key(float w) {
   const int32_t b = __float_as_int(w + 0.f);
   return w != w ? 0xfffffffeu : (uint32_t)b ^ ((uint32_t)(b >> 31) | 0x80000000u);
+}
+
+// The bins of the first pass: 32 an octave from 2^-40 to 2^24, where a weight
+// that decides anything lies; the first and the last bin take what is below and
+// above. (It is monotonic, so any row may be counted so; a row whose keep-th
+// key lies in one of the two end bins is counted again by the key's bits.)
+constexpr int kFineShift = 23 - 5;
+constexpr int kFineLow = (int)(0x80000000u >> kFineShift) + (127 - 40) * 32;
+__device__ __forceinline__ uint32_t fine_bin(uint32_t key) {
+  return (uint32_t)min(max((int)(key >> kFineShift) - kFineLow, 0), kBins - 1);
 }
 
 // The weight of a key, where it tells it; not finite for kProtected and NaN.
@@ -64,53 +73,70 @@ __device__ __forceinline__ void cluster_sync() {
 }
 __device__ __forceinline__ uint32_t cluster_addr(const void* p, int rank) {
   uint32_t remote;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_addr(p)), "r"(rank));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(remote)
+               : "r"(smem_addr(p)), "r"(rank));
   return remote;
 }
 // To the same shared-memory offset of cluster CTA `rank`.
 __device__ __forceinline__ void st_cluster(const int* p, int rank, int v) {
   asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(cluster_addr(p, rank)), "r"(v) : "memory");
 }
-__device__ __forceinline__ int take_cluster(const int* p, int rank, int add) {  // fetch and add
+__device__ __forceinline__ int ld_cluster(const int* p, int rank) {
   int v;
-  asm volatile("atom.shared::cluster.add.s32 %0, [%1], %2;"
-               : "=r"(v)
-               : "r"(cluster_addr(p, rank)), "r"(add)
-               : "memory");
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(p, rank)) : "memory");
   return v;
 }
-__device__ __forceinline__ void add_cluster(const int* p, int rank, int v) {
-  asm volatile("red.shared::cluster.add.s32 [%0], %1;" ::"r"(cluster_addr(p, rank)), "r"(v)
-               : "memory");
+// The sum of *p over the cluster's CTAs.
+__device__ __forceinline__ int sum_cluster(const int* p, int clusters) {
+  if (clusters == 1) return *p;
+  int x[kMaxCluster], sum = 0;
+#pragma unroll
+  for (int c = 0; c < kMaxCluster; ++c) x[c] = c < clusters ? ld_cluster(p, c) : 0;
+#pragma unroll
+  for (int c = 0; c < kMaxCluster; ++c) sum += x[c];
+  return sum;
+}
+__device__ __forceinline__ int inclusive_sum(int x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(kFull, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
 }
 
 // Staged: the CTA's share of the row is kept in shared memory.
 template <bool Staged>
 __global__ void __launch_bounds__(1024, 2)
     evict_select_kernel(const EvictSelectParams p, const int clusters) {
-  extern __shared__ __align__(16) uint32_t smem[];
-  int* acc = reinterpret_cast<int*>(smem);  // [kBins] of the cluster, in rank 0 (none without)
-  uint32_t* staged = smem + (clusters > 1 ? kBins : 0);
-  __shared__ __align__(16) int hist[kCopies * kCopyStride];
-  __shared__ int warp_sum[kScanThreads / 32];
+  extern __shared__ __align__(16) uint32_t staged[];
+  // (two of each in turn: the other CTAs read them, and one is written again
+  // only behind the barrier that follows every read of it)
+  __shared__ __align__(16) int hist[2][kBins];
+  __shared__ int group_sum[2][kGroups];  // of 32 bins, from the largest
   __shared__ int found[3];  // bin (or key), places left in it, its size
-  __shared__ __align__(16) int list[kRanked];  // of the cluster, in rank 0
+  __shared__ __align__(16) int list[kRanked];  // the CTA's keys, then
+  __shared__ __align__(16) int all[kRanked];   // the cluster's
   __shared__ int list_n;
   __shared__ int warp_gt[32], warp_eq[32];
   __shared__ int cta_gt[kMaxCluster], cta_eq[kMaxCluster];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   griddep_wait();
   griddep_launch_dependents();
-  const int rank = blockIdx.x % clusters, h = blockIdx.x / clusters, i = blockIdx.y;
+  uint32_t h, rank;  // a cluster, or a CTA on its own, has a row
+  asm("mov.u32 %0, %%clusterid.x;" : "=r"(h));
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  const int i = blockIdx.y;
   const int L = __ldg(p.seq_lens + i), keep = __ldg(p.keep_lens + i);
   const int row = p.rows ? __ldg(p.rows + i) : i;
   // the CTAs of a cluster share the row: these exits are uniform
   if (L < 0 || L > p.max_seq_len || keep < 0 || keep > L || keep > p.max_keep) {
-    if (threadIdx.x == 0 && blockIdx.x == 0) set_status(p.status, PKV_DEV_BAD_LENGTHS);
+    if (threadIdx.x == 0 && rank == 0 && h == 0) set_status(p.status, PKV_DEV_BAD_LENGTHS);
     return;
   }
   if (row < 0 || row >= p.num_rows) {
-    if (threadIdx.x == 0 && blockIdx.x == 0) set_status(p.status, PKV_DEV_BAD_ROW);
+    if (threadIdx.x == 0 && rank == 0 && h == 0) set_status(p.status, PKV_DEV_BAD_ROW);
     return;
   }
   if (keep == 0) return;
@@ -120,64 +146,99 @@ __global__ void __launch_bounds__(1024, 2)
   const int sink = min(p.num_sink, keep - recent);
   int left = keep;  // places for the keys that match the digits found so far
 
-  // the warp's share of the row: `groups` times 4 steps of 32 keys, in index
-  // order; key 32 j + lane of group g is component j of the lane's vector g
+  // the warp's share of the row: `groups` times 128 keys; a lane's vector of a
+  // group is its keys 4 lane to 4 lane + 3
   const int per_group = clusters * (int)blockDim.x * 4;
-  const int groups = (int)(((int64_t)L + per_group - 1) / per_group);
-  const int64_t first = (int64_t)(rank * warps + warp) * groups * 128;
-  const int base = (int)min((int64_t)L, first) + lane;
-  const int end = (int)min((int64_t)L, first + (int64_t)groups * 128);
+  const int groups = (int)(((uint32_t)L + (uint32_t)per_group - 1) / (uint32_t)per_group);
+  // (at most L + per_group: below 2^32)
+  const uint32_t first = (rank * warps + warp) * (uint32_t)groups * 128;
+  const int base = (int)min((uint32_t)L, first);
+  const int end = (int)min((uint32_t)L, first + (uint32_t)groups * 128);
   // (no weight has key 0: it stands behind the share's end)
   auto key_of = [&](int k, float x) {
     return k >= end ? 0u : k < sink || k >= L - recent ? kProtected : weight_key(x);
   };
-  auto count = [&](uint32_t bin) {
-    atomicAdd(&hist[(lane % kCopies) * kCopyStride + bin], 1);
+  auto clear = [&](int b, int last) {
+#pragma unroll 1
+    for (int v = threadIdx.x; v < kBins / 4; v += blockDim.x)
+      reinterpret_cast<int4*>(hist[b])[v] = make_int4(0, 0, 0, v == kBins / 4 - 1 ? last : 0);
   };
-  // (the protected keys are hundreds in one bin: added as a number, below)
-  auto count_first = [&](uint32_t key) {
-    if (key != kProtected && key != 0) count(key >> 21);
-  };
-  auto clear = [&] {
-    for (int b = threadIdx.x; b < kCopies * kCopyStride / 4; b += blockDim.x)
-      reinterpret_cast<int4*>(hist)[b] = make_int4(0, 0, 0, 0);
-  };
-  clear();
+  // (the protected keys would be hundreds in one bin: added as a number)
+  clear(0, rank == 0 ? sink + recent : 0);
   if (threadIdx.x == 0) list_n = 0;
+#pragma unroll 1
   for (int b = threadIdx.x; b < kRanked; b += blockDim.x) list[b] = 0;
-  if (clusters > 1)
-    for (int b = threadIdx.x; b < kBins; b += blockDim.x) acc[b] = 0;
   __syncthreads();
   uint4* mine = reinterpret_cast<uint4*>(staged) + warp * groups * 32 + lane;
-  // groups whose keys are all there and compete: nothing to check key by key
-  const int plain_lo = sink + lane, plain_hi = min(end, L - recent) - 128 + lane;
-  auto load_keys = [&](int k) {
-    const float* at_k = w + k;
-    if (k >= plain_lo && k <= plain_hi)  // (the same for the whole warp)
-      return make_uint4(weight_key(__ldg(at_k)), weight_key(__ldg(at_k + 32)),
-                        weight_key(__ldg(at_k + 64)), weight_key(__ldg(at_k + 96)));
-    float x[4];
+  // the weights of the lane's vectors of groups g and g + 1 (a row may be read
+  // to the end of its storage), and their keys
+  const bool vectors = ((p.row_len & 3) | (reinterpret_cast<uintptr_t>(p.weights) & 15)) == 0;
+  auto load_two = [&](int g, float4* x) {
+    const int k = base + g * 128 + lane * 4;
+    if (vectors) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = k + j * 32 < end ? __ldg(at_k + j * 32) : 0.f;
-    return make_uint4(key_of(k, x[0]), key_of(k + 32, x[1]), key_of(k + 64, x[2]),
-                      key_of(k + 96, x[3]));
+      for (int u = 0; u < 2; ++u) {
+        x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k + u * 128 < end) x[u] = __ldg(reinterpret_cast<const float4*>(w + k + u * 128));
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int at_k = k + u * 128;
+        x[u].x = at_k < end ? __ldg(w + at_k) : 0.f;
+        x[u].y = at_k + 1 < end ? __ldg(w + at_k + 1) : 0.f;
+        x[u].z = at_k + 2 < end ? __ldg(w + at_k + 2) : 0.f;
+        x[u].w = at_k + 3 < end ? __ldg(w + at_k + 3) : 0.f;
+      }
+    }
+  };
+  // groups whose keys are all there and compete: nothing to check key by key
+  const int plain_hi = min(end, L - recent) - 128;
+  auto plain = [&](int g) { return base + g * 128 >= sink && base + g * 128 <= plain_hi; };
+  auto keys_of = [&](int g, const float4& x) {
+    const int k = base + g * 128 + lane * 4;
+    if (plain(g))
+      return make_uint4(weight_key(x.x), weight_key(x.y), weight_key(x.z), weight_key(x.w));
+    return make_uint4(key_of(k, x.x), key_of(k + 1, x.y), key_of(k + 2, x.z), key_of(k + 3, x.w));
+  };
+  auto count_first = [&](uint32_t key) { atomicAdd(&hist[0][fine_bin(key)], 1); };
+  auto count_if = [&](uint32_t key) {
+    if (key != kProtected && key != 0) count_first(key);
   };
   // the keys, and the histogram of their first digit, in one pass
-#pragma unroll 2
-  for (int g = 0; g < groups; ++g) {
-    const uint4 key = load_keys(base + g * 128);
-    if (Staged) mine[g * 32] = key;
-    count_first(key.x);
-    count_first(key.y);
-    count_first(key.z);
-    count_first(key.w);
+  for (int g = 0; g < groups; g += 2) {
+    float4 x[2];
+    load_two(g, x);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (g + u == groups) break;
+      const uint4 key = keys_of(g + u, x[u]);
+      if (Staged) mine[(g + u) * 32] = key;
+      if (plain(g + u)) {
+        count_first(key.x);
+        count_first(key.y);
+        count_first(key.z);
+        count_first(key.w);
+      } else {
+        count_if(key.x);
+        count_if(key.y);
+        count_if(key.z);
+        count_if(key.w);
+      }
+    }
   }
-  if (clusters > 1) cluster_sync();  // every CTA's acc is clear
   // f(key) of the lane's keys (each lane reads what it wrote)
   auto for_keys = [&](auto f) {
 #pragma unroll 2
     for (int g = 0; g < groups; ++g) {
-      const uint4 key = Staged ? mine[g * 32] : load_keys(base + g * 128);
+      uint4 key;
+      if (Staged) {
+        key = mine[g * 32];
+      } else {
+        float4 x[2];
+        load_two(g, x);
+        key = keys_of(g, x[0]);
+      }
       f(key.x);
       f(key.y);
       f(key.z);
@@ -189,131 +250,119 @@ __global__ void __launch_bounds__(1024, 2)
   uint32_t prefix = 0, known = 0;  // the digits found, and their bits
   bool whole = false;              // whether every key that matches them is kept
   int gt = -1, eq = 0;  // the lane's keys above the prefix and matching it, once counted
-  for (int digit = 0; digit < 3; ++digit) {
-    const int shift = digit == 0 ? 21 : (digit == 1 ? 10 : 0);
-    const uint32_t mask = digit == 2 ? 1023u : 2047u;
-    if (digit > 0) {
-      clear();
+  int shift = kFineShift;
+  uint32_t mask = kBins - 1;
+  for (int pass = 0;; ++pass) {
+    const int* bins = hist[pass & 1];
+    if (pass > 0) {
+      clear(pass & 1, 0);
       __syncthreads();
       for_keys([&](uint32_t key) {
-        if ((key & known) == prefix) count((key >> shift) & mask);
+        if ((key & known) == prefix) atomicAdd(&hist[pass & 1][(key >> shift) & mask], 1);
       });
     }
     __syncthreads();
-    // a thread has 4 bins, counted from the largest
-    const int top = kBins - 1 - threadIdx.x * 4;
-    int n[4] = {0, 0, 0, 0};
-    if (threadIdx.x < kScanThreads) {
+#pragma unroll 1
+    for (int v = threadIdx.x; v < kBins / 4; v += blockDim.x) {
+      const int4 x = reinterpret_cast<const int4*>(bins)[kBins / 4 - 1 - v];
+      int sum = x.x + x.y + x.z + x.w;
 #pragma unroll
-      for (int c = 0; c < kCopies; ++c) {
-        const int4 x = *reinterpret_cast<const int4*>(hist + c * kCopyStride + top - 3);
-        n[0] += x.w;
-        n[1] += x.z;
-        n[2] += x.y;
-        n[3] += x.x;
-      }
-      if (digit == 0 && threadIdx.x == 0 && rank == 0) n[0] += sink + recent;
-    }
-    if (clusters > 1) {
-#pragma unroll
-      for (int b = 0; b < 4; ++b)
-        if (n[b] != 0) add_cluster(acc + top - b, 0, n[b]);
-      cluster_sync();
-      if (rank == 0 && threadIdx.x < kScanThreads) {
-        int4* own = reinterpret_cast<int4*>(acc + top - 3);
-        const int4 x = *own;
-        n[0] = x.w;
-        n[1] = x.z;
-        n[2] = x.y;
-        n[3] = x.x;
-        *own = make_int4(0, 0, 0, 0);  // for the next digit
-      }
-    }
-    if (rank == 0) {
-      // the bin of the left-th key: a scan over the threads
-      const int sum = n[0] + n[1] + n[2] + n[3];
-      int incl = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(kFull, incl, o);
-        if (lane >= o) incl += x;
-      }
-      if (lane == 31 && warp < kScanThreads / 32) warp_sum[warp] = incl;
-      __syncthreads();
-      const int before =
-          incl - sum + __reduce_add_sync(kFull, lane < min(warp, kScanThreads / 32) ? warp_sum[lane] : 0);
-      if (sum > 0 && before < left && before + sum >= left) {  // exactly one thread
-        int places = left - before, b = 0, size = n[0];
-#pragma unroll
-        for (int c = 0; c < 3; ++c)
-          if (b == c && places > n[c]) {
-            places -= n[c];
-            b = c + 1;
-            size = n[c + 1];
-          }
-        for (int c = 0; c < clusters; ++c) {
-          if (clusters > 1) {
-            st_cluster(found + 0, c, top - b);
-            st_cluster(found + 1, c, places);
-            st_cluster(found + 2, c, size);
-          } else {
-            found[0] = top - b;
-            found[1] = places;
-            found[2] = size;
-          }
-        }
-      }
+      for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(kFull, sum, o);
+      if ((lane & 7) == 0) group_sum[pass & 1][v / 8] = sum;
     }
     if (clusters > 1)
       cluster_sync();
     else
       __syncthreads();
-    prefix |= (uint32_t)found[0] << shift;
-    known |= mask << shift;
+    if (warp == 0) {
+      // the group of bins of the left-th key, then its bin
+      const int* sums = group_sum[pass & 1] + 2 * lane;
+      const int n0 = sum_cluster(sums, clusters), n1 = sum_cluster(sums + 1, clusters);
+      const int upto = inclusive_sum(n0 + n1, lane), upto0 = upto - n1;
+      const uint32_t at = __ballot_sync(kFull, upto >= left);  // the first of these
+      const int owner = at ? __ffs(at) - 1 : 31;
+      const bool second = upto0 < left;
+      const int group = __shfl_sync(kFull, 2 * lane + second, owner);
+      const int before = __shfl_sync(kFull, second ? upto0 : upto0 - n0, owner);
+      const int bin = kBins - 1 - (group * 32 + lane);
+      const int n = sum_cluster(bins + bin, clusters);
+      const int incl = before + inclusive_sum(n, lane);
+      if (incl - n < left && incl >= left) {  // exactly one lane
+        found[0] = bin;
+        found[1] = left - (incl - n);
+        found[2] = n;
+      }
+    }
+    __syncthreads();
+    // (`found` is written again only behind the next barriers)
+    if (pass > 0) {
+      prefix |= (uint32_t)found[0] << shift;
+      known |= mask << shift;
+    } else if (found[0] > 0 && found[0] < kBins - 1) {
+      prefix = (uint32_t)(found[0] + kFineLow) << shift;
+      known = ~0u << shift;
+    } else {
+      shift = 32 - 11;
+      continue;
+    }
     left = found[1];
     const int size = found[2];
     whole = size == left;  // every key with this prefix is kept
     if (whole || known == 0xffffffffu) break;
-    if (size > kRanked) continue;  // (`found` is written again only behind the next barriers)
-    // the bin's keys, in any order, to rank 0: the lane's one or none from a
+    if (size > kRanked) {
+      const int next = max(shift - 11, 0);
+      mask = (1u << (shift - next)) - 1;
+      shift = next;
+      continue;
+    }
+    // the bin's keys, in any order, to a list: the lane's one or none from a
     // register, several by another pass
     int matches = 0;
     uint32_t match = 0;
     gt = 0;
     for_keys([&](uint32_t key) {
-      gt += (key & known) > prefix;
-      if ((key & known) == prefix) {
+      gt += key > (prefix | ~known);
+      if (key - prefix <= ~known) {
         ++matches;
         match = key;
       }
     });
-    int place = matches;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(kFull, place, o);
-      if (lane >= o) place += x;
-    }
+    int place = inclusive_sum(matches, lane);
     int start = 0;
-    if (lane == 31 && place > 0)
-      start = clusters > 1 ? take_cluster(&list_n, 0, place) : atomicAdd(&list_n, place);
+    if (lane == 31 && place > 0) start = atomicAdd(&list_n, place);
     place += __shfl_sync(kFull, start, 31) - matches;
     auto put = [&](uint32_t key) {
-      if (clusters > 1)
-        st_cluster(list + place++, 0, (int)key);
-      else
-        list[place++] = (int)key;
+      if (place < kRanked) list[place++] = (int)key;  // (always, unless the weights change)
     };
     if (matches == 1) put(match);
     if (matches > 1)
       for_keys([&](uint32_t key) {
         if ((key & known) == prefix) put(key);
       });
-    if (clusters > 1)
+    const int* ranked = list;
+    if (clusters > 1) {
+      // every CTA collects the lists of all of them
+      ranked = all;
       cluster_sync();
-    else
-      __syncthreads();
-    if (rank == 0 && threadIdx.x < size) {
-      const uint32_t own = (uint32_t)list[threadIdx.x];
+#pragma unroll 1
+      for (int t = threadIdx.x; t < kRanked; t += blockDim.x) {
+        int j = t, from = -1, key = 0;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+          const int n = c < clusters ? min(max(ld_cluster(&list_n, c), 0), kRanked) : 0;
+          if (from < 0 && j < n)
+            from = c;
+          else if (from < 0)
+            j -= n;
+        }
+        if (from >= 0) key = ld_cluster(list + j, from);
+        all[t] = key;
+      }
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int t = threadIdx.x; t < size; t += blockDim.x) {
+      const uint32_t own = (uint32_t)ranked[t];
       int above = 0, same = 0;  // (the list's last vector is padded with 0)
       auto meet = [&](int key) {
         above += (uint32_t)key > own;
@@ -321,29 +370,19 @@ __global__ void __launch_bounds__(1024, 2)
       };
 #pragma unroll 4
       for (int j = 0; j < size; j += 4) {
-        const int4 four = *reinterpret_cast<const int4*>(list + j);
+        const int4 four = *reinterpret_cast<const int4*>(ranked + j);
         meet(four.x);
         meet(four.y);
         meet(four.z);
         meet(four.w);
       }
-      if (above < left && left <= above + same)  // (equal keys write the same)
-        for (int c = 0; c < clusters; ++c) {
-          if (clusters > 1) {
-            st_cluster(found + 0, c, (int)own);
-            st_cluster(found + 1, c, left - above);
-            st_cluster(found + 2, c, same);
-          } else {
-            found[0] = (int)own;
-            found[1] = left - above;
-            found[2] = same;
-          }
-        }
+      if (above < left && left <= above + same) {  // (equal keys write the same)
+        found[0] = (int)own;
+        found[1] = left - above;
+        found[2] = same;
+      }
     }
-    if (clusters > 1)
-      cluster_sync();
-    else
-      __syncthreads();
+    __syncthreads();
     const uint32_t key_found = (uint32_t)found[0];
     if (matches == 1) {
       gt += match > key_found;
@@ -366,8 +405,8 @@ __global__ void __launch_bounds__(1024, 2)
   if (gt < 0) {
     gt = 0;
     for_keys([&](uint32_t key) {
-      gt += (key & known) > prefix;
-      eq += (key & known) == prefix;
+      gt += key > (prefix | ~known);
+      eq += key - prefix <= ~known;
     });
   }
   gt = __reduce_add_sync(kFull, gt);
@@ -386,7 +425,7 @@ __global__ void __launch_bounds__(1024, 2)
       st_cluster(cta_eq + rank, lane, neq + eq);
     }
     cluster_sync();
-    for (int c = 0; c < rank; ++c) {
+    for (int c = 0; c < (int)rank; ++c) {
       ngt += cta_gt[c];
       neq += cta_eq[c];
     }
@@ -395,30 +434,58 @@ __global__ void __launch_bounds__(1024, 2)
   float* out = p.out ? p.out + at : nullptr;
   const uint32_t below = (1u << lane) - 1;
   ngt += whole ? neq : min(neq, left);  // the keys kept before this warp's share
-  for (int g = 0; g < groups; ++g) {
-    const uint4 four = Staged ? mine[g * 32] : load_keys(base + g * 128);
-    const uint32_t key[4] = {four.x, four.y, four.z, four.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {  // in step with the whole warp
-      const uint32_t digits = key[j] & known;
-      bool keep_it = digits >= prefix;
-      if (!whole) {
-        const uint32_t me = __ballot_sync(kFull, digits == prefix);
-        if (digits == prefix && neq + __popc(me & below) >= left) keep_it = false;
-        neq += __popc(me);
-      }
-      const uint32_t m = __ballot_sync(kFull, keep_it);
-      if (keep_it) {
-        const int o = ngt + __popc(m & below), k = base + g * 128 + j * 32;
-        kept[o] = k;
-        if (out) {
-          // (a key does not tell a zero's sign, a NaN's bits, a protected weight)
-          const float x = key_weight(key[j]);
-          out[o] = isfinite(x) && x != 0.f ? x : __ldg(w + k);
-        }
-      }
-      ngt += __popc(m);
+  // A group's kept keys go through shared memory, so that the lanes write them
+  // side by side: their indices where the group was staged, their keys where
+  // the histograms were (no CTA reads those any more).
+  int* heavy = &hist[0][0] + warp * 128;
+  for (int g = 0; g < groups; ++g) {  // in step with the whole warp
+    uint4 four;
+    if (Staged) {
+      four = mine[g * 32];
+    } else {
+      float4 x[2];
+      load_two(g, x);
+      four = keys_of(g, x[0]);
     }
+    int* at_k = reinterpret_cast<int*>(staged) + (Staged ? warp * groups + g : warp) * 128;
+    const uint32_t key[4] = {four.x, four.y, four.z, four.w};
+    bool keep_it[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) keep_it[j] = key[j] >= prefix;
+    if (!whole) {
+      int n = neq;  // matching keys before the lane's
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        n += __popc(__ballot_sync(kFull, key[j] - prefix <= ~known) & below);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (key[j] - prefix <= ~known && n++ >= left) keep_it[j] = false;
+      neq = __shfl_sync(kFull, n, 31);
+    }
+    int o = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o += __popc(__ballot_sync(kFull, keep_it[j]) & below);
+    __syncwarp();  // the keys of this group, and the buffers of the last one, have been read
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (keep_it[j]) {
+        at_k[o] = base + g * 128 + lane * 4 + j;
+        heavy[o] = (int)key[j];
+        ++o;
+      }
+    const int n = __shfl_sync(kFull, o, 31);
+    __syncwarp();
+    for (int t = lane; t < n; t += 32) {
+      const int k = at_k[t];
+      if (ngt + t >= keep) break;  // (never, unless the weights change while they are read)
+      kept[ngt + t] = k;
+      if (out) {
+        // (a key does not tell a zero's sign, a NaN's bits, a protected weight)
+        const float x = key_weight((uint32_t)heavy[t]);
+        out[ngt + t] = isfinite(x) && x != 0.f ? x : __ldg(w + k);
+      }
+    }
+    ngt += n;
   }
 }
 
@@ -509,21 +576,48 @@ cudaLaunchConfig_t config(dim3 grid, int threads, cudaStream_t stream, cudaLaunc
 
 namespace {
 
+// How many clusters of 1 to kMaxCluster CTAs the device holds at one CTA an SM
+// (the SMs of a cluster lie in one of its GPCs, which differ in size).
+class ClusterRoom {
+ public:
+  cudaError_t get(const int** fit) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (!done_[dev].load(std::memory_order_acquire)) {
+      std::lock_guard<std::mutex> lock(mu_);
+      if (!done_[dev].load(std::memory_order_relaxed)) {
+        e = fill(fit_[dev]);
+        if (e != cudaSuccess) return e;
+        done_[dev].store(true, std::memory_order_release);
+      }
+    }
+    *fit = fit_[dev];
+    return cudaSuccess;
+  }
+
+ private:
+  static cudaError_t fill(int* fit);
+  static constexpr int kMaxDevices = 64;
+  std::mutex mu_;
+  std::atomic<bool> done_[kMaxDevices] = {};
+  int fit_[kMaxDevices][kMaxCluster + 1] = {};
+};
+ClusterRoom cluster_room;
+
 template <bool Staged>
 cudaError_t launch_select(const EvictSelectParams& p, int clusters, int threads, int staged,
                           cudaStream_t stream) {
   auto kernel = evict_select_kernel<Staged>;
   static SmemLimit limit;
-  if (Staged) {
-    cudaError_t e =
-        limit.ensure(reinterpret_cast<const void*>(kernel), (kStaged + kBins) * 4);
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t e = limit.ensure(reinterpret_cast<const void*>(kernel), kStaged * 4);
+  if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg =
       config(dim3((unsigned)(p.num_kv_heads * clusters), (unsigned)p.num_seqs), threads, stream,
              attr);
-  cfg.dynamicSmemBytes = ((size_t)staged + (clusters > 1 ? kBins : 0)) * 4;
+  cfg.dynamicSmemBytes = (size_t)staged * 4;
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = (unsigned)clusters;
   attr[1].val.clusterDim.y = 1;
@@ -532,21 +626,49 @@ cudaError_t launch_select(const EvictSelectParams& p, int clusters, int threads,
   return cudaLaunchKernelEx(&cfg, kernel, p, clusters);
 }
 
+cudaError_t ClusterRoom::fill(int* fit) {
+  auto kernel = evict_select_kernel<true>;
+  cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kStaged * 4);
+  for (int c = 1; e == cudaSuccess && c <= kMaxCluster; ++c) {
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = config(dim3((unsigned)c), 1024, nullptr, attr);
+    cfg.dynamicSmemBytes = kStaged * 4;  // over half of an SM's
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)c;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    e = cudaOccupancyMaxActiveClusters(&fit[c], kernel, &cfg);
+  }
+  return e;
+}
+
 }  // namespace
 
 cudaError_t launch_evict_select(const EvictSelectParams& p, cudaStream_t stream) {
   const int64_t rows = (int64_t)p.num_seqs * p.num_kv_heads, L = p.max_seq_len;
-  // as few CTAs as keep a share at 8192 keys (four CTAs an SM), twice as many
-  // while the rows leave SMs without one and a share has over 2048 keys
+  const int* fit = nullptr;
+  cudaError_t e = cluster_room.get(&fit);
+  if (e != cudaSuccess) return e;
+  // Clusters only for rows of over 8192 keys that would leave SMs without work:
+  // the most CTAs a row, of 2048 keys at least, for which every CTA has an SM of
+  // its own (128K keys: 16 rows in clusters of 6: 18 us, of 8, of which 15 fit:
+  // 23 us, of 4: 24 us; 128 rows of 24K: one CTA each 12 us, clusters 17 us).
   int clusters = 1;
-  while (clusters < kMaxCluster && L > (int64_t)clusters * 8192) clusters *= 2;
-  while (clusters < kMaxCluster && rows * clusters * 2 <= 152 && L > (int64_t)clusters * 2048)
-    clusters *= 2;
-  const int threads = L > (int64_t)clusters * 8192 ? 1024 : 512;
+  if (L > 8192)
+    for (int c = 2; c <= kMaxCluster; ++c)
+      if (rows <= fit[c] && L >= 2048 * c) clusters = c;
+  // 1024 threads where a CTA has its SM alone (128 rows of 4096 keys: 6.1 us,
+  // with 512 7.3 us) or a long share (512 rows of 24K: 40 against 45 us), else
+  // 512 (512 rows of 4096: 12 us, with 1024 15.8, with 256 14.4 us)
+  const int64_t share_of = L / clusters;
+  const bool alone = rows * clusters <= fit[1];
+  const bool wide = clusters > 1 ? share_of > 8192 : share_of > (alone ? 2048 : 16384);
+  const int threads = wide ? 1024 : 512;
   const int64_t per_group = (int64_t)clusters * threads * 4;
   const int64_t share = (L + per_group - 1) / per_group * threads * 4;
   if (share <= kStaged) return launch_select<true>(p, clusters, threads, (int)share, stream);
-  return launch_select<false>(p, clusters, threads, 0, stream);
+  return launch_select<false>(p, clusters, threads, threads * 4, stream);
 }
 
 cudaError_t launch_evict_compact(const EvictCompactParams& p, cudaStream_t stream) {

@@ -458,6 +458,52 @@ def test_evict_select_long_rows(kind, L, keep):
     check_select(w, [L], [keep], [0], 3, 50, kept, None, torch.full_like(kept, -1), None)
 
 
+@pytest.mark.parametrize("kind", ["tiny", "huge", "negative", "around 2^-40", "around 2^24"])
+@pytest.mark.parametrize("L,keep", [(3001, 700), (600, 300), (150000, 60000)])
+def test_evict_select_outside_the_first_bins(kind, L, keep):
+    # the keep-th weight is below, above or at an end of the range that the first pass resolves
+    w = weight_rows_of("tail", (1, 2, L), 7)
+    if kind == "tiny":
+        w = w * 1e-30
+    elif kind == "huge":
+        w = w * 1e30
+    elif kind == "negative":
+        w = -w
+    else:
+        edge = torch.full_like(w, 2.0 ** -40 if kind == "around 2^-40" else 2.0 ** 24)
+        at = (w * 1000).to(torch.int32) % 5 - 2  # up to two neighbours to either side
+        w = (edge.view(torch.int32) + at).view(torch.float32)
+    kept, _ = pkv.evict_select(w, i32([L]), i32([keep]), L, keep, num_sink=2, num_recent=5)
+    check_select(w, [L], [keep], [0], 2, 5, kept, None, torch.full_like(kept, -1), None)
+
+
+@pytest.mark.parametrize("off", [0, 1])  # a row on a 16-byte boundary, or 4 bytes off it
+@pytest.mark.parametrize("seqs,hkv,L,keep", [
+    (19, 8, 4096, 512),     # a row for each SM
+    (20, 8, 2052, 700),     # more rows than SMs: rows of one, two and three groups of keys
+    (40, 8, 17000, 100),
+    (20, 8, 45000, 20000),  # too long to stage
+    (2, 8, 100004, 8192),   # few rows: CTAs in clusters of different sizes
+    (3, 8, 30000, 29999),
+    (9, 4, 30000, 1),
+    (5, 8, 9000, 4500),
+    (2, 2, 8196, 1000),
+])
+def test_evict_select_rows_and_lengths(seqs, hkv, L, keep, off):
+    flat = weight_rows_of("tail", (seqs * hkv * L + 4,), 9)
+    w = flat[off:off + seqs * hkv * L].view(seqs, hkv, L)
+    lens = [max(1, L - 37 * i * (L // 4000 + 1)) for i in range(seqs)]
+    ns = [min(n, keep) for n in lens]
+    out = torch.full((seqs, hkv, L), -7.0, device="cuda")
+    old_out = out.clone()
+    kept, _ = pkv.evict_select(w, i32(lens), i32(ns), L, keep, num_sink=4, num_recent=33,
+                               weights_out=out)
+    old_kept = torch.full_like(kept, -1)
+    for i, n in enumerate(ns):
+        old_kept[i, :, n:] = kept[i, :, n:]
+    check_select(w, lens, ns, list(range(seqs)), 4, 33, kept, out, old_kept, old_out)
+
+
 def test_evict_select_very_long_row():
     # longer than any on-chip copy of the row could be
     L, keep = 700001, 1234
