@@ -24,7 +24,7 @@ constexpr uint32_t kFull = 0xffffffffu;
 // then the 32 of one group, so that each finds the same bin for itself with one
 // barrier a pass. Rows of more than kStaged keys a CTA are read again in each
 // pass (from L2). The row's 4 bytes a key are little: the instructions bound it
-// (69 % of the issue slots of the SMs at work; the SMs that get a fourth row
+// (70 % of the issue slots of the SMs at work; the SMs that get a fourth row
 // end last), or barriers and latency when the rows are few. Measured: 64 x 8
 // rows of 1500 to 8192 keys, 1024 kept: 14.1 us; 2 x 8 rows of 128K, 8192 kept:
 // 18.3 us.
@@ -84,7 +84,10 @@ __device__ __forceinline__ void st_cluster(const int* p, int rank, int v) {
 }
 __device__ __forceinline__ int ld_cluster(const int* p, int rank) {
   int v;
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(p, rank)) : "memory");
+  asm volatile("ld.shared::cluster.s32 %0, [%1];"
+               : "=r"(v)
+               : "r"(cluster_addr(p, rank))
+               : "memory");
   return v;
 }
 // The sum of *p over the cluster's CTAs.

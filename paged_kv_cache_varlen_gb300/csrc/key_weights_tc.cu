@@ -16,9 +16,10 @@
 //     few items (one prompt: the first keys are seen by every query, the last
 //     by few); the partial sums meet in the first CTA's shared memory and are
 //     added in a fixed order;
-//   * warp 16 issues the TMA copies (Q ring of 4 tiles), warp 17 the MMAs
-//     (six accumulators of 64 columns, beside K in the 512 TMEM columns), warp 18
-//     loads the columns' -log2e * lse, warps 0-15 turn scores into weights
+//   * warp 16 issues the TMA copies (Q ring of 4 tiles), warp 17 loads the
+//     columns' -log2e * lse, warps 18 and 19 issue the MMAs of a K tile each
+//     (three accumulators of 64 columns, beside K in the 512 TMEM columns),
+//     warps 0-15 turn scores into weights
 //     (a warpgroup per K tile and half of the columns): a packed fma, ex2 and
 //     a packed add per pair of scores, no mask where every column sees
 //     every key of the warp;
@@ -31,8 +32,9 @@
 // 1024 a Q tile against 256 keys; the epilogue's warps alone take 1240 with
 // their other instructions, and about 1600 beside the issuing and copying
 // warps that wait. Measured: one 8192-token prompt, 32 query and 8 KV heads of
-// 128: 209 to 225 us, 1.24 to 1.33 PFLOP/s (65 to 70 % of the measured bf16
-// rate); 512 queries over 32K keys 131 us.
+// 128: 207 us, 1.35 PFLOP/s (71 % of the measured bf16 rate; 225 us over
+// three sets of inputs in turn); 512 queries over 32K keys 128 us. (One warp
+// issuing for both K tiles: 259 us.)
 #include <math.h>
 #include <stddef.h>
 
@@ -63,7 +65,7 @@ constexpr int kThreads = 32 * (kMmaWarp + kKT);
 constexpr int kMaxCluster = 4;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kAcc = 3;                  // accumulators of kHalf columns per K tile, in turn
-constexpr uint32_t kKCol = kKT * kAcc * kHalf; // then the K tiles: bf16 pairs, D / 2 columns each
+constexpr uint32_t kKCol = kKT * kAcc * kHalf;  // then the K tiles: bf16 pairs, D / 2 columns each
 static_assert(kKCol + kKT * 64 <= kTmemCols, "accumulators and K tiles fit in TMEM");
 
 struct Bars {  // kNumBars barriers, then the rest
@@ -447,7 +449,8 @@ __device__ __forceinline__ bool key_item(const CUtensorMap& q_map, const CUtenso
     }
     const float2 sc = make_float2(p.scale_log2, p.scale_log2);
     const uint32_t nl = smem_addr(lse_s + half * kHalf + 4 * (lane & 3));
-    const uint32_t s_full0 = smem_addr(&bars->s_full[x][0]), s_free0 = smem_addr(&bars->s_free[x][0]);
+    const uint32_t s_full0 = smem_addr(&bars->s_full[x][0]);
+    const uint32_t s_free0 = smem_addr(&bars->s_free[x][0]);
     const uint32_t l_full0 = smem_addr(&bars->l_full[0]), l_empty0 = smem_addr(&bars->l_empty[0]);
     const uint32_t masked0 = smem_addr(&bars->masked[0]);
     // sums of a few tiles, in two chains a key, then of the groups of tiles:

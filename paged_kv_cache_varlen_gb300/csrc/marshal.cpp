@@ -45,13 +45,15 @@ struct Call {
   int device = -1;
 
   const at::Tensor& any(PyObject* o, const char* name, at::ScalarType type, int64_t ndim) {
-    if (!THPVariable_Check(o)) throw Refused{PyExc_TypeError, std::string(name) + " must be a torch.Tensor"};
+    if (!THPVariable_Check(o))
+      throw Refused{PyExc_TypeError, std::string(name) + " must be a torch.Tensor"};
     const at::Tensor& t = THPVariable_Unpack(o);
     if (!t.is_cuda()) throw Refused{PyExc_ValueError, std::string(name) + " must be a CUDA tensor"};
     if (device < 0) device = t.get_device();
     if (t.get_device() != device)
       throw Refused{PyExc_ValueError, std::string(name) + " is on another device (cuda:" +
-                                          std::to_string(t.get_device()) + ") than the first tensor"};
+                                          std::to_string(t.get_device()) +
+                                          ") than the first tensor"};
     if (t.scalar_type() != type)
       throw Refused{PyExc_TypeError, std::string(name) + " must be " + type_name(type) + ", got " +
                                          type_name(t.scalar_type())};
@@ -62,7 +64,8 @@ struct Call {
   }
   const at::Tensor& dense(PyObject* o, const char* name, at::ScalarType type, int64_t ndim) {
     const at::Tensor& t = any(o, name, type, ndim);
-    if (!t.is_contiguous()) throw Refused{PyExc_ValueError, std::string(name) + " must be contiguous"};
+    if (!t.is_contiguous())
+      throw Refused{PyExc_ValueError, std::string(name) + " must be contiguous"};
     return t;
   }
   // [tokens, heads, head_dim] bf16, a token's heads contiguous; the distance
@@ -75,9 +78,9 @@ struct Call {
                                           shape_text({tokens, heads, head_dim}) + ", got " +
                                           shape_text(t.sizes())};
     if ((head_dim > 1 && t.stride(2) != 1) || (heads > 1 && t.stride(1) != head_dim))
-      throw Refused{PyExc_ValueError, std::string(name) +
-                                          ": the heads of a token must be contiguous, got strides " +
-                                          shape_text(t.strides())};
+      throw Refused{PyExc_ValueError,
+                    std::string(name) + ": the heads of a token must be contiguous, got strides " +
+                        shape_text(t.strides())};
     *stride = tokens > 1 ? t.stride(0) : heads * head_dim;
     return t;
   }
@@ -96,7 +99,8 @@ T* ptr(const at::Tensor& t) {
 }
 
 int32_t small(int64_t v) {
-  if (v > INT32_MAX || v < INT32_MIN) throw Refused{PyExc_ValueError, "a size does not fit 32 bits"};
+  if (v > INT32_MAX || v < INT32_MIN)
+    throw Refused{PyExc_ValueError, "a size does not fit 32 bits"};
   return (int32_t)v;
 }
 int64_t to_int(PyObject* o) {
@@ -114,13 +118,16 @@ float to_float(PyObject* o) {
 // integer handle) or torch's current one; raises PkvError on a status.
 template <class F>
 void run(const char* what, int device, PyObject* stream, F call) {
-  void* s = stream == Py_None
-                ? static_cast<void*>(c10::cuda::getCurrentCUDAStream(device).stream())
-                : reinterpret_cast<void*>(static_cast<uintptr_t>(PyLong_AsUnsignedLongLong(stream)));
+  void* s = nullptr;
+  if (stream == Py_None)
+    s = c10::cuda::getCurrentCUDAStream(device).stream();
+  else
+    s = reinterpret_cast<void*>(static_cast<uintptr_t>(PyLong_AsUnsignedLongLong(stream)));
   if (PyErr_Occurred()) throw Refused{nullptr, ""};
   int now = device;
   pkv_status st = PKV_ERR_CUDA;
-  if (cudaGetDevice(&now) == cudaSuccess && (now == device || cudaSetDevice(device) == cudaSuccess)) {
+  if (cudaGetDevice(&now) == cudaSuccess &&
+      (now == device || cudaSetDevice(device) == cudaSuccess)) {
     st = call(s);
     if (now != device) cudaSetDevice(now);
   }
@@ -248,7 +255,8 @@ PyObject* evict_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor& kept = c.dense(a[8], "kept", at::kInt, 3);
     const int64_t b = lens.size(0), hkv = weights.size(1);
     const int32_t max_len = small(to_int(a[3])), max_keep = small(to_int(a[4]));
-    if (keep.size(0) != b) throw Refused{PyExc_ValueError, "seq_lens and keep_lens differ in length"};
+    if (keep.size(0) != b)
+      throw Refused{PyExc_ValueError, "seq_lens and keep_lens differ in length"};
     if (kept.size(0) != b || kept.size(1) != hkv || kept.size(2) != max_keep)
       throw Refused{PyExc_ValueError, "kept must be [num_seqs, num_kv_heads, max_keep_len]"};
     float* out = nullptr;

@@ -56,7 +56,8 @@ def key_weights(weights, q, k_rows, lse, cu, lens, rows, prior, decay, scale, ou
                     err += np.where(w > 0, w * off, 0.0).sum(0)
             # summed one by one at worst
             err += total * eps * (n * g + 2)
-            before = np.where(np.arange(L) < old, np.asarray(weights[rows[i], h, :L], np.float64), 0)
+            before = np.asarray(weights[rows[i], h, :L], np.float64)
+            before = np.where(np.arange(L) < old, before, 0)
             if decay == 0:
                 before = np.zeros(L)
             out[rows[i], h, :L] = decay * before + total
