@@ -435,8 +435,8 @@ pkv_status pkv_rope_frequencies(double *inv_freq, float *factor, int32_t rotary_
  * v_new, are bit copies. Slots must be distinct, as in pkv_kv_cache_write.
  * head_dim: a multiple of 8 up to 512; rotary_dim: even, 2 .. head_dim. All
  * tensor pointers 16-byte aligned, strides multiples of 8 elements.
- * Errors: PKV_ERR_INVALID_ARG also when q_out overlaps k_new or v_new, or q
- * in any other way than the one allowed; PKV_DEV_BAD_POSITION (the token is
+ * Errors: PKV_ERR_INVALID_ARG also when q_out overlaps the pool, k_new or
+ * v_new, or q in any other way than the one allowed; PKV_DEV_BAD_POSITION (the token is
  * skipped, q_out's row included); PKV_DEV_BAD_SLOT (q_out's row is written).
  */
 pkv_status pkv_rope_kv_cache_write(void *q_out, void *kv_pool, const void *q, const void *k_new,

@@ -85,6 +85,7 @@ pkv_status pkv_rope_kv_cache_write(void* q_out, void* kv_pool, const void* q, co
       !aligned16(v_new) || (reinterpret_cast<uintptr_t>(inv_freq) & 7u) != 0)
     return PKV_ERR_INVALID_ARG;
   if (head_dim % 8 != 0 || head_dim > 512) return PKV_ERR_UNSUPPORTED;
+  if (num_tokens > INT32_MAX - (1 << 16)) return PKV_ERR_UNSUPPORTED;  // the grid counts past it
   const int64_t qrow = (int64_t)num_heads * head_dim, krow = (int64_t)num_kv_heads * head_dim;
   if (qrow + krow > INT32_MAX) return PKV_ERR_UNSUPPORTED;
   if (q_stride < qrow || k_stride < krow || v_stride < krow || q_stride % 8 != 0 ||
@@ -95,6 +96,8 @@ pkv_status pkv_rope_kv_cache_write(void* q_out, void* kv_pool, const void* q, co
     return PKV_ERR_UNSUPPORTED;
   const int64_t n = num_tokens - 1;
   const int64_t out_bytes = num_tokens * qrow * 2;
+  if (overlap(q_out, out_bytes, kv_pool, (int64_t)2 * num_blocks * block_size * krow * 2))
+    return PKV_ERR_INVALID_ARG;
   if (overlap(q_out, out_bytes, k_new, (n * k_stride + krow) * 2) ||
       overlap(q_out, out_bytes, v_new, (n * v_stride + krow) * 2) ||
       (overlap(q_out, out_bytes, q, (n * q_stride + qrow) * 2) &&

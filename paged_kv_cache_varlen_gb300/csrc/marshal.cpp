@@ -68,6 +68,14 @@ struct Call {
       throw Refused{PyExc_ValueError, std::string(name) + " must be contiguous"};
     return t;
   }
+  const at::Tensor& kv_pool(PyObject* o) {
+    const at::Tensor& t = dense(o, "kv_pool", at::kBFloat16, 5);
+    if (t.size(0) != 2)
+      throw Refused{PyExc_ValueError,
+                    "kv_pool must be [2, num_blocks, block_size, num_kv_heads, head_dim], got " +
+                        shape_text(t.sizes())};
+    return t;
+  }
   // [tokens, heads, head_dim] bf16, a token's heads contiguous; the distance
   // between tokens goes to *stride.
   const at::Tensor& rows(PyObject* o, const char* name, int64_t tokens, int64_t heads,
@@ -124,12 +132,17 @@ void run(const char* what, int device, PyObject* stream, F call) {
   else
     s = reinterpret_cast<void*>(static_cast<uintptr_t>(PyLong_AsUnsignedLongLong(stream)));
   if (PyErr_Occurred()) throw Refused{nullptr, ""};
-  int now = device;
+  struct Device {  // puts the current device back, whatever `call` throws
+    int now = -1, used = -1;
+    ~Device() {
+      if (used >= 0 && now != used) cudaSetDevice(now);
+    }
+  } current;
   pkv_status st = PKV_ERR_CUDA;
-  if (cudaGetDevice(&now) == cudaSuccess &&
-      (now == device || cudaSetDevice(device) == cudaSuccess)) {
+  if (cudaGetDevice(&current.now) == cudaSuccess &&
+      (current.now == device || cudaSetDevice(device) == cudaSuccess)) {
+    current.used = device;
     st = call(s);
-    if (now != device) cudaSetDevice(now);
   }
   if (st == PKV_OK) return;
   const std::string text = std::string(what) + ": " + pkv_status_string(st) + " (status " +
@@ -164,7 +177,7 @@ PyObject* guarded(Py_ssize_t got, Py_ssize_t want, F body) {
 PyObject* rope_kv_cache_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 12, [&]() -> PyObject* {
     Call c;
-    const at::Tensor& pool = c.dense(a[1], "kv_pool", at::kBFloat16, 5);
+    const at::Tensor& pool = c.kv_pool(a[1]);
     const at::Tensor& positions = c.dense(a[4], "positions", at::kInt, 1);
     const at::Tensor& slots = c.dense(a[5], "slot_mapping", at::kInt, 1);
     const at::Tensor& inv_freq = c.dense(a[6], "inv_freq", at::kDouble, 1);
@@ -185,6 +198,7 @@ PyObject* rope_kv_cache_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor& out = a[9] == Py_None ? made : THPVariable_Unpack(a[9]);
     int32_t* status = c.ints(a[10], "dev_status", -1);
     const int interleaved = PyObject_IsTrue(a[7]);
+    if (interleaved < 0) throw Refused{nullptr, ""};
     const float factor = to_float(a[8]);
     run("rope_kv_cache_write", c.device, a[11], [&](void* stream) {
       return pkv_rope_kv_cache_write(
@@ -205,7 +219,7 @@ PyObject* rope_kv_cache_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* attention_key_weights(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 16, [&]() -> PyObject* {
     Call c;
-    const at::Tensor& pool = c.dense(a[1], "kv_pool", at::kBFloat16, 5);
+    const at::Tensor& pool = c.kv_pool(a[1]);
     const at::Tensor& q = c.dense(a[0], "q", at::kBFloat16, 3);
     const at::Tensor& lse = c.dense(a[2], "lse", at::kFloat, 2);
     const at::Tensor& table = c.dense(a[3], "block_table", at::kInt, 2);
@@ -283,7 +297,7 @@ PyObject* evict_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* evict_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 7, [&]() -> PyObject* {
     Call c;
-    const at::Tensor& pool = c.dense(a[0], "kv_pool", at::kBFloat16, 5);
+    const at::Tensor& pool = c.kv_pool(a[0]);
     const at::Tensor& src = c.dense(a[1], "src_table", at::kInt, 2);
     const at::Tensor& dst = c.dense(a[2], "dst_table", at::kInt, 2);
     const at::Tensor& kept = c.dense(a[3], "kept", at::kInt, 3);

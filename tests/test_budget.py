@@ -116,6 +116,12 @@ def test_rope_refusals(lib, over, status):
     assert _rope(lib, **over) == status
 
 
+def test_rope_output_over_the_pool_and_token_counts_past_the_grid(lib):
+    assert _rope(lib, q_out=2 * A) == 1                    # over the K half
+    assert _rope(lib, q_out=2 * A + 4 * 16 * 256 * 2) == 1   # over the V half
+    assert _rope(lib, tokens=2 ** 31 - 1) == 2
+
+
 def test_rope_of_no_tokens_is_a_no_op(lib):
     assert _rope(lib, tokens=0, q=None, q_out=None) == 0
 

@@ -1,6 +1,9 @@
 """The rotary cache write and the cache-budget calls on the GPU, against plain
 64-bit forms written from their definitions."""
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -891,3 +894,62 @@ def test_debug_checks_name_the_bad_entry_of_budget_calls(monkeypatch):
     with pytest.raises(ValueError, match="positions"):
         pkv.rope_kv_cache_write(q, pool, k, v, i32(pos), i32(slots),
                                 pkv.rope_frequencies(64)[0].cuda())
+
+
+def test_a_pool_without_its_v_half_is_refused():
+    q, k, v, pool, pos, slots = rope_inputs(3, 4, 2, 64, 3)
+    inv = pkv.rope_frequencies(64)[0].cuda()
+    with pytest.raises(ValueError, match="kv_pool"):
+        pkv.rope_kv_cache_write(q, pool[:1], k, v, i32(pos), i32(slots), inv)
+    b = Batch([40, 20], [1, 1], 4, 2, 64, seed=3)
+    b.pool = b.pool[:1]
+    with pytest.raises(ValueError, match="kv_pool"):
+        b.call(torch.zeros((2, 2, 40), device="cuda"))
+    src, dst, kept, mpool = compaction([40, 20], [5, 5], 2, 64, 16, 1)
+    with pytest.raises(ValueError, match="kv_pool"):
+        pkv.evict_compact(mpool[:1], i32(src), i32(dst), i32(kept), i32([5, 5]))
+
+
+def test_first_calls_inside_a_capture():
+    """A process whose first calls are captured (nothing has been set up by an
+    eager one) replays the right results."""
+    code = """
+import torch, paged_kv_cache_varlen_gb300 as pkv
+w = torch.rand((2, 2, 50000), device="cuda")
+lens = torch.tensor([50000, 20000], dtype=torch.int32, device="cuda")
+keep = torch.tensor([700, 300], dtype=torch.int32, device="cuda")
+kept = torch.full((2, 2, 700), -1, dtype=torch.int32, device="cuda")
+q = torch.randn((70, 8, 128), device="cuda").bfloat16()
+k = torch.randn((70, 2, 128), device="cuda").bfloat16()
+pool = torch.zeros((2, 8, 16, 2, 128), dtype=torch.bfloat16, device="cuda")
+ids = torch.arange(70, dtype=torch.int32, device="cuda")
+inv = pkv.rope_frequencies(128)[0].cuda()
+q_out = torch.zeros_like(q)
+table = torch.arange(8, dtype=torch.int32, device="cuda")[None]
+cu = torch.tensor([0, 70], dtype=torch.int32, device="cuda")
+n = torch.tensor([70], dtype=torch.int32, device="cuda")
+lse = torch.full((70, 8), 4.0, device="cuda")
+sums = torch.zeros((1, 2, 128), device="cuda")
+def step():
+    pkv.rope_kv_cache_write(q, pool, k, k, ids, ids, inv, q_out=q_out)
+    pkv.attention_key_weights(q_out, pool, lse, table, cu, n, 70, 70, sums)
+    pkv.evict_select(w, lens, keep, 50000, 700, num_recent=9, kept=kept)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    step()
+graph.replay()
+torch.cuda.synchronize()
+got = [x.clone() for x in (q_out, pool, sums, kept)]
+for x in (q_out, pool, sums):
+    x.zero_()
+kept.fill_(-1)
+step()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, (q_out, pool, sums, kept)))
+assert int(kept[0, 0, 699]) == 49999 and float(sums.sum()) > 0
+print("the same")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "the same" in r.stdout, r.stderr[-2000:]
