@@ -480,8 +480,8 @@ pkv_status pkv_rope_kv_cache_write(void *q_out, void *kv_pool, const void *q, co
  *   pos_j = seq_len - query_len + j. An lse of -inf (a row without keys)
  *   contributes nothing. Sums are fp32 in a fixed order: the same call gives
  *   the same bits.
- * head_dim 64 or 128; block_size a multiple of 16 up to 256; row_len >=
- * max_seq_len; weights_in equal to weights_out or disjoint from it.
+ * head_dim 64 or 128; block_size a multiple of 16 up to 256; max_seq_len below
+ * 2^30; row_len >= max_seq_len; weights_in equal to weights_out or disjoint from it.
  * Errors: as the attention call (PKV_DEV_BAD_BLOCK: that page's keys keep their
  * old entries); PKV_DEV_BAD_ROW (the request is skipped).
  */
@@ -515,7 +515,8 @@ pkv_status pkv_attention_key_weights(float *weights_out, const float *weights_in
  *                min(num_sink, keep - r)
  * The rest of keep_lens[i] goes to the heaviest of the other keys; of equal
  * weights the lowest index is kept; a NaN counts as heavier than any number.
- * row_len >= max_seq_len (with weights_out, max_keep_len as well).
+ * max_seq_len below 2^30; row_len >= max_seq_len (with weights_out,
+ * max_keep_len as well).
  * Errors: PKV_DEV_BAD_LENGTHS, PKV_DEV_BAD_ROW (the request is skipped).
  */
 pkv_status pkv_evict_select(int32_t *kept, float *weights_out, const float *weights,

@@ -166,6 +166,7 @@ pkv_status pkv_attention_key_weights(float* weights_out, const float* weights_in
   if ((int64_t)max_blocks_per_seq * block_size > INT32_MAX) return PKV_ERR_UNSUPPORTED;
   const int32_t group = num_heads / num_kv_heads;
   if ((int64_t)max_query_len * group > INT32_MAX / 2) return PKV_ERR_UNSUPPORTED;
+  if (max_seq_len > INT32_MAX / 2) return PKV_ERR_UNSUPPORTED;  // indexes past the last tile
   // the grid's units, (16-key tiles, KV heads), are counted in 32 bits
   if (((int64_t)max_seq_len / 16 + 1) * num_kv_heads > INT32_MAX / 2) return PKV_ERR_UNSUPPORTED;
   pkv::KeyWeightsParams p;

@@ -461,8 +461,9 @@ __device__ __forceinline__ bool key_item(const CUtensorMap& q_map, const CUtenso
     for (int k = 0; k < 4; ++k) a[k] = make_float2(0.f, 0.f);
     uint32_t b = half, turn = 0;  // the accumulator, and how often it has been used
     // the first column of this half that sees the warp's first key, and the
-    // columns there are from this half's first one on
-    int first = (wkey - qpos0 - j0 - rank * QT) * G - half * kHalf;
+    // columns there are from this half's first one on (every query sees keys
+    // 64 places before it, and the distance times G may pass 32 bits)
+    int first = max(wkey - qpos0 - j0 - rank * QT, -64) * G - half * kHalf;
     int left = (r.qlen - j0 - rank * QT) * G - half * kHalf;
     const int step = ctas * QT * G;
     for (int t = 0; ok && t < n; ++t, first -= step, left -= step) {

@@ -122,6 +122,11 @@ def test_rope_output_over_the_pool_and_token_counts_past_the_grid(lib):
     assert _rope(lib, tokens=2 ** 31 - 1) == 2
 
 
+def test_contexts_past_the_index_range_are_refused(lib):
+    assert _weights(lib, max_len=2 ** 30, row_len=2 ** 30, inp=A) == 2
+    assert _select(lib, max_len=2 ** 30, row_len=2 ** 30) == 2
+
+
 def test_rope_of_no_tokens_is_a_no_op(lib):
     assert _rope(lib, tokens=0, q=None, q_out=None) == 0
 

@@ -953,3 +953,26 @@ print("the same")
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
                        timeout=300)
     assert r.returncode == 0 and "the same" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("n", [1, 2])
+def test_key_weights_far_before_the_queries(n):
+    """A key 70 million places before its queries, times 32 heads, passes 32 bits."""
+    L, G, d, bs, nb = 70_000_000, 32, 64, 256, 4
+    q = normal((n, G, d), 1)
+    pool = normal((2, nb, bs, 1, d), 2)
+    blocks = (L + bs - 1) // bs
+    table = torch.arange(blocks, dtype=torch.int32, device="cuda") % nb  # the same pages again
+    lse = torch.full((n, G), 1.0, device="cuda")
+    w = torch.zeros((1, 1, L), device="cuda")
+    st = status_word()
+    pkv.attention_key_weights(q, pool, lse, table[None], i32([0, n]), i32([L]), n, L, w,
+                              dev_status=st)
+    assert st.item() == 0
+    s = f64(pool[0, :, :, 0]).reshape(-1, d) @ f64(q).reshape(n * G, d).T / math.sqrt(d)
+    p = np.exp(s - 1.0)
+    page = torch.from_numpy(p.sum(1)).cuda()
+    want = page.repeat((L + nb * bs - 1) // (nb * bs))[:L]
+    want[L - 1] = p[(L - 1) % (nb * bs), (n - 1) * G:].sum()     # the last key: the last query alone
+    # sums of n * 32 weights, scores of 64 products in fp32: far inside 1e-4
+    assert float(((w[0, 0].double() - want).abs() / want).max()) < 1e-4
