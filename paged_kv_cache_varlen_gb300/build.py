@@ -90,7 +90,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     torch_lib = _torch_paths()[1]
     _link(MARSHAL, objs[:1],
           [f"-L{PKG}", "-l:libpkv.so", f"-L{torch_lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
-           "-ltorch_python", "-Xlinker", "-rpath,$ORIGIN", "-Xlinker", f"-rpath,{torch_lib}"])
+           "-ltorch_cuda", "-ltorch_python", "-Xlinker", "-rpath,$ORIGIN", "-Xlinker", f"-rpath,{torch_lib}"])
     return LIBRARY
 
 

@@ -4,7 +4,7 @@
 // binding.py does, takes their pointers and calls libpkv; in Python the same
 // checks took 7 to 15 us a call, more than the kernels of a small step.
 // It computes nothing and keeps nothing.
-#include <ATen/Functions.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAStream.h>
 #include <cuda_runtime.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -191,7 +191,9 @@ PyObject* rope_kv_cache_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor& v = c.rows(a[3], "v_new", t, hkv, d, &vs);
     at::Tensor made;
     if (a[9] == Py_None) {
-      made = at::empty({t, h, d}, q.options().memory_format(at::MemoryFormat::Contiguous));
+      // (torch.empty without its way through the dispatcher)
+      made = at::Tensor(
+          at::detail::empty_cuda({t, h, d}, at::kBFloat16, q.device(), std::nullopt));
     } else if (c.dense(a[9], "q_out", at::kBFloat16, 3).sizes() != q.sizes()) {
       throw Refused{PyExc_ValueError, "q_out must have the shape of q"};
     }
