@@ -684,14 +684,15 @@ def rope_kv_cache_write(q: torch.Tensor, kv_pool: torch.Tensor, k_new: torch.Ten
     ``2 * len(inv_freq)`` dimensions rotate. ``positions`` are independent of
     ``slot_mapping`` (-1: nothing is written). Returns ``q_out`` [T,H,D],
     which may be a dense q itself."""
-    if debug_checks.enabled():
+    native = _native or _marshal()
+    if native.debug_checks():
         debug_checks.check_slot_mapping(slot_mapping, num_blocks=kv_pool.shape[1],
                                         block_size=kv_pool.shape[2])
         debug_checks.check_positions(positions)
     if q_out is None and stream is not None:
         with _on_stream(stream, q.device):
             q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    return (_native or _marshal()).rope_kv_cache_write(
+    return native.rope_kv_cache_write(
         q, kv_pool, k_new, v_new, positions, slot_mapping, inv_freq, interleaved, factor, q_out,
         dev_status, _handle_of(stream))
 
@@ -711,14 +712,15 @@ def attention_key_weights(q: torch.Tensor, kv_pool: torch.Tensor, lse: torch.Ten
     ``weight_rows[i]`` (default i). Keys at or behind ``prior_lens[i]``
     (default: the step's own tokens) start from zero; ``decay`` scales the
     others' old sums. Writes and returns ``out`` (default: ``weights``, in place)."""
-    if debug_checks.enabled():
+    native = _native or _marshal()
+    if native.debug_checks():
         debug_checks.check_attention_tables(
             cu_seqlens, seq_lens, block_table, num_tokens=q.shape[0],
             max_query_len=int(max_query_len), max_seq_len=int(max_seq_len),
             num_blocks=kv_pool.shape[1], block_size=kv_pool.shape[2])
         debug_checks.check_weight_rows(weight_rows, num_seqs=seq_lens.shape[0],
                                        num_rows=weights.shape[0])
-    return (_native or _marshal()).attention_key_weights(
+    return native.attention_key_weights(
         q, kv_pool, lse, block_table, cu_seqlens, seq_lens, max_query_len, max_seq_len, weights,
         out, weight_rows, prior_lens, decay, scale, dev_status, _handle_of(stream))
 
@@ -736,7 +738,8 @@ def evict_select(weights: torch.Tensor, seq_lens: torch.Tensor, keep_lens: torch
     ascending, filled up to ``keep_lens[i]`` (a tensor made here holds -1
     behind that); ``weights_out``, when given, receives the kept keys' weights
     at the front of the same rows."""
-    if debug_checks.enabled():
+    native = _native or _marshal()
+    if native.debug_checks():
         debug_checks.check_weight_rows(weight_rows, num_seqs=seq_lens.shape[0],
                                        num_rows=weights.shape[0])
         debug_checks.check_keep_lens(seq_lens, keep_lens, max_seq_len=int(max_seq_len),
@@ -749,7 +752,7 @@ def evict_select(weights: torch.Tensor, seq_lens: torch.Tensor, keep_lens: torch
         else:
             with _on_stream(stream, device):
                 kept = torch.full(shape, -1, dtype=torch.int32, device=device)
-    (_native or _marshal()).evict_select(
+    native.evict_select(
         weights, seq_lens, keep_lens, max_seq_len, max_keep_len, num_sink, num_recent, weight_rows,
         kept, weights_out, dev_status, _handle_of(stream))
     return kept, weights_out
@@ -761,8 +764,9 @@ def evict_compact(kv_pool: torch.Tensor, src_table: torch.Tensor, dst_table: tor
     """Copy the kept keys' K and V rows (``kept`` of :func:`evict_select`) from
     the blocks of ``src_table`` to the front of those of ``dst_table``, which
     must be other blocks (``BlockManager.evict_step`` hands both out)."""
-    if debug_checks.enabled():
+    native = _native or _marshal()
+    if native.debug_checks():
         debug_checks.check_compaction(src_table, dst_table, kept, keep_lens,
                                       num_blocks=kv_pool.shape[1], block_size=kv_pool.shape[2])
-    (_native or _marshal()).evict_compact(kv_pool, src_table, dst_table, kept, keep_lens,
-                                          dev_status, _handle_of(stream))
+    native.evict_compact(kv_pool, src_table, dst_table, kept, keep_lens, dev_status,
+                         _handle_of(stream))
