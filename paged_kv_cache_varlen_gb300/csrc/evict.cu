@@ -653,21 +653,35 @@ cudaError_t launch_evict_select(const EvictSelectParams& p, cudaStream_t stream)
   const int* fit = nullptr;
   cudaError_t e = cluster_room.get(&fit);
   if (e != cudaSuccess) return e;
-  // Clusters only for rows of over 8192 keys that would leave SMs without work:
-  // the most CTAs a row, of 2048 keys at least, for which every CTA has an SM of
-  // its own (128K keys: 16 rows in clusters of 6: 18 us, of 8, of which 15 fit:
+  // Clusters for rows of over 8192 keys that would leave SMs without work: the
+  // most CTAs a row, of 2048 keys at least, for which every CTA has an SM of its
+  // own (128K keys: 16 rows in clusters of 6: 18 us, of 8, of which 15 fit:
   // 23 us, of 4: 24 us; 128 rows of 24K: one CTA each 12 us, clusters 17 us).
   int clusters = 1;
   if (L > 8192)
     for (int c = 2; c <= kMaxCluster; ++c)
       if (rows <= fit[c] && L >= 2048 * c) clusters = c;
-  // 1024 threads where a CTA has its SM alone (128 rows of 4096 keys: 6.1 us,
-  // with 512 7.3 us) or a long share (512 rows of 24K: 40 against 45 us), else
-  // 512 (512 rows of 4096: 12 us, with 1024 15.8, with 256 14.4 us)
-  const int64_t share_of = L / clusters;
   const bool alone = rows * clusters <= fit[1];
-  const bool wide = clusters > 1 ? share_of > 8192 : share_of > (alone ? 2048 : 16384);
-  const int threads = wide ? 1024 : 512;
+  // And for somewhat more rows than SMs, too long for one CTA to stage: some SMs
+  // would have two of them and end last (192 rows of 25K to 100K keys in
+  // clusters of 5: 51.7 us, a CTA each 74.8; 160 rows of 50K to 60K, of 3: 34.7
+  // and 51.6; but 256 rows of 128K, of 7: 151 and 139).
+  if (!alone && L > kStaged && rows * 2 < (int64_t)fit[1] * 3) {
+    const int64_t c = (L + kStaged / 2 - 1) / (kStaged / 2);
+    clusters = c < kMaxCluster ? (int)c : kMaxCluster;
+  }
+  // Threads: 1024 where a CTA has its SM alone (128 rows of 4096 keys: 6.1 us,
+  // with 512 7.3 us) or a long row (512 rows of 24K: 40 against 45 us), else 512
+  // (512 rows of 4096: 12 us, with 1024 15.8, with 256 14.4 us), fewer for
+  // short rows (1600 rows of 150 to 600 keys: 10.2 us, with 512 15.9).
+  const int64_t share_of = L / clusters;
+  int threads = 512;
+  if (clusters > 1)
+    threads = alone && share_of > 8192 ? 1024 : 512;
+  else if (share_of > (alone ? 2048 : 16384))
+    threads = 1024;
+  else if (!alone && share_of <= 2048)
+    threads = 256;
   const int64_t per_group = (int64_t)clusters * threads * 4;
   const int64_t share = (L + per_group - 1) / per_group * threads * 4;
   if (share <= kStaged) return launch_select<true>(p, clusters, threads, (int)share, stream);

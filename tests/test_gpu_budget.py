@@ -486,6 +486,9 @@ def test_evict_select_outside_the_first_bins(kind, L, keep):
     (20, 8, 2052, 700),     # more rows than SMs: rows of one, two and three groups of keys
     (40, 8, 17000, 100),
     (20, 8, 45000, 20000),  # too long to stage
+    (32, 8, 41000, 500),    # and more rows than clusters would help
+    (70, 4, 1500, 300),     # short rows
+    (170, 1, 200001, 5000),
     (2, 8, 100004, 8192),   # few rows: CTAs in clusters of different sizes
     (3, 8, 30000, 29999),
     (9, 4, 30000, 1),
