@@ -424,7 +424,8 @@ pkv_status pkv_rope_frequencies(double *inv_freq, float *factor, int32_t rotary_
  *   slot_mapping as pkv_kv_cache_write (-1: q is rotated, nothing is written)
  *   inv_freq     [rotary_dim / 2] double (device), radians per position;
  *                angles are formed modulo a full turn before they are rounded,
- *                so far positions lose nothing
+ *                so far positions lose nothing (the pair of a frequency that is
+ *                infinite or NaN becomes NaN)
  *   factor       scale of the rotated values
  *   interleaved  0: pair p is dimensions (p, p + rotary_dim / 2);
  *                1: dimensions (2p, 2p + 1)

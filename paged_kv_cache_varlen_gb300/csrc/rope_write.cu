@@ -53,6 +53,13 @@ __device__ __forceinline__ uint64_t turn_fraction(double f) {
   return (bits >> 63) ? 0 - r : r;
 }
 
+// An infinite or NaN frequency: its pair becomes NaN (a fraction of a turn cannot
+// say so).
+__device__ __forceinline__ bool no_number(double f) {
+  return ((uint64_t)__double_as_longlong(f) >> 52 & 2047) == 2047;
+}
+constexpr uint32_t kNan = 0x7fffffffu;
+
 // cos and sin of pos turns of `frac` 2^-64 each, times factor.
 __device__ __forceinline__ float2 rope_angle(uint64_t frac, uint32_t pos, float factor) {
   const int32_t hi = (int32_t)((frac * pos) >> 32);  // fraction of a turn, as a signed 32-bit one
@@ -98,8 +105,13 @@ __global__ void __launch_bounds__(kThreads, 4) rope_warp_kernel(const RopeWriteP
   float* sn = cs + pad;
   griddep_wait();
   griddep_launch_dependents();
-  for (int i = threadIdx.x; i < half; i += kThreads) frac[i] = turn_fraction(__ldg(p.inv_freq + i));
-  __syncthreads();
+  int lost = 0;  // whether some frequency is no number
+  for (int i = threadIdx.x; i < half; i += kThreads) {
+    const double f = __ldg(p.inv_freq + i);
+    frac[i] = turn_fraction(f);
+    lost |= no_number(f);
+  }
+  lost = __syncthreads_or(lost);
   const int64_t row = (int64_t)Hkv * D;
   const int vecs = (int)(row / 8);
   const int units = p.num_tokens * parts;  // (below 2^31: the host bounds parts by the tokens)
@@ -130,6 +142,9 @@ __global__ void __launch_bounds__(kThreads, 4) rope_warp_kernel(const RopeWriteP
       cs[i] = a.x;
       sn[i] = a.y;
     }
+    if (lost)
+      for (int i = lane; i < half; i += 32)
+        if (no_number(__ldg(p.inv_freq + i))) cs[i] = sn[i] = __uint_as_float(kNan);
     __syncwarp();
     if (!kInter) {
       const int U = half / 8;                // vector pairs per head
@@ -240,9 +255,10 @@ __global__ void __launch_bounds__(kThreads) rope_staged_kernel(const RopeWritePa
   const bool write = slot >= 0 && slot < p.num_slots;
   if (!write && slot != -1 && threadIdx.x == 0) set_status(p.status, PKV_DEV_BAD_SLOT);
   for (int i = threadIdx.x; i < half; i += kThreads) {
-    const float2 a = rope_angle(turn_fraction(__ldg(p.inv_freq + i)), (uint32_t)pos, p.factor);
-    cs[i] = a.x;
-    sn[i] = a.y;
+    const double f = __ldg(p.inv_freq + i);
+    const float2 a = rope_angle(turn_fraction(f), (uint32_t)pos, p.factor);
+    cs[i] = no_number(f) ? __uint_as_float(kNan) : a.x;
+    sn[i] = no_number(f) ? __uint_as_float(kNan) : a.y;
   }
   const uint16_t* q = p.q + (int64_t)t * p.q_stride;
   const uint16_t* k = p.k + (int64_t)t * p.k_stride;
