@@ -4,7 +4,10 @@
 // binding.py does, takes their pointers and calls libpkv; in Python the same
 // checks took 7 to 15 us a call, more than the kernels of a small step.
 // It computes nothing and keeps nothing.
+#include <ATen/Context.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <ATen/ops/empty.h>
+#include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/cuda/CUDAStream.h>
 #include <cuda_runtime.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -107,6 +110,17 @@ T* ptr(const at::Tensor& t) {
   return static_cast<T*>(t.data_ptr());
 }
 
+// torch.empty of bf16. Its way through the dispatcher (0.7 us a call) is left out
+// where nothing there would act: no dispatch mode, and no filling of new memory
+// in deterministic mode.
+at::Tensor new_output(at::IntArrayRef shape, c10::Device device) {
+  const at::Context& context = at::globalContext();
+  if (c10::impl::dispatch_mode_enabled() ||
+      (context.deterministicAlgorithms() && context.deterministicFillUninitializedMemory()))
+    return at::empty(shape, at::TensorOptions(device).dtype(at::kBFloat16));
+  return at::Tensor(at::detail::empty_cuda(shape, at::kBFloat16, device, std::nullopt));
+}
+
 int32_t small(int64_t v) {
   if (v > INT32_MAX || v < INT32_MIN)
     throw Refused{PyExc_ValueError, "a size does not fit 32 bits"};
@@ -192,9 +206,7 @@ PyObject* rope_kv_cache_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor& v = c.rows(a[3], "v_new", t, hkv, d, &vs);
     at::Tensor made;
     if (a[9] == Py_None) {
-      // (torch.empty without its way through the dispatcher)
-      made = at::Tensor(
-          at::detail::empty_cuda({t, h, d}, at::kBFloat16, q.device(), std::nullopt));
+      made = new_output({t, h, d}, q.device());
     } else if (c.dense(a[9], "q_out", at::kBFloat16, 3).sizes() != q.sizes()) {
       throw Refused{PyExc_ValueError, "q_out must have the shape of q"};
     }
