@@ -138,7 +138,9 @@ float to_float(PyObject* o) {
 }
 
 // `call(stream)` with the tensors' device current, on the given stream (an
-// integer handle) or torch's current one; raises PkvError on a status.
+// integer handle) or torch's current one; raises PkvError on a status. The
+// interpreter lock is given up meanwhile, as ctypes and torch do: a launch waits
+// while the stream's queue is full. (`call` touches no Python object.)
 template <class F>
 void run(const char* what, int device, PyObject* stream, F call) {
   void* s = nullptr;
@@ -147,17 +149,25 @@ void run(const char* what, int device, PyObject* stream, F call) {
   else
     s = reinterpret_cast<void*>(static_cast<uintptr_t>(PyLong_AsUnsignedLongLong(stream)));
   if (PyErr_Occurred()) throw Refused{nullptr, ""};
+  struct Unlocked {  // takes the lock again, whatever `call` throws
+    PyThreadState* state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+  };
   struct Device {  // puts the current device back, whatever `call` throws
     int now = -1, used = -1;
     ~Device() {
       if (used >= 0 && now != used) cudaSetDevice(now);
     }
-  } current;
+  };
   pkv_status st = PKV_ERR_CUDA;
-  if (cudaGetDevice(&current.now) == cudaSuccess &&
-      (current.now == device || cudaSetDevice(device) == cudaSuccess)) {
-    current.used = device;
-    st = call(s);
+  {
+    Unlocked unlocked;
+    Device current;
+    if (cudaGetDevice(&current.now) == cudaSuccess &&
+        (current.now == device || cudaSetDevice(device) == cudaSuccess)) {
+      current.used = device;
+      st = call(s);
+    }
   }
   if (st == PKV_OK) return;
   const std::string text = std::string(what) + ": " + pkv_status_string(st) + " (status " +
