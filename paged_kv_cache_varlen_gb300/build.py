@@ -5,10 +5,12 @@ linked into ``paged_kv_cache_varlen_gb300/libpkv.so`` (static cudart, no
 driver-library link: the tensor-map encoder is looked up at run time).
 ``_marshal.so`` beside it is the Python module that marshals the arguments of
 the per-step calls (host code against torch's and Python's headers; it calls
-libpkv.so).
+libpkv.so). The library needs nvcc alone: where torch is not installed, it is
+all that is built, and a binding module that fails to build leaves it there.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -48,7 +50,12 @@ def _newest_input() -> float:
 
 def up_to_date() -> bool:
     newest = _newest_input()
-    return all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in (LIBRARY, MARSHAL))
+    parts = (LIBRARY, MARSHAL) if _have_torch() else (LIBRARY,)
+    return all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in parts)
+
+
+def _have_torch() -> bool:
+    return importlib.util.find_spec("torch") is not None
 
 
 def _torch_paths() -> tuple[list[str], str]:
@@ -85,12 +92,17 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIBRARY
     os.makedirs(BUILD_DIR, exist_ok=True)
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as pool:
-        objs = list(pool.map(lambda s: _compile(s, verbose), [MARSHAL_SOURCE] + SOURCES))
-    _link(LIBRARY, objs[1:], [])
+        marshal = pool.submit(_compile, MARSHAL_SOURCE, verbose) if _have_torch() else None
+        objs = list(pool.map(lambda s: _compile(s, verbose), SOURCES))
+        _link(LIBRARY, objs, [])
+        if marshal is None:
+            return LIBRARY
+        obj = marshal.result()
     torch_lib = _torch_paths()[1]
-    _link(MARSHAL, objs[:1],
-          [f"-L{PKG}", "-l:libpkv.so", f"-L{torch_lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
-           "-ltorch_cuda", "-ltorch_python", "-Xlinker", "-rpath,$ORIGIN", "-Xlinker", f"-rpath,{torch_lib}"])
+    _link(MARSHAL, [obj],
+          [f"-L{os.path.dirname(LIBRARY)}", "-l:libpkv.so", f"-L{torch_lib}", "-lc10",
+           "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python",
+           "-Xlinker", "-rpath,$ORIGIN", "-Xlinker", f"-rpath,{torch_lib}"])
     return LIBRARY
 
 
