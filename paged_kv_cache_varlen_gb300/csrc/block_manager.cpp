@@ -253,6 +253,7 @@ pkv_status pkv_bm_evict_step(pkv_block_manager* bm, const int64_t* seq_ids,
     std::unordered_set<int64_t> seen;
     const int64_t bs = bm->block_size;
     int64_t need = 0;
+    size_t held = 0;
     for (int32_t i = 0; i < num_seqs; ++i) {
       seqs[i] = find(bm, seq_ids[i]);
       if (!seqs[i] || !seen.insert(seq_ids[i]).second) return PKV_ERR_INVALID_ARG;
@@ -262,10 +263,27 @@ pkv_status pkv_bm_evict_step(pkv_block_manager* bm, const int64_t* seq_ids,
         return PKV_ERR_INVALID_ARG;
       fresh[i].reserve(n);
       need += n;
+      held += seqs[i]->table.size();
     }
-    if (need > (int64_t)bm->free_pool.size()) return PKV_ERR_NO_BLOCKS;
-    // all fresh blocks first: no block released here is a destination of
-    // this batch
+    const size_t free_before = bm->free_pool.size();
+    if (need > (int64_t)free_before) return PKV_ERR_NO_BLOCKS;
+    // The old blocks join the back of the pool: the last step that allocates,
+    // undone when the host has no memory for it.
+    std::vector<int32_t> released;
+    released.reserve(held);
+    for (const pkv_block_manager::Seq* s : seqs)
+      for (int32_t b : s->table)
+        if (--bm->refs[b] == 0) released.push_back(b);
+    try {
+      for (int32_t b : released) bm->free_pool.push_back(b);
+    } catch (const std::exception&) {
+      bm->free_pool.resize(free_before);
+      for (const pkv_block_manager::Seq* s : seqs)
+        for (int32_t b : s->table) ++bm->refs[b];
+      throw;
+    }
+    // The fresh blocks come off its front, where `need` others stood: no block
+    // released here is a destination of this batch.
     for (int32_t i = 0; i < num_seqs; ++i) {
       const int64_t n = (keep_lens[i] + bs - 1) / bs;
       for (int64_t b = 0; b < n; ++b) {
@@ -282,8 +300,6 @@ pkv_status pkv_bm_evict_step(pkv_block_manager* bm, const int64_t* seq_ids,
         src[b] = b < (int32_t)s.table.size() ? s.table[b] : -1;
       for (int32_t b = 0; b < max_dst_blocks; ++b)
         dst[b] = b < (int32_t)fresh[i].size() ? fresh[i][b] : -1;
-      for (int32_t b : s.table)
-        if (--bm->refs[b] == 0) bm->free_pool.push_back(b);
       s.table.swap(fresh[i]);
       s.len = keep_lens[i];
     }
