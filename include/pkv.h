@@ -506,8 +506,11 @@ pkv_status pkv_attention_key_weights(float *weights_out, const float *weights_in
  *                later entries stay as they were
  *   weights_out  as weights, or NULL: entry [row][h][j] = the weight of the
  *                j-th kept key (the running sums of the shortened context);
- *                must not overlap weights
- *   weights      the accumulated weights
+ *                must not overlap weights. To go on with it in place of weights
+ *                is right only when every row in use was in the call; else copy
+ *                its rows' first keep_lens[i] entries back
+ *   weights      the accumulated weights; left as they were (those of the uncut
+ *                context)
  *   seq_lens     [num_seqs] int32 >= 0, at most max_seq_len
  *   keep_lens    [num_seqs] int32, 0 <= keep_lens[i] <= seq_lens[i], at most
  *                max_keep_len

@@ -737,7 +737,9 @@ def evict_select(weights: torch.Tensor, seq_lens: torch.Tensor, keep_lens: torch
     index). Returns ``(kept, weights_out)``: kept [B,Hkv,max_keep_len] int32,
     ascending, filled up to ``keep_lens[i]`` (a tensor made here holds -1
     behind that); ``weights_out``, when given, receives the kept keys' weights
-    at the front of the same rows."""
+    at the front of the same rows. ``weights`` keeps the sums of the uncut
+    contexts: go on with ``weights_out`` when every row in use was in the call,
+    else copy its rows back."""
     native = _native or _marshal()
     if native.debug_checks():
         debug_checks.check_weight_rows(weight_rows, num_seqs=seq_lens.shape[0],
