@@ -21,7 +21,10 @@
 // 49.5 us, 6.3 TB/s (92 % of the measured copy rate); 8 contexts of 32K to 128K
 // 236 us, 6.7 TB/s (98 %). The same with the tile staged by TMA, four 4 KB
 // slots a warp: 66.7 and 280 us (a third of the warps fit); with the next tile
-// in a second set of registers: 57.4 and 257 us.
+// in a second set of registers: 57.4 and 257 us. Steps of 4 and 8 tokens over
+// contexts like the first ones (16 and 32 columns): 55 and 81 us; 64 single
+// tokens of 256 heads on one KV head of 64 (128) dimensions, whose Q is read
+// again for every 16 keys: 108 (125) us.
 #include <math.h>
 
 #include "key_weights.cuh"
@@ -57,7 +60,8 @@ __global__ void __launch_bounds__(kWarps * 32)
     key_weights_kernel(const KeyWeightsParams p, const int chunk) {
   // Behind the tcgen05 grid of the same call (which started once everything
   // before it had finished) the CTAs do not wait for it, so that they fill the
-  // SMs it leaves; one extra CTA does, and with it this grid's completion.
+  // SMs it leaves; those of one extra slice do, and with them this grid's
+  // completion.
   if (!p.after_tc || blockIdx.y == p.num_seqs) griddep_wait();
   griddep_launch_dependents();
   if (blockIdx.y == p.num_seqs) return;

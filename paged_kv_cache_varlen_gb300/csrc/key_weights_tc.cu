@@ -23,18 +23,23 @@
 //     (a warpgroup per K tile and half of the columns): a packed fma, ex2 and
 //     a packed add per pair of scores, no mask where every column sees
 //     every key of the warp;
-//   * a key's sum over 16 tiles runs in eight chains (four threads, two
-//     each), the groups of 16 tiles are added up apart: chains of 128 and a
-//     few dozen additions keep a sum over 10^5 columns within 2^-21.
+//   * a key's sum over 16 tiles runs in eight chains for each half of the
+//     columns (four threads, two each), the groups of 16 tiles are added up
+//     apart: chains of 128 additions and one for each group, so the additions
+//     leave a sum over 10^5 columns within about 2^-16.5 (177 roundings of
+//     2^-24). Each addend is off by ex2's 2^-22 and by its exponent's roundings,
+//     3 2^-24 (|scale s| + |lse|). Seen against 64 bits: 3.2e-7 of the sums (an
+//     8192-token prompt, lse and scores of a few units).
 //
 // Bound: one ex2 a score (32 a cycle and SM) and 2 D flops a score
 // (8192 a cycle and SM dense): 512 cycles each for 128 x 128 at D = 128, so
 // 1024 a Q tile against 256 keys; the epilogue's warps alone take 1240 with
 // their other instructions, and about 1600 beside the issuing and copying
 // warps that wait. Measured: one 8192-token prompt, 32 query and 8 KV heads of
-// 128: 207 us, 1.35 PFLOP/s (71 % of the measured bf16 rate; 225 us over
-// three sets of inputs in turn); 512 queries over 32K keys 128 us. (One warp
-// issuing for both K tiles: 259 us.)
+// 128, three sets of inputs in turn: 223 us, 1.25 PFLOP/s (65 % of the measured
+// bf16 rate; 204 us in a burst of 30 calls); 512 queries over 32K keys 128 us;
+// 64 single tokens of 64 or 128 heads on one KV head of 64 (128) dimensions: 26
+// (33) us. (One warp issuing for both K tiles took a quarter longer.)
 #include <math.h>
 #include <stddef.h>
 
@@ -703,6 +708,10 @@ cudaError_t launch(const KeyWeightsParams& p, const CUtensorMap& q_map, const CU
   // 136 us, 131 with a CTA for each, which the hardware hands out as SMs fall
   // free; 13 requests, 1040 items in bounds, 484 there: 83 and 59 us, the
   // difference being the single tokens' grid, which then waits to the end.)
+  // Not listed are items split over a cluster and batches of more than kListed
+  // requests: there every request, a single token too, has its CTAs in bounds,
+  // about 1 us each on one SM after the other (64 single tokens and a chunk of
+  // 2048, contexts to 4096: 259 us; in calls of their own 46 and 62).
   const int64_t bound = key_tiles * p.num_kv_heads * p.num_seqs;
   const bool listed =
       clusters == 1 && p.num_seqs <= kListed && bound > 12 * sms && bound < (1 << 30);

@@ -20,8 +20,10 @@
 // a token, or a share of its heads when the tokens are few; the token's sines
 // and cosines, two or so a lane, meet in shared memory, and in the layout of
 // halves a lane keeps those of its 8 pairs for all its heads.
-// Measured: 8192 tokens of 32 + 8 heads of 128: 34.8 us, 5.8 TB/s (85 % of the
-// measured copy rate); 64 tokens: 3.9 us a call, most of it the host's.
+// Measured: 8192 tokens of 32 + 8 heads of 128: 35.0 us, 5.8 TB/s (85 % of the
+// measured copy rate); 64 tokens: 4.5 us a call, most of it the host's. Halves
+// of any length (40 of the 128 dimensions rotated): 64 tokens 4.3, 1024 9.8,
+// 8192 60.7 us, a CTA a token and two trips through shared memory.
 #include "common.cuh"
 #include "launch.h"
 
