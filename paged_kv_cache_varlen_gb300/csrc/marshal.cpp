@@ -149,9 +149,11 @@ void run(const char* what, int device, PyObject* stream, F call) {
   else
     s = reinterpret_cast<void*>(static_cast<uintptr_t>(PyLong_AsUnsignedLongLong(stream)));
   if (PyErr_Occurred()) throw Refused{nullptr, ""};
-  struct Unlocked {  // takes the lock again, whatever `call` throws
+  // Takes the lock again, whatever `call` throws. (At the interpreter's end that
+  // unwinds a daemon thread, which a destructor must let through.)
+  struct Unlocked {
     PyThreadState* state = PyEval_SaveThread();
-    ~Unlocked() { PyEval_RestoreThread(state); }
+    ~Unlocked() noexcept(false) { PyEval_RestoreThread(state); }
   };
   struct Device {  // puts the current device back, whatever `call` throws
     int now = -1, used = -1;
