@@ -450,6 +450,96 @@ pkv_status pkv_rope_kv_cache_write(void *q_out, void *kv_pool, const void *q, co
                                    int32_t *dev_status, void *stream);
 
 /*
+ * pkv_qk_norm_rope_kv_cache_write -- pkv_rope_kv_cache_write with a norm over
+ * each query and key head before the rotation, in the same pass.
+ *
+ * Arguments as pkv_rope_kv_cache_write, plus
+ *   q_weight, k_weight  [head_dim] bf16, or fp32 when weights_f32 is set: the
+ *                norms' weights; NULL: those heads are not normed
+ *   weight_offset  added to every weight (1 for weights kept as w - 1)
+ *   eps          >= 0, added to the mean square
+ *
+ *   y = x * (mean over the head of x^2 + eps)^(-1/2) * (weight + weight_offset),
+ * then the rotation of y, in fp32, rounded once to bf16. Dimensions >=
+ * rotary_dim are normed only. rotary_dim may be 0 (nothing is rotated, inv_freq
+ * unused). v_new is a bit copy. A head whose sum of squares passes the fp32
+ * range becomes 0.
+ * Errors: as pkv_rope_kv_cache_write; PKV_ERR_INVALID_ARG for eps < 0 or a
+ * value that is not finite.
+ */
+pkv_status pkv_qk_norm_rope_kv_cache_write(
+    void *q_out, void *kv_pool, const void *q, const void *k_new, const void *v_new,
+    int64_t q_stride, int64_t k_stride, int64_t v_stride, const int32_t *positions,
+    const int32_t *slot_mapping, const double *inv_freq, const void *q_weight,
+    const void *k_weight, int32_t weights_f32, float weight_offset, float eps, float factor,
+    int32_t interleaved, int32_t num_tokens, int32_t num_heads, int32_t num_kv_heads,
+    int32_t head_dim, int32_t rotary_dim, int32_t num_blocks, int32_t block_size,
+    int32_t *dev_status, void *stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The 8-bit cache: half the bytes of the bf16 pool.
+ *
+ *   kv_pool   [2][num_blocks][block_size][num_kv_heads][head_dim] e4m3 (1 sign,
+ *             4 exponent, 3 fraction bits; largest value 448, no infinities),
+ *             16-byte aligned
+ *   kv_scales [2][num_blocks][num_kv_heads] fp32 > 0: a cached value stands for
+ *             its e4m3 value times the scale of its half, block and KV head
+ *
+ * head_dim 64 or 128; block_size a multiple of 16 up to 256.
+ * ---------------------------------------------------------------------------
+ * pkv_kv_cache_append_fp8 -- write a step's keys and values into the 8-bit pool.
+ *
+ *   k_new, v_new num_tokens rows of [num_kv_heads][head_dim] bf16, k_stride and
+ *                v_stride elements apart (multiples of 8)
+ *   block_table, cu_seqlens_q, seq_lens, max_query_len: as
+ *                pkv_paged_attention_varlen; token j of request i goes to
+ *                position seq_lens[i] - query_len + j of its table
+ *
+ * For each block that a request's new tokens reach, half and KV head:
+ *   need  = 2^ceil(log2(max |x| / 448)) over the block's new rows, at least
+ *           2^-100 (infinities and NaN do not count);
+ *   scale = need where every row of the block up to the last new one is new,
+ *           else max(need, the block's scale so far);
+ *   new rows become x / scale, rounded once to the nearest e4m3 value (ties to
+ *           even; infinities to +-448, NaN stays NaN); the rows that were there
+ *           become their value times (old scale / scale), rounded the same way,
+ *           where the scale has grown (by a power of two: exact, except for
+ *           values that fall below 2^-6 of the new scale);
+ *   rows behind the request's last token stay as they were.
+ * The blocks written belong to one request of the call (copy shared ones first:
+ * pkv_copy_blocks_fp8), each of its rows once.
+ * Errors: PKV_DEV_BAD_LENGTHS (the request is skipped), PKV_DEV_BAD_BLOCK (that
+ * block's rows are not written).
+ */
+pkv_status pkv_kv_cache_append_fp8(void *kv_pool, float *kv_scales, const void *k_new,
+                                   const void *v_new, int64_t k_stride, int64_t v_stride,
+                                   const int32_t *block_table, int32_t max_blocks_per_seq,
+                                   const int32_t *cu_seqlens_q, const int32_t *seq_lens,
+                                   int32_t num_seqs, int32_t num_tokens, int32_t max_query_len,
+                                   int32_t num_kv_heads, int32_t head_dim, int32_t num_blocks,
+                                   int32_t block_size, int32_t *dev_status, void *stream);
+
+/*
+ * pkv_qk_norm_rope_kv_cache_append_fp8 -- the norms and the rotation of
+ * pkv_qk_norm_rope_kv_cache_write on the way into the 8-bit pool: the keys are
+ * quantised from fp32 (rounded once), the queries written to q_out in bf16, the
+ * values quantised as they are. Arguments as the two calls (positions are
+ * independent of the slots; q_weight and k_weight NULL: rotation alone).
+ * Errors: as the two calls; PKV_DEV_BAD_POSITION (the token is skipped, q_out's
+ * row included); q_out's rows of a bad block are written.
+ */
+pkv_status pkv_qk_norm_rope_kv_cache_append_fp8(
+    void *q_out, void *kv_pool, float *kv_scales, const void *q, const void *k_new,
+    const void *v_new, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+    const int32_t *positions, const int32_t *block_table, int32_t max_blocks_per_seq,
+    const int32_t *cu_seqlens_q, const int32_t *seq_lens, const double *inv_freq,
+    const void *q_weight, const void *k_weight, int32_t weights_f32, float weight_offset, float eps,
+    float factor, int32_t interleaved, int32_t num_seqs, int32_t num_tokens, int32_t max_query_len,
+    int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t rotary_dim,
+    int32_t num_blocks, int32_t block_size, int32_t *dev_status, void *stream);
+
+/*
  * ---------------------------------------------------------------------------
  * Holding a request inside a cache budget: the attention weight that each
  * cached key has received is accumulated step by step, and when a request's

@@ -12,12 +12,15 @@ from .binding import (  # noqa: F401
     attention_workspace_size,
     evict_compact,
     evict_select,
+    kv_cache_append_fp8,
     kv_cache_write,
     library_path,
     lse_merge,
     paged_attention_varlen,
     paged_attention_varlen_append,
     paged_attention_varlen_range,
+    qk_norm_rope_kv_cache_append_fp8,
+    qk_norm_rope_kv_cache_write,
     rope_frequencies,
     rope_kv_cache_write,
 )
@@ -29,12 +32,15 @@ __all__ = [
     "attention_workspace_size",
     "evict_compact",
     "evict_select",
+    "kv_cache_append_fp8",
     "kv_cache_write",
     "library_path",
     "lse_merge",
     "paged_attention_varlen",
     "paged_attention_varlen_append",
     "paged_attention_varlen_range",
+    "qk_norm_rope_kv_cache_append_fp8",
+    "qk_norm_rope_kv_cache_write",
     "rope_frequencies",
     "rope_kv_cache_write",
 ]

@@ -54,6 +54,14 @@ _SIGNATURES = {
     "pkv_rope_kv_cache_write": (
         _i32, [_vp] * 5 + [ctypes.c_int64] * 3 + [_vp] * 3 + [ctypes.c_float] + [_i32] * 8
         + [_vp, _vp]),
+    "pkv_qk_norm_rope_kv_cache_write": (
+        _i32, [_vp] * 5 + [ctypes.c_int64] * 3 + [_vp] * 5 + [_i32] + [ctypes.c_float] * 3
+        + [_i32] * 8 + [_vp, _vp]),
+    "pkv_kv_cache_append_fp8": (
+        _i32, [_vp] * 4 + [ctypes.c_int64] * 2 + [_vp, _i32, _vp, _vp] + [_i32] * 7 + [_vp, _vp]),
+    "pkv_qk_norm_rope_kv_cache_append_fp8": (
+        _i32, [_vp] * 6 + [ctypes.c_int64] * 3 + [_vp, _vp, _i32] + [_vp] * 5 + [_i32]
+        + [ctypes.c_float] * 3 + [_i32] * 10 + [_vp, _vp]),
     "pkv_attention_key_weights": (
         _i32, [_vp] * 6 + [_i32] + [_vp] * 4 + [_i32] * 11
         + [ctypes.c_float, ctypes.c_float, _vp, _vp]),
@@ -695,6 +703,89 @@ def rope_kv_cache_write(q: torch.Tensor, kv_pool: torch.Tensor, k_new: torch.Ten
     return native.rope_kv_cache_write(
         q, kv_pool, k_new, v_new, positions, slot_mapping, inv_freq, interleaved, factor, q_out,
         dev_status, _handle_of(stream))
+
+
+def qk_norm_rope_kv_cache_write(q: torch.Tensor, kv_pool: torch.Tensor, k_new: torch.Tensor,
+                                v_new: torch.Tensor, positions: torch.Tensor,
+                                slot_mapping: torch.Tensor, inv_freq: torch.Tensor | None,
+                                q_weight: torch.Tensor | None, k_weight: torch.Tensor | None, *,
+                                eps: float = 1e-6, weight_offset: float = 0.0,
+                                interleaved: bool = False, factor: float = 1.0,
+                                q_out: torch.Tensor | None = None,
+                                dev_status: torch.Tensor | None = None,
+                                stream=None) -> torch.Tensor:
+    """:func:`rope_kv_cache_write` with a norm over each query and key head first.
+
+    ``q_weight`` / ``k_weight`` [D], bf16 or fp32 (None: not normed):
+    ``x * rsqrt(mean(x^2) + eps) * (weight + weight_offset)`` over each head,
+    then the rotation (``inv_freq`` None: none). Returns ``q_out`` [T,H,D],
+    which may be a dense q itself."""
+    native = _native or _marshal()
+    if native.debug_checks():
+        debug_checks.check_slot_mapping(slot_mapping, num_blocks=kv_pool.shape[1],
+                                        block_size=kv_pool.shape[2])
+        debug_checks.check_positions(positions)
+    if q_out is None and stream is not None:
+        with _on_stream(stream, q.device):
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    return native.qk_norm_rope_kv_cache_write(
+        q, kv_pool, k_new, v_new, positions, slot_mapping, inv_freq, q_weight, k_weight, eps,
+        weight_offset, interleaved, factor, q_out, dev_status, _handle_of(stream))
+
+
+def kv_cache_append_fp8(kv_pool: torch.Tensor, kv_scales: torch.Tensor, k_new: torch.Tensor,
+                        v_new: torch.Tensor, block_table: torch.Tensor, cu_seqlens: torch.Tensor,
+                        seq_lens: torch.Tensor, max_query_len: int, *,
+                        dev_status: torch.Tensor | None = None, stream=None) -> None:
+    """Write a step's k_new/v_new [T,Hkv,D] bf16 into the 8-bit pool.
+
+    ``kv_pool`` [2,NB,BS,Hkv,D] float8_e4m3fn, ``kv_scales`` [2,NB,Hkv] fp32.
+    Token j of request i goes to position ``seq_lens[i] - query_len + j`` of its
+    table (what :meth:`BlockManager.build_step` returns says where). A block's
+    scale is the power of two that its largest magnitude needs; rows that are
+    there are rescaled where it grows (``pkv_kv_cache_append_fp8`` in
+    ``include/pkv.h``)."""
+    native = _native or _marshal()
+    if native.debug_checks():
+        _check_append_tables(kv_pool, k_new, block_table, cu_seqlens, seq_lens, max_query_len)
+    native.kv_cache_append_fp8(kv_pool, kv_scales, k_new, v_new, block_table, cu_seqlens, seq_lens,
+                               max_query_len, dev_status, _handle_of(stream))
+
+
+def qk_norm_rope_kv_cache_append_fp8(q: torch.Tensor, kv_pool: torch.Tensor,
+                                     kv_scales: torch.Tensor, k_new: torch.Tensor,
+                                     v_new: torch.Tensor, positions: torch.Tensor,
+                                     block_table: torch.Tensor, cu_seqlens: torch.Tensor,
+                                     seq_lens: torch.Tensor, max_query_len: int,
+                                     inv_freq: torch.Tensor | None,
+                                     q_weight: torch.Tensor | None = None,
+                                     k_weight: torch.Tensor | None = None, *, eps: float = 1e-6,
+                                     weight_offset: float = 0.0, interleaved: bool = False,
+                                     factor: float = 1.0, q_out: torch.Tensor | None = None,
+                                     dev_status: torch.Tensor | None = None,
+                                     stream=None) -> torch.Tensor:
+    """The norms and the rotation of :func:`qk_norm_rope_kv_cache_write` on the way
+    into the 8-bit pool of :func:`kv_cache_append_fp8`: keys are quantised from
+    the fp32 result, queries come back in bf16. Without weights the heads are
+    rotated only."""
+    native = _native or _marshal()
+    if native.debug_checks():
+        _check_append_tables(kv_pool, k_new, block_table, cu_seqlens, seq_lens, max_query_len)
+        debug_checks.check_positions(positions)
+    if q_out is None and stream is not None:
+        with _on_stream(stream, q.device):
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    return native.qk_norm_rope_kv_cache_append_fp8(
+        q, kv_pool, kv_scales, k_new, v_new, positions, block_table, cu_seqlens, seq_lens,
+        max_query_len, inv_freq, q_weight, k_weight, eps, weight_offset, interleaved, factor, q_out,
+        dev_status, _handle_of(stream))
+
+
+def _check_append_tables(kv_pool, k_new, block_table, cu_seqlens, seq_lens, max_query_len):
+    debug_checks.check_append_tables(
+        cu_seqlens, seq_lens, block_table, num_tokens=k_new.shape[0],
+        max_query_len=int(max_query_len), num_blocks=kv_pool.shape[1],
+        block_size=kv_pool.shape[2])
 
 
 def attention_key_weights(q: torch.Tensor, kv_pool: torch.Tensor, lse: torch.Tensor,

@@ -216,6 +216,35 @@ struct RopeWriteParams {
 };
 cudaError_t launch_rope_write(const RopeWriteParams& p, cudaStream_t stream);
 
+// Norms of the query and key heads, rotation and cache write. Into a bf16 pool
+// through `slots`, or (append) into an 8-bit pool through the requests' tables.
+struct NormRopeParams {
+  uint16_t* q_out;            // [T][H][D] bf16
+  void* pool;                 // [2][NB][BS][Hkv][D] bf16, or e4m3
+  float* scales;              // append: [2][NB][Hkv]
+  const uint16_t* q;          // rows of [H][D], q_stride elements apart (append: may be null)
+  const uint16_t* k;          // rows of [Hkv][D]
+  const uint16_t* v;
+  int64_t q_stride, k_stride, v_stride;
+  const int32_t* positions;   // [T]; null: nothing is rotated
+  const int32_t* slots;       // [T] (bf16 pool)
+  const double* inv_freq;     // [rotary_dim / 2] radians per position
+  const void* q_weight;       // [D] bf16 or fp32; null: not normed
+  const void* k_weight;
+  int32_t weight_f32;
+  float weight_offset, eps, factor;
+  int32_t interleaved;
+  int32_t num_tokens, num_heads, num_kv_heads, head_dim, rotary_dim;
+  int64_t num_slots;          // NB * BS
+  const int32_t* block_table; // append: [B][max_blocks]
+  const int32_t* cu_seqlens;  // [B+1]
+  const int32_t* seq_lens;    // [B]
+  int32_t max_blocks, num_seqs, max_query_len, block_size, num_blocks;
+  int32_t* status;
+};
+cudaError_t launch_norm_rope(const NormRopeParams& p, cudaStream_t stream);
+cudaError_t launch_append_fp8(const NormRopeParams& p, cudaStream_t stream);
+
 struct KeyWeightsParams {
   float* out;                 // [rows][Hkv][row_len]
   const float* in;            // the same shape; may be out

@@ -40,6 +40,7 @@ const char* type_name(at::ScalarType t) {
     case at::kFloat: return "torch.float32";
     case at::kDouble: return "torch.float64";
     case at::kInt: return "torch.int32";
+    case at::kFloat8_e4m3fn: return "torch.float8_e4m3fn";
     default: return c10::toString(t);
   }
 }
@@ -80,6 +81,44 @@ struct Call {
                         shape_text(t.sizes())};
     return t;
   }
+  // The 8-bit pool and its scales.
+  const at::Tensor& kv_pool8(PyObject* o, PyObject* scales) {
+    const at::Tensor& t = dense(o, "kv_pool", at::kFloat8_e4m3fn, 5);
+    const at::Tensor& s = dense(scales, "kv_scales", at::kFloat, 3);
+    if (t.size(0) != 2)
+      throw Refused{PyExc_ValueError,
+                    "kv_pool must be [2, num_blocks, block_size, num_kv_heads, head_dim], got " +
+                        shape_text(t.sizes())};
+    if (s.size(0) != 2 || s.size(1) != t.size(1) || s.size(2) != t.size(3))
+      throw Refused{PyExc_ValueError, "kv_scales must be " +
+                                          shape_text({2, t.size(1), t.size(3)}) + ", got " +
+                                          shape_text(s.sizes())};
+    return t;
+  }
+  // A norm's weights [head_dim], bf16 or fp32 (the first ones given say which;
+  // *f32 < 0: none so far); null for None.
+  const void* norm_weight(PyObject* o, const char* name, int64_t head_dim, int* f32) {
+    if (o == Py_None) return nullptr;
+    const bool is32 = THPVariable_Check(o) && THPVariable_Unpack(o).scalar_type() == at::kFloat;
+    const at::Tensor& t = dense(o, name, is32 ? at::kFloat : at::kBFloat16, 1);
+    if (t.size(0) != head_dim)
+      throw Refused{PyExc_ValueError, std::string(name) + " must be " + shape_text({head_dim}) +
+                                          ", got " + shape_text(t.sizes())};
+    if (*f32 >= 0 && *f32 != (int)is32)
+      throw Refused{PyExc_TypeError, "q_weight and k_weight must be of one type"};
+    *f32 = is32;
+    return t.data_ptr();
+  }
+  // Block table, cu_seqlens and seq_lens of one step; returns the requests.
+  int64_t tables(PyObject* table, PyObject* cu, PyObject* lens) {
+    const int64_t b = dense(lens, "seq_lens", at::kInt, 1).size(0);
+    if (dense(cu, "cu_seqlens", at::kInt, 1).size(0) != b + 1 ||
+        dense(table, "block_table", at::kInt, 2).size(0) != b)
+      throw Refused{PyExc_ValueError, "cu_seqlens must be [B+1] and block_table [B, max_blocks]"};
+    return b;
+  }
+  // q_out: `o`, or a new tensor in *made.
+  const at::Tensor& q_output(PyObject* o, const at::Tensor& q, at::Tensor* made);
   // [tokens, heads, head_dim] bf16, a token's heads contiguous; the distance
   // between tokens goes to *stride.
   const at::Tensor& rows(PyObject* o, const char* name, int64_t tokens, int64_t heads,
@@ -119,6 +158,16 @@ at::Tensor new_output(at::IntArrayRef shape, c10::Device device) {
       (context.deterministicAlgorithms() && context.deterministicFillUninitializedMemory()))
     return at::empty(shape, at::TensorOptions(device).dtype(at::kBFloat16));
   return at::Tensor(at::detail::empty_cuda(shape, at::kBFloat16, device, std::nullopt));
+}
+
+const at::Tensor& Call::q_output(PyObject* o, const at::Tensor& q, at::Tensor* made) {
+  if (o == Py_None) {
+    *made = new_output(q.sizes(), q.device());
+    return *made;
+  }
+  const at::Tensor& t = dense(o, "q_out", at::kBFloat16, 3);
+  if (t.sizes() != q.sizes()) throw Refused{PyExc_ValueError, "q_out must have the shape of q"};
+  return t;
 }
 
 int32_t small(int64_t v) {
@@ -237,6 +286,117 @@ PyObject* rope_kv_cache_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (a[9] == Py_None) return THPVariable_Wrap(made);
     Py_INCREF(a[9]);
     return a[9];
+  });
+}
+
+// q, kv_pool, k_new, v_new, positions, slot_mapping, inv_freq (None: no
+// rotation), q_weight, k_weight, eps, weight_offset, interleaved, factor, q_out,
+// dev_status, stream
+PyObject* qk_norm_rope_kv_cache_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 16, [&]() -> PyObject* {
+    Call c;
+    const at::Tensor& pool = c.kv_pool(a[1]);
+    const at::Tensor& positions = c.dense(a[4], "positions", at::kInt, 1);
+    const at::Tensor& slots = c.dense(a[5], "slot_mapping", at::kInt, 1);
+    const at::Tensor* inv_freq = nullptr;
+    if (a[6] != Py_None) inv_freq = &c.dense(a[6], "inv_freq", at::kDouble, 1);
+    const int64_t t = slots.size(0), hkv = pool.size(3), d = pool.size(4);
+    if (positions.size(0) != t)
+      throw Refused{PyExc_ValueError, "positions and slot_mapping differ in length"};
+    const int64_t h = c.any(a[0], "q", at::kBFloat16, 3).size(1);
+    int64_t qs, ks, vs;
+    const at::Tensor& q = c.rows(a[0], "q", t, h, d, &qs);
+    const at::Tensor& k = c.rows(a[2], "k_new", t, hkv, d, &ks);
+    const at::Tensor& v = c.rows(a[3], "v_new", t, hkv, d, &vs);
+    int f32 = -1;
+    const void* qw = c.norm_weight(a[7], "q_weight", d, &f32);
+    const void* kw = c.norm_weight(a[8], "k_weight", d, &f32);
+    const float eps = to_float(a[9]), offset = to_float(a[10]), factor = to_float(a[12]);
+    const int interleaved = PyObject_IsTrue(a[11]);
+    if (interleaved < 0) throw Refused{nullptr, ""};
+    int32_t* status = c.ints(a[14], "dev_status", -1);
+    at::Tensor made;
+    const at::Tensor& out = c.q_output(a[13], q, &made);
+    run("qk_norm_rope_kv_cache_write", c.device, a[15], [&](void* stream) {
+      return pkv_qk_norm_rope_kv_cache_write(
+          ptr(out), ptr(pool), ptr(q), ptr(k), ptr(v), qs, ks, vs, ptr<int32_t>(positions),
+          ptr<int32_t>(slots), inv_freq ? ptr<double>(*inv_freq) : nullptr, qw, kw, f32 > 0, offset,
+          eps, factor, interleaved, small(t), small(h), small(hkv), small(d),
+          inv_freq ? small(2 * inv_freq->size(0)) : 0, small(pool.size(1)), small(pool.size(2)),
+          status, stream);
+    });
+    if (a[13] == Py_None) return THPVariable_Wrap(made);
+    Py_INCREF(a[13]);
+    return a[13];
+  });
+}
+
+// kv_pool, kv_scales, k_new, v_new, block_table, cu_seqlens, seq_lens,
+// max_query_len, dev_status, stream
+PyObject* kv_cache_append_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 10, [&]() -> PyObject* {
+    Call c;
+    const at::Tensor& pool = c.kv_pool8(a[0], a[1]);
+    const int64_t b = c.tables(a[4], a[5], a[6]), hkv = pool.size(3), d = pool.size(4);
+    const at::Tensor& table = THPVariable_Unpack(a[4]);
+    const int64_t t = c.any(a[2], "k_new", at::kBFloat16, 3).size(0);
+    int64_t ks, vs;
+    const at::Tensor& k = c.rows(a[2], "k_new", t, hkv, d, &ks);
+    const at::Tensor& v = c.rows(a[3], "v_new", t, hkv, d, &vs);
+    const int32_t max_q = small(to_int(a[7]));
+    int32_t* status = c.ints(a[8], "dev_status", -1);
+    run("kv_cache_append_fp8", c.device, a[9], [&](void* stream) {
+      return pkv_kv_cache_append_fp8(
+          ptr(pool), ptr<float>(THPVariable_Unpack(a[1])), ptr(k), ptr(v), ks, vs,
+          ptr<int32_t>(table), small(table.size(1)), ptr<int32_t>(THPVariable_Unpack(a[5])),
+          ptr<int32_t>(THPVariable_Unpack(a[6])), small(b), small(t), max_q, small(hkv), small(d),
+          small(pool.size(1)), small(pool.size(2)), status, stream);
+    });
+    Py_RETURN_NONE;
+  });
+}
+
+// q, kv_pool, kv_scales, k_new, v_new, positions, block_table, cu_seqlens,
+// seq_lens, max_query_len, inv_freq (None: no rotation), q_weight, k_weight, eps,
+// weight_offset, interleaved, factor, q_out, dev_status, stream
+PyObject* qk_norm_rope_kv_cache_append_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 20, [&]() -> PyObject* {
+    Call c;
+    const at::Tensor& pool = c.kv_pool8(a[1], a[2]);
+    const int64_t b = c.tables(a[6], a[7], a[8]), hkv = pool.size(3), d = pool.size(4);
+    const at::Tensor& table = THPVariable_Unpack(a[6]);
+    const at::Tensor& positions = c.dense(a[5], "positions", at::kInt, 1);
+    const at::Tensor* inv_freq = nullptr;
+    if (a[10] != Py_None) inv_freq = &c.dense(a[10], "inv_freq", at::kDouble, 1);
+    const int64_t t = positions.size(0);
+    const int64_t h = c.any(a[0], "q", at::kBFloat16, 3).size(1);
+    int64_t qs, ks, vs;
+    const at::Tensor& q = c.rows(a[0], "q", t, h, d, &qs);
+    const at::Tensor& k = c.rows(a[3], "k_new", t, hkv, d, &ks);
+    const at::Tensor& v = c.rows(a[4], "v_new", t, hkv, d, &vs);
+    const int32_t max_q = small(to_int(a[9]));
+    int f32 = -1;
+    const void* qw = c.norm_weight(a[11], "q_weight", d, &f32);
+    const void* kw = c.norm_weight(a[12], "k_weight", d, &f32);
+    const float eps = to_float(a[13]), offset = to_float(a[14]), factor = to_float(a[16]);
+    const int interleaved = PyObject_IsTrue(a[15]);
+    if (interleaved < 0) throw Refused{nullptr, ""};
+    int32_t* status = c.ints(a[18], "dev_status", -1);
+    at::Tensor made;
+    const at::Tensor& out = c.q_output(a[17], q, &made);
+    run("qk_norm_rope_kv_cache_append_fp8", c.device, a[19], [&](void* stream) {
+      return pkv_qk_norm_rope_kv_cache_append_fp8(
+          ptr(out), ptr(pool), ptr<float>(THPVariable_Unpack(a[2])), ptr(q), ptr(k), ptr(v), qs, ks,
+          vs, ptr<int32_t>(positions), ptr<int32_t>(table), small(table.size(1)),
+          ptr<int32_t>(THPVariable_Unpack(a[7])), ptr<int32_t>(THPVariable_Unpack(a[8])),
+          inv_freq ? ptr<double>(*inv_freq) : nullptr, qw, kw, f32 > 0, offset, eps, factor,
+          interleaved, small(b), small(t), max_q, small(h), small(hkv), small(d),
+          inv_freq ? small(2 * inv_freq->size(0)) : 0, small(pool.size(1)), small(pool.size(2)),
+          status, stream);
+    });
+    if (a[17] == Py_None) return THPVariable_Wrap(made);
+    Py_INCREF(a[17]);
+    return a[17];
   });
 }
 
@@ -363,6 +523,9 @@ PyObject* set_error(PyObject*, PyObject* type) {
 #define PKV_FAST(f) \
   { #f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr }
 PyMethodDef kMethods[] = {PKV_FAST(rope_kv_cache_write),
+                          PKV_FAST(qk_norm_rope_kv_cache_write),
+                          PKV_FAST(kv_cache_append_fp8),
+                          PKV_FAST(qk_norm_rope_kv_cache_append_fp8),
                           PKV_FAST(attention_key_weights),
                           PKV_FAST(evict_select),
                           PKV_FAST(evict_compact),

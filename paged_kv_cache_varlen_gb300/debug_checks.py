@@ -40,8 +40,10 @@ def _host(t) -> np.ndarray:
 
 def check_attention_tables(cu_seqlens, seq_lens, block_table, *, num_tokens: int,
                            max_query_len: int, max_seq_len: int, num_blocks: int,
-                           block_size: int, key_start=None, query_start=None) -> None:
-    """Raise ValueError on the first entry the attention kernels would reject."""
+                           block_size: int, key_start=None, query_start=None, window: int = 0,
+                           num_sink: int = 0) -> None:
+    """Raise ValueError on the first entry the attention kernels would reject.
+    Blocks that a window hides from every query of a request may be anything."""
     cu = _host(cu_seqlens).astype(np.int64)
     lens = _host(seq_lens).astype(np.int64)
     table = _host(block_table).astype(np.int64)
@@ -90,11 +92,39 @@ def check_attention_tables(cu_seqlens, seq_lens, block_table, *, num_tokens: int
         if qlen[i] == 0:
             continue
         ids = table[i, :nblk[i]]
-        out = np.nonzero((ids < 0) | (ids >= num_blocks))[0]
+        first = np.arange(nblk[i]) * block_size
+        seen = (first < num_sink) | (first + block_size > lens[i] - qlen[i] - window + 1)
+        out = np.nonzero(((ids < 0) | (ids >= num_blocks)) & (seen | (window == 0)))[0]
         if out.size:
             j = int(out[0])
             raise ValueError(f"request {i}: block_table[{i}][{j}] = {ids[j]} outside the pool "
                              f"[0, {num_blocks})")
+
+
+def check_append_tables(cu_seqlens, seq_lens, block_table, *, num_tokens: int,
+                        max_query_len: int, num_blocks: int, block_size: int) -> None:
+    """For the writes into the 8-bit pool: raise ValueError on the first entry
+    that they would reject, and when two requests write one block."""
+    cu = _host(cu_seqlens).astype(np.int64)
+    lens = _host(seq_lens).astype(np.int64)
+    table = _host(block_table).astype(np.int64)
+    most = max(int(lens.max(initial=0)), 1)
+    # the written blocks are the tail of each table row: the checks of a window
+    # that sees the new tokens alone
+    check_attention_tables(cu, lens, table, num_tokens=num_tokens, max_query_len=max_query_len,
+                           max_seq_len=most, num_blocks=num_blocks, block_size=block_size,
+                           window=1)
+    taken: dict[int, int] = {}
+    for i in range(lens.shape[0]):
+        n = int(cu[i + 1] - cu[i])
+        if n == 0:
+            continue
+        for b in range(int(lens[i] - n) // block_size, int(lens[i] - 1) // block_size + 1):
+            d = int(table[i, b])
+            if d in taken:
+                raise ValueError(f"block_table[{i}][{b}] = {d} is written for request {taken[d]} "
+                                 "too")
+            taken[d] = i
 
 
 def check_append_slots(cu_seqlens, seq_lens, block_table, slot_mapping, *,
