@@ -541,6 +541,66 @@ pkv_status pkv_qk_norm_rope_kv_cache_append_fp8(
 
 /*
  * ---------------------------------------------------------------------------
+ * Attention through a window, and over the 8-bit cache.
+ * ---------------------------------------------------------------------------
+ * pkv_paged_attention_varlen_window -- pkv_paged_attention_varlen where a query
+ * sees only the last `window` keys up to its own position and the first num_sink
+ * keys of its context:
+ *   the query at position p sees key j iff
+ *     j <= p and (window == 0 or p - j < window or j < num_sink)
+ * (window 0: every key before it; 1: its own key and the sinks).
+ * Blocks that hold no key that any query of the request sees are not read: their
+ * table entries may hold anything (blocks given back), and so may hidden keys in
+ * blocks that are read (NaN included), as long as they lie before the window of
+ * the request's first query.
+ *
+ *   out          [num_tokens][num_heads][head_dim] bf16, or fp32 when out_f32 is
+ *                set, 16-byte aligned; rounded once from fp32 (the softmax weights
+ *                are rounded to fp16 in requests of more than 32 / G queries and
+ *                over the 8-bit cache, to 16 bits of fraction elsewhere)
+ *   partition_size  as there, counted in keys that some query of the request sees;
+ *                requests of up to 32 / G queries are split; -1: by the batch (as
+ *                many partitions as fill the GPU, of at least 256 keys)
+ *   workspace    at least pkv_window_attention_workspace_size(...) bytes, 256-byte
+ *                aligned. It needs no clearing. One for each concurrent call, and
+ *                for each captured graph that may run beside another
+ * Other arguments, streams and errors as pkv_paged_attention_varlen; num_heads /
+ * num_kv_heads may be any number up to 128 (any at all for requests of one query).
+ * max_seq_len below 2^30.
+ */
+size_t pkv_window_attention_workspace_size(int32_t num_seqs, int32_t max_query_len,
+                                           int32_t num_heads, int32_t num_kv_heads,
+                                           int32_t head_dim, int32_t max_seq_len, int32_t window,
+                                           int32_t num_sink, int32_t partition_size,
+                                           int32_t eight_bit);
+pkv_status pkv_paged_attention_varlen_window(
+    void *out, int32_t out_f32, float *out_lse, const void *q, const void *kv_pool,
+    const int32_t *block_table, int32_t max_blocks_per_seq, const int32_t *cu_seqlens_q,
+    const int32_t *seq_lens, int32_t num_seqs, int32_t num_tokens, int32_t max_query_len,
+    int32_t max_seq_len, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+    int32_t block_size, int32_t num_blocks, int32_t window, int32_t num_sink, float scale,
+    int32_t partition_size, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+    void *stream);
+
+/*
+ * pkv_paged_attention_varlen_fp8 -- the same over an 8-bit pool: attention over
+ * the keys and values that it stands for (e4m3 value times kv_scales; any positive
+ * finite scales, the library's own are powers of two), computed in fp32 from
+ * exact products. Arguments as pkv_paged_attention_varlen_window (eight_bit = 1
+ * for the workspace), plus
+ *   kv_scales    [2][num_blocks][num_kv_heads] fp32
+ */
+pkv_status pkv_paged_attention_varlen_fp8(
+    void *out, int32_t out_f32, float *out_lse, const void *q, const void *kv_pool,
+    const float *kv_scales, const int32_t *block_table, int32_t max_blocks_per_seq,
+    const int32_t *cu_seqlens_q, const int32_t *seq_lens, int32_t num_seqs, int32_t num_tokens,
+    int32_t max_query_len, int32_t max_seq_len, int32_t num_heads, int32_t num_kv_heads,
+    int32_t head_dim, int32_t block_size, int32_t num_blocks, int32_t window, int32_t num_sink,
+    float scale, int32_t partition_size, void *workspace, size_t workspace_bytes,
+    int32_t *dev_status, void *stream);
+
+/*
+ * ---------------------------------------------------------------------------
  * Holding a request inside a cache budget: the attention weight that each
  * cached key has received is accumulated step by step, and when a request's
  * context is cut back, each KV head keeps the keys with the most of it. The

@@ -18,11 +18,14 @@ from .binding import (  # noqa: F401
     lse_merge,
     paged_attention_varlen,
     paged_attention_varlen_append,
+    paged_attention_varlen_fp8,
     paged_attention_varlen_range,
+    paged_attention_varlen_window,
     qk_norm_rope_kv_cache_append_fp8,
     qk_norm_rope_kv_cache_write,
     rope_frequencies,
     rope_kv_cache_write,
+    window_attention_workspace_size,
 )
 
 __all__ = [
@@ -38,9 +41,12 @@ __all__ = [
     "lse_merge",
     "paged_attention_varlen",
     "paged_attention_varlen_append",
+    "paged_attention_varlen_fp8",
     "paged_attention_varlen_range",
+    "paged_attention_varlen_window",
     "qk_norm_rope_kv_cache_append_fp8",
     "qk_norm_rope_kv_cache_write",
     "rope_frequencies",
     "rope_kv_cache_write",
+    "window_attention_workspace_size",
 ]

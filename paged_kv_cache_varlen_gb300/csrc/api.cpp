@@ -296,6 +296,21 @@ bool encode_kv_view(CUtensorMap* map, const void* kv_pool, int32_t num_blocks, i
   return encode_4d(map, kv_pool, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+bool encode_kv8_view(CUtensorMap* map, const void* kv_pool, int32_t num_blocks, int32_t block_size,
+                     int32_t num_kv_heads, int32_t head_dim) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)2 * num_blocks * block_size,
+                              (cuuint64_t)num_kv_heads};
+  const cuuint64_t strides[2] = {(cuuint64_t)num_kv_heads * head_dim, (cuuint64_t)head_dim};
+  const cuuint32_t box[3] = {(cuuint32_t)head_dim, 16, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(kv_pool), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // q [T][H][D] with a box of {64, G, 128/G} (one Q tile of up to 128 rows per
 // chunk).
 bool encode_q_tiles(CUtensorMap* map, const void* q, int32_t num_tokens, int32_t num_heads,

@@ -123,7 +123,37 @@ struct AttnParams {
   // of the requests' query positions: CTAs of a plain decode batch read the
   // keys before the first query's position without waiting for it
   int32_t early_pool;
+  // The calls with a window or an 8-bit pool: query position p sees key j iff
+  // j <= p and (window == 0 or p - j < window or j < num_sink). out_bf16: `out`
+  // holds bf16. scales: [2][NB][Hkv] of an e4m3 pool, else null.
+  int32_t window, num_sink;
+  int32_t out_bf16;
+  const float* scales;
+  // their split-KV partials: row (request i, query j, head h) of partition c is
+  // ((c * num_seqs + i) * ws_q + j) * H + h of ws_out and ws_lse
+  int32_t ws_q;
 };
+
+// The keys that the queries of one request see, in units of `tile` keys: the
+// first `sink` units and those from unit `low` on, `count` in all up to the end
+// of the context. (Without a window all of them.) Unit v of these is unit
+// v < sink ? v : v - sink + low of the context.
+struct Visible {
+  int sink, low, count;
+  __host__ __device__ int unit(int v) const { return v < sink ? v : v - sink + low; }
+};
+// qpos0: position of the first query; kv_end: one past the last key needed.
+__host__ __device__ inline Visible visible_units(int window, int num_sink, int qpos0, int kv_end,
+                                                 int tile) {
+  Visible v;
+  const int first = window > 0 && qpos0 >= window ? qpos0 - window + 1 : 0;
+  v.low = first / tile;
+  // (in 64 bits: num_sink may be any int)
+  const int64_t s = ((int64_t)num_sink + tile - 1) / tile;
+  v.sink = window > 0 ? (int)(s < v.low ? s : v.low) : 0;
+  v.count = v.sink + (kv_end + tile - 1) / tile - v.low;
+  return v;
+}
 
 cudaError_t launch_kv_write(const KvWriteParams& p, cudaStream_t stream);
 
@@ -150,6 +180,13 @@ int32_t attention_with_scratch(float* out, float* out_lse, const void* q, const 
 cudaError_t launch_decode_mma(const AttnParams& p, const CUtensorMap& kv_map,
                               cudaStream_t stream);
 
+// The decode kernel of an 8-bit pool (requests of up to decode_max_q queries).
+// `kv_map` views the pool as [Hkv][2*NB*BS rows][D] bytes with a box of {D, 16,
+// 1}, swizzled by its rows' length. Split requests are merged by a second grid.
+cudaError_t launch_decode_fp8(const AttnParams& p, const CUtensorMap& kv_map, cudaStream_t stream);
+// The merge grid of launch_decode_fp8 and of the windowed decode grid.
+cudaError_t launch_merge_rows(const AttnParams& p, cudaStream_t stream);
+
 // Chunked-prefill kernel (query_len > 1 requests), tcgen05 tensor cores.
 // `q_map`: q as [T][H][D] with a box of {64, G, 128/G}, 128-byte swizzle.
 // `kv_map`: the pool viewed as for the decode kernel but with a box of
@@ -163,7 +200,8 @@ cudaError_t launch_prefill(const AttnParams& p, const CUtensorMap& q_map,
 // Whether the prefill kernel's shared memory (its K/V/Q stages plus the work
 // list of num_seqs requests) fits the 227 KB a CTA may have: up to 8575
 // requests at head_dim 128, 33151 at 64. False for other head dims.
-bool prefill_fits(int32_t num_seqs, int32_t head_dim);
+// (`eight`: of the 8-bit pool's form).
+bool prefill_fits(int32_t num_seqs, int32_t head_dim, bool eight = false);
 
 // Shared-prefix (cascade) merge: row r of out (num_rows = B * H rows of
 // head_dim) from the tail partial (slot 0) and the prefix segments (slots
@@ -194,6 +232,10 @@ cudaError_t launch_lse_merge(float* out, float* out_lse, const float* part_out,
 // `chunks` 64-column chunks.
 bool encode_kv_view(CUtensorMap* map, const void* kv_pool, int32_t num_blocks, int32_t block_size,
                     int32_t num_kv_heads, int32_t head_dim, uint32_t chunks);
+// The 8-bit pool as [Hkv][2*NB*BS rows][D] bytes, boxes of 16 rows of one KV
+// head, 128-byte swizzle for 128-byte rows, 64-byte for 64.
+bool encode_kv8_view(CUtensorMap* map, const void* kv_pool, int32_t num_blocks, int32_t block_size,
+                     int32_t num_kv_heads, int32_t head_dim);
 // q [T][H][D] in boxes of {64 columns, G heads, 128/G tokens}.
 bool encode_q_tiles(CUtensorMap* map, const void* q, int32_t num_tokens, int32_t num_heads,
                     int32_t num_kv_heads, int32_t head_dim);

@@ -149,15 +149,16 @@ T* ptr(const at::Tensor& t) {
   return static_cast<T*>(t.data_ptr());
 }
 
-// torch.empty of bf16. Its way through the dispatcher (0.7 us a call) is left out
+// torch.empty of bf16 (or another type). Its way through the dispatcher (0.7 us a call) is left out
 // where nothing there would act: no dispatch mode, and no filling of new memory
 // in deterministic mode.
-at::Tensor new_output(at::IntArrayRef shape, c10::Device device) {
+at::Tensor new_output(at::IntArrayRef shape, c10::Device device,
+                      at::ScalarType type = at::kBFloat16) {
   const at::Context& context = at::globalContext();
   if (c10::impl::dispatch_mode_enabled() ||
       (context.deterministicAlgorithms() && context.deterministicFillUninitializedMemory()))
-    return at::empty(shape, at::TensorOptions(device).dtype(at::kBFloat16));
-  return at::Tensor(at::detail::empty_cuda(shape, at::kBFloat16, device, std::nullopt));
+    return at::empty(shape, at::TensorOptions(device).dtype(type));
+  return at::Tensor(at::detail::empty_cuda(shape, type, device, std::nullopt));
 }
 
 const at::Tensor& Call::q_output(PyObject* o, const at::Tensor& q, at::Tensor* made) {
@@ -328,6 +329,80 @@ PyObject* qk_norm_rope_kv_cache_write(PyObject*, PyObject* const* a, Py_ssize_t 
     if (a[13] == Py_None) return THPVariable_Wrap(made);
     Py_INCREF(a[13]);
     return a[13];
+  });
+}
+
+// q, kv_pool, kv_scales (None: the pool is bf16), block_table, cu_seqlens,
+// seq_lens, max_query_len, max_seq_len, window, num_sink, out, out_lse, scale
+// (None: 1 / sqrt(head_dim)), partition_size, workspace, dev_status, stream;
+// returns out
+PyObject* window_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 17, [&]() -> PyObject* {
+    Call c;
+    const bool eight = a[2] != Py_None;
+    const at::Tensor& pool = eight ? c.kv_pool8(a[1], a[2]) : c.kv_pool(a[1]);
+    const at::Tensor& q = c.dense(a[0], "q", at::kBFloat16, 3);
+    const int64_t b = c.tables(a[3], a[4], a[5]);
+    const at::Tensor& table = THPVariable_Unpack(a[3]);
+    const int64_t t = q.size(0), h = q.size(1), d = q.size(2), hkv = pool.size(3);
+    if (pool.size(4) != d) throw Refused{PyExc_ValueError, "q and kv_pool head_dim differ"};
+    const int32_t max_q = small(to_int(a[6])), max_len = small(to_int(a[7]));
+    const int32_t window = small(to_int(a[8])), sink = small(to_int(a[9]));
+    const float scale = a[12] == Py_None ? (float)(1.0 / std::sqrt((double)d)) : to_float(a[12]);
+    const int32_t part = small(to_int(a[13]));
+    at::Tensor made;
+    bool f32 = false;
+    if (a[10] == Py_None) {
+      made = new_output({t, h, d}, q.device());
+    } else {
+      f32 = THPVariable_Check(a[10]) && THPVariable_Unpack(a[10]).scalar_type() == at::kFloat;
+      if (c.dense(a[10], "out", f32 ? at::kFloat : at::kBFloat16, 3).sizes() != q.sizes())
+        throw Refused{PyExc_ValueError, "out must have the shape of q"};
+    }
+    const at::Tensor& out = a[10] == Py_None ? made : THPVariable_Unpack(a[10]);
+    float* lse = nullptr;
+    if (a[11] != Py_None) {
+      const at::Tensor& l = c.dense(a[11], "out_lse", at::kFloat, 2);
+      if (l.size(0) != t || l.size(1) != h)
+        throw Refused{PyExc_ValueError, "out_lse must be [num_tokens, num_heads]"};
+      lse = ptr<float>(l);
+    }
+    int32_t* status = c.ints(a[15], "dev_status", -1);
+    // scratch for the call alone, where none is given (work of the current stream)
+    at::Tensor scratch;
+    void* ws = nullptr;
+    size_t bytes = 0;
+    if (a[14] == Py_None) {
+      if (t > 0) bytes = pkv_window_attention_workspace_size(
+          small(b), max_q, small(h), small(hkv), small(d), max_len, window, sink, part, eight);
+      if (bytes > 0) {
+        scratch = new_output({(int64_t)bytes}, q.device(), at::kByte);
+        ws = ptr(scratch);
+      }
+    } else {
+      const at::Tensor& w = c.dense(a[14], "workspace", at::kByte, 1);
+      ws = ptr(w);
+      bytes = (size_t)w.size(0);
+    }
+    const char* what = eight ? "paged_attention_varlen_fp8" : "paged_attention_varlen_window";
+    run(what, c.device, a[16], [&](void* stream) {
+      const int32_t* tab = ptr<int32_t>(table);
+      const int32_t* cu = ptr<int32_t>(THPVariable_Unpack(a[4]));
+      const int32_t* lens = ptr<int32_t>(THPVariable_Unpack(a[5]));
+      if (eight)
+        return pkv_paged_attention_varlen_fp8(
+            ptr(out), f32, lse, ptr(q), ptr(pool), ptr<float>(THPVariable_Unpack(a[2])), tab,
+            small(table.size(1)), cu, lens, small(b), small(t), max_q, max_len, small(h),
+            small(hkv), small(d), small(pool.size(2)), small(pool.size(1)), window, sink, scale,
+            part, ws, bytes, status, stream);
+      return pkv_paged_attention_varlen_window(
+          ptr(out), f32, lse, ptr(q), ptr(pool), tab, small(table.size(1)), cu, lens, small(b),
+          small(t), max_q, max_len, small(h), small(hkv), small(d), small(pool.size(2)),
+          small(pool.size(1)), window, sink, scale, part, ws, bytes, status, stream);
+    });
+    if (a[10] == Py_None) return THPVariable_Wrap(made);
+    Py_INCREF(a[10]);
+    return a[10];
   });
 }
 
@@ -525,6 +600,7 @@ PyObject* set_error(PyObject*, PyObject* type) {
 PyMethodDef kMethods[] = {PKV_FAST(rope_kv_cache_write),
                           PKV_FAST(qk_norm_rope_kv_cache_write),
                           PKV_FAST(kv_cache_append_fp8),
+                          PKV_FAST(window_attention),
                           PKV_FAST(qk_norm_rope_kv_cache_append_fp8),
                           PKV_FAST(attention_key_weights),
                           PKV_FAST(evict_select),
