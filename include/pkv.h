@@ -558,20 +558,21 @@ pkv_status pkv_qk_norm_rope_kv_cache_append_fp8(
  *                set, 16-byte aligned; rounded once from fp32 (the softmax weights
  *                are rounded to fp16 in requests of more than 32 / G queries and
  *                over the 8-bit cache, to 16 bits of fraction elsewhere)
- *   partition_size  as there, counted in keys that some query of the request sees;
- *                requests of up to 32 / G queries are split; -1: by the batch (as
- *                many partitions as fill the GPU, of at least 256 keys)
  *   workspace    at least pkv_window_attention_workspace_size(...) bytes, 256-byte
- *                aligned. It needs no clearing. One for each concurrent call, and
+ *                aligned (13 MB at most). It needs no clearing. One for each concurrent call, and
  *                for each captured graph that may run beside another
+ * There is no partition_size: the work of the requests of up to 32 / G queries is
+ * cut into equal shares of the keys that they see, whatever their lengths, and the
+ * pieces are joined by log-sum-exp. The cuts follow the whole batch's lengths, so a
+ * request's result may differ in its last bits from one batch to another; the same
+ * call gives the same bits.
  * Other arguments, streams and errors as pkv_paged_attention_varlen; num_heads /
  * num_kv_heads may be any number up to 128 (any at all for requests of one query).
  * max_seq_len below 2^30.
  */
-size_t pkv_window_attention_workspace_size(int32_t num_seqs, int32_t max_query_len,
-                                           int32_t num_heads, int32_t num_kv_heads,
-                                           int32_t head_dim, int32_t max_seq_len, int32_t window,
-                                           int32_t num_sink, int32_t partition_size,
+size_t pkv_window_attention_workspace_size(int32_t max_query_len, int32_t num_heads,
+                                           int32_t num_kv_heads, int32_t head_dim,
+                                           int32_t max_seq_len, int32_t window, int32_t num_sink,
                                            int32_t eight_bit);
 pkv_status pkv_paged_attention_varlen_window(
     void *out, int32_t out_f32, float *out_lse, const void *q, const void *kv_pool,
@@ -579,8 +580,7 @@ pkv_status pkv_paged_attention_varlen_window(
     const int32_t *seq_lens, int32_t num_seqs, int32_t num_tokens, int32_t max_query_len,
     int32_t max_seq_len, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
     int32_t block_size, int32_t num_blocks, int32_t window, int32_t num_sink, float scale,
-    int32_t partition_size, void *workspace, size_t workspace_bytes, int32_t *dev_status,
-    void *stream);
+    void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
 
 /*
  * pkv_paged_attention_varlen_fp8 -- the same over an 8-bit pool: attention over
@@ -596,8 +596,7 @@ pkv_status pkv_paged_attention_varlen_fp8(
     const int32_t *cu_seqlens_q, const int32_t *seq_lens, int32_t num_seqs, int32_t num_tokens,
     int32_t max_query_len, int32_t max_seq_len, int32_t num_heads, int32_t num_kv_heads,
     int32_t head_dim, int32_t block_size, int32_t num_blocks, int32_t window, int32_t num_sink,
-    float scale, int32_t partition_size, void *workspace, size_t workspace_bytes,
-    int32_t *dev_status, void *stream);
+    float scale, void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
 
 /*
  * ---------------------------------------------------------------------------

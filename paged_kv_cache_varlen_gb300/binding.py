@@ -62,13 +62,13 @@ _SIGNATURES = {
     "pkv_qk_norm_rope_kv_cache_append_fp8": (
         _i32, [_vp] * 6 + [ctypes.c_int64] * 3 + [_vp, _vp, _i32] + [_vp] * 5 + [_i32]
         + [ctypes.c_float] * 3 + [_i32] * 10 + [_vp, _vp]),
-    "pkv_window_attention_workspace_size": (ctypes.c_size_t, [_i32] * 10),
+    "pkv_window_attention_workspace_size": (ctypes.c_size_t, [_i32] * 8),
     "pkv_paged_attention_varlen_window": (
         _i32, [_vp, _i32] + [_vp] * 4 + [_i32, _vp, _vp] + [_i32] * 11
-        + [ctypes.c_float, _i32, _vp, ctypes.c_size_t, _vp, _vp]),
+        + [ctypes.c_float, _vp, ctypes.c_size_t, _vp, _vp]),
     "pkv_paged_attention_varlen_fp8": (
         _i32, [_vp, _i32] + [_vp] * 5 + [_i32, _vp, _vp] + [_i32] * 11
-        + [ctypes.c_float, _i32, _vp, ctypes.c_size_t, _vp, _vp]),
+        + [ctypes.c_float, _vp, ctypes.c_size_t, _vp, _vp]),
     "pkv_attention_key_weights": (
         _i32, [_vp] * 6 + [_i32] + [_vp] * 4 + [_i32] * 11
         + [ctypes.c_float, ctypes.c_float, _vp, _vp]),
@@ -795,15 +795,14 @@ def _check_append_tables(kv_pool, k_new, block_table, cu_seqlens, seq_lens, max_
         block_size=kv_pool.shape[2])
 
 
-def window_attention_workspace_size(num_seqs: int, max_query_len: int, num_heads: int,
-                                    num_kv_heads: int, head_dim: int, max_seq_len: int,
-                                    window: int = 0, num_sink: int = 0, partition_size: int = -1,
-                                    eight_bit: bool = False) -> int:
+def window_attention_workspace_size(max_query_len: int, num_heads: int, num_kv_heads: int,
+                                    head_dim: int, max_seq_len: int, window: int = 0,
+                                    num_sink: int = 0, eight_bit: bool = False) -> int:
     """Bytes of scratch of :func:`paged_attention_varlen_window` and, with
     ``eight_bit``, of :func:`paged_attention_varlen_fp8`."""
     return int(load_library().pkv_window_attention_workspace_size(
-        num_seqs, max_query_len, num_heads, num_kv_heads, head_dim, max_seq_len, window, num_sink,
-        partition_size, int(eight_bit)))
+        max_query_len, num_heads, num_kv_heads, head_dim, max_seq_len, window, num_sink,
+        int(eight_bit)))
 
 
 def paged_attention_varlen_window(q: torch.Tensor, kv_pool: torch.Tensor,
@@ -812,7 +811,7 @@ def paged_attention_varlen_window(q: torch.Tensor, kv_pool: torch.Tensor,
                                   window: int, *, num_sink: int = 0,
                                   out: torch.Tensor | None = None,
                                   out_lse: torch.Tensor | None = None, scale: float | None = None,
-                                  partition_size: int = -1, workspace: torch.Tensor | None = None,
+                                  workspace: torch.Tensor | None = None,
                                   dev_status: torch.Tensor | None = None, stream=None):
     """:func:`paged_attention_varlen` where the query at position p sees key j only
     if ``p - j < window`` or ``j < num_sink`` (window 0: every key before it).
@@ -823,8 +822,8 @@ def paged_attention_varlen_window(q: torch.Tensor, kv_pool: torch.Tensor,
     (``window_attention_workspace_size`` bytes, uint8) needs no clearing and is
     allocated for the call where none is given."""
     return _window_attention(q, kv_pool, None, block_table, cu_seqlens, seq_lens, max_query_len,
-                             max_seq_len, window, num_sink, out, out_lse, scale, partition_size,
-                             workspace, dev_status, stream)
+                             max_seq_len, window, num_sink, out, out_lse, scale, workspace,
+                             dev_status, stream)
 
 
 def paged_attention_varlen_fp8(q: torch.Tensor, kv_pool: torch.Tensor, kv_scales: torch.Tensor,
@@ -833,7 +832,7 @@ def paged_attention_varlen_fp8(q: torch.Tensor, kv_pool: torch.Tensor, kv_scales
                                window: int = 0, num_sink: int = 0,
                                out: torch.Tensor | None = None,
                                out_lse: torch.Tensor | None = None, scale: float | None = None,
-                               partition_size: int = -1, workspace: torch.Tensor | None = None,
+                               workspace: torch.Tensor | None = None,
                                dev_status: torch.Tensor | None = None, stream=None):
     """Causal GQA attention over the 8-bit pool [2,NB,BS,Hkv,D] float8_e4m3fn,
     whose values stand for themselves times ``kv_scales`` [2,NB,Hkv] fp32; through
@@ -841,12 +840,12 @@ def paged_attention_varlen_fp8(q: torch.Tensor, kv_pool: torch.Tensor, kv_scales
     other arguments and results these are)."""
     return _window_attention(q, kv_pool, kv_scales, block_table, cu_seqlens, seq_lens,
                              max_query_len, max_seq_len, window, num_sink, out, out_lse, scale,
-                             partition_size, workspace, dev_status, stream)
+                             workspace, dev_status, stream)
 
 
 def _window_attention(q, kv_pool, kv_scales, block_table, cu_seqlens, seq_lens, max_query_len,
-                      max_seq_len, window, num_sink, out, out_lse, scale, partition_size, workspace,
-                      dev_status, stream):
+                      max_seq_len, window, num_sink, out, out_lse, scale, workspace, dev_status,
+                      stream):
     native = _native or _marshal()
     if native.debug_checks():
         debug_checks.check_attention_tables(
@@ -861,13 +860,11 @@ def _window_attention(q, kv_pool, kv_scales, block_table, cu_seqlens, seq_lens, 
                 out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
             if workspace is None:
                 workspace = torch.empty(window_attention_workspace_size(
-                    seq_lens.shape[0], int(max_query_len), q.shape[1], kv_pool.shape[3], q.shape[2],
-                    int(max_seq_len), int(window), int(num_sink), int(partition_size),
-                    kv_scales is not None), dtype=torch.uint8, device=q.device)
+                    int(max_query_len), q.shape[1], kv_pool.shape[3], q.shape[2], int(max_seq_len),
+                    int(window), int(num_sink), kv_scales is not None), dtype=torch.uint8, device=q.device)
     out = native.window_attention(
         q, kv_pool, kv_scales, block_table, cu_seqlens, seq_lens, max_query_len, max_seq_len,
-        window, num_sink, out, out_lse, scale, partition_size, workspace, dev_status,
-        _handle_of(stream))
+        window, num_sink, out, out_lse, scale, workspace, dev_status, _handle_of(stream))
     return out, out_lse
 
 

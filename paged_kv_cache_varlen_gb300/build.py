@@ -24,7 +24,7 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIBRARY = os.path.join(PKG, "libpkv.so")
 MARSHAL = os.path.join(PKG, "_marshal.so")
 MARSHAL_SOURCE = "marshal.cpp"
-SOURCES = ["kv_write.cu", "decode_mma.cu", "decode_fp8.cu", "merge.cu", "prefill_tc.cu",
+SOURCES = ["kv_write.cu", "decode_mma.cu", "decode_rows.cu", "merge.cu", "prefill_tc.cu",
            "copy_blocks.cu", "rope_write.cu", "norm_write.cu", "key_weights.cu",
            "key_weights_tc.cu", "evict.cu", "api.cpp", "budget_api.cpp", "cache8_api.cpp",
            "window_api.cpp", "api_noalloc.cu", "block_manager.cpp"]

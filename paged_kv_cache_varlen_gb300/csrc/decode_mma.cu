@@ -114,11 +114,7 @@ __device__ __forceinline__ uint32_t swz(int token, int unit) {
 // a query position, and (every thread) before its output stores. Separate
 // instantiations, so that every prologue's loads stay branch-free (a
 // run-time choice there cost up to 5 %).
-// WIN: queries see a window of the keys before them and the first num_sink
-// ones (AttnParams::window). A partition is part_size of the keys that some query
-// of the request sees, chunks that none sees are not read, and requests of
-// several queries are split too.
-template <int D, int SPW, int MINB, bool UNITQ, bool ORDERED, bool EARLY, bool WIN>
+template <int D, int SPW, int MINB, bool UNITQ, bool ORDERED, bool EARLY>
 __global__ void __launch_bounds__(kWarps * 32, MINB)
     decode_mma_kernel(const __grid_constant__ CUtensorMap kv_map, const AttnParams p) {
   constexpr int KS = D / 16;            // k-steps of QK^T
@@ -173,23 +169,14 @@ __global__ void __launch_bounds__(kWarps * 32, MINB)
   // several queries (a verification step) take partition 0 only, kbeg = 0
   const int32_t kbeg = part * p.part_size;
   const int32_t* bt = p.block_table + (int64_t)i * p.max_blocks;
-  Visible vis{0, 0, 0};                             // WIN: the chunks that are read
-  const int32_t vis0 = part * (p.part_size / kChunk);  // the partition's first of them
   // lane j of the warp caches the block id of the warp's chunk (kb + j)
   auto load_ids = [&](int kb) -> int32_t {
     const int64_t c = warp + (int64_t)(kb + lane) * kWarps;
-    int64_t blk = (kbeg + c * kChunk) / p.block_size;
-    if constexpr (WIN) {
-      if (vis0 + c >= vis.count) return -1;
-      blk = (int64_t)vis.unit((int)(vis0 + c)) * kChunk / p.block_size;
-    }
+    const int64_t blk = (kbeg + c * kChunk) / p.block_size;
     return blk < p.max_blocks ? __ldg(bt + blk) : -1;
   };
-  int32_t ids_cur = -1, ids_next = -1;
-  if constexpr (!WIN) {
-    ids_cur = load_ids(0);
-    ids_next = load_ids(32);
-  }
+  int32_t ids_cur = load_ids(0);
+  int32_t ids_next = load_ids(32);
 
   if (t0 < 0 || t1 < t0 || t1 > p.num_tokens) {
     if (leader) set_status(p.status, PKV_DEV_BAD_LENGTHS);
@@ -216,26 +203,11 @@ __global__ void __launch_bounds__(kWarps * 32, MINB)
       ranged ? (int32_t)max(-(1 << 30), min(1 << 30, qstart - kstart)) : L - qlen;
   // several queries: one partition over every key, with the causal limit per
   // row; one query: the split-KV partitions
-  if constexpr (!WIN) {
-    if (qlen > 1 && part > 0) return;
-    if (kbeg >= L) return;
-  } else {
-    vis = visible_units(p.window, p.num_sink, qpos0, L, kChunk);
-    if (vis0 >= vis.count) return;
-    ids_cur = load_ids(0);
-    ids_next = load_ids(32);
-  }
-  const int32_t kend = (WIN || qlen > 1) ? L : min(L, kbeg + p.part_size);
-  const int nchunks = WIN ? min(p.part_size / kChunk, vis.count - vis0)
-                          : (kend - kbeg + kChunk - 1) / kChunk;
+  if (qlen > 1 && part > 0) return;
+  if (kbeg >= L) return;
+  const int32_t kend = qlen > 1 ? L : min(L, kbeg + p.part_size);
+  const int nchunks = (kend - kbeg + kChunk - 1) / kChunk;
   const int my_chunks = (nchunks - warp + kWarps - 1) / kWarps;
-  // the first key of the warp's chunk k
-  auto chunk_key = [&](int k) {
-    if constexpr (WIN) return vis.unit(vis0 + warp + k * kWarps) * kChunk;
-    return kbeg + (warp + k * kWarps) * kChunk;
-  };
-  // no query sees keys [num_sink, lo_any)
-  const int32_t lo_any = WIN ? max(0, qpos0 - p.window + 1) : 0;
 
   if (lane == 0) {
     for (int s = 0; s < SPW; ++s) mbar_init(smem_addr(&bars[warp * SPW + s]), 1);
@@ -255,7 +227,7 @@ __global__ void __launch_bounds__(kWarps * 32, MINB)
       return;
     }
     const uint32_t dst = smem_addr(slots + (warp * SPW + slot) * SLOT);
-    const int key0 = chunk_key(k);
+    const int key0 = kbeg + (warp + k * kWarps) * kChunk;
     if constexpr (EARLY) {
       if (!waited && key0 + kChunk > qpos0) {  // the chunk holds a query position
         griddep_wait();
@@ -337,7 +309,7 @@ __global__ void __launch_bounds__(kWarps * 32, MINB)
     consumed = k + 1;
     const int32_t id = __shfl_sync(kFull, ids_cur, k - kb);
     const bool chunk_ok = (id >= 0 && id < p.num_blocks);
-    const int key0 = chunk_key(k);
+    const int key0 = kbeg + (warp + k * kWarps) * kChunk;
     const int nvalid = chunk_ok ? min(kChunk, kend - key0) : 0;
     uint8_t* kbase = slots + (warp * SPW + slot) * SLOT;
     uint8_t* vbase = kbase + HALF;
@@ -349,16 +321,6 @@ __global__ void __launch_bounds__(kWarps * 32, MINB)
         *reinterpret_cast<uint4*>(vbase + swz<D>(tok, e % (D / 8))) = make_uint4(0u, 0u, 0u, 0u);
       }
       __syncwarp();
-    }
-    if constexpr (WIN) {
-      // so do rows of a chunk that are hidden from every query
-      const int h0 = max(0, p.num_sink - key0), h1 = min(kChunk, lo_any - key0);
-      if (h0 < h1) {
-        for (int e = lane; e < (h1 - h0) * (D / 8); e += 32)
-          *reinterpret_cast<uint4*>(vbase + swz<D>(h0 + e / (D / 8), e % (D / 8))) =
-              make_uint4(0u, 0u, 0u, 0u);
-        __syncwarp();
-      }
     }
     const uint32_t ka = smem_addr(kbase), va = smem_addr(vbase);
 
@@ -383,13 +345,6 @@ __global__ void __launch_bounds__(kWarps * 32, MINB)
         const int tok = nt * 8 + cq + j;
         if (tok >= nvalid || key0 + tok >= lim0) s[nt][j] = -INFINITY;
         if (tok >= nvalid || key0 + tok >= lim1) s[nt][2 + j] = -INFINITY;
-        if constexpr (WIN) {
-          const int key = key0 + tok;
-          if (key >= p.num_sink) {
-            if (key < lim0 - p.window) s[nt][j] = -INFINITY;
-            if (key < lim1 - p.window) s[nt][2 + j] = -INFINITY;
-          }
-        }
         mx0 = fmaxf(mx0, s[nt][j]);
         mx1 = fmaxf(mx1, s[nt][2 + j]);
       }
@@ -493,44 +448,6 @@ __global__ void __launch_bounds__(kWarps * 32, MINB)
   }
   __syncthreads();
 
-  if constexpr (WIN) {
-    const int per_part = p.part_size / kChunk;
-    const bool split = vis.count > per_part;
-    for (int idx = threadIdx.x; idx < rows * (D / 2); idx += kWarps * 32) {
-      const int g = idx / (D / 2), d = (idx - g * (D / 2)) * 2;
-      float M = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, red_ml[(w * kRows + g) * 2]);
-      float wsum = 0.f, a0 = 0.f, a1 = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float mw = red_ml[(w * kRows + g) * 2], lw = red_ml[(w * kRows + g) * 2 + 1];
-        if (lw == 0.f) continue;  // no key (a sum that is NaN goes on)
-        const float a = fast_exp2(mw - M);
-        wsum += a * lw;
-        const float2 x = *reinterpret_cast<const float2*>(red_o + (w * kRows + g) * RS + d);
-        a0 += a * x.x;
-        a1 += a * x.y;
-      }
-      const bool none = wsum == 0.f;
-      const float v0 = none ? 0.f : a0 / wsum, v1 = none ? 0.f : a1 / wsum;
-      const float lse = none ? -INFINITY : (M + fast_log2(wsum)) * kLn2;
-      if (split) {
-        const int64_t rr = (((int64_t)part * p.num_seqs + i) * p.ws_q + (row0 + g) / group) *
-                               p.num_heads + row_head(g);
-        *reinterpret_cast<float2*>(p.ws_out + rr * D + d) = make_float2(v0, v1);
-        if (d == 0) p.ws_lse[rr] = lse;
-        continue;
-      }
-      const int64_t orow = (int64_t)row_token(g) * p.num_heads + row_head(g);
-      if (p.out_bf16)
-        reinterpret_cast<uint32_t*>(p.out)[(orow * D + d) / 2] = pack_bf16x2(v0, v1);
-      else
-        *reinterpret_cast<float2*>(p.out + orow * D + d) = make_float2(v0, v1);
-      if (d == 0 && p.out_lse) p.out_lse[orow] = lse;
-    }
-    return;
-  }
   const int parts_i = qlen > 1 ? 1 : (L + p.part_size - 1) / p.part_size;
   const int h0 = kvh * group + row0;  // one query: row g is head h0 + g
   for (int idx = threadIdx.x; idx < rows * D; idx += kWarps * 32) {
@@ -708,15 +625,12 @@ cudaError_t launch_decode_mma_d(const AttnParams& p, const CUtensorMap& kv_map,
   const bool unitq = p.cu_seqlens == nullptr;
   const bool ordered = p.order != nullptr && !unitq && !p.after_prefill && p.num_seqs <= 256;
   const bool early = p.early_pool && !unitq && !ordered && !p.after_prefill && !p.key_start;
-  const bool windowed = p.window > 0;  // (with one query a request from cu_seqlens)
-  auto kernel = windowed  ? decode_mma_kernel<D, SPW, MINB, false, false, false, true>
-                : unitq   ? decode_mma_kernel<D, SPW, MINB, true, false, false, false>
-                : ordered ? decode_mma_kernel<D, SPW, MINB, false, true, false, false>
-                : early   ? decode_mma_kernel<D, SPW, MINB, false, false, true, false>
-                          : decode_mma_kernel<D, SPW, MINB, false, false, false, false>;
-  static SmemLimit limit_cu, limit_unit, limit_ordered, limit_early, limit_window;
-  SmemLimit& limit = windowed  ? limit_window
-                     : unitq   ? limit_unit
+  auto kernel = unitq     ? decode_mma_kernel<D, SPW, MINB, true, false, false>
+                : ordered ? decode_mma_kernel<D, SPW, MINB, false, true, false>
+                : early   ? decode_mma_kernel<D, SPW, MINB, false, false, true>
+                          : decode_mma_kernel<D, SPW, MINB, false, false, false>;
+  static SmemLimit limit_cu, limit_unit, limit_ordered, limit_early;
+  SmemLimit& limit = unitq     ? limit_unit
                      : ordered ? limit_ordered
                      : early   ? limit_early
                                : limit_cu;
@@ -744,7 +658,6 @@ cudaError_t launch_decode_mma_d(const AttnParams& p, const CUtensorMap& kv_map,
   }
   cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, kv_map, p);
   if (e != cudaSuccess || p.num_parts < 2) return e;
-  if (windowed) return launch_merge_rows(p, stream);
   // few partitions: a warp per row; many: eight warps split a row's
   cudaLaunchConfig_t mcfg = cfg;
   mcfg.dynamicSmemBytes = 0;

@@ -16,7 +16,8 @@ namespace pkv {
 // process may drive several GPUs from several host threads).
 class SmemLimit {
  public:
-  cudaError_t ensure(const void* func, int bytes) {
+  // carveout >= 0: the preferred share of an SM's memory that is shared memory, in %.
+  cudaError_t ensure(const void* func, int bytes, int carveout = -1) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -25,6 +26,8 @@ class SmemLimit {
     std::lock_guard<std::mutex> lock(mu_);
     if (done_[dev].load(std::memory_order_relaxed)) return cudaSuccess;
     e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && carveout >= 0)
+      e = cudaFuncSetAttribute(func, cudaFuncAttributePreferredSharedMemoryCarveout, carveout);
     if (e == cudaSuccess) done_[dev].store(true, std::memory_order_release);
     return e;
   }
@@ -129,9 +132,10 @@ struct AttnParams {
   int32_t window, num_sink;
   int32_t out_bf16;
   const float* scales;
-  // their split-KV partials: row (request i, query j, head h) of partition c is
-  // ((c * num_seqs + i) * ws_q + j) * H + h of ws_out and ws_lse
-  int32_t ws_q;
+  // their decode grid (decode_rows.cu): the shares that the contexts are cut into;
+  // with whole_segments no context is divided. ws_out: the pieces of divided
+  // contexts, ws_lse: where the shares begin
+  int32_t num_shares, whole_segments;
 };
 
 // The keys that the queries of one request see, in units of `tile` keys: the
@@ -180,12 +184,15 @@ int32_t attention_with_scratch(float* out, float* out_lse, const void* q, const 
 cudaError_t launch_decode_mma(const AttnParams& p, const CUtensorMap& kv_map,
                               cudaStream_t stream);
 
-// The decode kernel of an 8-bit pool (requests of up to decode_max_q queries).
-// `kv_map` views the pool as [Hkv][2*NB*BS rows][D] bytes with a box of {D, 16,
-// 1}, swizzled by its rows' length. Split requests are merged by a second grid.
-cudaError_t launch_decode_fp8(const AttnParams& p, const CUtensorMap& kv_map, cudaStream_t stream);
-// The merge grid of launch_decode_fp8 and of the windowed decode grid.
-cudaError_t launch_merge_rows(const AttnParams& p, cudaStream_t stream);
+// The decode kernel of the calls with a window or an 8-bit pool (requests of up to
+// decode_max_q queries). `kv_map`: of a bf16 pool as for launch_decode_mma, of an
+// 8-bit one encode_kv8_view. Divided contexts are joined by a second grid, unless
+// p.whole_segments.
+cudaError_t launch_decode_rows(const AttnParams& p, const CUtensorMap& kv_map, cudaStream_t stream);
+// Bytes of its pieces and cuts (which start at *cuts) for requests of up to
+// max_rows (query, head) rows.
+size_t decode_rows_workspace(int32_t num_kv_heads, int32_t max_rows, int32_t head_dim, bool eight,
+                             size_t* cuts);
 
 // Chunked-prefill kernel (query_len > 1 requests), tcgen05 tensor cores.
 // `q_map`: q as [T][H][D] with a box of {64, G, 128/G}, 128-byte swizzle.

@@ -334,10 +334,9 @@ PyObject* qk_norm_rope_kv_cache_write(PyObject*, PyObject* const* a, Py_ssize_t 
 
 // q, kv_pool, kv_scales (None: the pool is bf16), block_table, cu_seqlens,
 // seq_lens, max_query_len, max_seq_len, window, num_sink, out, out_lse, scale
-// (None: 1 / sqrt(head_dim)), partition_size, workspace, dev_status, stream;
-// returns out
+// (None: 1 / sqrt(head_dim)), workspace, dev_status, stream; returns out
 PyObject* window_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 17, [&]() -> PyObject* {
+  return guarded(n, 16, [&]() -> PyObject* {
     Call c;
     const bool eight = a[2] != Py_None;
     const at::Tensor& pool = eight ? c.kv_pool8(a[1], a[2]) : c.kv_pool(a[1]);
@@ -349,7 +348,6 @@ PyObject* window_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t max_q = small(to_int(a[6])), max_len = small(to_int(a[7]));
     const int32_t window = small(to_int(a[8])), sink = small(to_int(a[9]));
     const float scale = a[12] == Py_None ? (float)(1.0 / std::sqrt((double)d)) : to_float(a[12]);
-    const int32_t part = small(to_int(a[13]));
     at::Tensor made;
     bool f32 = false;
     if (a[10] == Py_None) {
@@ -367,25 +365,25 @@ PyObject* window_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         throw Refused{PyExc_ValueError, "out_lse must be [num_tokens, num_heads]"};
       lse = ptr<float>(l);
     }
-    int32_t* status = c.ints(a[15], "dev_status", -1);
+    int32_t* status = c.ints(a[14], "dev_status", -1);
     // scratch for the call alone, where none is given (work of the current stream)
     at::Tensor scratch;
     void* ws = nullptr;
     size_t bytes = 0;
-    if (a[14] == Py_None) {
+    if (a[13] == Py_None) {
       if (t > 0) bytes = pkv_window_attention_workspace_size(
-          small(b), max_q, small(h), small(hkv), small(d), max_len, window, sink, part, eight);
+          max_q, small(h), small(hkv), small(d), max_len, window, sink, eight);
       if (bytes > 0) {
         scratch = new_output({(int64_t)bytes}, q.device(), at::kByte);
         ws = ptr(scratch);
       }
     } else {
-      const at::Tensor& w = c.dense(a[14], "workspace", at::kByte, 1);
+      const at::Tensor& w = c.dense(a[13], "workspace", at::kByte, 1);
       ws = ptr(w);
       bytes = (size_t)w.size(0);
     }
     const char* what = eight ? "paged_attention_varlen_fp8" : "paged_attention_varlen_window";
-    run(what, c.device, a[16], [&](void* stream) {
+    run(what, c.device, a[15], [&](void* stream) {
       const int32_t* tab = ptr<int32_t>(table);
       const int32_t* cu = ptr<int32_t>(THPVariable_Unpack(a[4]));
       const int32_t* lens = ptr<int32_t>(THPVariable_Unpack(a[5]));
@@ -394,11 +392,11 @@ PyObject* window_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
             ptr(out), f32, lse, ptr(q), ptr(pool), ptr<float>(THPVariable_Unpack(a[2])), tab,
             small(table.size(1)), cu, lens, small(b), small(t), max_q, max_len, small(h),
             small(hkv), small(d), small(pool.size(2)), small(pool.size(1)), window, sink, scale,
-            part, ws, bytes, status, stream);
+            ws, bytes, status, stream);
       return pkv_paged_attention_varlen_window(
           ptr(out), f32, lse, ptr(q), ptr(pool), tab, small(table.size(1)), cu, lens, small(b),
           small(t), max_q, max_len, small(h), small(hkv), small(d), small(pool.size(2)),
-          small(pool.size(1)), window, sink, scale, part, ws, bytes, status, stream);
+          small(pool.size(1)), window, sink, scale, ws, bytes, status, stream);
     });
     if (a[10] == Py_None) return THPVariable_Wrap(made);
     Py_INCREF(a[10]);

@@ -54,7 +54,7 @@
 //     that some query of it sees, the mask has a lower border), and the same over
 //     an 8-bit pool: K and V tiles land as e4m3 and the converter warps make bf16
 //     (K) and fp16 (V) of them in place, both exactly; a block's two scales act on
-//     the scores, as in decode_fp8.cu;
+//     the scores, as in decode_rows.cu;
 //   * every wait is bounded; on a timeout the CTA drains its copies and
 //     MMAs, frees its TMEM and leaves with PKV_DEV_TIMEOUT set.
 #include <math.h>
@@ -1185,7 +1185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   if (u[32 * ch + 2 * c + 1] == 0xff800000u) p1 = 0.f;
                 }
                 pk[c] = pack_f16x2(p0, p1);
-                // (before the rounding: see decode_fp8.cu)
+                // (before the rounding: see decode_rows.cu)
                 ra += p0;
                 rb += p1;
               }

@@ -156,14 +156,22 @@ def test_single_token_groups(eight, h, hkv):
 
 
 @BOTH
-@pytest.mark.parametrize("part", [16, 48, 256, 0, -1])
 @pytest.mark.parametrize("window,sink", [(0, 0), (700, 40), (333, 0)])
-def test_partitions(eight, part, window, sink):
-    s = Step([1500, 20, 1, 777], [1, 1, 1, 1], 8, 2, 128, 16, window, sink, eight, seed=part + 9)
-    s.check(*s.call(partition_size=part))
-    # several queries are split too
-    s = Step([1500, 20, 3, 777], [5, 2, 3, 8], 8, 2, 64, 16, window, sink, eight, seed=part + 10)
-    s.check(*s.call(partition_size=part))
+@pytest.mark.parametrize("times", [1, 9, 70])
+def test_shares(eight, window, sink, times):
+    # contexts in one share, cut by several, and many in one
+    case([1500, 20, 1, 777] * times, [1, 1, 1, 1] * times, 8, 2, 128, 16, window, sink, eight,
+         seed=9)
+    # several queries are divided too
+    case([1500, 20, 3, 777] * times, [5, 2, 3, 8] * times, 8, 2, 64, 16, window, sink, eight,
+         seed=10)
+
+
+@BOTH
+def test_one_long_context(eight):
+    # every share cuts the one context; requests without queries before and behind it
+    case([40, 20000, 5], [0, 1, 0], 8, 1, 64, 64, 0, 0, eight, seed=11)
+    case([20000], [3], 2, 1, 128, 64, 0, 0, eight, seed=12)
 
 
 @BOTH
@@ -334,13 +342,13 @@ def test_rows_behind_the_last_request_stay(eight):
 @pytest.mark.parametrize("ql", [[1, 1, 1], [1, 70, 3]])
 def test_streams_workspaces_and_graphs(eight, ql):
     s = Step([900, 300, 40], ql, 8, 2, 128, 16, 200, 4, eight, seed=14)
-    want, wl = s.call(partition_size=64)
+    want, wl = s.call()
     a = (s.q, s.pool) + ((s.scales,) if eight else ()) + (
         i32(s.table), i32(s.cu), i32(s.lens), max(ql), 900)
     f = pkv.paged_attention_varlen_fp8 if eight else pkv.paged_attention_varlen_window
-    w = (lambda **k: f(*a, window=200, num_sink=4, partition_size=64, **k)) if eight else (
-        lambda **k: f(*a, 200, num_sink=4, partition_size=64, **k))
-    need = pkv.window_attention_workspace_size(3, max(ql), 8, 2, 128, 900, 200, 4, 64, eight)
+    w = (lambda **k: f(*a, window=200, num_sink=4, **k)) if eight else (
+        lambda **k: f(*a, 200, num_sink=4, **k))
+    need = pkv.window_attention_workspace_size(max(ql), 8, 2, 128, 900, 200, 4, eight)
     # a workspace of anything, within guards
     buf, ws = guarded((need,), torch.uint8)
     ws.fill_(0xee)
