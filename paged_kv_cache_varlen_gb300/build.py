@@ -25,11 +25,12 @@ LIBRARY = os.path.join(PKG, "libpkv.so")
 MARSHAL = os.path.join(PKG, "_marshal.so")
 MARSHAL_SOURCE = "marshal.cpp"
 SOURCES = ["kv_write.cu", "decode_mma.cu", "decode_rows.cu", "merge.cu", "prefill_tc.cu",
-           "copy_blocks.cu", "rope_write.cu", "norm_write.cu", "key_weights.cu",
-           "key_weights_tc.cu", "evict.cu", "api.cpp", "budget_api.cpp", "cache8_api.cpp",
+           "prefill_rows.cu", "copy_blocks.cu", "rope_write.cu", "norm_write.cu",
+           "key_weights.cu", "key_weights_tc.cu", "evict.cu", "api.cpp", "budget_api.cpp", "cache8_api.cpp",
            "window_api.cpp", "api_noalloc.cu", "block_manager.cpp"]
 HEADERS = [os.path.join(CSRC, "common.cuh"), os.path.join(CSRC, "launch.h"),
            os.path.join(CSRC, "key_weights.cuh"), os.path.join(CSRC, "rope.cuh"),
+           os.path.join(CSRC, "wait.cuh"),
            os.path.join(ROOT, "include", "pkv.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",

@@ -44,6 +44,7 @@
 #include <stddef.h>
 
 #include "key_weights.cuh"
+#include "wait.cuh"
 
 #ifdef PKV_TEST_HOLD_ARRIVAL
 // Test builds only: while set, epilogue warp 0 of CTA 0 withholds its release
@@ -192,17 +193,6 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
-}
-
-// True for one lane of the (converged) warp, in a form that tells the compiler
-// so: the tcgen05 instructions then take their operands from uniform
-// registers without a loop over lanes.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t one;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}"
-      : "=r"(one));
-  return one != 0;
 }
 
 // Where a column's lse stands in its stage: the four columns 8 c + 2 q + e

@@ -207,8 +207,14 @@ cudaError_t launch_prefill(const AttnParams& p, const CUtensorMap& q_map,
 // Whether the prefill kernel's shared memory (its K/V/Q stages plus the work
 // list of num_seqs requests) fits the 227 KB a CTA may have: up to 8575
 // requests at head_dim 128, 33151 at 64. False for other head dims.
-// (`eight`: of the 8-bit pool's form).
-bool prefill_fits(int32_t num_seqs, int32_t head_dim, bool eight = false);
+bool prefill_fits(int32_t num_seqs, int32_t head_dim);
+
+// The same of the calls with a window or an 8-bit pool: requests of more than
+// decode_max_q queries. `kv_map`: of a bf16 pool as for launch_prefill, of an 8-bit
+// one encode_kv8_view. p.sched[0] is zero before the launch.
+cudaError_t launch_prefill_rows(const AttnParams& p, const CUtensorMap& q_map,
+                                const CUtensorMap& kv_map, cudaStream_t stream);
+bool prefill_rows_fits(int32_t num_seqs, int32_t head_dim);
 
 // Shared-prefix (cascade) merge: row r of out (num_rows = B * H rows of
 // head_dim) from the tail partial (slot 0) and the prefix segments (slots

@@ -1,0 +1,1031 @@
+// prefill_rows.cu -- paged attention for requests of more than 32 (query, head) rows
+// through a window, over a bf16 pool or over one held in 8 bits, on the
+// 5th-generation tensor cores (tcgen05). The formulas stand in decode_rows.cu.
+//
+//   * persistent CTAs, one per SM; a work item is (request, KV head, two query
+//     tiles A and B of 128 rows, 128 / G queries of G heads each), taken in the
+//     order of the heaviest requests from a ticket counter in the workspace;
+//   * the keys that some query of an item sees, its sinks' 16-key chunks and then
+//     its window's, are numbered through: a tile is consecutive ones of them, wherever
+//     they lie in the context, so that a few sinks cost a quarter of a tile and a
+//     window no more than its ends. In these numbers a row sees the columns
+//     [low, lim] and those before num_sink;
+//   * S = Q K^T over 64 keys (bf16), O += P V (fp16 P and V), fp32 accumulators in
+//     tensor memory: two S and one O of both query tiles fill its 512 columns, P
+//     (fp16) lies over the first half of its S;
+//   * one issuing thread a query tile: S(0), S(1), then PV(j), S(j + 2): a softmax
+//     goes from one tile to the next without waiting for products;
+//   * a softmax thread owns a row: 64 scores in registers, one pass;
+//   * K and V arrive by TMA in 16-key boxes into two-stage rings. V becomes fp16 in
+//     place (four converter warps); at 8 bits K becomes bf16 and V fp16, both
+//     exactly, and a block's two scales act on the scores;
+//   * every wait is bounded; on a timeout the CTA drains its copies and products,
+//     frees its tensor memory and leaves with PKV_DEV_TIMEOUT set.
+#include <math.h>
+
+#include "common.cuh"
+#include "launch.h"
+#include "wait.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kBM = 128;      // rows of a query tile
+constexpr int kBN = 128;      // keys of a K stage
+constexpr int kSub = 16;      // keys of a TMA box
+constexpr int kBoxes = kBN / kSub;
+constexpr int kNS = 2;        // stages of the K ring
+constexpr int kHalf = 64;     // keys of a score tile, and of a V stage: a stage is copied,
+                              // converted and held until both query tiles have used it
+constexpr int kHalfBoxes = kHalf / kSub;
+constexpr int kVS = 5;        // stages of the V ring
+constexpr int kThreads = 512;
+// warps: 0-3 softmax of A, 4-7 of B, 8-11 converters, 12 and 13 the products of A
+// and of B, 14 tickets and K, 15 Q and V
+constexpr int kConvWarp0 = 8, kMmaWarp = 12, kKWarp = 14, kVWarp = 15;
+constexpr int kConverters = 128;
+// registers a thread: launched with 128; the softmax warpgroups take more of them
+constexpr int kSoftmaxRegs = 152, kOtherRegs = 104;
+static_assert(2 * kSoftmaxRegs + 2 * kOtherRegs == 4 * (65536 / kThreads),
+              "the register split adds up to the launch's registers");
+constexpr uint32_t kTmemCols = 512;
+constexpr int kRing = 4;  // items announced ahead of their readers
+constexpr int kItemReaders = 8 + 4 + 3;  // softmax and converter warps, products, V
+constexpr int kSortMax = 2048;
+constexpr float kRescaleThreshold = 8.f;
+constexpr uint32_t kFull = 0xffffffffu;
+constexpr uint32_t kMinusInf = 0xff800000u;
+
+constexpr size_t list_ints(int num_seqs) {
+  return (num_seqs <= kSortMax ? 4 : 1) * ((size_t)num_seqs + 1);
+}
+
+template <int D>
+struct Layout {
+  static constexpr int NCH = D / 64;               // 128-byte column chunks of a row
+  static constexpr int CH_BYTES = 128 * 128;
+  static constexpr int TILE_BYTES = NCH * CH_BYTES;
+  static constexpr int VCH_BYTES = kHalf * 128;    // a chunk of a V stage
+  static constexpr int VS_BYTES = NCH * VCH_BYTES;
+  static constexpr int Q_OFF = 0;
+  static constexpr int K_OFF = Q_OFF + 2 * TILE_BYTES;
+  static constexpr int V_OFF = K_OFF + kNS * TILE_BYTES;
+  static constexpr int BAR_OFF = V_OFF + kVS * VS_BYTES;
+  static constexpr int LIST_OFF = BAR_OFF + 640;
+  // one CTA an SM (each takes all of its tensor memory)
+  static size_t bytes(int num_seqs) {
+    const size_t need = 1024 + LIST_OFF + list_ints(num_seqs) * 4;
+    return need > 120 * 1024 ? need : 120 * 1024;
+  }
+  __device__ static constexpr uint32_t s_col(int x) { return 128u * (uint32_t)x; }  // 2 x 64
+  __device__ static constexpr uint32_t o_col(int x) { return 256u + 128u * (uint32_t)x; }
+};
+
+struct Bars {
+  uint64_t q_full[2], q_empty[2];
+  uint64_t k_landed[kNS], k_full[kNS], k_empty[kNS];  // (landed: 8 bits)
+  uint64_t v_landed[kVS], v_full[kVS], v_empty[kVS];
+  uint64_t s_full[2][2];   // S(j) of a query tile is there: [x][j & 1]
+  uint64_t p_ready[2][2];  // P(j) is stored (and O rescaled)
+  uint64_t o_done[2][2];   // PV(j) is done
+  uint64_t o_free[2];      // the item's O has been read
+  uint64_t mma_done;
+  uint64_t item_full[kRing], item_empty[kRing];
+  int32_t item_id[kRing];
+  uint32_t tmem_base;
+  int32_t abort;
+  uint32_t k_mask[kNS], v_mask[kVS];  // boxes of a stage that were loaded
+  int32_t scan[kThreads / 32];
+  float red[2][kThreads / 32];
+};
+static_assert(sizeof(Bars) <= 640, "the barriers fit below the work list");
+
+struct Item {
+  int req, kvh, j0, j1, t0;
+  int n;       // score tiles
+  int shift;   // from a column behind the sinks' to its key
+  int columns; // of the sinks' chunks: columns before it are keys themselves
+  int count;   // 16-key chunks
+  int qpos0;   // position of the request's first query
+  int end;     // columns before it are needed keys
+  int lo_any;  // no query of the item sees columns [num_sink, lo_any)
+
+  __device__ __forceinline__ int key(int column) const {
+    return column < columns ? column : column + shift;
+  }
+};
+
+// Work units (pairs of query tiles, QP queries) of request r: 0 for requests that
+// the decode grid takes; bad lengths flagged by one CTA.
+__device__ __forceinline__ int units_of(const AttnParams& p, int r, int QP, bool flag) {
+  const int32_t t0 = __ldg(p.cu_seqlens + r), t1 = __ldg(p.cu_seqlens + r + 1);
+  const int32_t n = t1 - t0;
+  bool bad = t0 < 0 || t1 < t0 || t1 > p.num_tokens;
+  if (!bad && n <= p.decode_max_q) {
+    if (flag && p.no_decode && n > 0) set_status(p.status, PKV_DEV_BAD_LENGTHS);
+    return 0;
+  }
+  if (!bad) {
+    const int32_t L = __ldg(p.seq_lens + r);
+    bad = n > p.max_query_len || L < n || L > p.max_seq_len || L > p.max_blocks * p.block_size;
+  }
+  if (bad && flag) set_status(p.status, PKV_DEV_BAD_LENGTHS);
+  return bad ? 0 : (n + QP - 1) / QP;
+}
+
+__device__ __forceinline__ int tiles_of(const AttnParams& p, int first, int end) {
+  return (visible_units(p.window, p.num_sink, first, end, kSub).count + kHalfBoxes - 1) /
+         kHalfBoxes;
+}
+
+// Exclusive prefix sum of one value a thread; *total gets the sum. All threads.
+__device__ __forceinline__ int block_scan(int v, int32_t* scan, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(kFull, incl, o);
+    if (lane >= o) incl += t;
+  }
+  if (lane == 31) scan[warp] = incl;
+  __syncthreads();
+  int base = 0, all = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) base += scan[w];
+    all += scan[w];
+  }
+  __syncthreads();
+  *total = all;
+  return base + incl - v;
+}
+
+// The units in the order that they are handed out: position k is request
+// order[k] (null: k), units before it pref[k], pref[n] all.
+struct List {
+  const int *order, *pref;
+  int n;
+};
+
+// Requests with work, those with the most tiles in a unit first (batches of more
+// than kSortMax requests: as they come). All threads.
+__device__ __forceinline__ List build_list(const AttnParams& p, int* base, int32_t* scan, int QP,
+                                           int* total) {
+  const int B = p.num_seqs, tid = threadIdx.x;
+  const bool flag = blockIdx.x == 0;
+  const bool sorted = B <= kSortMax;
+  int* pref = base;
+  int* order = base + (B + 1);
+  int* cand = order + (B + 1);
+  int* weight = cand + (B + 1);
+  int n = B;
+  if (sorted) {
+    const int per = (B + kThreads - 1) / kThreads;
+    const int r0 = min(B, tid * per), r1 = min(B, r0 + per);
+    int count = 0;
+    for (int r = r0; r < r1; ++r) {
+      weight[r] = 0;
+      if (units_of(p, r, QP, flag) == 0) continue;
+      const int32_t L = __ldg(p.seq_lens + r);
+      weight[r] = tiles_of(p, max(0, L - QP), L);
+      ++count;
+    }
+    int at = block_scan(count, scan, &n);
+    for (int r = r0; r < r1; ++r)
+      if (weight[r] > 0) cand[at++] = r;
+    __syncthreads();
+    for (int i = tid; i < n; i += kThreads) {
+      const int r = cand[i], w = weight[r];
+      int rank = 0;
+      for (int j = 0; j < n; ++j) {
+        const int w2 = weight[cand[j]];
+        rank += w2 > w || (w2 == w && j < i);
+      }
+      order[rank] = r;
+    }
+    __syncthreads();
+  }
+  const int per = (n + kThreads - 1) / kThreads;
+  const int k0 = min(n, tid * per), k1 = min(n, k0 + per);
+  int sum = 0;
+  for (int k = k0; k < k1; ++k) sum += units_of(p, sorted ? order[k] : k, QP, flag && !sorted);
+  int run = block_scan(sum, scan, total);
+  for (int k = k0; k < k1; ++k) {
+    pref[k] = run;
+    run += units_of(p, sorted ? order[k] : k, QP, false);
+  }
+  if (tid == 0) pref[n] = *total;
+  __syncthreads();
+  return List{sorted ? order : nullptr, pref, n};
+}
+
+// The split of the SMs in a call with both kinds of request: cycles that a tile pair
+// takes here, and bytes of the pool that an SM of the decode grid reads in a cycle.
+constexpr float kPairCycles = 1500.f;
+constexpr float kDecodeBytesPerCycle = 40.f;
+
+// CTAs of this grid that take work when a decode grid shares the call: its work's
+// share of p.shared_sms by the estimate above. All threads.
+template <bool EIGHT>
+__device__ __noinline__ int own_share(const AttnParams& p, int QP, float (*red)[kThreads / 32]) {
+  const int B = p.num_seqs;
+  const int per = (B + kThreads - 1) / kThreads;
+  const int r0 = min(B, (int)threadIdx.x * per), r1 = min(B, r0 + per);
+  float pairs = 0.f, keys = 0.f;
+  for (int r = r0; r < r1; ++r) {
+    const int32_t n = __ldg(p.cu_seqlens + r + 1) - __ldg(p.cu_seqlens + r);
+    const int32_t L = __ldg(p.seq_lens + r);
+    if (n < 1 || L < n || L > p.max_seq_len) continue;
+    if (n <= p.decode_max_q) {
+      keys += 16.f * (float)visible_units(p.window, p.num_sink, L - n, L, kSub).count;
+      continue;
+    }
+    for (int j = 0; j < n; j += QP)
+      pairs += (float)tiles_of(p, L - n + j, L - n + min(n, j + QP));
+  }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    pairs += __shfl_xor_sync(kFull, pairs, o);
+    keys += __shfl_xor_sync(kFull, keys, o);
+  }
+  if (lane == 0) {
+    red[0][warp] = pairs;
+    red[1][warp] = keys;
+  }
+  __syncthreads();
+  float pt = 0.f, kt = 0.f;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    pt += red[0][w];
+    kt += red[1][w];
+  }
+  __syncthreads();
+  const float a = kt * (float)(p.num_kv_heads * p.head_dim * (EIGHT ? 2 : 4)) / kDecodeBytesPerCycle;
+  const float b = pt * (float)p.num_kv_heads * kPairCycles;
+  const int S = p.shared_sms;
+  const int keep = a + b > 0.f ? S - (int)((float)S * a / (a + b) + 0.5f) : S;
+  return max(1, min(S, keep));
+}
+
+__device__ __forceinline__ Item item_of(const AttnParams& p, const List& list, int QP, int it) {
+  Item d;
+  const int u = it / p.num_kv_heads;
+  d.kvh = it - u * p.num_kv_heads;
+  int lo = 0, hi = list.n;  // largest lo with pref[lo] <= u
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (list.pref[mid] <= u)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  d.req = list.order ? list.order[lo] : lo;
+  d.t0 = __ldg(p.cu_seqlens + d.req);
+  const int n = __ldg(p.cu_seqlens + d.req + 1) - d.t0;
+  d.qpos0 = __ldg(p.seq_lens + d.req) - n;
+  const int unit = (n + QP - 1) / QP - 1 - (u - list.pref[lo]);  // later (heavier) units first
+  d.j0 = unit * QP;
+  d.j1 = min(n, d.j0 + QP);
+  const int first = d.qpos0 + d.j0, end = d.qpos0 + d.j1;
+  const Visible v = visible_units(p.window, p.num_sink, first, end, kSub);
+  d.shift = (v.low - v.sink) * kSub;
+  d.columns = v.sink * kSub;
+  d.count = v.count;
+  d.n = (v.count + kHalfBoxes - 1) / kHalfBoxes;
+  d.end = end - d.shift;
+  d.lo_any = max(0, first - p.window + 1) - d.shift;
+  return d;
+}
+
+// The K warp takes the next ticket and announces it in a small ring; every other
+// role reads the same sequence from there (as in prefill_tc.cu).
+__device__ __forceinline__ int take_item(Bars* bars, const AttnParams& p, int total, int k,
+                                         volatile int32_t* abort) {
+  const int slot = k % kRing;
+  int it = -1;
+  if (k < kRing ||
+      short_wait(smem_addr(&bars->item_empty[slot]), ((k / kRing) - 1) & 1, p.status, abort)) {
+    const int t = atomicAdd(p.sched, 1);
+    it = t < total ? t : -1;
+  }
+  *reinterpret_cast<volatile int32_t*>(&bars->item_id[slot]) = it;
+  mbar_arrive(smem_addr(&bars->item_full[slot]));
+  return it;
+}
+__device__ __forceinline__ int read_item(Bars* bars, const AttnParams& p, int k,
+                                         volatile int32_t* abort) {
+  const int slot = k % kRing;
+  int it = -1;
+  if (short_wait(smem_addr(&bars->item_full[slot]), (k / kRing) & 1, p.status, abort))
+    it = *reinterpret_cast<volatile int32_t*>(&bars->item_id[slot]);
+  mbar_arrive(smem_addr(&bars->item_empty[slot]));
+  return it;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                      uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+               "r"(d)
+               : "memory");
+}
+
+// The lowest n bits (none below 0, all from 32 on).
+__device__ __forceinline__ uint32_t bits_below(int n) {
+  uint32_t r;
+  asm("shl.b32 %0, %1, %2;" : "=r"(r) : "r"(~0u), "r"(max(n, 0)));  // (0 from 32 on)
+  return ~r;
+}
+
+// Two e4m3 values (the low or the high half of w) as fp16x2, exactly.
+__device__ __forceinline__ uint32_t e4m3_lo(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
+      : "=r"(r)
+      : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3_hi(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}"
+      : "=r"(r)
+      : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t h) {
+  float a, b;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+      "cvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
+      : "=f"(a), "=f"(b)
+      : "r"(h));
+  return pack_bf16x2(a, b);
+}
+
+// 64 rows of a tile, whose boxes were loaded (a bit of `load` each), into the 16-bit
+// rows that the products read; 128 threads. Rows not loaded, behind the needed keys or
+// hidden from every query ([h0, h1)) become zeros. CH: from one 128-byte chunk of the
+// rows to the next.
+// bf16 to fp16 in place (exact below 2^16; `most` gathers the largest magnitudes, per
+// half of a word, NaN above all).
+template <int D, int CH>
+__device__ __forceinline__ void convert_bf16(uint32_t base, int ct, uint32_t load, int end, int h0,
+                                             int h1, uint32_t& most) {
+  constexpr int RP = D / 8;                        // 16-byte pieces of a row
+  constexpr int N = kHalf * RP / kConverters;      // pieces of a thread
+  constexpr int STEP = kConverters / RP;           // their rows are so far apart
+  const bool all =
+      end >= kHalf && load == (1u << kHalfBoxes) - 1 && (h0 >= kHalf || h1 <= 0 || h0 >= h1);
+  const int pc = ct % RP, k0 = ct / RP;
+  const uint32_t col = base + (pc >> 3) * CH;
+  uint4 v[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const int k = k0 + STEP * e;
+    v[e] = lds16(col + k * 128 + (((uint32_t)(pc & 7) ^ (uint32_t)(k & 7)) << 4));
+  }
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const int k = k0 + STEP * e;
+    uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
+    if (!all && !(k < end && ((load >> (k / kSub)) & 1u) && (k < h0 || k >= h1)))
+      w[0] = w[1] = w[2] = w[3] = 0u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      w[j] = pack_f16x2(bf16_lo(w[j]), bf16_hi(w[j]));
+      asm("{\n\t.reg .b32 a;\n\tabs.f16x2 a, %1;\n\tmax.NaN.f16x2 %0, %0, a;\n\t}"
+          : "+r"(most)
+          : "r"(w[j]));
+    }
+    sts16(col + k * 128 + (((uint32_t)(pc & 7) ^ (uint32_t)(k & 7)) << 4), w[0], w[1], w[2], w[3]);
+  }
+}
+// e4m3 in place: box b landed at 2048 b bytes, its rows D bytes apart, swizzled by
+// their length, so that a box lies where the same warp writes its 16 rows: it reads
+// them, then writes them. To bf16 (BF) or fp16.
+template <int D, bool BF, int CH>
+__device__ __forceinline__ void convert_e4m3(uint32_t base, int ct, uint32_t load, int end, int h0,
+                                             int h1) {
+  constexpr int NP = D / 16;   // 16-byte pieces of a row
+  constexpr int N = NP / 2;    // pieces of a thread: 16 rows of them, 32 lanes
+  const int box = ct >> 5, lane = ct & 31;
+  uint4 w[N];
+  // piece e of a lane: 8 lanes take one piece of 8 rows (different bank groups)
+  auto row = [&](int e) { return (lane & 7) + 8 * (e & 1); };
+  auto part = [&](int e) { return (lane >> 3) + 4 * (e >> 1); };
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const int r = row(e), k = box * kSub + r, pc = part(e);
+    const uint32_t at = base + box * 2048 + r * D +
+                        ((pc ^ (D == 128 ? (r & 7) : ((r >> 1) & 3))) << 4);
+    w[e] = make_uint4(0u, 0u, 0u, 0u);
+    if (k < end && ((load >> box) & 1u) && (k < h0 || k >= h1)) w[e] = lds16(at);
+  }
+  __syncwarp();
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const int r = row(e), pc = part(e);
+    uint32_t x[8] = {e4m3_lo(w[e].x), e4m3_hi(w[e].x), e4m3_lo(w[e].y), e4m3_hi(w[e].y),
+                     e4m3_lo(w[e].z), e4m3_hi(w[e].z), e4m3_lo(w[e].w), e4m3_hi(w[e].w)};
+    if (BF)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = f16x2_to_bf16x2(x[i]);
+    const uint32_t to = base + (pc >> 2) * CH + box * 2048 + r * 128;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      sts16(to + ((((pc & 3) * 2 + h) ^ (r & 7)) << 4), x[4 * h], x[4 * h + 1], x[4 * h + 2],
+            x[4 * h + 3]);
+  }
+}
+
+template <int R>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+template <int D, bool EIGHT>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_rows_kernel(const __grid_constant__ CUtensorMap q_map,
+                        const __grid_constant__ CUtensorMap kv_map, const AttnParams p) {
+  using Lay = Layout<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  Bars* bars = reinterpret_cast<Bars*>(smem + Lay::BAR_OFF);
+  griddep_wait();
+  griddep_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = p.num_heads / p.num_kv_heads;
+  const int QT = kBM / G;  // queries of a tile (rows G QT .. 127 belong to none)
+  const int QP = 2 * QT;   // queries of an item
+
+  if (threadIdx.x == 0) {
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(smem_addr(&bars->q_full[x]), 1);
+      mbar_init(smem_addr(&bars->q_empty[x]), 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(smem_addr(&bars->s_full[x][b]), 1);
+        mbar_init(smem_addr(&bars->p_ready[x][b]), 4);
+        mbar_init(smem_addr(&bars->o_done[x][b]), 1);
+      }
+      mbar_init(smem_addr(&bars->o_free[x]), 4);
+    }
+    for (int s = 0; s < kNS; ++s) {
+      mbar_init(smem_addr(&bars->k_landed[s]), 1);
+      mbar_init(smem_addr(&bars->k_full[s]), EIGHT ? kConverters : 1);
+      mbar_init(smem_addr(&bars->k_empty[s]), 2);
+    }
+    for (int s = 0; s < kVS; ++s) {
+      mbar_init(smem_addr(&bars->v_landed[s]), 1);
+      mbar_init(smem_addr(&bars->v_full[s]), kConverters);
+      mbar_init(smem_addr(&bars->v_empty[s]), 2);
+    }
+    mbar_init(smem_addr(&bars->mma_done), 2);
+    for (int k = 0; k < kRing; ++k) {
+      mbar_init(smem_addr(&bars->item_full[k]), 1);
+      mbar_init(smem_addr(&bars->item_empty[k]), kItemReaders);
+    }
+    bars->abort = 0;
+    fence_barrier_init();
+  }
+  int units = 0;
+  const List list = build_list(p, reinterpret_cast<int*>(smem + Lay::LIST_OFF), bars->scan, QP,
+                               &units);  // (synchronises)
+  const int total = units * p.num_kv_heads;
+  const int active = p.shared_sms > 0 ? own_share<EIGHT>(p, QP, bars->red) : (int)gridDim.x;
+  if ((int)blockIdx.x >= min(total, active)) return;  // uniform; nothing allocated yet
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_addr(&bars->tmem_base), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  volatile int32_t* abort = &bars->abort;
+  const uint32_t q_s = smem_addr(smem + Lay::Q_OFF);
+  const uint32_t k_s = smem_addr(smem + Lay::K_OFF);
+  const uint32_t v_s = smem_addr(smem + Lay::V_OFF);
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return short_wait(smem_addr(bar), parity, p.status, abort);
+  };
+  // a warp's wait, by every lane; by one lane
+  auto all_wait = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(kFull, wait(bar, parity)) != 0;
+  };
+  auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
+    int w = 1;
+    if (lane == 0) w = wait(bar, parity);
+    return __shfl_sync(kFull, w, 0) != 0;
+  };
+  auto next_item = [&](int k) {
+    int it = -1;
+    if (lane == 0) it = read_item(bars, p, k, abort);
+    return __shfl_sync(kFull, it, 0);
+  };
+
+  if (warp >= kConvWarp0) {
+    fewer_registers<kOtherRegs>();
+    if (warp == kKWarp || warp == kVWarp) {
+      // ===== copies of K (and the tickets); of Q and V =====
+      const bool vrole = warp == kVWarp;
+      const int32_t first_row = vrole ? p.num_blocks * p.block_size : 0;
+      const uint32_t ring = vrole ? v_s : k_s;
+      uint64_t* empty = vrole ? bars->v_empty : bars->k_empty;
+      uint64_t* landed = vrole ? bars->v_landed : EIGHT ? bars->k_landed : bars->k_full;
+      uint32_t* mask = vrole ? bars->v_mask : bars->k_mask;
+      // a stage: a tile of K, half a tile of V
+      const int boxes = vrole ? kHalfBoxes : kBoxes, stages = vrole ? kVS : kNS;
+      const uint32_t stage_bytes = vrole ? Lay::VS_BYTES : Lay::TILE_BYTES;
+      const uint32_t chunk_bytes = vrole ? Lay::VCH_BYTES : Lay::CH_BYTES;
+      if (lane == 0) prefetch_tmap(vrole ? &q_map : &kv_map);
+      int st = 0, filled = 0, copied = 0;
+      uint32_t parity = 1;  // of the stage's last release (none before the first lap)
+      bool ok = true, bad_block = false;
+      for (int k = 0; ok; ++k) {
+        int it = -1;
+        if (lane == 0)
+          it = vrole ? read_item(bars, p, k, abort) : take_item(bars, p, total, k, abort);
+        it = __shfl_sync(kFull, it, 0);
+        if (it < 0) break;
+        const Item d = item_of(p, list, QP, it);
+        const int32_t* bt = p.block_table + (int64_t)d.req * p.max_blocks;
+        int32_t row = -1;
+#pragma unroll 1
+        for (int box0 = 0; box0 < d.n * kHalfBoxes; box0 += boxes) {
+          if ((box0 & 31) == 0) {  // the next 32 boxes, one a lane: first row in the pool
+            const int box = box0 + lane;
+            row = -1;
+            if (box < d.count) {
+              const int key = d.key(box * kSub);
+              const int32_t id = __ldg(bt + key / p.block_size);
+              if (id >= 0 && id < p.num_blocks)
+                row = first_row + id * p.block_size + key % p.block_size;
+              else
+                bad_block = true;
+            }
+          }
+          if (filled >= stages) ok = warp_wait(&empty[st], parity);
+          if (!ok) break;
+          const uint32_t load =
+              (__ballot_sync(kFull, row >= 0) >> (box0 & 31)) & ((1u << boxes) - 1);
+          if (lane == 0) {
+            *reinterpret_cast<volatile uint32_t*>(&mask[st]) = load;
+            mbar_arrive_expect_tx(smem_addr(&landed[st]),
+                                  __popc(load) * (EIGHT ? kSub * D : Lay::NCH * kSub * 128));
+          }
+          // a lane a copy: one after the other by one lane they take long enough for
+          // the stages to run dry
+          const int b = lane & (boxes - 1), c = lane / boxes;
+          const int32_t r = __shfl_sync(kFull, row, (box0 & 31) + b);
+          if (r >= 0 && c < (EIGHT ? 1 : Lay::NCH)) {
+            const uint32_t at = ring + st * stage_bytes + b * kSub * 128 + c * chunk_bytes;
+            if (EIGHT)
+              tma_load_3d(at, &kv_map, smem_addr(&landed[st]), 0, r, d.kvh);
+            else
+              tma_load_4d(at, &kv_map, smem_addr(&landed[st]), 0, r, d.kvh, c);
+          }
+          __syncwarp();
+          ++filled;
+          st = st + 1 == stages ? 0 : st + 1;
+          parity ^= st == 0 ? 1u : 0u;
+          if (!vrole || box0 != min(1, d.n - 1) * kHalfBoxes) continue;
+          // behind the item's first two V tiles (whose stages are free by then): Q, free
+          // when the last scores of the item before are there. Rows behind the last
+          // token read as zeros, rows of the next request belong to no valid output row
+#pragma unroll 1
+          for (int x = 0; ok && x < 2; ++x) {
+            if (k > 0) ok = warp_wait(&bars->q_empty[x], (k - 1) & 1);
+            if (!ok) break;
+            ++copied;
+            if (lane == 0) {
+              mbar_arrive_expect_tx(smem_addr(&bars->q_full[x]), Lay::NCH * QT * G * 128);
+#pragma unroll 1
+              for (int c = 0; c < Lay::NCH; ++c)
+                tma_load_3d(q_s + x * Lay::TILE_BYTES + c * Lay::CH_BYTES, &q_map,
+                            smem_addr(&bars->q_full[x]), c * 64, d.kvh * G, d.t0 + d.j0 + x * QT);
+            }
+          }
+          if (!ok) break;
+        }
+      }
+      if (bad_block) set_status(p.status, PKV_DEV_BAD_BLOCK);
+      // our copies, and the arrivals that they trigger, land before the CTA can exit
+      if (lane == 0) {
+        for (int x = 0; x < 2; ++x)  // copies of Q: A's of items 0, 1 .., B's
+          if (copied > x)
+            short_wait(smem_addr(&bars->q_full[x]), ((copied - x + 1) / 2 - 1) & 1, nullptr);
+        for (int g = max(0, filled - stages); g < filled; ++g)
+          short_wait(smem_addr(&landed[g % stages]), (g / stages) & 1, nullptr);
+      }
+    } else if (warp < kMmaWarp) {
+      // ===== converters =====
+      const int ct = threadIdx.x - kConvWarp0 * 32;
+      uint32_t most = 0;  // of V, as fp16
+      int gt = 0, vst = 0;
+      uint32_t vparity = 0;
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        const int it = next_item(k);
+        if (it < 0) break;
+        const Item d = item_of(p, list, QP, it);
+#pragma unroll 1
+        for (int j = 0; ok && j < d.n; ++j) {
+          const int c0 = j * kHalf;
+          if (EIGHT && (j & 1) == 0) {
+            const int st = gt % kNS;
+            ok = warp_wait(&bars->k_landed[st], (gt / kNS) & 1);
+            if (!ok) break;
+            const uint32_t load = *reinterpret_cast<volatile uint32_t*>(&bars->k_mask[st]);
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h)
+              convert_e4m3<D, true, Lay::CH_BYTES>(
+                  k_s + st * Lay::TILE_BYTES + h * kHalf * 128, ct, load >> (h * kHalfBoxes),
+                  d.end - c0 - h * kHalf, p.num_sink - c0 - h * kHalf, d.lo_any - c0 - h * kHalf);
+            fence_proxy_async_smem();
+            mbar_arrive(smem_addr(&bars->k_full[st]));
+            ++gt;
+          }
+          ok = warp_wait(&bars->v_landed[vst], vparity);
+          if (!ok) break;
+          const uint32_t load = *reinterpret_cast<volatile uint32_t*>(&bars->v_mask[vst]);
+          const uint32_t base = v_s + vst * Lay::VS_BYTES;
+          if (EIGHT)
+            convert_e4m3<D, false, Lay::VCH_BYTES>(base, ct, load, d.end - c0, p.num_sink - c0,
+                                                   d.lo_any - c0);
+          else
+            convert_bf16<D, Lay::VCH_BYTES>(base, ct, load, d.end - c0, p.num_sink - c0,
+                                            d.lo_any - c0, most);
+          fence_proxy_async_smem();
+          mbar_arrive(smem_addr(&bars->v_full[vst]));
+          vst = vst + 1 == kVS ? 0 : vst + 1;
+          vparity ^= vst == 0 ? 1u : 0u;
+        }
+      }
+      // infinities and NaN of fp16: magnitudes that round past 65504, or were those
+      if ((most & 0xffffu) >= 0x7c00u || (most >> 16) >= 0x7c00u)
+        set_status(p.status, PKV_DEV_V_RANGE);
+    } else {
+      // ===== the products of query tile x: the warp waits, one lane issues =====
+      const int x = warp - kMmaWarp;
+      constexpr uint32_t idesc_qk = umma_idesc_bf16(kBM, kHalf, false, false);
+      constexpr uint32_t idesc_pv = umma_idesc_f16(kBM, D, false, true);
+      const uint64_t qd = smem_desc_sw128(q_s + x * Lay::TILE_BYTES, 16, 1024);
+      const uint64_t kd = smem_desc_sw128(k_s, 16, 1024);
+      const uint64_t vd = smem_desc_sw128(v_s, Lay::VCH_BYTES, 1024);
+      constexpr uint32_t kTile16 = Lay::TILE_BYTES >> 4;
+      static_assert(kNS == 2, "two stages");
+      const uint32_t s_tm = tmem + Lay::s_col(x), o_tm = tmem + Lay::o_col(x);
+      // S(g) of the tile in half h of K stage kt, and what follows it
+      auto issue_qk = [&](int g, int kt, int h, bool release, bool last) {
+        const uint64_t k = kd + (kt & 1) * kTile16 + h * (uint32_t)((kHalf * 128) >> 4);
+        const uint32_t s = s_tm + (uint32_t)((g & 1) * kHalf);
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const uint32_t off = ((i >> 2) * Lay::CH_BYTES + (i & 3) * 32) >> 4;
+            umma_ss(s, qd + off, k + off, idesc_qk, i > 0);
+          }
+          umma_commit(smem_addr(&bars->s_full[x][g & 1]));
+          if (release) umma_commit(smem_addr(&bars->k_empty[kt % kNS]));
+          if (last) umma_commit(smem_addr(&bars->q_empty[x]));  // Q is read no more
+        }
+        __syncwarp();
+      };
+      int g = 0, kt = 0, vst = 0;  // score tiles, K stages, V stage so far
+      uint32_t vparity = 0;
+      bool ok = true;
+#pragma unroll 1
+      for (int k = 0; ok; ++k) {
+        const int it = next_item(k);
+        if (it < 0) break;
+        const int n = item_of(p, list, QP, it).n;
+        ok = all_wait(&bars->q_full[x], k & 1);
+        // tile j's product with P behind tile j + 2's scores' issue, from j = -2 on
+#pragma unroll 1
+        for (int j = -2; ok && j < n; ++j) {
+          if (j >= 0) {
+            ok = all_wait(&bars->v_full[vst], vparity) &&
+                 all_wait(&bars->p_ready[x][g & 1], (g >> 1) & 1) &&
+                 (j > 0 || k == 0 || all_wait(&bars->o_free[x], (k - 1) & 1));
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t v = vd + vst * (uint32_t)(Lay::VS_BYTES >> 4);
+            const uint32_t pt = s_tm + (uint32_t)((g & 1) * kHalf);
+            if (elect_one()) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                umma_ts(o_tm, pt + 8u * i, v + (uint32_t)((i * 16 * 128) >> 4), idesc_pv,
+                        j > 0 || i > 0);
+              umma_commit(smem_addr(&bars->o_done[x][g & 1]));
+              umma_commit(smem_addr(&bars->v_empty[vst]));
+            }
+            __syncwarp();
+            vst = vst + 1 == kVS ? 0 : vst + 1;
+            vparity ^= vst == 0 ? 1u : 0u;
+            ++g;
+          }
+          const int j2 = j + 2;
+          if (j2 >= n) continue;
+          const int kt2 = kt + (j2 >> 1);
+          ok = (j2 & 1) || all_wait(&bars->k_full[kt2 % kNS], (kt2 / kNS) & 1);
+          if (!ok) break;
+          // (before the loop's first product g counts no tile of this item yet)
+          issue_qk(j >= 0 ? g + 1 : g + j2, kt2, j2 & 1, (j2 & 1) || j2 == n - 1, j2 == n - 1);
+        }
+        kt += (n + 1) >> 1;
+      }
+      // every product has completed before tensor memory is released (one lane issued them)
+      if (elect_one()) umma_commit(smem_addr(&bars->mma_done));
+      __syncwarp();
+      short_wait(smem_addr(&bars->mma_done), 0, nullptr);
+    }
+  } else {
+    more_registers<kSoftmaxRegs>();
+    // ===== softmax and output: warpgroup x owns query tile x, thread r its row r =====
+    const int x = warp >> 2, r = threadIdx.x & (kBM - 1);
+    const int rq = r / G, g = r % G;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t sa0 = tmem + lanes + Lay::s_col(x), oa = tmem + lanes + Lay::o_col(x);
+    const float sl2 = p.scale_log2;
+    bool ok = true;
+    int gt = 0;
+    for (int k = 0; ok; ++k) {
+      const int it = next_item(k);
+      if (it < 0) break;
+      const Item d = item_of(p, list, QP, it);
+      const int qj = d.j0 + x * QT + rq;
+      const bool valid = qj < d.j1 && rq < QT;
+      // the columns [low, lim] and those before num_sink are visible to the row
+      const int lim0 = valid ? d.qpos0 + qj - d.shift : d.end - 1;
+      const int low0 = lim0 - p.window + 1;
+      float m = -INFINITY, l = 0.f;
+      // 8 bits: lane i holds the block id and the scales of the item's 16-key chunk
+      // 32 b + i: the scores' factor, log2 of the values' scale, one over it
+      auto chunk_id = [&](int box) -> int32_t {
+        if (box >= d.count) return -1;
+        const int32_t id = __ldg(p.block_table + (int64_t)d.req * p.max_blocks +
+                                 d.key(box * kSub) / p.block_size);
+        return id < p.num_blocks ? id : -1;
+      };
+      float sc_a = 0.f, sc_l = 0.f, sc_i = 1.f, nx_a = 0.f, nx_l = 0.f, nx_i = 1.f;
+      int32_t nx_id = -1;
+      auto chunk_scales = [&](int32_t id) {
+        nx_a = nx_i = 1.f;
+        nx_l = 0.f;
+        if (id >= 0) {
+          // (at least 2^-100 both: a hidden score's -inf times 0 would be NaN)
+          constexpr float kLeast = 7.888609e-31f;
+          nx_a = fmaxf(__ldg(p.scales + (int64_t)id * p.num_kv_heads + d.kvh), kLeast) * sl2;
+          const float v = fmaxf(
+              __ldg(p.scales + ((int64_t)p.num_blocks + id) * p.num_kv_heads + d.kvh), kLeast);
+          nx_l = fast_log2(v);
+          nx_i = 1.f / v;
+        }
+      };
+      if (EIGHT) chunk_scales(chunk_id(lane));
+#pragma unroll 1
+      for (int j = 0; j < d.n; ++j, ++gt) {
+        if (EIGHT) {  // in time for the next 8 tiles
+          if ((j & 7) == 0) {
+            sc_a = nx_a;
+            sc_l = nx_l;
+            sc_i = nx_i;
+            nx_id = chunk_id((j + 8) * kHalfBoxes + lane);
+          } else if ((j & 7) == 4) {
+            chunk_scales(nx_id);
+          }
+        }
+        const uint32_t sa = sa0 + (uint32_t)((gt & 1) * kHalf);
+        ok = __all_sync(kFull, wait(&bars->s_full[x][gt & 1], (gt >> 1) & 1));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t u[kHalf];
+        PKV_TMEM_LD32(sa, u);
+        PKV_TMEM_LD32(sa + 32, (u + 32));
+        tmem_wait_ld();
+        const int lim = lim0 - j * kHalf, low = low0 - j * kHalf, sink = p.num_sink - j * kHalf;
+        // hidden scores become -inf where some row has any
+        if (!__all_sync(kFull, lim >= kHalf - 1 && (low <= 0 || sink >= kHalf))) {
+#pragma unroll
+          for (int c0 = 0; c0 < kHalf; c0 += 32) {
+            const uint32_t seen =
+                bits_below(lim + 1 - c0) & (~bits_below(low - c0) | bits_below(sink - c0));
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!(seen & (1u << c))) u[c0 + c] = kMinusInf;
+          }
+        }
+        // the row's maximum, in log2 units
+        float mx;
+        const int from = (j & 7) * kHalfBoxes;  // the lane of the tile's first chunk
+        if (EIGHT) {
+          mx = -INFINITY;
+#pragma unroll
+          for (int q = 0; q < kHalfBoxes; ++q) {
+            float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+            for (int c = 16 * q; c < 16 * q + 16; c += 4) {
+              a = max3(a, __uint_as_float(u[c]), __uint_as_float(u[c + 1]));
+              b = max3(b, __uint_as_float(u[c + 2]), __uint_as_float(u[c + 3]));
+            }
+            mx = fmaxf(mx, fmaf(fmaxf(a, b), __shfl_sync(kFull, sc_a, from + q),
+                                __shfl_sync(kFull, sc_l, from + q)));
+          }
+        } else {
+          float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < kHalf; c += 4) {
+            a = max3(a, __uint_as_float(u[c]), __uint_as_float(u[c + 1]));
+            b = max3(b, __uint_as_float(u[c + 2]), __uint_as_float(u[c + 3]));
+          }
+          mx = fmaxf(a, b) * sl2;
+        }
+        const float mnew = fmaxf(m, mx);
+        const bool grow = mnew > m + kRescaleThreshold;
+        if (__any_sync(kFull, grow)) {
+          const float alpha = grow ? fast_exp2(m - mnew) : 1.f;  // 0 while m is -inf
+          if (grow) m = mnew;
+          l *= alpha;
+          if (j > 0) {  // O once the product before has written it
+            ok = __all_sync(kFull, wait(&bars->o_done[x][(gt - 1) & 1], ((gt - 1) >> 1) & 1));
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t v[32];
+              PKV_TMEM_LD32(oa + c, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+              PKV_TMEM_ST32(oa + c, v);
+            }
+          }
+        }
+        const float mu = m == -INFINITY ? 0.f : m;
+        // weights: the sum takes them before they are rounded to fp16
+        float2 sum = make_float2(0.f, 0.f);
+        float sum8 = 0.f;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          uint32_t pk[16];
+          if (EIGHT) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const int box = 2 * b + q;
+              const float fa = __shfl_sync(kFull, sc_a, from + box);
+              const float fl = __shfl_sync(kFull, sc_l, from + box) - mu;
+              const float fi = __shfl_sync(kFull, sc_i, from + box);
+              float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                const uint32_t ua = u[16 * box + 2 * c], ub = u[16 * box + 2 * c + 1];
+                const float2 y = __ffma2_rn(
+                    make_float2(__uint_as_float(ua), __uint_as_float(ub)), make_float2(fa, fa),
+                    make_float2(fl, fl));
+                const float2 w = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+                pk[8 * q + c] = pack_f16x2(w.x, w.y);
+                s2 = __fadd2_rn(s2, w);
+              }
+              sum8 = fmaf(s2.x + s2.y, fi, sum8);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              const int e = 32 * b + 2 * c;
+              const float2 y = __ffma2_rn(
+                  make_float2(__uint_as_float(u[e]), __uint_as_float(u[e + 1])),
+                  make_float2(sl2, sl2), make_float2(-mu, -mu));
+              const float2 w = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+              pk[c] = pack_f16x2(w.x, w.y);
+              sum = __fadd2_rn(sum, w);
+            }
+          }
+          PKV_TMEM_ST16(sa + 16 * b, pk);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&bars->p_ready[x][gt & 1]));
+        l += EIGHT ? sum8 : sum.x + sum.y;
+      }
+      if (!ok) break;
+      // ---- the item's rows: O / l, lse
+      ok = __all_sync(kFull, wait(&bars->o_done[x][(gt - 1) & 1], ((gt - 1) >> 1) & 1));
+      if (!ok) break;
+      tc_fence_after();
+      const float inv = 1.f / l;
+      const int64_t orow = (int64_t)(d.t0 + qj) * p.num_heads + d.kvh * G + g;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t v[32];
+        PKV_TMEM_LD32(oa + c, v);
+        tmem_wait_ld();
+        if (!valid) continue;
+        if (p.out_bf16) {
+          uint16_t* out = reinterpret_cast<uint16_t*>(p.out) + orow * D + c;
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              w[i] = pack_bf16x2(__uint_as_float(v[e + 2 * i]) * inv,
+                                 __uint_as_float(v[e + 2 * i + 1]) * inv);
+            *reinterpret_cast<uint4*>(out + e) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(p.out + orow * D + c + e) =
+                make_float4(__uint_as_float(v[e]) * inv, __uint_as_float(v[e + 1]) * inv,
+                            __uint_as_float(v[e + 2]) * inv, __uint_as_float(v[e + 3]) * inv);
+        }
+      }
+      if (valid && p.out_lse) p.out_lse[orow] = (m + fast_log2(l)) * kLn2;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&bars->o_free[x]));
+    }
+  }
+
+  // ---- the CTA's tcgen05 work is complete: tensor memory is released (its address
+  // read again: the roles ran with different register budgets)
+  tc_fence_before();
+  __syncthreads();
+  if ((threadIdx.x >> 5) == kMmaWarp) {
+    const Bars* b = reinterpret_cast<const Bars*>(
+        ((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023)) +
+        Lay::BAR_OFF);
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(*reinterpret_cast<const volatile uint32_t*>(&b->tmem_base), kTmemCols);
+  }
+}
+
+template <int D, bool EIGHT>
+cudaError_t launch_d(const AttnParams& p, const CUtensorMap& q_map, const CUtensorMap& kv_map,
+                     cudaStream_t stream) {
+  const size_t smem = Layout<D>::bytes(p.num_seqs);
+  if (smem > 227 * 1024) return cudaErrorInvalidValue;
+  auto kernel = prefill_rows_kernel<D, EIGHT>;
+  static SmemLimit limit;
+  if (cudaError_t e = limit.ensure(reinterpret_cast<const void*>(kernel), 227 * 1024);
+      e != cudaSuccess)
+    return e;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int QP = 2 * (kBM / (p.num_heads / p.num_kv_heads));
+  const int64_t bound =
+      (int64_t)p.num_seqs * ((p.max_query_len + QP - 1) / QP) * p.num_kv_heads;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(bound < sms ? bound : sms));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, q_map, kv_map, p);
+}
+
+}  // namespace
+
+bool prefill_rows_fits(int32_t num_seqs, int32_t head_dim) {
+  return num_seqs >= 0 && (head_dim == 128 ? Layout<128>::bytes(num_seqs)
+                                           : Layout<64>::bytes(num_seqs)) <= 227 * 1024;
+}
+
+cudaError_t launch_prefill_rows(const AttnParams& p, const CUtensorMap& q_map,
+                                const CUtensorMap& kv_map, cudaStream_t stream) {
+  if (p.scales)
+    return p.head_dim == 128 ? launch_d<128, true>(p, q_map, kv_map, stream)
+                             : launch_d<64, true>(p, q_map, kv_map, stream);
+  return p.head_dim == 128 ? launch_d<128, false>(p, q_map, kv_map, stream)
+                           : launch_d<64, false>(p, q_map, kv_map, stream);
+}
+
+}  // namespace pkv

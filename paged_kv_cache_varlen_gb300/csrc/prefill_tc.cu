@@ -49,12 +49,6 @@
 //     values to the row sum (so that O and l see the same weights); O is
 //     rescaled in TMEM when needed; a tile every key of which is visible to
 //     the warp's rows skips the mask and uses packed fp32x2 arithmetic;
-//   * two more forms of the kernel (Kind): queries that see a window of the keys
-//     before them and the first num_sink ones (an item goes through the key tiles
-//     that some query of it sees, the mask has a lower border), and the same over
-//     an 8-bit pool: K and V tiles land as e4m3 and the converter warps make bf16
-//     (K) and fp16 (V) of them in place, both exactly; a block's two scales act on
-//     the scores, as in decode_rows.cu;
 //   * every wait is bounded; on a timeout the CTA drains its copies and
 //     MMAs, frees its TMEM and leaves with PKV_DEV_TIMEOUT set.
 #include <math.h>
@@ -118,12 +112,7 @@ __host__ __device__ constexpr size_t work_list_ints(int num_seqs) {
   return num_seqs <= kSortMax ? 4 * ((size_t)num_seqs + 1) : (size_t)num_seqs + 1;
 }
 
-// kPlain: the pool in bf16, causal; kWindow: with a window (AttnParams::window, not
-// 0), groups of any size up to 128, `out` in either type; kEight: the same over an
-// 8-bit pool.
-enum Kind { kPlain, kWindow, kEight };
-
-template <int D, int KIND = kPlain>
+template <int D>
 struct PrefillLayout {
   static constexpr int NCH = D / 64;                       // 128-byte column chunks of a row
   static constexpr int CH_BYTES = 128 * 128;               // one chunk of 128 rows
@@ -132,7 +121,7 @@ struct PrefillLayout {
   static constexpr int K_OFF = Q_OFF + kQT * TILE_BYTES;   // [kNS] K tiles
   static constexpr int V_OFF = K_OFF + kNS * TILE_BYTES;   // [kNS] V tiles
   static constexpr int BAR_OFF = V_OFF + kNS * TILE_BYTES;
-  static constexpr int PREF_OFF = BAR_OFF + (KIND == kEight ? 640 : 512);  // the work list
+  static constexpr int PREF_OFF = BAR_OFF + 512;   // the work list (see WorkList)
   // keep one CTA per SM (each CTA allocates all 512 TMEM columns)
   static size_t bytes(int num_seqs) {
     const size_t need = 1024 + PREF_OFF + work_list_ints(num_seqs) * 4;
@@ -180,28 +169,12 @@ struct Bars {
 
 static_assert(sizeof(Bars) <= 512, "the barriers fit below the work list");
 
-// An 8-bit pool's K tiles are converted like V's.
-struct Bars8 : Bars {
-  uint64_t k_landed[kNS];
-  uint32_t k_mask[kNS];
-};
-static_assert(sizeof(Bars8) <= 640, "the barriers fit below the work list");
-
 struct PrefillItem {
   int req, kvh, j0, j1, t0, qlen, L, kv_end, n_tiles;
   int n_sub;  // S tiles of kSN keys: the needed keys of the n_tiles K/V tiles (at least 1)
   int qpos0;  // position of the request's first query among its keys
   int jb;   // first key tile of the item (a key segment in prefix mode)
   int seg;  // key segment (prefix mode), else 0
-  // window: the item's tiles are the first v_sink ones and those from v_low on
-  int v_sink, v_low;
-  int lo_any;  // none of its queries sees keys [num_sink, lo_any)
-
-  template <int KIND>
-  __device__ __forceinline__ int tile(int j) const {
-    if (KIND == kPlain) return jb + j;
-    return j < v_sink ? j : j - v_sink + v_low;
-  }
 };
 
 static_assert(kBN == 128, "prefix segments count 128-key tiles");
@@ -243,11 +216,8 @@ __device__ __forceinline__ int prefill_units(const AttnParams& p, int r, int QP,
 
 // Key tiles of request r's heaviest work unit (its last queries see the
 // most keys), for the heaviest-first order; call only for requests with work.
-template <int KIND>
-__device__ __forceinline__ int prefill_weight(const AttnParams& p, int r, int QP) {
+__device__ __forceinline__ int prefill_weight(const AttnParams& p, int r) {
   const int32_t L = __ldg(p.seq_lens + r);
-  if (KIND != kPlain)
-    return visible_units(p.window, p.num_sink, max(0, L - QP), L, kBN).count;
   if (p.prefix_mode) return prefix_tiles_per_segment(L, p.kv_splits);
   const int32_t qlen = __ldg(p.cu_seqlens + r + 1) - __ldg(p.cu_seqlens + r);
   int64_t end = L;  // ordinary call: the last query sees every key
@@ -291,7 +261,6 @@ struct WorkList {
 };
 
 // Builds the work list (all threads); returns it and sets *total_units.
-template <int KIND>
 __device__ __forceinline__ WorkList prefill_work_list(const AttnParams& p, int* base,
                                                       int32_t* scan, int QP, int* total_units) {
   const int B = p.num_seqs;
@@ -326,7 +295,7 @@ __device__ __forceinline__ WorkList prefill_work_list(const AttnParams& p, int* 
   int cnt = 0;
   for (int r = r0; r < r1; ++r) {
     const bool work = prefill_units(p, r, QP, flag) > 0;
-    key[r] = work ? prefill_weight<KIND>(p, r, QP) : -1;
+    key[r] = work ? prefill_weight(p, r) : -1;
     cnt += work ? 1 : 0;
   }
   int n = 0;
@@ -379,7 +348,6 @@ constexpr float kDecodeBytesPerCycle = 40.f;
 // SMs: out of p.shared_sms, the prefill work's share of the estimated SM
 // time (its tile pairs against the decode requests' K/V bytes), at least 1.
 // All threads (two __syncthreads); every CTA computes the same value.
-template <int KIND>
 __device__ __noinline__ int prefill_share(const AttnParams& p, int QP, float (*red)[kThreads / 32]) {
   const int B = p.num_seqs;
   const int per = (B + kThreads - 1) / kThreads;
@@ -390,21 +358,14 @@ __device__ __noinline__ int prefill_share(const AttnParams& p, int QP, float (*r
     const int32_t L = __ldg(p.seq_lens + r);
     if (qlen < 1 || L < 1 || L > p.max_seq_len) continue;
     if (qlen <= p.decode_max_q) {
-      if (KIND == kPlain)
-        dkeys += (float)L;
-      else
-        dkeys += 16.f * (float)visible_units(p.window, p.num_sink, max(0, L - qlen), L, 16).count;
+      dkeys += (float)L;
       continue;
     }
     int64_t q0 = (int64_t)L - qlen;  // position of the first query among the keys
     if (p.key_start) q0 = (int64_t)__ldg(p.query_start + r) - __ldg(p.key_start + r);
     for (int j1 = min(qlen, QP);; j1 = min(qlen, j1 + QP)) {
       const int64_t end = max((int64_t)0, min((int64_t)L, q0 + j1));
-      if (KIND == kPlain)
-        pairs += (float)max((int64_t)1, (end + kBN - 1) / kBN);
-      else
-        pairs += (float)max(1, visible_units(p.window, p.num_sink, max(0, (int)q0 + (j1 - 1) / QP * QP),
-                                             (int)end, kBN).count);
+      pairs += (float)max((int64_t)1, (end + kBN - 1) / kBN);
       if (j1 == qlen) break;
     }
   }
@@ -425,15 +386,13 @@ __device__ __noinline__ int prefill_share(const AttnParams& p, int QP, float (*r
     dt += red[1][w];
   }
   __syncthreads();
-  const float a = dt * (float)(p.num_kv_heads * p.head_dim * (KIND == kEight ? 2 : 4)) /
-                  kDecodeBytesPerCycle;
+  const float a = dt * (float)(p.num_kv_heads * p.head_dim * 4) / kDecodeBytesPerCycle;
   const float b = pt * (float)p.num_kv_heads * kPairCycles;
   const int S = p.shared_sms;
   const int keep = a + b > 0.f ? S - (int)((float)S * a / (a + b) + 0.5f) : S;
   return max(1, min(S, keep));
 }
 
-template <int KIND>
 __device__ __forceinline__ PrefillItem prefill_item(const AttnParams& p, const WorkList& wl, int QP,
                                                     int it) {
   PrefillItem d;
@@ -481,15 +440,6 @@ __device__ __forceinline__ PrefillItem prefill_item(const AttnParams& p, const W
   d.n_sub = max(1, (d.kv_end + kSN - 1) / kSN);
   d.jb = 0;
   d.seg = 0;
-  if (KIND != kPlain) {
-    const int q0 = d.qpos0 + d.j0;  // position of the item's first query
-    const Visible v = visible_units(p.window, p.num_sink, q0, d.kv_end, kBN);
-    d.v_sink = v.sink;
-    d.v_low = v.low;
-    d.n_tiles = v.count;
-    d.n_sub = 2 * v.count - (((d.kv_end - 1) / kSN & 1) ? 0 : 1);  // the last tile's needed half
-    d.lo_any = q0 >= p.window ? q0 - p.window + 1 : 0;
-  }
   return d;
 }
 
@@ -573,80 +523,6 @@ __device__ __forceinline__ void v_piece_to_f16(uint32_t addr, uint32_t& emax) {
                : "memory");
 }
 
-// 16 e4m3 values at `src` (16 bytes) to 16-bit ones, exactly.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w, bool high) {
-  uint32_t r;
-  if (high)
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}"
-        : "=r"(r)
-        : "r"(w));
-  else
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
-        : "=r"(r)
-        : "r"(w));
-  return r;
-}
-__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t h) {
-  float a, b;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
-      "cvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
-      : "=f"(a), "=f"(b)
-      : "r"(h));
-  return pack_bf16x2(a, b);
-}
-
-// One e4m3 tile of 128 rows, landed in 16-row boxes at the rows' final places
-// (box b at 2048 b bytes, its rows D bytes apart, swizzled by their length),
-// converted in place: a row's bytes lie where the same warp writes, so a warp
-// reads its 32 rows, then writes them. Rows not loaded, behind the needed keys or
-// hidden from every query ([h0, h1)) become zeros. BF: to bf16, else fp16.
-template <int D, bool BF>
-__device__ __forceinline__ void convert_tile8(uint32_t base, uint32_t ch_bytes, int warp, int lane,
-                                              uint32_t load, int nvalid, int h0, int h1) {
-  constexpr int NP = D / 16;  // 16-byte pieces of a row
-  uint32_t w[NP][4];
-  // piece e of a lane: 8 lanes read one piece of 8 rows (different bank groups)
-#pragma unroll
-  for (int e = 0; e < NP; ++e) {
-    const int k = warp * 32 + (NP == 8 ? e >> 1 : e) * 8 + (lane & 7);
-    const int pc = (lane >> 3) + (NP == 8 ? 4 * (e & 1) : 0);
-    const int r = k & 15;
-    const uint32_t at = base + (k >> 4) * 2048 + r * D +
-                        ((pc ^ (D == 128 ? (r & 7) : ((r >> 1) & 3))) << 4);
-    const bool there = k < nvalid && ((load >> (k >> 4)) & 1u) && (k < h0 || k >= h1);
-    if (there)
-      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(w[e][0]), "=r"(w[e][1]), "=r"(w[e][2]), "=r"(w[e][3])
-                   : "r"(at)
-                   : "memory");
-    else
-      w[e][0] = w[e][1] = w[e][2] = w[e][3] = 0u;
-  }
-  __syncwarp();
-#pragma unroll
-  for (int e = 0; e < NP; ++e) {
-    const int k = warp * 32 + (NP == 8 ? e >> 1 : e) * 8 + (lane & 7);
-    const int pc = (lane >> 3) + (NP == 8 ? 4 * (e & 1) : 0);
-    uint32_t x[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = e4m3x2_to_f16x2(w[e][i], false);
-      x[2 * i + 1] = e4m3x2_to_f16x2(w[e][i], true);
-    }
-    if (BF)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = f16x2_to_bf16x2(x[i]);
-    const uint32_t row = base + (pc >> 2) * ch_bytes + k * 128;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int u = (pc & 3) * 2 + h;
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((u ^ (k & 7)) << 4)),
-                   "r"(x[4 * h]), "r"(x[4 * h + 1]), "r"(x[4 * h + 2]), "r"(x[4 * h + 3])
-                   : "memory");
-    }
-  }
-}
-
 template <int R>
 __device__ __forceinline__ void setmaxnreg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
@@ -665,18 +541,16 @@ __device__ __forceinline__ void cta_finished(const AttnParams& p) {  // one thre
   }
 }
 
-template <int D, int KIND>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap q_map,
                    const __grid_constant__ CUtensorMap kv_map, const AttnParams p) {
-  using Lay = PrefillLayout<D, KIND>;
-  constexpr bool EIGHT = KIND == kEight;
+  using Lay = PrefillLayout<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // 1024-byte alignment for the 128-byte swizzle atoms
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   Bars* bars = reinterpret_cast<Bars*>(smem + Lay::BAR_OFF);
-  Bars8* bars8 = static_cast<Bars8*>(bars);  // EIGHT only
   int* list_base = reinterpret_cast<int*>(smem + Lay::PREF_OFF);
 
   griddep_wait();  // the KV write (and all earlier work) has landed
@@ -693,9 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_addr(&bars->q_full), 1);
     mbar_init(smem_addr(&bars->q_empty), kQT);  // one commit per MMA thread
     for (int s = 0; s < kNS; ++s) {
-      // the producer's arrival + TMA bytes (EIGHT: those land first)
-      mbar_init(smem_addr(&bars->k_full[s]), EIGHT ? kConverters : 1);
-      if (EIGHT) mbar_init(smem_addr(&bars8->k_landed[s]), 1);
+      mbar_init(smem_addr(&bars->k_full[s]), 1);  // the producer's arrival + TMA bytes
       mbar_init(smem_addr(&bars->k_empty[s]), kQT);
       mbar_init(smem_addr(&bars->v_full[s]), kConverters);
       mbar_init(smem_addr(&bars->v_empty[s]), kQT);
@@ -717,9 +589,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_barrier_init();
   }
   int total_units = 0;
-  const WorkList wl = prefill_work_list<KIND>(p, list_base, bars->scan, QP, &total_units);  // syncs
+  const WorkList wl = prefill_work_list(p, list_base, bars->scan, QP, &total_units);  // syncs
   const int total = total_units * p.num_kv_heads;
-  const int active = p.shared_sms > 0 ? prefill_share<KIND>(p, QP, bars->red) : (int)gridDim.x;  // syncs
+  const int active = p.shared_sms > 0 ? prefill_share(p, QP, bars->red) : (int)gridDim.x;  // syncs
   if ((int)blockIdx.x >= min(total, active)) {  // uniform; nothing allocated yet
     if (threadIdx.x == 0) cta_finished(p);
     return;
@@ -769,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           it = vrole ? read_item(bars, p, gi, abort) : take_item(bars, p, total, gi, abort);
         it = __shfl_sync(kFullMask, it, 0);
         if (it < 0) break;
-        const PrefillItem d = prefill_item<KIND>(p, wl, QP, it);
+        const PrefillItem d = prefill_item(p, wl, QP, it);
         const int32_t* bt = p.block_table + (int64_t)d.req * p.max_blocks;
         if (!vrole) {
           int w = 1;
@@ -780,11 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) {
             // rows past the last token read as zeros; rows of the next request
             // are loaded but belong to no valid output row
-            // (a group that does not divide 128 leaves the tile's last rows as
-            // they are: rows of no query)
-            mbar_arrive_expect_tx(smem_addr(&bars->q_full),
-                                  KIND == kPlain ? kQT * Lay::TILE_BYTES
-                                                 : kQT * Lay::NCH * QT * G * 128);
+            mbar_arrive_expect_tx(smem_addr(&bars->q_full), kQT * Lay::TILE_BYTES);
             for (int x = 0; x < kQT; ++x)
               for (int c = 0; c < Lay::NCH; ++c)
                 tma_load_3d(q_s + x * Lay::TILE_BYTES + c * Lay::CH_BYTES, &q_map,
@@ -794,32 +662,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         int32_t ids = -1;
         for (int j = 0; j < d.n_tiles; ++j, ++gt) {
-          const int jj = d.tile<KIND>(j);  // key tile
-          // whether a box holds a key that some query of the item sees
-          auto needed = [&](int key) {
-            return key < d.kv_end &&
-                   (KIND == kPlain || key < p.num_sink || key + kSub > d.lo_any);
-          };
+          const int jj = d.jb + j;  // key tile
           if ((j & 3) == 0) {  // block ids of the next 4 tiles, one 16-key box per lane
-            const int key = KIND == kPlain
-                                ? (jj * (kBN / kSub) + lane) * kSub
-                                : d.tile<KIND>(j + (lane >> 3)) * kBN + (lane & 7) * kSub;
-            ids = needed(key) ? __ldg(bt + key / p.block_size) : -1;
+            const int key = (jj * (kBN / kSub) + lane) * kSub;
+            ids = (key < d.kv_end) ? __ldg(bt + key / p.block_size) : -1;
           }
           // lane b < 8: box b of the tile -- loaded or not, and its first row
           const int b = lane & 7;
           const int32_t id = __shfl_sync(kFullMask, ids, (j & 3) * (kBN / kSub) + b);
           const int key = jj * kBN + b * kSub;
-          const bool in_range = lane < 8 && needed(key);
+          const bool in_range = lane < 8 && key < d.kv_end;
           const bool good = in_range && id >= 0 && id < p.num_blocks;
           bad_block |= in_range && !good;
           const uint32_t load = __ballot_sync(kFullMask, good);
-          const uint32_t zero = (vrole || EIGHT) ? 0u : __ballot_sync(kFullMask, in_range && !good);
+          const uint32_t zero = vrole ? 0u : __ballot_sync(kFullMask, in_range && !good);
           const int32_t row = good ? half_rows + id * p.block_size + key % p.block_size : 0;
           const int st = gt % kNS;
           uint64_t* empty = vrole ? &bars->v_empty[st] : &bars->k_empty[st];
-          uint64_t* full = vrole ? &bars->v_landed[st]
-                           : EIGHT ? &bars8->k_landed[st] : &bars->k_full[st];
+          uint64_t* full = vrole ? &bars->v_landed[st] : &bars->k_full[st];
           int w = 1;
           if (lane == 0 && gt >= kNS)
             w = mbar_wait(smem_addr(empty), ((gt / kNS) - 1) & 1, p.status, abort);
@@ -838,19 +698,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async_smem();
           }
           if (vrole && lane == 0) *reinterpret_cast<volatile uint32_t*>(&bars->v_mask[st]) = load;
-          if (EIGHT && !vrole && lane == 0)
-            *reinterpret_cast<volatile uint32_t*>(&bars8->k_mask[st]) = load;
           __syncwarp();
           if (lane == 0)
-            mbar_arrive_expect_tx(smem_addr(full),
-                                  __popc(load) * (EIGHT ? kSub * D : Lay::NCH * kSub * 128));
+            mbar_arrive_expect_tx(smem_addr(full), __popc(load) * Lay::NCH * kSub * 128);
 #pragma unroll
           for (int bb = 0; bb < kBN / kSub; ++bb) {
             const int32_t r = __shfl_sync(kFullMask, row, bb);
-            if (EIGHT) {
-              if (lane == 0 && ((load >> bb) & 1))
-                tma_load_3d(dst0 + bb * kSub * 128, &kv_map, smem_addr(full), 0, r, d.kvh);
-            } else if (lane == 0 && ((load >> bb) & 1))
+            if (lane == 0 && ((load >> bb) & 1))
               for (int c = 0; c < Lay::NCH; ++c)
                 tma_load_4d(dst0 + c * Lay::CH_BYTES + bb * kSub * 128, &kv_map, smem_addr(full), 0,
                             r, d.kvh, c);
@@ -862,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (bad_block) set_status(p.status, PKV_DEV_BAD_BLOCK);
       // our copies, and the barrier arrivals they trigger, land before the CTA can exit
       if (lane == 0) {
-        uint64_t* landed = vrole ? bars->v_landed : EIGHT ? bars8->k_landed : bars->k_full;
+        uint64_t* landed = vrole ? bars->v_landed : bars->k_full;
         for (int g = max(0, armed - kNS); g < armed; ++g)
           mbar_wait(smem_addr(&landed[g % kNS]), (g / kNS) & 1, nullptr);
         if (!vrole && q_issued > 0)
@@ -885,49 +739,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) it = read_item(bars, p, gi, abort);
         it = __shfl_sync(kFullMask, it, 0);
         if (it < 0) break;
-        const PrefillItem d = prefill_item<KIND>(p, wl, QP, it);
+        const PrefillItem d = prefill_item(p, wl, QP, it);
         for (int j = 0; j < d.n_tiles; ++j, ++gt) {
           const int st = gt % kNS;
           int w = 1;
-          const int tile0 = d.tile<KIND>(j) * kBN;
-          const int nvalid = d.kv_end - tile0;  // rows below it are needed keys
-          // rows [h0, h1) are keys that no query of the item sees
-          const int h0 = KIND == kPlain ? 0 : p.num_sink - tile0;
-          const int h1 = KIND == kPlain ? 0 : d.lo_any - tile0;
-          if constexpr (EIGHT) {  // the K tile, then the V tile
-            for (int kv = 0; kv < 2; ++kv) {
-              if (lane == 0)
-                w = mbar_wait(smem_addr(kv ? &bars->v_landed[st] : &bars8->k_landed[st]),
-                              (gt / kNS) & 1, p.status, abort);
-              ok = __shfl_sync(kFullMask, w, 0) != 0;
-              if (!ok) break;
-              const uint32_t load = *reinterpret_cast<volatile uint32_t*>(
-                  kv ? &bars->v_mask[st] : &bars8->k_mask[st]);
-              if (kv)
-                convert_tile8<D, false>(v_s + st * Lay::TILE_BYTES, Lay::CH_BYTES, warp - kConvWarp0,
-                                        lane, load, nvalid, h0, h1);
-              else
-                convert_tile8<D, true>(k_s + st * Lay::TILE_BYTES, Lay::CH_BYTES, warp - kConvWarp0,
-                                       lane, load, nvalid, h0, h1);
-              fence_proxy_async_smem();
-              mbar_arrive(smem_addr(kv ? &bars->v_full[st] : &bars->k_full[st]));
-            }
-            if (!ok) break;
-            continue;
-          }
           if (lane == 0)
             w = mbar_wait(smem_addr(&bars->v_landed[st]), (gt / kNS) & 1, p.status, abort);
           ok = __shfl_sync(kFullMask, w, 0) != 0;
           if (!ok) break;
           const uint32_t base = v_s + st * Lay::TILE_BYTES;
           const uint32_t load = *reinterpret_cast<volatile uint32_t*>(&bars->v_mask[st]);
+          const int nvalid = d.kv_end - (d.jb + j) * kBN;  // rows below it are needed keys
 #pragma unroll 4
           for (int i = ct; i < kBN * RP; i += kConverters) {
             const int k = i / RP, pc = i % RP;
             const uint32_t a = base + (pc >> 3) * Lay::CH_BYTES + k * 128 +
                                (((uint32_t)(pc & 7) ^ (uint32_t)(k & 7)) << 4);
-            if (k < nvalid && ((load >> (k / kSub)) & 1u) &&
-                (KIND == kPlain || k < h0 || k >= h1))
+            if (k < nvalid && ((load >> (k / kSub)) & 1u))
               v_piece_to_f16(a, emax);
             else
               st_shared_zero16(a);
@@ -1011,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (; ok; ++gi) {
         const int it = read_item(bars, p, gi, abort);
         if (it < 0) break;
-        const PrefillItem d = prefill_item<KIND>(p, wl, QP, it);
+        const PrefillItem d = prefill_item(p, wl, QP, it);
         const int ns = d.n_sub;
         // both S buffers are free: the previous item's PVs were issued first
         ok = wait(&bars->q_full, gi & 1) && wait(&bars->k_full[gt % kNS], (gt / kNS) & 1);
@@ -1058,69 +886,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool out32 = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
     bool ok = true;
     int gs = 0;  // S tiles of this Q tile so far (all items)
-    // EIGHT: lane i of the warp holds the scales of the i-th 16-key group from the
-    // current eighth S tile on: the scores' factor, log2 of the values' scale, one
-    // over it
-    float sc_a = 0.f, sc_l = 0.f, sc_i = 1.f, nx_a = 0.f, nx_l = 0.f, nx_i = 1.f;
-    int32_t nx_id = -1;
     for (int k = 0; ok; ++k) {
       int it = -1;
       if (lane == 0) it = read_item(bars, p, k, abort);
       it = __shfl_sync(kFullMask, it, 0);
       if (it < 0) break;
-      const PrefillItem d = prefill_item<KIND>(p, wl, QP, it);
+      const PrefillItem d = prefill_item(p, wl, QP, it);
       const int qj = d.j0 + x * QT + rq;
-      const bool row_valid = qj < d.j1 && (KIND == kPlain || rq < QT);
+      const bool row_valid = qj < d.j1;
       // the row's last visible key (a key range may end before the query)
       const int pos =
           (row_valid && !p.prefix_mode) ? min(d.qpos0 + qj, d.kv_end - 1) : (d.kv_end - 1);
       float m = -INFINITY, l = 0.f;
-      // EIGHT: the block id and the scales of the lane's group among the 32 from S
-      // tile j0 on
-      auto group_id = [&](int j0) -> int32_t {
-        const int j = j0 + (lane >> 2);
-        const int key = d.tile<KIND>(j >> 1) * kBN + (j & 1) * kSN + (lane & 3) * kSub;
-        const bool in = j < d.n_sub && key < d.kv_end &&
-                        (key < p.num_sink || key + kSub > d.lo_any);
-        const int32_t id =
-            in ? __ldg(p.block_table + (int64_t)d.req * p.max_blocks + key / p.block_size) : -1;
-        return id < p.num_blocks ? id : -1;
-      };
-      auto group_scales = [&](int32_t id, float& a, float& lc, float& ic) {
-        a = lc = 0.f;
-        ic = 1.f;
-        if (id >= 0) {
-          a = __ldg(p.scales + (int64_t)id * p.num_kv_heads + d.kvh) * sl2;
-          const float v = fmaxf(
-              __ldg(p.scales + ((int64_t)p.num_blocks + id) * p.num_kv_heads + d.kvh),
-              7.888609e-31f);  // 2^-100
-          lc = fast_log2(v);
-          ic = 1.f / v;
-        }
-      };
-      if constexpr (EIGHT) group_scales(group_id(0), nx_a, nx_l, nx_i);
       for (int j = 0; j < d.n_sub; ++j) {
         const int gg = gs + j;
-        if constexpr (EIGHT) {
-          if ((j & 7) == 0) {
-            sc_a = nx_a;
-            sc_l = nx_l;
-            sc_i = nx_i;
-            nx_id = group_id(j + 8);
-          } else if ((j & 7) == 4) {
-            group_scales(nx_id, nx_a, nx_l, nx_i);
-          }
-        }
         const uint32_t sa = sa0 + (uint32_t)((gg & 1) * kSN);
         ok = __all_sync(kFullMask, mbar_wait(smem_addr(&bars->s_full[x][gg & 1]), (gg >> 1) & 1,
                                              p.status, abort));
         if (!ok) break;
         tc_fence_after();
-        // keys c <= lim of this tile are visible (window: those >= low or < sink)
-        const int key0 = d.tile<KIND>(j >> 1) * kBN + (j & 1) * kSN;
-        const int lim = pos - key0;
-        const int low = KIND == kPlain ? 0 : lim - p.window + 1;
-        const int sink = KIND == kPlain ? 0 : p.num_sink - key0;
+        const int lim = pos - (d.jb * kBN + j * kSN);  // keys c <= lim of this tile are visible
         // the row's kSN scores in registers: one TMEM round trip
         uint32_t u[kSN];
         PKV_TMEM_LD32(sa, u);
@@ -1128,74 +913,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_ld();
         float alpha = 1.f, rsa = 0.f, rsb = 0.f;
         bool resc;
-        if constexpr (EIGHT) {
-          // the scores with their block's factor and the values' scale; what the
-          // sum adds back is one over the latter
-          const bool all = __all_sync(kFullMask, lim >= kSN - 1 && (low <= 0 || sink >= kSN));
-          const int g0 = (j & 7) * 4;
-          float ga[4], gl[4], gi[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            ga[q] = __shfl_sync(kFullMask, sc_a, g0 + q);
-            gl[q] = __shfl_sync(kFullMask, sc_l, g0 + q);
-            gi[q] = __shfl_sync(kFullMask, sc_i, g0 + q);
-          }
-          if (!all) {
-#pragma unroll
-            for (int c = 0; c < kSN; ++c)
-              if (c > lim || (c < low && c >= sink)) u[c] = 0xff800000u;  // -inf
-          }
-          float mx = -INFINITY;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            float a = -INFINITY, b = -INFINITY;
-#pragma unroll
-            for (int c = 16 * q; c < 16 * q + 16; c += 4) {
-              a = max3(a, __uint_as_float(u[c]), __uint_as_float(u[c + 1]));
-              b = max3(b, __uint_as_float(u[c + 2]), __uint_as_float(u[c + 3]));
-            }
-            a = fmaxf(a, b);
-            // (a group without a visible key: its factor may be 0, and 0 * inf is NaN)
-            if (a != -INFINITY) mx = fmaxf(mx, fmaf(a, ga[q], gl[q]));
-          }
-          const float mnew = fmaxf(m, mx);
-          resc = mnew > m + kRescaleThreshold;
-          if (resc) {
-            alpha = fast_exp2(m - mnew);  // 0 on the first tile
-            m = mnew;
-          }
-          const float mu = m == -INFINITY ? 0.f : m;
-          float sum = 0.f;
-#pragma unroll
-          for (int ch = 0; ch < kSN / 32; ++ch) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const float2 f2 = make_float2(ga[2 * ch + q], ga[2 * ch + q]);
-              const float2 o2 = make_float2(gl[2 * ch + q] - mu, gl[2 * ch + q] - mu);
-              float ra = 0.f, rb = 0.f;
-#pragma unroll
-              for (int c = 8 * q; c < 8 * q + 8; ++c) {
-                const float2 x2 = __ffma2_rn(make_float2(__uint_as_float(u[32 * ch + 2 * c]),
-                                                         __uint_as_float(u[32 * ch + 2 * c + 1])),
-                                             f2, o2);
-                float p0 = fast_exp2(x2.x), p1 = fast_exp2(x2.y);
-                if (!all) {  // (a hidden key's score may have met a factor of 0)
-                  if (u[32 * ch + 2 * c] == 0xff800000u) p0 = 0.f;
-                  if (u[32 * ch + 2 * c + 1] == 0xff800000u) p1 = 0.f;
-                }
-                pk[c] = pack_f16x2(p0, p1);
-                // (before the rounding: see decode_rows.cu)
-                ra += p0;
-                rb += p1;
-              }
-              sum = fmaf(ra + rb, gi[2 * ch + q], sum);
-            }
-            PKV_TMEM_ST16(sa + ch * 16, pk);
-          }
-          rsa = sum;
-        } else if (__all_sync(kFullMask, lim >= kSN - 1 &&
-                                             (KIND == kPlain || low <= 0 || sink >= kSN))) {
+        if (__all_sync(kFullMask, lim >= kSN - 1)) {
           // ---- every key of the tile is visible to every row of the warp:
           // row maximum (two independent chains of 3-input maxima), then the
           // probabilities as fp16 pairs, written over the first half of the
@@ -1233,8 +951,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float mx = -INFINITY;
 #pragma unroll
           for (int c = 0; c < kSN; ++c)
-            if (c <= lim && (KIND == kPlain || c >= low || c < sink))
-              mx = fmaxf(mx, __uint_as_float(u[c]));
+            if (c <= lim) mx = fmaxf(mx, __uint_as_float(u[c]));
           const float mnew = fmaxf(m, mx * sl2);
           resc = mnew > m + kRescaleThreshold;
           if (resc) {
@@ -1249,8 +966,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int c0 = 32 * ch + 2 * c;
               float p0 = fast_exp2(fmaf(__uint_as_float(u[c0]), sl2, -m));
               float p1 = fast_exp2(fmaf(__uint_as_float(u[c0 + 1]), sl2, -m));
-              if (c0 > lim || (KIND != kPlain && c0 < low && c0 >= sink)) p0 = 0.f;
-              if (c0 + 1 > lim || (KIND != kPlain && c0 + 1 < low && c0 + 1 >= sink)) p1 = 0.f;
+              if (c0 > lim) p0 = 0.f;
+              if (c0 + 1 > lim) p1 = 0.f;
               pk[c] = pack_f16x2(p0, p1);
               add_f16x2_to(rsa, rsb, pk[c]);
             }
@@ -1292,7 +1009,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                            (last >> 1) & 1, p.status, abort));
       if (!ok) break;
       tc_fence_after();
-      const float inv = KIND == kPlain ? (l > 0.f ? 1.f / l : 0.f) : 1.f / l;
+      const float inv = l > 0.f ? 1.f / l : 0.f;
       float* orow = p.out + d.seg * p.split_out_stride +
                     ((int64_t)(d.t0 + qj) * p.num_heads + d.kvh * G + g) * D;
       // each thread writes its own row: 32-byte stores (whole sectors) when
@@ -1302,20 +1019,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t u[32];
         PKV_TMEM_LD32(oa + 32 * c, u);
         tmem_wait_ld();
-        if (KIND != kPlain && p.out_bf16) {
-          uint16_t* ob = reinterpret_cast<uint16_t*>(p.out) +
-                         ((int64_t)(d.t0 + qj) * p.num_heads + d.kvh * G + g) * D + 32 * c;
-          if (row_valid)
-#pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              uint32_t w[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                w[i] = pack_bf16x2(__uint_as_float(u[e + 2 * i]) * inv,
-                                   __uint_as_float(u[e + 2 * i + 1]) * inv);
-              *reinterpret_cast<uint4*>(ob + e) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-        } else if (row_valid) {
+        if (row_valid) {
           if (out32) {
 #pragma unroll
             for (int e = 0; e < 32; e += 8)
@@ -1359,13 +1063,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) cta_finished(p);
 }
 
-template <int D, int KIND>
+template <int D>
 cudaError_t launch_prefill_d(const AttnParams& p, const CUtensorMap& q_map,
                              const CUtensorMap& kv_map, cudaStream_t stream) {
-  using Lay = PrefillLayout<D, KIND>;
+  using Lay = PrefillLayout<D>;
   const size_t smem = Lay::bytes(p.num_seqs);
   if (smem > 227 * 1024) return cudaErrorInvalidValue;
-  auto kernel = prefill_kernel<D, KIND>;
+  auto kernel = prefill_kernel<D>;
   static SmemLimit limit;
   if (cudaError_t e = limit.ensure(reinterpret_cast<const void*>(kernel), 227 * 1024);
       e != cudaSuccess)
@@ -1393,13 +1097,8 @@ cudaError_t launch_prefill_d(const AttnParams& p, const CUtensorMap& q_map,
 
 }  // namespace
 
-bool prefill_fits(int32_t num_seqs, int32_t head_dim, bool eight) {
+bool prefill_fits(int32_t num_seqs, int32_t head_dim) {
   if (num_seqs < 0) return false;
-  if (eight) {
-    if (head_dim == 128) return PrefillLayout<128, kEight>::bytes(num_seqs) <= 227 * 1024;
-    if (head_dim == 64) return PrefillLayout<64, kEight>::bytes(num_seqs) <= 227 * 1024;
-    return false;
-  }
   if (head_dim == 128) return PrefillLayout<128>::bytes(num_seqs) <= 227 * 1024;
   if (head_dim == 64) return PrefillLayout<64>::bytes(num_seqs) <= 227 * 1024;
   return false;
@@ -1407,16 +1106,9 @@ bool prefill_fits(int32_t num_seqs, int32_t head_dim, bool eight) {
 
 cudaError_t launch_prefill(const AttnParams& p, const CUtensorMap& q_map,
                            const CUtensorMap& kv_map, cudaStream_t stream) {
-  if (p.head_dim != 128 && p.head_dim != 64) return cudaErrorInvalidValue;
-  const bool wide = p.head_dim == 128;
-  if (p.scales)
-    return wide ? launch_prefill_d<128, kEight>(p, q_map, kv_map, stream)
-                : launch_prefill_d<64, kEight>(p, q_map, kv_map, stream);
-  if (p.window > 0)
-    return wide ? launch_prefill_d<128, kWindow>(p, q_map, kv_map, stream)
-                : launch_prefill_d<64, kWindow>(p, q_map, kv_map, stream);
-  return wide ? launch_prefill_d<128, kPlain>(p, q_map, kv_map, stream)
-              : launch_prefill_d<64, kPlain>(p, q_map, kv_map, stream);
+  if (p.head_dim == 128) return launch_prefill_d<128>(p, q_map, kv_map, stream);
+  if (p.head_dim == 64) return launch_prefill_d<64>(p, q_map, kv_map, stream);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace pkv

@@ -88,7 +88,7 @@ pkv_status attention(void* out, int32_t out_f32, float* out_lse, const void* q, 
   const Plan sp = plan_calls(max_query_len, num_heads, num_kv_heads, head_dim, max_seq_len, window,
                              num_sink, eight);
   const bool prefill = max_query_len > sp.max_q;
-  if (prefill && (group > 128 || !pkv::prefill_fits(num_seqs, head_dim, eight)))
+  if (prefill && (group > 128 || !pkv::prefill_rows_fits(num_seqs, head_dim)))
     return PKV_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < sp.total || !aligned(workspace, 256))
     return PKV_ERR_WORKSPACE;
@@ -114,8 +114,9 @@ pkv_status attention(void* out, int32_t out_f32, float* out_lse, const void* q, 
   p.block_size = block_size;
   p.num_blocks = num_blocks;
   p.scale_log2 = scale * 1.4426950408889634f;
-  // without a window every key lies in it
-  p.window = window > 0 ? window : INT32_MAX;
+  // without a window, or with one past every context, every key lies in it (2^30:
+  // positions minus it stay in 32 bits)
+  p.window = window > 0 && window < (1 << 30) ? window : 1 << 30;
   p.num_sink = num_sink;
   char* ws = static_cast<char*>(workspace);
   p.whole_segments = sp.whole;
@@ -159,7 +160,7 @@ pkv_status attention(void* out, int32_t out_f32, float* out_lse, const void* q, 
   } else {
     pp.no_decode = 1;
   }
-  if (pkv::launch_prefill(pp, q_map, eight ? rows : boxes, st) != cudaSuccess) return PKV_ERR_CUDA;
+  if (pkv::launch_prefill_rows(pp, q_map, eight ? rows : boxes, st) != cudaSuccess) return PKV_ERR_CUDA;
   if (!any_short) return PKV_OK;
   p.after_prefill = 1;
   return decode(p);
