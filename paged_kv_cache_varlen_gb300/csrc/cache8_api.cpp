@@ -26,7 +26,7 @@ pkv_status check_rows(const pkv::NormRopeParams& p, int64_t value_bytes) {
   if (p.head_dim % 8 != 0 || p.head_dim > 512) return PKV_ERR_UNSUPPORTED;
   if (p.num_tokens > INT32_MAX - (1 << 16)) return PKV_ERR_UNSUPPORTED;  // the grid counts past it
   const int64_t qrow = (int64_t)p.num_heads * p.head_dim, krow = (int64_t)p.num_kv_heads * p.head_dim;
-  if (qrow + krow > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+  if (qrow + 2 * krow > INT32_MAX) return PKV_ERR_UNSUPPORTED;
   if (!aligned(p.pool, 16) || !aligned(p.k, 16) || !aligned(p.v, 16)) return PKV_ERR_INVALID_ARG;
   if (p.k_stride < krow || p.v_stride < krow || p.k_stride % 8 != 0 || p.v_stride % 8 != 0)
     return PKV_ERR_INVALID_ARG;

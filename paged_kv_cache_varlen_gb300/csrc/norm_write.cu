@@ -17,6 +17,12 @@
 //
 // A head is held by a group of lanes, two 16-byte vectors a lane, so that the
 // sum of squares meets in a few shuffles and the halves of a pair in one lane.
+//
+// What bounds them: bytes, for prompts (8192 tokens of 32 + 8 heads of 128: 201 MB
+// into a bf16 pool, 36 us, 5.6 TB/s; 185 MB into an 8-bit one, 43 us, 4.3 TB/s, where
+// the angles, the magnitudes and the roundings keep the issue slots half busy);
+// latency, for single tokens (3.4 us for one, 5.1 us for 64 of them at 8 bits: a chain
+// of lengths, block, scale, rows).
 #include "common.cuh"
 #include "launch.h"
 #include "rope.cuh"
@@ -26,7 +32,14 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+// of the block kernel: smaller CTAs whose setups overlap (8192 tokens: 43 us; 256
+// threads 46, 64 threads 47)
+constexpr int kBlockThreads = 128;
+constexpr int kBlockWarps = kBlockThreads / 32;
 constexpr uint32_t kFull = 0xffffffffu;
+constexpr int kAhead = 3;  // passes whose copies are under way (5: as fast)
+// CTAs an SM; three of them spill (8192 tokens: 36 us, 40 with three)
+constexpr int kRowCtas = 2;
 
 // Where a pair's two dimensions are: kHalves p and p + r / 2, with r / 2 a
 // multiple of 8 (two vectors of one lane); kPairs 2p and 2p + 1 (one vector);
@@ -84,6 +97,7 @@ __device__ __forceinline__ float norm_factor(const float (&y)[16], int GS, float
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) ss = fmaf(y[i], y[i], ss);
+#pragma unroll
   for (int o = 1; o < GS; o <<= 1) ss += __shfl_xor_sync(kFull, ss, o);
   return rsqrtf(fmaf(ss, inv_dim, eps));
 }
@@ -148,171 +162,20 @@ __device__ __forceinline__ float weight_at(const void* w, int f32, float offset,
   return x + offset;
 }
 
-// A lane's 16 weights from shared memory (vectors that it has none of: 0).
-__device__ __forceinline__ void load_weights(float (&w)[16], const float* ws, const LaneVecs& l) {
+// A lane's values times the norm's factor and the weights, from shared memory.
+__device__ __forceinline__ void scale16(float (&y)[16], float f, const float* ws,
+                                        const LaneVecs& l) {
+  const float* wa = ws + max(l.a, 0) * 8;  // (of a vector that the lane has not: any)
+  const float* wb = ws + max(l.b, 0) * 8;
 #pragma unroll
-  for (int i = 0; i < 8; i += 4) {
-    const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float4 a = l.a >= 0 ? *reinterpret_cast<const float4*>(ws + l.a * 8 + i) : z;
-    const float4 b = l.b >= 0 ? *reinterpret_cast<const float4*>(ws + l.b * 8 + i) : z;
-    *reinterpret_cast<float4*>(w + i) = a;
-    *reinterpret_cast<float4*>(w + 8 + i) = b;
+  for (int i = 0; i < 16; i += 4) {
+    const float4 w = *reinterpret_cast<const float4*>((i < 8 ? wa : wb) + i % 8);
+    y[i] = y[i] * f * w.x;
+    y[i + 1] = y[i + 1] * f * w.y;
+    y[i + 2] = y[i + 2] * f * w.z;
+    y[i + 3] = y[i + 3] * f * w.w;
   }
 }
-
-// Into a bf16 pool through slots: `parts` warps share a token, as in
-// rope_write.cu.
-template <int MODE>
-__global__ void __launch_bounds__(kThreads, 2) norm_rope_kernel(const NormRopeParams p,
-                                                                const int parts) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int D = p.head_dim, H = p.num_heads, Hkv = p.num_kv_heads;
-  const int half = p.rotary_dim / 2;
-  const int V = D / 8, GS = group_lanes(D);
-  const int slots = 32 / GS;          // heads at a time
-  const int pad = 8 * GS;             // pairs, rounded up
-  uint64_t* frac = reinterpret_cast<uint64_t*>(smem);                // [pad]
-  float* wq = reinterpret_cast<float*>(frac + pad);                  // [2 pad]
-  float* wk = wq + 2 * pad;                                          // [2 pad]
-  float* cs = wk + 2 * pad + warp * 2 * pad;                         // [pad]
-  float* sn = cs + pad;
-  float* st = wk + 2 * pad + kWarps * 2 * pad + warp * 512;          // [512] (kAny)
-  griddep_wait();
-  griddep_launch_dependents();
-  int lost = 0;  // whether some frequency is no number
-  for (int i = threadIdx.x; i < half; i += kThreads) {
-    const double f = __ldg(p.inv_freq + i);
-    frac[i] = turn_fraction(f);
-    lost |= no_number(f);
-  }
-  for (int i = threadIdx.x; i < D; i += kThreads) {
-    wq[i] = weight_at(p.q_weight, p.weight_f32, p.weight_offset, i);
-    wk[i] = weight_at(p.k_weight, p.weight_f32, p.weight_offset, i);
-  }
-  lost = __syncthreads_or(lost);
-  const int u = lane % GS, head_slot = lane / GS;
-  const LaneVecs l = lane_vecs<MODE>(u, V, half);
-  const float inv_dim = 1.f / (float)D;
-  const int64_t row = (int64_t)Hkv * D;
-  const int vecs = (int)(row / 8);
-  const int units = p.num_tokens * parts;  // (below 2^31: the host bounds parts by the tokens)
-  for (int unit = blockIdx.x * kWarps + warp; unit < units; unit += gridDim.x * kWarps) {
-    const int t = unit / parts, part = unit - t * parts;
-    const int32_t pos = __ldg(p.positions + t);
-    const int64_t slot = __ldg(p.slots + t);
-    if (pos < 0) {  // uniform: the token is skipped
-      if (lane == 0 && part == 0) set_status(p.status, PKV_DEV_BAD_POSITION);
-      continue;
-    }
-    const bool write = slot >= 0 && slot < p.num_slots;
-    if (!write && slot != -1 && lane == 0 && part == 0) set_status(p.status, PKV_DEV_BAD_SLOT);
-    const uint16_t* q = p.q + (int64_t)t * p.q_stride;
-    const uint16_t* k = p.k + (int64_t)t * p.k_stride;
-    uint16_t* qo = p.q_out + (int64_t)t * H * D;
-    uint16_t* ko = static_cast<uint16_t*>(p.pool) + (write ? slot : 0) * row;
-    const int heads = write ? H + Hkv : H;
-    // the warp's share: heads [h0, h1) of q's and then k's, vectors of v
-    const int h0 = (int)((int64_t)heads * part / parts);
-    const int h1 = (int)((int64_t)heads * (part + 1) / parts);
-
-    __syncwarp();  // the last token's angles have been read
-    for (int i = lane; i < half; i += 32) {
-      const float2 a = rope_angle(frac[i], (uint32_t)pos, p.factor);
-      cs[i] = a.x;
-      sn[i] = a.y;
-    }
-    if (lost)
-      for (int i = lane; i < half; i += 32)
-        if (no_number(__ldg(p.inv_freq + i))) cs[i] = sn[i] = __uint_as_float(kNan);
-    __syncwarp();
-    float c[8], s[8];
-    load_cs(c, s, cs, sn, u);
-#pragma unroll 1
-    for (int kind = 0; kind < 2; ++kind) {  // queries, keys
-      const int a0 = kind == 0 ? h0 : max(h0, H) - H, a1 = kind == 0 ? min(h1, H) : h1 - H;
-      if (a0 >= a1) continue;
-      const uint16_t* in = kind == 0 ? q : k;
-      uint16_t* out = kind == 0 ? qo : ko;
-      const bool normed = (kind == 0 ? p.q_weight : p.k_weight) != nullptr;
-      float w[16];
-      load_weights(w, kind == 0 ? wq : wk, l);
-      constexpr int B = MODE == kAny ? 1 : 2;  // loads of so many heads in flight
-      for (int hb = a0; hb < a1; hb += B * slots) {
-        Vec8 xa[B], xb[B];
-#pragma unroll
-        for (int i = 0; i < B; ++i) {
-          const int h = hb + i * slots + head_slot;
-          xa[i] = xb[i] = Vec8{{0u, 0u, 0u, 0u}};
-          if (h < a1 && l.a >= 0) xa[i] = load8(in + h * D + l.a * 8);
-          if (h < a1 && l.b >= 0) xb[i] = load8(in + h * D + l.b * 8);
-        }
-#pragma unroll
-        for (int i = 0; i < B; ++i) {
-          const int h = hb + i * slots + head_slot;
-          float y[16];
-          unpack8(xa[i], y);
-          unpack8(xb[i], y + 8);
-          if (normed) {
-            const float r = norm_factor(y, GS, inv_dim, p.eps);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) y[j] = y[j] * r * w[j];
-          }
-          turn16<MODE>(y, c, s, l, u, half, cs, sn, st + head_slot * (GS * 16));
-          if (h < a1 && l.a >= 0) store8(out + h * D + l.a * 8, pack8(y));
-          if (h < a1 && l.b >= 0) store8(out + h * D + l.b * 8, pack8(y + 8));
-        }
-      }
-    }
-    if (write) {
-      const uint16_t* v = p.v + (int64_t)t * p.v_stride;
-      uint16_t* vo = ko + p.num_slots * row;
-      const int v1 = (int)((int64_t)vecs * (part + 1) / parts);
-      constexpr int B = 4;
-      for (int i = (int)((int64_t)vecs * part / parts) + lane; i < v1; i += B * 32) {
-        Vec8 a[B];
-#pragma unroll
-        for (int j = 0; j < B; ++j)
-          if (i + j * 32 < v1) a[j] = load8(v + (int64_t)(i + j * 32) * 8);
-#pragma unroll
-        for (int j = 0; j < B; ++j)
-          if (i + j * 32 < v1) store8(vo + (int64_t)(i + j * 32) * 8, a[j]);
-      }
-    }
-  }
-}
-
-template <int MODE>
-cudaError_t launch_norm_rope_mode(const NormRopeParams& p, cudaStream_t stream) {
-  const int pad = 8 * group_lanes(p.head_dim);
-  size_t smem = (size_t)pad * 8 + 4 * pad * sizeof(float) + kWarps * 2 * pad * sizeof(float);
-  if (MODE == kAny) smem += kWarps * 512 * sizeof(float);
-  // (at most 40 KB, at head_dim 512)
-  // warps per token: enough to spread a step over the GPU, no more than leave
-  // a warp about four heads
-  const int heads = p.num_heads + p.num_kv_heads;
-  int parts = 1;
-  while (parts < 16 && parts * 8 <= heads && (int64_t)p.num_tokens * parts < 152 * 16) parts *= 2;
-  const int64_t units = (int64_t)p.num_tokens * parts;
-  int64_t ctas = (units + kWarps - 1) / kWarps;
-  const int64_t most = 152 * 8;  // CTAs that stay for several tokens share what they set up
-  if (ctas > most) ctas = most;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, norm_rope_kernel<MODE>, p, parts);
-}
-
-// ---------------------------------------------------------------------------
-// Into an 8-bit pool
-// ---------------------------------------------------------------------------
 
 // Four values as e4m3 (round to nearest even; beyond the range +-448; NaN stays
 // NaN), the first in the low byte.
@@ -349,16 +212,326 @@ __device__ __forceinline__ float finite_magnitude(float x) {
   return a <= 3.402823466e38f ? a : 0.f;
 }
 
+// Eight values over a scale, as e4m3. The scale of every one of these writes is a power of
+// two: its reciprocal is exact (one that was there before need not be).
+__device__ __forceinline__ uint2 quantise8(const float* y, float scale) {
+  float z[8];
+  if ((__float_as_uint(scale) & 0x7fffffu) == 0) {
+    const float inv = 1.f / scale;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) z[j] = y[j] * inv;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) z[j] = __fdiv_rn(y[j], scale);
+  }
+  return make_uint2(pack_e4m3x4(z[0], z[1], z[2], z[3]), pack_e4m3x4(z[4], z[5], z[6], z[7]));
+}
+// Four stored values under a scale that is `ratio` times smaller than the new one.
+__device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
+  const float2 a = unpack_e4m3x2(w), b = unpack_e4m3x2(w >> 16);
+  return pack_e4m3x4(a.x * ratio, a.y * ratio, b.x * ratio, b.y * ratio);
+}
+
+// Rows of their own: into a bf16 pool through slots, or (EIGHT) one token a request
+// into an 8-bit pool. A pass of a warp takes as many heads as it has groups, of a
+// token's query, key and value heads in this order; every warp has an equal run of the
+// passes of all tokens. A lane fetches its own vectors kAhead passes early into shared
+// memory, where only it reads them: nothing has to be waited for but the lane's own
+// copies, which start before the angles are formed. DIM: the heads' size, 0 for any.
+template <int DIM, int MODE, bool EIGHT>
+__global__ void __launch_bounds__(kThreads, kRowCtas) norm_rope_kernel(const NormRopeParams p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int D = DIM ? DIM : p.head_dim;
+  const int H = EIGHT && !p.q ? 0 : p.num_heads, Hkv = p.num_kv_heads;
+  const int half = p.rotary_dim / 2;
+  const int V = D / 8, GS = group_lanes(D);
+  const int slots = 32 / GS;          // heads of a pass
+  const int pad = 8 * GS;             // pairs, rounded up
+  uint64_t* frac = reinterpret_cast<uint64_t*>(smem);                // [pad]
+  float* wq = reinterpret_cast<float*>(frac + pad);                  // [2 pad]
+  float* wk = wq + 2 * pad;                                          // [2 pad]
+  float* cs = wk + 2 * pad + warp * 2 * pad;                         // [pad]
+  float* sn = cs + pad;
+  uint8_t* ring = reinterpret_cast<uint8_t*>(wk + 2 * pad + kWarps * 2 * pad) +
+                  warp * (kAhead + 1) * 1024 + lane * 16;            // [kAhead + 1][2][32][16]
+  float* st = wk + 2 * pad + kWarps * 2 * pad + kWarps * (kAhead + 1) * 256 + warp * 512;  // kAny
+  griddep_wait();
+  griddep_launch_dependents();
+  const int u = lane % GS, head_slot = lane / GS;
+  const LaneVecs l = lane_vecs<MODE>(u, V, half);
+  const bool has_a = DIM || l.a >= 0, has_b = DIM || l.b >= 0;
+  const float inv_dim = 1.f / (float)D;
+  const int64_t row = (int64_t)Hkv * D;
+  const int passes = (H + 2 * Hkv + slots - 1) / slots;
+  // the warp's run: n passes from pass `pass` of row t on
+  const int64_t total = (int64_t)(EIGHT ? p.num_seqs : p.num_tokens) * passes;
+  const int64_t warps = min(total, (int64_t)gridDim.x * kWarps);
+  const int64_t w = (int64_t)blockIdx.x * kWarps + warp;
+  const int64_t begin = w < warps ? total * w / warps : 0;
+  const int n = w < warps ? (int)(total * (w + 1) / warps - begin) : 0;
+  int t = (int)(begin / passes), pass = (int)(begin - (int64_t)t * passes);
+
+  // EIGHT: request r's token, -1 where it has none (or lengths that are no good)
+  auto token_of = [&](int r, int32_t& len, bool& bad) -> int {
+    const int32_t a = __ldg(p.cu_seqlens + r), b = __ldg(p.cu_seqlens + r + 1);
+    len = __ldg(p.seq_lens + r);
+    bad = a < 0 || b < a || b > p.num_tokens ||
+          (b > a && (len < 1 || b - a > 1 || len > p.max_blocks * p.block_size));
+    return bad || b == a ? -1 : a;
+  };
+  struct Row {
+    int token;     // -1: none
+    int32_t pos;
+    int64_t slot;  // the pool's row
+    int32_t id;    // EIGHT: the block, the rows that it held
+    int held;
+    bool bad;
+  };
+  auto look = [&](int i) {
+    Row x;
+    x.bad = false;
+    x.id = -1;
+    x.held = 0;
+    x.slot = -1;
+    if (EIGHT) {
+      int32_t len;
+      x.token = token_of(i, len, x.bad);
+      if (x.token >= 0) {
+        const int block = (len - 1) / p.block_size;
+        x.id = __ldg(p.block_table + (int64_t)i * p.max_blocks + block);
+        x.held = len - 1 - block * p.block_size;
+        if (x.id >= 0 && x.id < p.num_blocks) x.slot = (int64_t)x.id * p.block_size + x.held;
+      }
+    } else {
+      x.token = i;
+      x.slot = __ldg(p.slots + i);
+    }
+    x.pos = (!EIGHT || p.positions) && x.token >= 0 ? __ldg(p.positions + x.token) : 0;
+    return x;
+  };
+
+  // the copies' place in the run
+  int left = n, ft = t, fpass = pass, to = 0, ftok = -1;
+  const uint16_t *fq = nullptr, *fk = nullptr, *fv = nullptr;  // of the row, less heads before
+  auto fetch = [&] {
+    if (left > 0) {
+      if (left == n || fpass == 0) {
+        int32_t len;
+        bool bad;
+        ftok = EIGHT ? token_of(ft, len, bad) : ft;
+        fq = p.q + ftok * p.q_stride;
+        fk = p.k + ftok * p.k_stride - H * D;
+        fv = p.v + ftok * p.v_stride - (H + Hkv) * D;
+      }
+      const int h = fpass * slots + head_slot;
+      const uint16_t* x = (h < H ? fq : h < H + Hkv ? fk : fv) + h * D;
+      const uint32_t at = smem_addr(ring + to * 1024);
+      if (ftok >= 0 && h < H + 2 * Hkv) {
+        if (has_a) cp_async_16(at, x + l.a * 8, 16);
+        if (has_b) cp_async_16(at + 512, x + l.b * 8, 16);
+      }
+      --left;
+      if (++fpass == passes) {
+        fpass = 0;
+        ++ft;
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    to = to == kAhead ? 0 : to + 1;
+  };
+#pragma unroll 1
+  for (int i = 0; i < kAhead; ++i) fetch();
+  Row next{};
+  if (n > 0) next = look(t);
+
+  int lost = 0;  // whether some frequency is no number
+  for (int i = threadIdx.x; i < half; i += kThreads) {
+    const double f = __ldg(p.inv_freq + i);
+    frac[i] = turn_fraction(f);
+    lost |= no_number(f);
+  }
+  for (int i = threadIdx.x; i < D; i += kThreads) {
+    wq[i] = weight_at(p.q_weight, p.weight_f32, p.weight_offset, i);
+    wk[i] = weight_at(p.k_weight, p.weight_f32, p.weight_offset, i);
+  }
+  lost = __syncthreads_or(lost);
+
+  Row now{};
+  bool good = false, write = false;
+  uint16_t *oq = nullptr, *ok = nullptr, *ov = nullptr;  // where the row goes, less heads before
+  uint8_t *ek = nullptr, *ev = nullptr;                  // (EIGHT)
+  float c[8], s[8];
+  float had = 0.f;  // EIGHT: the scale that the lane's head of the next pass finds
+  // EIGHT: where the scale of the lane's head of a pass is
+  auto scale_of = [&](int i) -> float* {
+    const int h = i * slots + head_slot - H;
+    if (!write || h < 0 || h >= 2 * Hkv) return nullptr;
+    return p.scales + (h < Hkv ? (int64_t)now.id * Hkv + h
+                               : ((int64_t)p.num_blocks + now.id) * Hkv + h - Hkv);
+  };
+  int from = 0;
+#pragma unroll 1
+  for (int i = 0; i < n; ++i, ++pass) {
+    if (pass == passes) pass = 0;
+    if (i == 0 || pass == 0) {  // the next row
+      now = next;
+      good = now.token >= 0 && now.pos >= 0;
+      write = now.token >= 0 && now.slot >= 0 && now.slot < p.num_slots;
+      if (lane == 0 && pass == 0) {
+        if (now.bad) set_status(p.status, PKV_DEV_BAD_LENGTHS);
+        if (now.token >= 0 && now.pos < 0) set_status(p.status, PKV_DEV_BAD_POSITION);
+        if (EIGHT && now.token >= 0 && !write) set_status(p.status, PKV_DEV_BAD_BLOCK);
+        if (!EIGHT && good && !write && now.slot != -1) set_status(p.status, PKV_DEV_BAD_SLOT);
+      }
+      oq = p.q_out + (int64_t)now.token * H * D;
+      const int64_t first = (write ? now.slot : 0) * row - H * D;
+      if (EIGHT) {
+        ek = static_cast<uint8_t*>(p.pool) + first;
+        ev = ek + p.num_slots * row - Hkv * D;
+      } else {
+        ok = static_cast<uint16_t*>(p.pool) + first;
+        ov = ok + p.num_slots * row - Hkv * D;
+      }
+      if (EIGHT && now.held > 0 && scale_of(pass)) had = *scale_of(pass);
+      ++t;
+      if (i + passes - pass < n) next = look(t);
+      __syncwarp();  // the last row's angles have been read
+      for (int e = lane; e < half; e += 32) {
+        const float2 a = rope_angle(frac[e], (uint32_t)now.pos, p.factor);
+        cs[e] = a.x;
+        sn[e] = a.y;
+      }
+      if (lost)
+        for (int e = lane; e < half; e += 32)
+          if (no_number(__ldg(p.inv_freq + e))) cs[e] = sn[e] = __uint_as_float(kNan);
+      __syncwarp();
+      load_cs(c, s, cs, sn, u);
+    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+    Vec8 xa = Vec8{{0u, 0u, 0u, 0u}}, xb = xa;
+    if (has_a) xa = load8(reinterpret_cast<const uint16_t*>(ring + from * 1024));
+    if (has_b) xb = load8(reinterpret_cast<const uint16_t*>(ring + from * 1024 + 512));
+    from = from == kAhead ? 0 : from + 1;
+    fetch();  // (into the stage read in the pass before)
+    const int h = pass * slots + head_slot;
+    const bool query = h < H, key = !query && h < H + Hkv;
+    const bool store = good && h < H + 2 * Hkv && (query || write);
+    float y[16];
+    if (EIGHT || pass * slots < H + Hkv) {  // uniform: not bf16 values alone
+      const bool normed = query ? p.q_weight != nullptr : key && p.k_weight != nullptr;
+      unpack8(xa, y);
+      unpack8(xb, y + 8);
+      if (pass * slots < H + Hkv) {
+        const float f = norm_factor(y, GS, inv_dim, p.eps);
+        if (normed) scale16(y, f, query ? wq : wk, l);
+        turn16<MODE>(y, c, s, l, u, half, cs, sn, st + head_slot * (GS * 16));
+        if (EIGHT && !query && !key) {  // a value beside keys
+          unpack8(xa, y);
+          unpack8(xb, y + 8);
+        }
+      }
+    }
+    if (!EIGHT || pass * slots < H) {
+      if (query || (!EIGHT && key)) {
+        xa = pack8(y);
+        xb = pack8(y + 8);
+      }
+      uint16_t* out = (query ? oq : EIGHT ? nullptr : key ? ok : ov) + h * D;
+      if (store && (!EIGHT || query)) {
+        if (has_a) store8(out + l.a * 8, xa);
+        if (has_b) store8(out + l.b * 8, xb);
+      }
+    }
+    if (EIGHT) {
+      float top = 0.f;
+      if (good)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) top = fmaxf(top, finite_magnitude(y[j]));
+      for (int o = 1; o < GS; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+      const float old = had;
+      float* scale_at = scale_of(pass);
+      had = now.held > 0 && pass + 1 < passes && scale_of(pass + 1) ? *scale_of(pass + 1) : 0.f;
+      if (scale_at) {
+        const float scale = fmaxf(old, block_scale(top));
+        uint8_t* rows = (key ? ek : ev) + h * D;
+        if (scale != old) {
+          const float ratio = old > 0.f ? old / scale : 0.f;
+          for (int e = 1; e <= now.held; ++e) {  // 16 bytes of each of the block's rows
+            uint4* o = reinterpret_cast<uint4*>(rows - e * row + u * 16);
+            const uint4 x = *o;
+            *o = make_uint4(rescale4(x.x, ratio), rescale4(x.y, ratio), rescale4(x.z, ratio),
+                            rescale4(x.w, ratio));
+          }
+          if (u == 0) *scale_at = scale;
+        }
+        if (store && has_a) *reinterpret_cast<uint2*>(rows + l.a * 8) = quantise8(y, scale);
+        if (store && has_b) *reinterpret_cast<uint2*>(rows + l.b * 8) = quantise8(y + 8, scale);
+      }
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+template <int DIM, int MODE, bool EIGHT>
+cudaError_t launch_rows_mode(const NormRopeParams& p, cudaStream_t stream) {
+  const int pad = 8 * group_lanes(p.head_dim), slots = 32 / group_lanes(p.head_dim);
+  size_t smem = (size_t)pad * 8 + 4 * pad * sizeof(float) + kWarps * 2 * pad * sizeof(float) +
+                kWarps * (kAhead + 1) * 1024;
+  if (MODE == kAny) smem += kWarps * 512 * sizeof(float);
+  auto kernel = norm_rope_kernel<DIM, MODE, EIGHT>;
+  if (smem > 48 * 1024) {  // (at most 72 KB, at head_dim 512)
+    static SmemLimit limit;
+    cudaError_t e = limit.ensure(reinterpret_cast<const void*>(kernel), 80 * 1024);
+    if (e != cudaSuccess) return e;
+  }
+  const int passes = ((EIGHT && !p.q ? 0 : p.num_heads) + 2 * p.num_kv_heads + slots - 1) / slots;
+  const int64_t total = (int64_t)(EIGHT ? p.num_seqs : p.num_tokens) * passes;
+  const int64_t ctas = (total + kWarps - 1) / kWarps, most = 152 * kRowCtas;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(ctas < most ? ctas : most));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <int DIM, bool EIGHT>
+cudaError_t launch_rows_dim(const NormRopeParams& p, cudaStream_t stream) {
+  if (p.interleaved || p.rotary_dim == 0) return launch_rows_mode<DIM, kPairs, EIGHT>(p, stream);
+  if ((p.rotary_dim / 2) % 8 == 0) return launch_rows_mode<DIM, kHalves, EIGHT>(p, stream);
+  return launch_rows_mode<DIM, kAny, EIGHT>(p, stream);
+}
+// The common head sizes have kernels of their own: all vectors are there, and loops
+// over lanes unroll.
+template <bool EIGHT>
+cudaError_t launch_rows(const NormRopeParams& p, cudaStream_t stream) {
+  if (p.head_dim == 128) return launch_rows_dim<128, EIGHT>(p, stream);
+  if (p.head_dim == 64) return launch_rows_dim<64, EIGHT>(p, stream);
+  if (EIGHT) return cudaErrorInvalidValue;
+  return launch_rows_dim<0, false>(p, stream);
+}
+
+// ---------------------------------------------------------------------------
+// Into an 8-bit pool, several tokens of a request
+// ---------------------------------------------------------------------------
+
 // One CTA: the rows that the step adds to one block of one request, a share of
-// the heads. A warp holds the rows of one head, 16 at a time, in registers: their
-// largest magnitude gives the scale, and they are written without being read
-// again (blocks of more than 16 rows read them twice, the second time from L2).
-template <int D, int MODE>
-__global__ void __launch_bounds__(kThreads, 2) append_fp8_kernel(const NormRopeParams p,
+// the heads. A warp holds a group of rows of one head in registers: their largest
+// magnitude gives the scale, and they are written without being read again (blocks of
+// several groups read them twice, the second time from L2). The next group's rows
+// come into shared memory meanwhile (50 us without, 46 with, at 256 threads).
+template <int D, int MODE, int NP>
+__global__ void __launch_bounds__(kBlockThreads, 512 / kBlockThreads) append_fp8_kernel(const NormRopeParams p,
                                                                  const int parts) {
   constexpr int V = D / 8, GS = group_lanes(D);
   constexpr int RP = 32 / GS;   // rows at a time
-  constexpr int NP = 16 / RP;   // of 16
+  constexpr int RG = NP * RP;   // of a group
   constexpr int PAD = D / 2;    // pairs, rounded up
   extern __shared__ __align__(16) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -367,7 +540,12 @@ __global__ void __launch_bounds__(kThreads, 2) append_fp8_kernel(const NormRopeP
   float* wq = reinterpret_cast<float*>(smem);  // [D]
   float* wk = wq + D;                          // [D]
   float* st = wk + D + warp * 512;             // [512] (kAny)
-  float* cs = wk + D + (MODE == kAny ? kWarps * 512 : 0);  // [BS][PAD], then the sines
+  // the warp's ring: [2][NP][2][32][16], a lane's vectors of the rows of a head
+  uint8_t* ring = reinterpret_cast<uint8_t*>(wk + D + (MODE == kAny ? kBlockWarps * 512 : 0)) +
+                  warp * 2 * NP * 1024 + lane * 16;
+  uint8_t* good = reinterpret_cast<uint8_t*>(wk + D + (MODE == kAny ? kBlockWarps * 512 : 0)) +
+                  kBlockWarps * 2 * NP * 1024;             // [256]: whether a row's position is good
+  float* cs = reinterpret_cast<float*>(good + 256);   // [BS][PAD], then the sines
   float* sn = cs + BS * PAD;
   griddep_wait();
   griddep_launch_dependents();
@@ -375,20 +553,17 @@ __global__ void __launch_bounds__(kThreads, 2) append_fp8_kernel(const NormRopeP
 
   // Item x of the grid belongs to the request r with f(r) <= x < f(r + 1), where
   // f(r) = cu[r] / BS + 2 r leaves each request room for every block it touches.
-  int r = item, local = 0;
-  if (p.max_query_len > 1) {
-    int count = 0;
-    for (int base = 0; base < p.num_seqs; base += kThreads) {
-      const int i = base + threadIdx.x;
-      const bool at = i < p.num_seqs && __ldg(p.cu_seqlens + i) / BS + 2 * i <= item;
-      const int n = __syncthreads_count(at);
-      count += n;
-      if (n < kThreads) break;
-    }
-    r = count - 1;
-    if (r < 0) return;
-    local = item - (__ldg(p.cu_seqlens + r) / BS + 2 * r);
+  int count = 0;
+  for (int base = 0; base < p.num_seqs; base += kBlockThreads) {
+    const int i = base + threadIdx.x;
+    const bool at = i < p.num_seqs && __ldg(p.cu_seqlens + i) / BS + 2 * i <= item;
+    const int n = __syncthreads_count(at);
+    count += n;
+    if (n < kBlockThreads) break;
   }
+  const int r = count - 1;
+  if (r < 0) return;
+  const int local = item - (__ldg(p.cu_seqlens + r) / BS + 2 * r);
   auto bad_lengths = [&](int i) {
     const int32_t a = __ldg(p.cu_seqlens + i), b = __ldg(p.cu_seqlens + i + 1);
     if (a < 0 || b < a || b > p.num_tokens) return true;
@@ -396,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_fp8_kernel(const NormRopeP
     return b > a && (len < b - a || b - a > p.max_query_len || len > p.max_blocks * BS);
   };
   if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < p.num_seqs; i += kThreads)
+    for (int i = threadIdx.x; i < p.num_seqs; i += kBlockThreads)
       if (bad_lengths(i)) set_status(p.status, PKV_DEV_BAD_LENGTHS);
   if (bad_lengths(r)) return;
   const int32_t t0 = __ldg(p.cu_seqlens + r), qlen = __ldg(p.cu_seqlens + r + 1) - t0;
@@ -410,12 +585,55 @@ __global__ void __launch_bounds__(kThreads, 2) append_fp8_kernel(const NormRopeP
   const bool write = id >= 0 && id < p.num_blocks;
   if (!write && threadIdx.x == 0) set_status(p.status, PKV_DEV_BAD_BLOCK);
 
-  for (int i = threadIdx.x; i < D; i += kThreads) {
+  const int u = lane % GS, row_slot = lane / GS;
+  const LaneVecs l = lane_vecs<MODE>(u, V, half);
+  constexpr float inv_dim = 1.f / (float)D;
+  const int g0 = first / RG, g1 = (last - 1) / RG;  // groups of rows
+  // A job is a head: of the keys, the values, the queries. The rows of one come into
+  // the ring while those before are worked on.
+  const int kv = write ? 2 * Hkv : 0, jobs = kv + (p.q ? H : 0);
+  const int job0 = part * kBlockWarps + warp, stride_jobs = parts * kBlockWarps;
+  // keys and values of more than one group are read twice
+  auto sweeps = [&](int job) { return job < kv && g0 != g1 ? 2 : 1; };
+  int fjob = job0, fg = g0, fsweep = 0, to = 0;
+  auto fetch = [&] {
+    if (fjob < jobs) {
+      const bool query = fjob >= kv, key = !query && fjob < Hkv;
+      const int h = query ? fjob - kv : key ? fjob : fjob - Hkv;
+      const int64_t stride = query ? p.q_stride : key ? p.k_stride : p.v_stride;
+      const uint16_t* x = (query ? p.q : key ? p.k : p.v) + h * D;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const int row = fg * RG + i * RP + row_slot;
+        if (row < first || row >= last) continue;
+        const uint16_t* at = x + (tok0 + row) * stride;
+        const uint32_t dst = smem_addr(ring + (to * NP + i) * 1024);
+        cp_async_16(dst, at + l.a * 8, 16);
+        cp_async_16(dst + 512, at + l.b * 8, 16);
+      }
+      if (++fg > g1) {
+        fg = g0;
+        if (++fsweep == sweeps(fjob)) {
+          fsweep = 0;
+          fjob += stride_jobs;
+        }
+      }
+      to ^= 1;
+    }
+  };
+  fetch();
+
+  for (int i = threadIdx.x; i < D; i += kBlockThreads) {
     wq[i] = weight_at(p.q_weight, p.weight_f32, p.weight_offset, i);
     wk[i] = weight_at(p.k_weight, p.weight_f32, p.weight_offset, i);
   }
+  for (int row = first + threadIdx.x; row < last; row += kBlockThreads) {
+    const bool ok = !p.positions || __ldg(p.positions + tok0 + row) >= 0;
+    good[row] = ok;
+    if (!ok && part == 0) set_status(p.status, PKV_DEV_BAD_POSITION);
+  }
   if (half > 0)
-    for (int e = threadIdx.x; e < (last - first) * half; e += kThreads) {
+    for (int e = threadIdx.x; e < (last - first) * half; e += kBlockThreads) {
       const int row = first + e / half, i = e % half;
       const double f = __ldg(p.inv_freq + i);
       const int32_t pos = __ldg(p.positions + tok0 + row);
@@ -426,50 +644,30 @@ __global__ void __launch_bounds__(kThreads, 2) append_fp8_kernel(const NormRopeP
     }
   __syncthreads();
 
-  const int u = lane % GS, row_slot = lane / GS;
-  const LaneVecs l = lane_vecs<MODE>(u, V, half);
-  constexpr float inv_dim = 1.f / (float)D;
-  const int g0 = first / 16, g1 = (last - 1) / 16;  // groups of 16 rows
-  // whether a row is one of the new ones (and its position good)
-  auto is_new = [&](int row) {
-    return row >= first && row < last &&
-           (!p.positions || __ldg(p.positions + tok0 + row) >= 0);
-  };
-  if (p.positions && part == 0)
-    for (int row = first + threadIdx.x; row < last; row += kThreads)
-      if (__ldg(p.positions + tok0 + row) < 0) set_status(p.status, PKV_DEV_BAD_POSITION);
-  // rows of group g of one head, normed and turned
-  auto rows_of = [&](const uint16_t* in, int64_t stride, bool normed, const float* ws, bool turned,
-                     int g, float (&y)[NP][16], bool (&ok)[NP]) {
-    Vec8 xa[NP], xb[NP];
+  // the next rows of the ring, group g of one head, normed and turned
+  int from = 0;
+  auto rows_of = [&](bool normed, const float* ws, bool turned, int g, float (&y)[NP][16],
+                     bool (&ok)[NP]) {
+    cp_async_wait_all();
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const int row = g * 16 + i * RP + row_slot;
-      ok[i] = is_new(row);
-      xa[i] = xb[i] = Vec8{{0u, 0u, 0u, 0u}};
-      const uint16_t* x = in + (int64_t)(tok0 + row) * stride;
-      if (ok[i] && l.a >= 0) xa[i] = load8(x + l.a * 8);
-      if (ok[i] && l.b >= 0) xb[i] = load8(x + l.b * 8);
+      const int row = g * RG + i * RP + row_slot;
+      ok[i] = row >= first && row < last && good[row];
+      const uint8_t* at = ring + (from * NP + i) * 1024;
+      const Vec8 none = Vec8{{0u, 0u, 0u, 0u}};
+      unpack8(ok[i] ? load8(reinterpret_cast<const uint16_t*>(at)) : none, y[i]);
+      unpack8(ok[i] ? load8(reinterpret_cast<const uint16_t*>(at + 512)) : none, y[i] + 8);
     }
+    from ^= 1;
+    fetch();  // (into the stage read before this one)
+    if (normed)
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      unpack8(xa[i], y[i]);
-      unpack8(xb[i], y[i] + 8);
-    }
-    if (normed) {
-      float w[16];
-      load_weights(w, ws, l);
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const float f = norm_factor(y[i], GS, inv_dim, p.eps);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) y[i][j] = y[i][j] * f * w[j];
-      }
-    }
+      for (int i = 0; i < NP; ++i)
+        scale16(y[i], norm_factor(y[i], GS, inv_dim, p.eps), ws, l);
     if (turned)
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        const int row = min(max(g * 16 + i * RP + row_slot, first), last - 1);
+        const int row = min(max(g * RG + i * RP + row_slot, first), last - 1);
         float c[8], s[8];
         if (MODE != kAny) load_cs(c, s, cs + row * PAD, sn + row * PAD, u);
         turn16<MODE>(y[i], c, s, l, u, half, cs + row * PAD, sn + row * PAD,
@@ -477,33 +675,29 @@ __global__ void __launch_bounds__(kThreads, 2) append_fp8_kernel(const NormRopeP
       }
   };
 
-  const int jobs = (write ? 2 * Hkv : 0) + (p.q ? H : 0);
-  for (int job = part * kWarps + warp; job < jobs; job += parts * kWarps) {
-    const int kv = write ? 2 * Hkv : 0;
+  for (int job = job0; job < jobs; job += stride_jobs) {
     float y[NP][16];
     bool ok[NP];
     if (job >= kv) {  // a query head
       const int h = job - kv;
       for (int g = g0; g <= g1; ++g) {
-        rows_of(p.q + h * D, p.q_stride, p.q_weight != nullptr, wq, half > 0, g, y, ok);
+        rows_of(p.q_weight != nullptr, wq, half > 0, g, y, ok);
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-          const int row = g * 16 + i * RP + row_slot;
+          const int row = g * RG + i * RP + row_slot;
           uint16_t* out = p.q_out + ((int64_t)(tok0 + row) * H + h) * D;
-          if (ok[i] && l.a >= 0) store8(out + l.a * 8, pack8(y[i]));
-          if (ok[i] && l.b >= 0) store8(out + l.b * 8, pack8(y[i] + 8));
+          if (ok[i]) store8(out + l.a * 8, pack8(y[i]));
+          if (ok[i]) store8(out + l.b * 8, pack8(y[i] + 8));
         }
       }
       continue;
     }
     const bool key = job < Hkv;
     const int h = key ? job : job - Hkv;
-    const uint16_t* in = (key ? p.k : p.v) + h * D;
-    const int64_t stride = key ? p.k_stride : p.v_stride;
     const bool normed = key && p.k_weight != nullptr, turned = key && half > 0;
     float top = 0.f;
     for (int g = g0; g <= g1; ++g) {
-      rows_of(in, stride, normed, wk, turned, g, y, ok);
+      rows_of(normed, wk, turned, g, y, ok);
 #pragma unroll
       for (int i = 0; i < NP; ++i)
 #pragma unroll
@@ -523,61 +717,45 @@ __global__ void __launch_bounds__(kThreads, 2) append_fp8_kernel(const NormRopeP
       const float ratio = old > 0.f ? old / scale : 0.f;
       for (int e = lane; e < first * (D / 4); e += 32) {
         uint32_t* at = reinterpret_cast<uint32_t*>(rows + (e / (D / 4)) * step) + e % (D / 4);
-        const float2 a = unpack_e4m3x2(*at), b = unpack_e4m3x2(*at >> 16);
-        *at = pack_e4m3x4(a.x * ratio, a.y * ratio, b.x * ratio, b.y * ratio);
+        *at = rescale4(*at, ratio);
       }
     }
     __syncwarp();  // every lane has read the old scale
     if (lane == 0 && scale != old) *scale_at = scale;
-    // a power of two (every scale of these writes): its reciprocal is exact
-    const bool exact = (__float_as_uint(scale) & 0x7fffffu) == 0;
-    const float inv = 1.f / scale;
     for (int g = g0; g <= g1; ++g) {
-      if (g0 != g1) rows_of(in, stride, normed, wk, turned, g, y, ok);
+      if (g0 != g1) rows_of(normed, wk, turned, g, y, ok);
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        uint8_t* out = rows + (g * 16 + i * RP + row_slot) * step;
-        if (!exact)
-#pragma unroll
-          for (int j = 0; j < 16; ++j) y[i][j] = __fdiv_rn(y[i][j], scale);
-        else
-#pragma unroll
-          for (int j = 0; j < 16; ++j) y[i][j] *= inv;
-        if (ok[i] && l.a >= 0)
-          *reinterpret_cast<uint2*>(out + l.a * 8) =
-              make_uint2(pack_e4m3x4(y[i][0], y[i][1], y[i][2], y[i][3]),
-                         pack_e4m3x4(y[i][4], y[i][5], y[i][6], y[i][7]));
-        if (ok[i] && l.b >= 0)
-          *reinterpret_cast<uint2*>(out + l.b * 8) =
-              make_uint2(pack_e4m3x4(y[i][8], y[i][9], y[i][10], y[i][11]),
-                         pack_e4m3x4(y[i][12], y[i][13], y[i][14], y[i][15]));
+        uint8_t* out = rows + (g * RG + i * RP + row_slot) * step;
+        if (ok[i]) *reinterpret_cast<uint2*>(out + l.a * 8) = quantise8(y[i], scale);
+        if (ok[i])
+          *reinterpret_cast<uint2*>(out + l.b * 8) = quantise8(y[i] + 8, scale);
       }
     }
   }
 }
 
-template <int D, int MODE>
-cudaError_t launch_append_mode(const NormRopeParams& p, cudaStream_t stream) {
-  size_t smem = 2 * D * sizeof(float) + (MODE == kAny ? kWarps * 512 * sizeof(float) : 0);
+template <int D, int MODE, int NP>
+cudaError_t launch_append_rows(const NormRopeParams& p, cudaStream_t stream) {
+  size_t smem = 2 * D * sizeof(float) + (MODE == kAny ? kBlockWarps * 512 * sizeof(float) : 0) +
+                kBlockWarps * 2 * NP * 1024 + 256;
   if (p.rotary_dim > 0) smem += (size_t)p.block_size * D * sizeof(float);
-  auto kernel = append_fp8_kernel<D, MODE>;
+  auto kernel = append_fp8_kernel<D, MODE, NP>;
   if (smem > 48 * 1024) {
     static SmemLimit limit;
-    cudaError_t e = limit.ensure(reinterpret_cast<const void*>(kernel), 200 * 1024);
+    cudaError_t e = limit.ensure(reinterpret_cast<const void*>(kernel), 216 * 1024);
     if (e != cudaSuccess) return e;
   }
-  const int64_t items = p.max_query_len == 1
-                            ? p.num_seqs
-                            : (int64_t)p.num_tokens / p.block_size + 2 * (int64_t)p.num_seqs;
+  const int64_t items = (int64_t)p.num_tokens / p.block_size + 2 * (int64_t)p.num_seqs;
   // shares of a block's heads: enough CTAs for the GPU, no more than leave a
   // warp one head
   const int jobs = 2 * p.num_kv_heads + (p.q ? p.num_heads : 0);
   const int64_t blocks = p.num_tokens / p.block_size + p.num_seqs;  // about
   int parts = 1;
-  while (parts * kWarps < jobs && blocks * parts < 152 * 4) ++parts;
+  while (parts * kBlockWarps < jobs && blocks * parts < 152 * 4) ++parts;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(items * parts));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kBlockThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -586,6 +764,16 @@ cudaError_t launch_append_mode(const NormRopeParams& p, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, p, parts);
+}
+
+// A group of rows: 16 at 128 dimensions, and at 64 where the blocks are no longer; 32
+// at 64 dimensions otherwise.
+template <int D, int MODE>
+cudaError_t launch_append_mode(const NormRopeParams& p, cudaStream_t stream) {
+  if constexpr (D == 64) {
+    if (p.block_size == 16) return launch_append_rows<D, MODE, 2>(p, stream);
+  }
+  return launch_append_rows<D, MODE, 4>(p, stream);
 }
 
 template <int D>
@@ -598,15 +786,16 @@ cudaError_t launch_append_d(const NormRopeParams& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_append_fp8(const NormRopeParams& p, cudaStream_t stream) {
+  // a token a request: by rows (64 requests of 32 + 8 heads: 5.1 us; 10.0 by blocks,
+  // most of whose lanes hold rows that there are not)
+  if (p.max_query_len == 1) return launch_rows<true>(p, stream);
   if (p.head_dim == 128) return launch_append_d<128>(p, stream);
   if (p.head_dim == 64) return launch_append_d<64>(p, stream);
   return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_norm_rope(const NormRopeParams& p, cudaStream_t stream) {
-  if (p.interleaved || p.rotary_dim == 0) return launch_norm_rope_mode<kPairs>(p, stream);
-  if ((p.rotary_dim / 2) % 8 == 0) return launch_norm_rope_mode<kHalves>(p, stream);
-  return launch_norm_rope_mode<kAny>(p, stream);
+  return launch_rows<false>(p, stream);
 }
 
 }  // namespace pkv
