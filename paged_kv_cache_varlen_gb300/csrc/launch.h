@@ -136,6 +136,8 @@ struct AttnParams {
   // with whole_segments no context is divided. ws_out: the pieces of divided
   // contexts, ws_lse: where the shares begin
   int32_t num_shares, whole_segments;
+  float* prefill_parts;       // their prefill grid's pieces of divided items
+  int32_t prefill_join;       // a grid of its own joins these
 };
 
 // The keys that the queries of one request see, in units of `tile` keys: the
@@ -211,10 +213,20 @@ bool prefill_fits(int32_t num_seqs, int32_t head_dim);
 
 // The same of the calls with a window or an 8-bit pool: requests of more than
 // decode_max_q queries. `kv_map`: of a bf16 pool as for launch_prefill, of an 8-bit
-// one encode_kv8_view. p.sched[0] is zero before the launch.
+// one encode_kv8_view. prefill_rows_sched() bytes of p.sched are zero before the
+// launch; p.prefill_parts has prefill_rows_workspace() bytes.
+size_t prefill_rows_sched();
+size_t prefill_rows_workspace(int32_t head_dim);
 cudaError_t launch_prefill_rows(const AttnParams& p, const CUtensorMap& q_map,
                                 const CUtensorMap& kv_map, cudaStream_t stream);
 bool prefill_rows_fits(int32_t num_seqs, int32_t head_dim);
+// Behind that grid (and the decode grid's), where p.prefill_join is set: joins the items
+// that were cut. That is faster where each is cut into many pieces, in calls of few
+// items (64 queries of 32 heads over 65536 keys, 8 items, 8 bits: 103 us; 121 when the
+// CTA that comes last joins its item's pieces); the launch costs more than it saves
+// where there are two of each (a mixed batch: 47 us, 40).
+bool prefill_rows_join(const AttnParams& p);
+cudaError_t launch_prefill_rows_join(const AttnParams& p, cudaStream_t stream);
 
 // Shared-prefix (cascade) merge: row r of out (num_rows = B * H rows of
 // head_dim) from the tail partial (slot 0) and the prefix segments (slots

@@ -51,13 +51,27 @@ static_assert(2 * kSoftmaxRegs + 2 * kOtherRegs == 4 * (65536 / kThreads),
 constexpr uint32_t kTmemCols = 512;
 constexpr int kRing = 4;  // items announced ahead of their readers
 constexpr int kItemReaders = 8 + 4 + 3;  // softmax and converter warps, products, V
-constexpr int kSortMax = 2048;
+constexpr int kSortMax = 768;
+// In 64-key tiles' time: what an item costs to begin, what cutting costs a CTA; cycles
+// of one, and bytes of the pool that an SM of the decode grid reads in a cycle (for the
+// split of the SMs in a call with both kinds of request).
+constexpr int kItemTiles = 4;
+constexpr float kPieceTiles = 9.f;
+constexpr float kTileCycles = 2000.f;
+constexpr float kDecodeBytesPerCycle = 40.f;
+constexpr int kCutUnits = 2 * kThreads;  // calls of more units are not cut
+constexpr int kCutKeys = 1 << 24;        // nor of longer contexts (the sums stay in 32 bits)
+constexpr int kMinShare = 4;             // tiles
+// p.sched from here on: of each CTA, what it says of the item that begins in its share
+// and is cut: 8 warps' counts of finished pieces, or (prefill_join) a record
+constexpr int kRecords = 64;
+constexpr int kMaxCtas = 152;  // shares at most: their pieces have room in the workspace
 constexpr float kRescaleThreshold = 8.f;
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr uint32_t kMinusInf = 0xff800000u;
 
 constexpr size_t list_ints(int num_seqs) {
-  return (num_seqs <= kSortMax ? 4 : 1) * ((size_t)num_seqs + 1);
+  return (num_seqs <= kSortMax ? 5 : 1) * ((size_t)num_seqs + 1);
 }
 
 template <int D>
@@ -71,7 +85,7 @@ struct Layout {
   static constexpr int K_OFF = Q_OFF + 2 * TILE_BYTES;
   static constexpr int V_OFF = K_OFF + kNS * TILE_BYTES;
   static constexpr int BAR_OFF = V_OFF + kVS * VS_BYTES;
-  static constexpr int LIST_OFF = BAR_OFF + 640;
+  static constexpr int LIST_OFF = BAR_OFF + 768;
   // one CTA an SM (each takes all of its tensor memory)
   static size_t bytes(int num_seqs) {
     const size_t need = 1024 + LIST_OFF + list_ints(num_seqs) * 4;
@@ -79,6 +93,21 @@ struct Layout {
   }
   __device__ static constexpr uint32_t s_col(int x) { return 128u * (uint32_t)x; }  // 2 x 64
   __device__ static constexpr uint32_t o_col(int x) { return 256u + 128u * (uint32_t)x; }
+};
+
+// A run of tiles of an item (all of them, where the work is not cut): tiles
+// [first, first + n); `pieces` of it from CTA `head` on.
+struct Piece {
+  int32_t id, first, n, head, pieces;
+};
+
+// What the threads of a CTA pass one another while they plan.
+struct Sums {
+  unsigned long long chunks, row;
+  int32_t scan[kThreads / 32];
+  int32_t start[3];  // a share's first unit, KV head, place in the item
+  int32_t cands;
+  int32_t lightest, heaviest;  // the items' lengths
 };
 
 struct Bars {
@@ -91,47 +120,31 @@ struct Bars {
   uint64_t o_free[2];      // the item's O has been read
   uint64_t mma_done;
   uint64_t item_full[kRing], item_empty[kRing];
-  int32_t item_id[kRing];
+  Piece item[kRing];
   uint32_t tmem_base;
   int32_t abort;
   uint32_t k_mask[kNS], v_mask[kVS];  // boxes of a stage that were loaded
-  int32_t scan[kThreads / 32];
-  float red[2][kThreads / 32];
+  Sums sums;
 };
-static_assert(sizeof(Bars) <= 640, "the barriers fit below the work list");
+static_assert(sizeof(Bars) <= 768, "the barriers fit below the work list");
 
 struct Item {
   int req, kvh, j0, j1, t0;
+  // of the piece; columns are counted from its first
   int n;       // score tiles
+  int base;    // the item's column that is the piece's first
   int shift;   // from a column behind the sinks' to its key
-  int columns; // of the sinks' chunks: columns before it are keys themselves
+  int columns; // of the sinks' chunks: columns before it are base less than their keys
   int count;   // 16-key chunks
   int qpos0;   // position of the request's first query
+  int sink;    // columns before it are sinks
   int end;     // columns before it are needed keys
-  int lo_any;  // no query of the item sees columns [num_sink, lo_any)
+  int lo_any;  // no query of the item sees columns [sink, lo_any)
 
   __device__ __forceinline__ int key(int column) const {
-    return column < columns ? column : column + shift;
+    return column + (column < columns ? base : shift);
   }
 };
-
-// Work units (pairs of query tiles, QP queries) of request r: 0 for requests that
-// the decode grid takes; bad lengths flagged by one CTA.
-__device__ __forceinline__ int units_of(const AttnParams& p, int r, int QP, bool flag) {
-  const int32_t t0 = __ldg(p.cu_seqlens + r), t1 = __ldg(p.cu_seqlens + r + 1);
-  const int32_t n = t1 - t0;
-  bool bad = t0 < 0 || t1 < t0 || t1 > p.num_tokens;
-  if (!bad && n <= p.decode_max_q) {
-    if (flag && p.no_decode && n > 0) set_status(p.status, PKV_DEV_BAD_LENGTHS);
-    return 0;
-  }
-  if (!bad) {
-    const int32_t L = __ldg(p.seq_lens + r);
-    bad = n > p.max_query_len || L < n || L > p.max_seq_len || L > p.max_blocks * p.block_size;
-  }
-  if (bad && flag) set_status(p.status, PKV_DEV_BAD_LENGTHS);
-  return bad ? 0 : (n + QP - 1) / QP;
-}
 
 __device__ __forceinline__ int tiles_of(const AttnParams& p, int first, int end) {
   return (visible_units(p.window, p.num_sink, first, end, kSub).count + kHalfBoxes - 1) /
@@ -150,9 +163,11 @@ __device__ __forceinline__ int block_scan(int v, int32_t* scan, int* total) {
   if (lane == 31) scan[warp] = incl;
   __syncthreads();
   int base = 0, all = 0;
+#pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) base += scan[w];
-    all += scan[w];
+    const int x = scan[w];
+    if (w < warp) base += x;
+    all += x;
   }
   __syncthreads();
   *total = all;
@@ -166,107 +181,9 @@ struct List {
   int n;
 };
 
-// Requests with work, those with the most tiles in a unit first (batches of more
-// than kSortMax requests: as they come). All threads.
-__device__ __forceinline__ List build_list(const AttnParams& p, int* base, int32_t* scan, int QP,
-                                           int* total) {
-  const int B = p.num_seqs, tid = threadIdx.x;
-  const bool flag = blockIdx.x == 0;
-  const bool sorted = B <= kSortMax;
-  int* pref = base;
-  int* order = base + (B + 1);
-  int* cand = order + (B + 1);
-  int* weight = cand + (B + 1);
-  int n = B;
-  if (sorted) {
-    const int per = (B + kThreads - 1) / kThreads;
-    const int r0 = min(B, tid * per), r1 = min(B, r0 + per);
-    int count = 0;
-    for (int r = r0; r < r1; ++r) {
-      weight[r] = 0;
-      if (units_of(p, r, QP, flag) == 0) continue;
-      const int32_t L = __ldg(p.seq_lens + r);
-      weight[r] = tiles_of(p, max(0, L - QP), L);
-      ++count;
-    }
-    int at = block_scan(count, scan, &n);
-    for (int r = r0; r < r1; ++r)
-      if (weight[r] > 0) cand[at++] = r;
-    __syncthreads();
-    for (int i = tid; i < n; i += kThreads) {
-      const int r = cand[i], w = weight[r];
-      int rank = 0;
-      for (int j = 0; j < n; ++j) {
-        const int w2 = weight[cand[j]];
-        rank += w2 > w || (w2 == w && j < i);
-      }
-      order[rank] = r;
-    }
-    __syncthreads();
-  }
-  const int per = (n + kThreads - 1) / kThreads;
-  const int k0 = min(n, tid * per), k1 = min(n, k0 + per);
-  int sum = 0;
-  for (int k = k0; k < k1; ++k) sum += units_of(p, sorted ? order[k] : k, QP, flag && !sorted);
-  int run = block_scan(sum, scan, total);
-  for (int k = k0; k < k1; ++k) {
-    pref[k] = run;
-    run += units_of(p, sorted ? order[k] : k, QP, false);
-  }
-  if (tid == 0) pref[n] = *total;
-  __syncthreads();
-  return List{sorted ? order : nullptr, pref, n};
-}
-
-// The split of the SMs in a call with both kinds of request: cycles that a tile pair
-// takes here, and bytes of the pool that an SM of the decode grid reads in a cycle.
-constexpr float kPairCycles = 1500.f;
-constexpr float kDecodeBytesPerCycle = 40.f;
-
-// CTAs of this grid that take work when a decode grid shares the call: its work's
-// share of p.shared_sms by the estimate above. All threads.
-template <bool EIGHT>
-__device__ __noinline__ int own_share(const AttnParams& p, int QP, float (*red)[kThreads / 32]) {
-  const int B = p.num_seqs;
-  const int per = (B + kThreads - 1) / kThreads;
-  const int r0 = min(B, (int)threadIdx.x * per), r1 = min(B, r0 + per);
-  float pairs = 0.f, keys = 0.f;
-  for (int r = r0; r < r1; ++r) {
-    const int32_t n = __ldg(p.cu_seqlens + r + 1) - __ldg(p.cu_seqlens + r);
-    const int32_t L = __ldg(p.seq_lens + r);
-    if (n < 1 || L < n || L > p.max_seq_len) continue;
-    if (n <= p.decode_max_q) {
-      keys += 16.f * (float)visible_units(p.window, p.num_sink, L - n, L, kSub).count;
-      continue;
-    }
-    for (int j = 0; j < n; j += QP)
-      pairs += (float)tiles_of(p, L - n + j, L - n + min(n, j + QP));
-  }
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    pairs += __shfl_xor_sync(kFull, pairs, o);
-    keys += __shfl_xor_sync(kFull, keys, o);
-  }
-  if (lane == 0) {
-    red[0][warp] = pairs;
-    red[1][warp] = keys;
-  }
-  __syncthreads();
-  float pt = 0.f, kt = 0.f;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    pt += red[0][w];
-    kt += red[1][w];
-  }
-  __syncthreads();
-  const float a = kt * (float)(p.num_kv_heads * p.head_dim * (EIGHT ? 2 : 4)) / kDecodeBytesPerCycle;
-  const float b = pt * (float)p.num_kv_heads * kPairCycles;
-  const int S = p.shared_sms;
-  const int keep = a + b > 0.f ? S - (int)((float)S * a / (a + b) + 0.5f) : S;
-  return max(1, min(S, keep));
-}
-
-__device__ __forceinline__ Item item_of(const AttnParams& p, const List& list, int QP, int it) {
+// Item `it`, tiles [first, first + n) of it (n < 0: all).
+__device__ __forceinline__ Item item_of(const AttnParams& p, const List& list, int QP, int it,
+                                        int first_tile, int n_tiles) {
   Item d;
   const int u = it / p.num_kv_heads;
   d.kvh = it - u * p.num_kv_heads;
@@ -287,38 +204,292 @@ __device__ __forceinline__ Item item_of(const AttnParams& p, const List& list, i
   d.j1 = min(n, d.j0 + QP);
   const int first = d.qpos0 + d.j0, end = d.qpos0 + d.j1;
   const Visible v = visible_units(p.window, p.num_sink, first, end, kSub);
-  d.shift = (v.low - v.sink) * kSub;
-  d.columns = v.sink * kSub;
-  d.count = v.count;
-  d.n = (v.count + kHalfBoxes - 1) / kHalfBoxes;
+  const int shift = (v.low - v.sink) * kSub;
+  d.base = first_tile * kHalf;
+  d.shift = shift + d.base;
+  d.columns = v.sink * kSub - d.base;
+  d.count = v.count - first_tile * kHalfBoxes;
+  d.n = n_tiles < 0 ? (v.count + kHalfBoxes - 1) / kHalfBoxes : n_tiles;
+  d.sink = p.num_sink - d.base;
   d.end = end - d.shift;
   d.lo_any = max(0, first - p.window + 1) - d.shift;
   return d;
 }
 
-// The K warp takes the next ticket and announces it in a small ring; every other
-// role reads the same sequence from there (as in prefill_tc.cu).
-__device__ __forceinline__ int take_item(Bars* bars, const AttnParams& p, int total, int k,
-                                         volatile int32_t* abort) {
-  const int slot = k % kRing;
-  int it = -1;
-  if (k < kRing ||
-      short_wait(smem_addr(&bars->item_empty[slot]), ((k / kRing) - 1) & 1, p.status, abort)) {
-    const int t = atomicAdd(p.sched, 1);
-    it = t < total ? t : -1;
+// Shares: the items stand in a row, unit after unit, the KV heads of a unit one after
+// the other; an item is as long as its tiles and kItemTiles, what it costs to begin
+// one. A CTA has the tiles that lie in its share of the row, `ctas` shares of `size` or
+// (the first `more`) size + 1.
+struct Share {
+  uint32_t ctas;      // 0: items are handed out by tickets
+  uint32_t size, more;
+  uint32_t at, end;   // the CTA's place in the row, and the end of its share
+  int unit, kvh;      // where that is
+  int in;             // in the item
+  int tiles;          // of the unit's items (0: not known yet)
+
+  __device__ __forceinline__ uint32_t start(uint32_t cta) const {
+    return cta * size + min(cta, more);
   }
-  *reinterpret_cast<volatile int32_t*>(&bars->item_id[slot]) = it;
-  mbar_arrive(smem_addr(&bars->item_full[slot]));
-  return it;
+  __device__ __forceinline__ int cta_of(uint32_t x) const {
+    const uint32_t longer = more * (size + 1);
+    return (int)(x < longer ? x / (size + 1) : more + (x - longer) / size);
+  }
+};
+
+// The next piece: of the CTA's share, or a whole item by the next ticket. One lane of
+// the K warp announces it in a small ring; every other role reads it from there.
+template <bool CUT>
+__device__ __forceinline__ Piece next_piece(const AttnParams& p, const List& list, int QP,
+                                            int items, Share& sh) {
+  Piece c{-1, 0, -1, 0, 1};
+  if (!CUT || sh.ctas == 0) {
+    const int t = atomicAdd(p.sched, 1);
+    c.id = t < items ? t : -1;
+    return c;
+  }
+  if (sh.in < kItemTiles) {
+    sh.at += kItemTiles - sh.in;
+    sh.in = kItemTiles;
+  }
+  if (sh.at >= sh.end) return c;
+  if (sh.tiles == 0) sh.tiles = item_of(p, list, QP, sh.unit * p.num_kv_heads, 0, -1).n;
+  c.id = sh.unit * p.num_kv_heads + sh.kvh;
+  c.first = sh.in - kItemTiles;
+  c.n = min(sh.tiles - c.first, (int)(sh.end - sh.at));
+  const uint32_t begin = sh.at - c.first;  // the item's first tile
+  c.head = sh.cta_of(begin);
+  c.pieces = sh.cta_of(begin + sh.tiles - 1) - c.head + 1;
+  sh.at += c.n;
+  sh.in += c.n;
+  if (c.first + c.n == sh.tiles) {
+    sh.in = 0;
+    if (++sh.kvh == p.num_kv_heads) {
+      sh.kvh = 0;
+      sh.tiles = 0;
+      ++sh.unit;
+    }
+  }
+  return c;
 }
-__device__ __forceinline__ int read_item(Bars* bars, const AttnParams& p, int k,
-                                         volatile int32_t* abort) {
+template <bool CUT>
+__device__ __forceinline__ Piece take_item(Bars* bars, const AttnParams& p, const List& list,
+                                           int QP, int items, Share& sh, int k,
+                                           volatile int32_t* abort) {
   const int slot = k % kRing;
-  int it = -1;
-  if (short_wait(smem_addr(&bars->item_full[slot]), (k / kRing) & 1, p.status, abort))
-    it = *reinterpret_cast<volatile int32_t*>(&bars->item_id[slot]);
+  Piece c{-1, 0, -1, 0, 1};
+  if (k < kRing ||
+      short_wait(smem_addr(&bars->item_empty[slot]), ((k / kRing) - 1) & 1, p.status, abort))
+    c = next_piece<CUT>(p, list, QP, items, sh);
+  bars->item[slot] = c;  // (before the barrier's release)
+  mbar_arrive(smem_addr(&bars->item_full[slot]));
+  return c;
+}
+__device__ __forceinline__ Piece read_item(Bars* bars, const AttnParams& p, int k,
+                                           volatile int32_t* abort) {
+  const int slot = k % kRing;
+  Piece c{-1, 0, -1, 0, 1};
+  if (short_wait(smem_addr(&bars->item_full[slot]), (k / kRing) & 1, p.status, abort)) {
+    const volatile Piece* x = &bars->item[slot];
+    c.id = x->id;
+    c.first = x->first;
+    c.n = x->n;
+    c.head = x->head;
+    c.pieces = x->pieces;
+  }
   mbar_arrive(smem_addr(&bars->item_empty[slot]));
-  return it;
+  return c;
+}
+template <bool CUT>
+__device__ __forceinline__ Piece all_lanes(Piece c) {
+  c.id = __shfl_sync(kFull, c.id, 0);
+  if (!CUT) return Piece{c.id, 0, -1, 0, 1};
+  c.first = __shfl_sync(kFull, c.first, 0);
+  c.n = __shfl_sync(kFull, c.n, 0);
+  c.head = __shfl_sync(kFull, c.head, 0);
+  c.pieces = __shfl_sync(kFull, c.pieces, 0);
+  return c;
+}
+
+struct Work {
+  List list;
+  int items;    // units x KV heads
+  int active;   // CTAs of the grid that take some
+  Share share;
+};
+
+// The call's work: the requests with more than decode_max_q queries, those with the
+// most tiles in a unit first (batches of more than kSortMax requests: as they come;
+// bad lengths flagged by one CTA), the CTAs that work on them, and whether their items
+// are cut. All threads of every CTA come to the same result.
+template <bool EIGHT, bool CUT>
+__device__ __noinline__ void plan_work(const AttnParams& p, int QP, int* ints, Sums* sums,
+                                       Work* out) {
+  const int B = p.num_seqs, tid = threadIdx.x, lane = tid & 31;
+  const bool flag = blockIdx.x == 0, sorted = B <= kSortMax;
+  int* pref = ints;
+  int* order = ints + (B + 1);
+  int* cand = order + (B + 1);  // request, units, tiles of its heaviest unit
+  // units of request r (0: none, or the decode grid's); the 16-key chunks that one of
+  // the latter sees
+  auto look = [&](int r, int& weight, int& chunks) {
+    const int32_t t0 = __ldg(p.cu_seqlens + r), t1 = __ldg(p.cu_seqlens + r + 1);
+    const int32_t L = __ldg(p.seq_lens + r);
+    const int32_t n = t1 - t0;
+    weight = chunks = 0;
+    bool bad = t0 < 0 || t1 < t0 || t1 > p.num_tokens;
+    const bool short_one = !bad && n <= p.decode_max_q;
+    const bool len_ok = L >= n && L <= p.max_seq_len && L <= p.max_blocks * p.block_size;
+    if (short_one) {
+      if (flag && p.no_decode && n > 0) set_status(p.status, PKV_DEV_BAD_LENGTHS);
+      if (n > 0 && len_ok) chunks = visible_units(p.window, p.num_sink, L - n, L, kSub).count;
+      return 0;
+    }
+    bad = bad || n > p.max_query_len || !len_ok;
+    if (bad) {
+      if (flag) set_status(p.status, PKV_DEV_BAD_LENGTHS);
+      return 0;
+    }
+    weight = tiles_of(p, max(0, L - QP), L);
+    return (n + QP - 1) / QP;
+  };
+  if (tid == 0) {
+    *sums = Sums{};
+    sums->lightest = INT32_MAX;
+  }
+  __syncthreads();
+  unsigned long long chunks = 0;
+  int n, units;
+  if (sorted) {
+    for (int r = tid; r < B; r += kThreads) {
+      int w, c;
+      const int u = look(r, w, c);
+      chunks += c;
+      if (u == 0) continue;
+      const int at = atomicAdd(&sums->cands, 1);
+      cand[3 * at] = r;
+      cand[3 * at + 1] = u;
+      cand[3 * at + 2] = w;
+    }
+    if (p.shared_sms > 0 && chunks > 0) atomicAdd(&sums->chunks, chunks);
+    __syncthreads();
+    n = sums->cands;
+    for (int i = tid; i < n; i += kThreads) {
+      const int r = cand[3 * i], u = cand[3 * i + 1], w = cand[3 * i + 2];
+      int rank = 0, before = 0;
+      for (int j = 0; j < n; ++j) {
+        const bool ahead = cand[3 * j + 2] > w || (cand[3 * j + 2] == w && cand[3 * j] < r);
+        rank += ahead;
+        before += ahead ? cand[3 * j + 1] : 0;
+      }
+      order[rank] = r;
+      pref[rank] = before;
+      if (rank == n - 1) pref[n] = before + u;
+    }
+    if (n == 0 && tid == 0) pref[0] = 0;
+    __syncthreads();
+    units = pref[n];
+  } else {
+    n = B;
+    const int per = (B + kThreads - 1) / kThreads;
+    const int r0 = min(B, tid * per), r1 = min(B, r0 + per);
+    int sum = 0, all;
+    for (int r = r0; r < r1; ++r) {
+      int w, c;
+      pref[r] = look(r, w, c);
+      sum += pref[r];
+      chunks += c;
+    }
+    if (p.shared_sms > 0 && chunks > 0) atomicAdd(&sums->chunks, chunks);
+    int run = block_scan(sum, sums->scan, &all);
+    for (int r = r0; r < r1; ++r) {
+      const int u = pref[r];
+      pref[r] = run;
+      run += u;
+    }
+    if (tid == 0) pref[B] = all;
+    __syncthreads();
+    units = all;
+  }
+  const List list{sorted ? order : nullptr, pref, n};
+  out->list = list;
+  const int items = out->items = units * p.num_kv_heads;
+  int active = out->active = (int)gridDim.x;
+  Share& sh = out->share;
+  sh = Share{};
+
+  // the tiles of the units (and what beginning them costs)
+  const int Hkv = p.num_kv_heads;
+  const bool may_cut = CUT && units <= kCutUnits && p.max_seq_len <= kCutKeys;
+  int before = 0, all = 0;
+  int len[2] = {0, 0};
+  float row = 0.f;
+  if (may_cut) {
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i)
+      if (2 * tid + i < units)
+        (i == 0 ? len[0] : len[1]) =
+            item_of(p, list, QP, (2 * tid + i) * Hkv, 0, -1).n + kItemTiles;
+    const int least = __reduce_min_sync(
+        kFull, len[1] > 0 ? min(len[0], len[1]) : len[0] > 0 ? len[0] : INT32_MAX);
+    const int most = __reduce_max_sync(kFull, max(len[0], len[1]));
+    if (lane == 0) {
+      atomicMin(&sums->lightest, least);
+      atomicMax(&sums->heaviest, most);
+    }
+    before = block_scan(len[0] + len[1], sums->scan, &all);
+    row = (float)all;
+  } else if (p.shared_sms > 0) {
+    unsigned long long sum = 0;
+    for (int u = tid; u < units; u += kThreads)
+      sum += item_of(p, list, QP, u * Hkv, 0, -1).n + kItemTiles;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    if (lane == 0) atomicAdd(&sums->row, sum);
+    __syncthreads();
+    row = (float)sums->row;
+  }
+  if (p.shared_sms > 0) {  // a decode grid works beside: the estimates' shares of the SMs
+    const float a = (float)sums->chunks * (float)(kSub * p.num_kv_heads * p.head_dim) *
+                    (EIGHT ? 2.f : 4.f) / kDecodeBytesPerCycle;
+    const float b = row * (float)Hkv * kTileCycles;
+    const int keep = a + b > 0.f ? p.shared_sms - (int)((float)p.shared_sms * a / (a + b) + 0.5f)
+                                 : p.shared_sms;
+    active = out->active = max(1, min(min(p.shared_sms, (int)gridDim.x), keep));
+  }
+  // Cut, where the last round of tickets, of which some CTAs get none, costs more than
+  // to hand over pieces, about kPieceTiles. (Items that differ fill the rounds better,
+  // the light ones last.) 13 requests, 513-key window, 156 items: 42 us by tickets, 38
+  // cut.
+  if (!may_cut || units == 0 || (int64_t)all * Hkv >= 1 << 30) return;
+  const uint32_t total = (uint32_t)all * Hkv;
+  const uint32_t ctas = max(1u, min((uint32_t)min(active, kMaxCtas),
+                                    total / (uint32_t)(kItemTiles + kMinShare)));
+  const int rounds = (items + active - 1) / active;
+  const float light = (float)sums->lightest, ratio = light / (float)sums->heaviest;
+  const float idle = ((float)rounds - (float)items / (float)active) * light * ratio * ratio;
+  if (idle <= kPieceTiles) return;
+  sh.ctas = ctas;
+  sh.size = total / ctas;
+  sh.more = total - sh.size * ctas;
+  if (blockIdx.x >= ctas) return;  // (uniform)
+  sh.at = sh.start(blockIdx.x);
+  sh.end = sh.start(blockIdx.x + 1);
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    const int own = i == 0 ? len[0] : len[1];
+    const uint32_t x = sh.at - (uint32_t)before * Hkv;  // (of the unit where the share begins)
+    if (sh.at >= (uint32_t)before * Hkv && x < (uint32_t)own * Hkv) {
+      sums->start[0] = 2 * tid + i;
+      sums->start[1] = x / own;
+      sums->start[2] = x % own;
+    }
+    before += own;
+  }
+  __syncthreads();
+  sh.unit = sums->start[0];
+  sh.kvh = sums->start[1];
+  sh.in = sums->start[2];
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -453,6 +624,75 @@ __device__ __forceinline__ void convert_e4m3(uint32_t base, int ct, uint32_t loa
   }
 }
 
+// A warp's part of a piece: O, 4 dimensions of its 32 rows after the other, then m and l.
+template <int D>
+constexpr int kWarpFloats = 32 * (D + 2);
+
+// 32 values of a row of the output from dimension c on.
+template <int D>
+__device__ __forceinline__ void put32(const AttnParams& p, int64_t row, int c,
+                                      const float (&v)[32]) {
+  if (p.out_bf16) {
+    uint16_t* out = reinterpret_cast<uint16_t*>(p.out) + row * D + c;
+#pragma unroll
+    for (int e = 0; e < 32; e += 8)
+      *reinterpret_cast<uint4*>(out + e) =
+          make_uint4(pack_bf16x2(v[e], v[e + 1]), pack_bf16x2(v[e + 2], v[e + 3]),
+                     pack_bf16x2(v[e + 4], v[e + 5]), pack_bf16x2(v[e + 6], v[e + 7]));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 32; e += 4)
+      *reinterpret_cast<float4*>(p.out + row * D + c + e) =
+          make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+  }
+}
+
+// The part of warp `warp` of a CTA's piece of an item, of the one that it begins or of
+// the one that it continues.
+template <int D>
+__device__ __forceinline__ float* part_of(const AttnParams& p, int cta, bool begins, int warp) {
+  return p.prefill_parts + ((int64_t)(2 * cta + (begins ? 1 : 0)) * 8 + warp) * kWarpFloats<D>;
+}
+
+// Dimensions [c0, c0 + N) of a warp's rows from the item's `pieces`, the first of them
+// CTA `head`'s, in their order.
+template <int D, int N>
+__device__ __forceinline__ void join_rows(const AttnParams& p, int head, int pieces, int warp,
+                                          int c0, bool valid, int64_t row) {
+  const int lane = threadIdx.x & 31;
+  float m = -INFINITY, l = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < pieces; ++i) {
+    const float* from = part_of<D>(p, head + i, i == 0, warp) + 32 * D + lane;
+    const float mi = __ldcg(from), li = __ldcg(from + 32);
+    const float mn = fmaxf(m, mi), mu = mn == -INFINITY ? 0.f : mn;
+    l = fmaf(l, fast_exp2(m - mu), li * fast_exp2(mi - mu));
+    m = mn;
+  }
+  const float mu = m == -INFINITY ? 0.f : m, inv = 1.f / l;
+#pragma unroll 1
+  for (int c = c0; c < c0 + N; c += 32) {
+    float v[32];
+#pragma unroll
+    for (int e = 0; e < 32; ++e) v[e] = 0.f;
+#pragma unroll 2
+    for (int i = 0; i < pieces; ++i) {
+      const float* from = part_of<D>(p, head + i, i == 0, warp);
+      const float w = fast_exp2(__ldcg(from + 32 * D + lane) - mu) * inv;
+#pragma unroll
+      for (int e = 0; e < 32; e += 4) {
+        const float4 o = __ldcg(reinterpret_cast<const float4*>(from) + (c + e) / 4 * 32 + lane);
+        v[e] = fmaf(o.x, w, v[e]);
+        v[e + 1] = fmaf(o.y, w, v[e + 1]);
+        v[e + 2] = fmaf(o.z, w, v[e + 2]);
+        v[e + 3] = fmaf(o.w, w, v[e + 3]);
+      }
+    }
+    if (valid) put32<D>(p, row, c, v);
+  }
+  if (c0 == 0 && valid && p.out_lse) p.out_lse[row] = (m + fast_log2(l)) * kLn2;
+}
+
 template <int R>
 __device__ __forceinline__ void more_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
@@ -462,65 +702,15 @@ __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
-template <int D, bool EIGHT>
-__global__ void __launch_bounds__(kThreads, 1)
-    prefill_rows_kernel(const __grid_constant__ CUtensorMap q_map,
-                        const __grid_constant__ CUtensorMap kv_map, const AttnParams p) {
+// The roles of the warps. CUT: items may be cut, their pieces' places are read with them.
+template <int D, bool EIGHT, bool CUT>
+__device__ __forceinline__ void work_on(const CUtensorMap& q_map, const CUtensorMap& kv_map,
+                                        const AttnParams& p, uint8_t* smem, const List& list,
+                                        Share& share, int total, uint32_t tmem) {
   using Lay = Layout<D>;
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   Bars* bars = reinterpret_cast<Bars*>(smem + Lay::BAR_OFF);
-  griddep_wait();
-  griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int G = p.num_heads / p.num_kv_heads;
-  const int QT = kBM / G;  // queries of a tile (rows G QT .. 127 belong to none)
-  const int QP = 2 * QT;   // queries of an item
-
-  if (threadIdx.x == 0) {
-    for (int x = 0; x < 2; ++x) {
-      mbar_init(smem_addr(&bars->q_full[x]), 1);
-      mbar_init(smem_addr(&bars->q_empty[x]), 1);
-      for (int b = 0; b < 2; ++b) {
-        mbar_init(smem_addr(&bars->s_full[x][b]), 1);
-        mbar_init(smem_addr(&bars->p_ready[x][b]), 4);
-        mbar_init(smem_addr(&bars->o_done[x][b]), 1);
-      }
-      mbar_init(smem_addr(&bars->o_free[x]), 4);
-    }
-    for (int s = 0; s < kNS; ++s) {
-      mbar_init(smem_addr(&bars->k_landed[s]), 1);
-      mbar_init(smem_addr(&bars->k_full[s]), EIGHT ? kConverters : 1);
-      mbar_init(smem_addr(&bars->k_empty[s]), 2);
-    }
-    for (int s = 0; s < kVS; ++s) {
-      mbar_init(smem_addr(&bars->v_landed[s]), 1);
-      mbar_init(smem_addr(&bars->v_full[s]), kConverters);
-      mbar_init(smem_addr(&bars->v_empty[s]), 2);
-    }
-    mbar_init(smem_addr(&bars->mma_done), 2);
-    for (int k = 0; k < kRing; ++k) {
-      mbar_init(smem_addr(&bars->item_full[k]), 1);
-      mbar_init(smem_addr(&bars->item_empty[k]), kItemReaders);
-    }
-    bars->abort = 0;
-    fence_barrier_init();
-  }
-  int units = 0;
-  const List list = build_list(p, reinterpret_cast<int*>(smem + Lay::LIST_OFF), bars->scan, QP,
-                               &units);  // (synchronises)
-  const int total = units * p.num_kv_heads;
-  const int active = p.shared_sms > 0 ? own_share<EIGHT>(p, QP, bars->red) : (int)gridDim.x;
-  if ((int)blockIdx.x >= min(total, active)) return;  // uniform; nothing allocated yet
-  if (warp == kMmaWarp) {
-    tmem_alloc(smem_addr(&bars->tmem_base), kTmemCols);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = bars->tmem_base;
+  const int G = p.num_heads / p.num_kv_heads, QT = kBM / G, QP = 2 * QT;
   volatile int32_t* abort = &bars->abort;
   const uint32_t q_s = smem_addr(smem + Lay::Q_OFF);
   const uint32_t k_s = smem_addr(smem + Lay::K_OFF);
@@ -538,9 +728,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     return __shfl_sync(kFull, w, 0) != 0;
   };
   auto next_item = [&](int k) {
-    int it = -1;
-    if (lane == 0) it = read_item(bars, p, k, abort);
-    return __shfl_sync(kFull, it, 0);
+    Piece c;
+    if (lane == 0) c = read_item(bars, p, k, abort);
+    return all_lanes<CUT>(c);
   };
 
   if (warp >= kConvWarp0) {
@@ -561,15 +751,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       int st = 0, filled = 0, copied = 0;
       uint32_t parity = 1;  // of the stage's last release (none before the first lap)
       bool ok = true, bad_block = false;
+      // both tiles of Q. Rows behind the last token read as zeros, rows of the next
+      // request belong to no valid output row
+      auto copy_q = [&](int k, const Item& d) {
+#pragma unroll 1
+        for (int x = 0; x < 2; ++x) {
+          if (k > 0) ok = warp_wait(&bars->q_empty[x], (k - 1) & 1);
+          if (!ok) break;
+          ++copied;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(smem_addr(&bars->q_full[x]), Lay::NCH * QT * G * 128);
+#pragma unroll 1
+            for (int c = 0; c < Lay::NCH; ++c)
+              tma_load_3d(q_s + x * Lay::TILE_BYTES + c * Lay::CH_BYTES, &q_map,
+                          smem_addr(&bars->q_full[x]), c * 64, d.kvh * G, d.t0 + d.j0 + x * QT);
+          }
+        }
+      };
       for (int k = 0; ok; ++k) {
-        int it = -1;
+        Piece c;
         if (lane == 0)
-          it = vrole ? read_item(bars, p, k, abort) : take_item(bars, p, total, k, abort);
-        it = __shfl_sync(kFull, it, 0);
-        if (it < 0) break;
-        const Item d = item_of(p, list, QP, it);
+          c = vrole ? read_item(bars, p, k, abort)
+                    : take_item<CUT>(bars, p, list, QP, total, share, k, abort);
+        c = all_lanes<CUT>(c);
+        if (c.id < 0) break;
+        const Item d = item_of(p, list, QP, c.id, c.first, c.n);
         const int32_t* bt = p.block_table + (int64_t)d.req * p.max_blocks;
         int32_t row = -1;
+        if (vrole && k == 0) copy_q(k, d);
 #pragma unroll 1
         for (int box0 = 0; box0 < d.n * kHalfBoxes; box0 += boxes) {
           if ((box0 & 31) == 0) {  // the next 32 boxes, one a lane: first row in the pool
@@ -608,23 +817,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++filled;
           st = st + 1 == stages ? 0 : st + 1;
           parity ^= st == 0 ? 1u : 0u;
-          if (!vrole || box0 != min(1, d.n - 1) * kHalfBoxes) continue;
           // behind the item's first two V tiles (whose stages are free by then): Q, free
-          // when the last scores of the item before are there. Rows behind the last
-          // token read as zeros, rows of the next request belong to no valid output row
-#pragma unroll 1
-          for (int x = 0; ok && x < 2; ++x) {
-            if (k > 0) ok = warp_wait(&bars->q_empty[x], (k - 1) & 1);
-            if (!ok) break;
-            ++copied;
-            if (lane == 0) {
-              mbar_arrive_expect_tx(smem_addr(&bars->q_full[x]), Lay::NCH * QT * G * 128);
-#pragma unroll 1
-              for (int c = 0; c < Lay::NCH; ++c)
-                tma_load_3d(q_s + x * Lay::TILE_BYTES + c * Lay::CH_BYTES, &q_map,
-                            smem_addr(&bars->q_full[x]), c * 64, d.kvh * G, d.t0 + d.j0 + x * QT);
-            }
-          }
+          // when the last scores of the item before are there
+          if (vrole && k > 0 && box0 == min(1, d.n - 1) * kHalfBoxes) copy_q(k, d);
           if (!ok) break;
         }
       }
@@ -645,9 +840,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t vparity = 0;
       bool ok = true;
       for (int k = 0; ok; ++k) {
-        const int it = next_item(k);
-        if (it < 0) break;
-        const Item d = item_of(p, list, QP, it);
+        const Piece c = next_item(k);
+        if (c.id < 0) break;
+        const Item d = item_of(p, list, QP, c.id, c.first, c.n);
 #pragma unroll 1
         for (int j = 0; ok && j < d.n; ++j) {
           const int c0 = j * kHalf;
@@ -660,7 +855,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int h = 0; h < 2; ++h)
               convert_e4m3<D, true, Lay::CH_BYTES>(
                   k_s + st * Lay::TILE_BYTES + h * kHalf * 128, ct, load >> (h * kHalfBoxes),
-                  d.end - c0 - h * kHalf, p.num_sink - c0 - h * kHalf, d.lo_any - c0 - h * kHalf);
+                  d.end - c0 - h * kHalf, d.sink - c0 - h * kHalf, d.lo_any - c0 - h * kHalf);
             fence_proxy_async_smem();
             mbar_arrive(smem_addr(&bars->k_full[st]));
             ++gt;
@@ -670,10 +865,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t load = *reinterpret_cast<volatile uint32_t*>(&bars->v_mask[vst]);
           const uint32_t base = v_s + vst * Lay::VS_BYTES;
           if (EIGHT)
-            convert_e4m3<D, false, Lay::VCH_BYTES>(base, ct, load, d.end - c0, p.num_sink - c0,
+            convert_e4m3<D, false, Lay::VCH_BYTES>(base, ct, load, d.end - c0, d.sink - c0,
                                                    d.lo_any - c0);
           else
-            convert_bf16<D, Lay::VCH_BYTES>(base, ct, load, d.end - c0, p.num_sink - c0,
+            convert_bf16<D, Lay::VCH_BYTES>(base, ct, load, d.end - c0, d.sink - c0,
                                             d.lo_any - c0, most);
           fence_proxy_async_smem();
           mbar_arrive(smem_addr(&bars->v_full[vst]));
@@ -717,9 +912,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
 #pragma unroll 1
       for (int k = 0; ok; ++k) {
-        const int it = next_item(k);
-        if (it < 0) break;
-        const int n = item_of(p, list, QP, it).n;
+        const Piece c = next_item(k);
+        if (c.id < 0) break;
+        const int n = item_of(p, list, QP, c.id, c.first, c.n).n;
         ok = all_wait(&bars->q_full[x], k & 1);
         // tile j's product with P behind tile j + 2's scores' issue, from j = -2 on
 #pragma unroll 1
@@ -782,12 +977,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       return there;
     };
     for (int k = 0; ok; ++k) {
-      const int it = next_item(k);
-      if (it < 0) break;
-      const Item d = item_of(p, list, QP, it);
+      const Piece piece = next_item(k);
+      if (piece.id < 0) break;
+      const Item d = item_of(p, list, QP, piece.id, piece.first, piece.n);
+      // (head, pieces, whether it begins the item: in a word over the loop)
+      const int cut = piece.head | piece.pieces << 8 | (piece.first == 0 ? 1 << 16 : 0);
       const int qj = d.j0 + x * QT + rq;
       const bool valid = qj < d.j1 && rq < QT;
-      // the columns [low, lim] and those before num_sink are visible to the row
+      // the columns [low, lim] and those before d.sink are visible to the row
       const int lim0 = valid ? d.qpos0 + qj - d.shift : d.end - 1;
       const int low0 = lim0 - p.window + 1;
       float m = -INFINITY, l = 0.f;
@@ -816,7 +1013,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       if (EIGHT) chunk_scales(chunk_id(lane));
       // the columns [all0, all1] are visible to every row of the warp
-      const int all0 = __reduce_max_sync(kFull, low0 <= p.num_sink ? 0 : low0);
+      const int all0 = __reduce_max_sync(kFull, low0 <= d.sink ? 0 : low0);
       const int all1 = __reduce_min_sync(kFull, lim0);
       uint32_t u[kHalf];
       ok = load_scores(gt, u);
@@ -833,7 +1030,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             chunk_scales(nx_id);
           }
         }
-        const int lim = lim0 - j * kHalf, low = low0 - j * kHalf, sink = p.num_sink - j * kHalf;
+        const int lim = lim0 - j * kHalf, low = low0 - j * kHalf, sink = d.sink - j * kHalf;
         // hidden scores become -inf
         if (j * kHalf < all0 || j * kHalf + kHalf - 1 > all1) {
 #pragma unroll
@@ -946,39 +1143,119 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = all_wait(&bars->o_done[x][(gt - 1) & 1], ((gt - 1) >> 1) & 1);
       if (!ok) break;
       tc_fence_after();
-      const float inv = 1.f / l;
       const int64_t orow = (int64_t)(d.t0 + qj) * p.num_heads + d.kvh * G + g;
+      const int head = cut & 255, pieces = cut >> 8 & 255;
+      const bool whole = pieces == 1, begins = cut >> 16;
+      if (whole) {
+        const float inv = 1.f / l;
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        uint32_t v[32];
-        PKV_TMEM_LD32(oa + c, v);
-        tmem_wait_ld();
-        if (!valid) continue;
-        if (p.out_bf16) {
-          uint16_t* out = reinterpret_cast<uint16_t*>(p.out) + orow * D + c;
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          PKV_TMEM_LD32(oa + c, o);
+          tmem_wait_ld();
+          if (!valid) continue;
+          float v[32];
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              w[i] = pack_bf16x2(__uint_as_float(v[e + 2 * i]) * inv,
-                                 __uint_as_float(v[e + 2 * i + 1]) * inv);
-            *reinterpret_cast<uint4*>(out + e) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        } else {
+          for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]) * inv;
+          put32<D>(p, orow, c, v);
+        }
+        if (valid && p.out_lse) p.out_lse[orow] = (m + fast_log2(l)) * kLn2;
+      } else {  // a piece of an item goes to the workspace as it is, with m and l
+        float* part = part_of<D>(p, (int)blockIdx.x, begins, warp);
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          PKV_TMEM_LD32(oa + c, o);
+          tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4*>(p.out + orow * D + c + e) =
-                make_float4(__uint_as_float(v[e]) * inv, __uint_as_float(v[e + 1]) * inv,
-                            __uint_as_float(v[e + 2]) * inv, __uint_as_float(v[e + 3]) * inv);
+            reinterpret_cast<uint4*>(part)[(c + e) / 4 * 32 + lane] =
+                make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
+        part[32 * D + lane] = m;
+        part[32 * D + 32 + lane] = l;
+        if (p.prefill_join && begins && threadIdx.x == 0)
+          reinterpret_cast<int4*>(p.sched + kRecords)[blockIdx.x] =
+              make_int4(d.t0 + d.j0, d.j1 - d.j0, d.kvh, pieces);
       }
-      if (valid && p.out_lse) p.out_lse[orow] = (m + fast_log2(l)) * kLn2;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&bars->o_free[x]));
+      if (whole || p.prefill_join) continue;
+      // the warp that comes last joins the pieces
+      __threadfence();
+      __syncwarp();
+      int done = 0;
+      if (lane == 0) done = atomicAdd(p.sched + kRecords + head * 8 + warp, 1) + 1;
+      if (__shfl_sync(kFull, done, 0) != pieces) continue;
+      __threadfence();
+      join_rows<D, D>(p, head, pieces, warp, 0, valid, orow);
     }
   }
+}
+
+template <int D, bool EIGHT, bool CUT>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_rows_kernel(const __grid_constant__ CUtensorMap q_map,
+                        const __grid_constant__ CUtensorMap kv_map, const AttnParams p) {
+  using Lay = Layout<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  Bars* bars = reinterpret_cast<Bars*>(smem + Lay::BAR_OFF);
+  griddep_wait();
+  griddep_launch_dependents();
+  const int warp = threadIdx.x >> 5;
+  const int G = p.num_heads / p.num_kv_heads;
+  const int QT = kBM / G;  // queries of a tile (rows G QT .. 127 belong to none)
+  const int QP = 2 * QT;   // queries of an item
+
+  if (threadIdx.x == 0) {
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(smem_addr(&bars->q_full[x]), 1);
+      mbar_init(smem_addr(&bars->q_empty[x]), 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(smem_addr(&bars->s_full[x][b]), 1);
+        mbar_init(smem_addr(&bars->p_ready[x][b]), 4);
+        mbar_init(smem_addr(&bars->o_done[x][b]), 1);
+      }
+      mbar_init(smem_addr(&bars->o_free[x]), 4);
+    }
+    for (int s = 0; s < kNS; ++s) {
+      mbar_init(smem_addr(&bars->k_landed[s]), 1);
+      mbar_init(smem_addr(&bars->k_full[s]), EIGHT ? kConverters : 1);
+      mbar_init(smem_addr(&bars->k_empty[s]), 2);
+    }
+    for (int s = 0; s < kVS; ++s) {
+      mbar_init(smem_addr(&bars->v_landed[s]), 1);
+      mbar_init(smem_addr(&bars->v_full[s]), kConverters);
+      mbar_init(smem_addr(&bars->v_empty[s]), 2);
+    }
+    mbar_init(smem_addr(&bars->mma_done), 2);
+    for (int k = 0; k < kRing; ++k) {
+      mbar_init(smem_addr(&bars->item_full[k]), 1);
+      mbar_init(smem_addr(&bars->item_empty[k]), kItemReaders);
+    }
+    bars->abort = 0;
+    fence_barrier_init();
+  }
+  Work work;
+  plan_work<EIGHT, CUT>(p, QP, reinterpret_cast<int*>(smem + Lay::LIST_OFF), &bars->sums,
+                   &work);  // (synchronises)
+  const List list = work.list;
+  const int total = work.items;
+  Share share = work.share;
+  // (uniform; nothing allocated yet)
+  if ((int)blockIdx.x >= (share.ctas > 0 ? (int)share.ctas : min(total, work.active))) return;
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_addr(&bars->tmem_base), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  work_on<D, EIGHT, CUT>(q_map, kv_map, p, smem, list, share, total, tmem);
 
   // ---- the CTA's tcgen05 work is complete: tensor memory is released (its address
   // read again: the roles ran with different register budgets)
@@ -994,12 +1271,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D, bool EIGHT>
-cudaError_t launch_d(const AttnParams& p, const CUtensorMap& q_map, const CUtensorMap& kv_map,
+// The items that were cut: CTA (h, x, c) joins 32 dimensions of query tile x of the one
+// that begins in CTA h's share, a row a thread.
+template <int D>
+__global__ void __launch_bounds__(kBM) join_pieces_kernel(const AttnParams p) {
+  griddep_wait();  // (no early trigger: as in join_rows_kernel)
+  const int4 rec = __ldcg(reinterpret_cast<const int4*>(p.sched + kRecords) + blockIdx.x);
+  if (rec.w < 2) return;
+  const int x = blockIdx.y, r = threadIdx.x;
+  const int G = p.num_heads / p.num_kv_heads, QT = kBM / G;
+  const int j = x * QT + r / G;
+  const bool valid = r < QT * G && j < rec.y;
+  join_rows<D, 32>(p, blockIdx.x, rec.w, x * 4 + (r >> 5), blockIdx.z * 32, valid,
+                   (int64_t)(rec.x + j) * p.num_heads + rec.z * G + r % G);
+}
+
+template <int D, bool EIGHT, bool CUT>
+cudaError_t launch_form(const AttnParams& p, const CUtensorMap& q_map, const CUtensorMap& kv_map,
                      cudaStream_t stream) {
   const size_t smem = Layout<D>::bytes(p.num_seqs);
   if (smem > 227 * 1024) return cudaErrorInvalidValue;
-  auto kernel = prefill_rows_kernel<D, EIGHT>;
+  auto kernel = prefill_rows_kernel<D, EIGHT, CUT>;
   static SmemLimit limit;
   if (cudaError_t e = limit.ensure(reinterpret_cast<const void*>(kernel), 227 * 1024);
       e != cudaSuccess)
@@ -1008,11 +1300,8 @@ cudaError_t launch_d(const AttnParams& p, const CUtensorMap& q_map, const CUtens
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const int QP = 2 * (kBM / (p.num_heads / p.num_kv_heads));
-  const int64_t bound =
-      (int64_t)p.num_seqs * ((p.max_query_len + QP - 1) / QP) * p.num_kv_heads;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(bound < sms ? bound : sms));
+  cfg.gridDim = dim3((unsigned)sms);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -1024,11 +1313,31 @@ cudaError_t launch_d(const AttnParams& p, const CUtensorMap& q_map, const CUtens
   return cudaLaunchKernelEx(&cfg, kernel, q_map, kv_map, p);
 }
 
+// Items are cut in calls of up to three rounds of them (the places of the pieces cost
+// the loops something: 8 bits, chunks of 2048 tokens, 496 items, 354 us, 365 in the form
+// that may cut).
+template <int D, bool EIGHT>
+cudaError_t launch_d(const AttnParams& p, const CUtensorMap& q_map, const CUtensorMap& kv_map,
+                     cudaStream_t stream) {
+  const int QP = 2 * (kBM / (p.num_heads / p.num_kv_heads));
+  // (items at least, those of requests that the decode grid may take left out)
+  const int64_t items =
+      ((int64_t)p.num_tokens - (int64_t)p.num_seqs * p.decode_max_q) / QP * p.num_kv_heads;
+  return items <= 3 * kMaxCtas ? launch_form<D, EIGHT, true>(p, q_map, kv_map, stream)
+                               : launch_form<D, EIGHT, false>(p, q_map, kv_map, stream);
+}
+
 }  // namespace
 
 bool prefill_rows_fits(int32_t num_seqs, int32_t head_dim) {
   return num_seqs >= 0 && (head_dim == 128 ? Layout<128>::bytes(num_seqs)
                                            : Layout<64>::bytes(num_seqs)) <= 227 * 1024;
+}
+
+size_t prefill_rows_sched() { return (kRecords + 8 * kMaxCtas) * sizeof(int32_t); }
+
+size_t prefill_rows_workspace(int32_t head_dim) {
+  return (size_t)kMaxCtas * 2 * 8 * 32 * (head_dim + 2) * sizeof(float);
 }
 
 cudaError_t launch_prefill_rows(const AttnParams& p, const CUtensorMap& q_map,
@@ -1038,6 +1347,26 @@ cudaError_t launch_prefill_rows(const AttnParams& p, const CUtensorMap& q_map,
                              : launch_d<64, true>(p, q_map, kv_map, stream);
   return p.head_dim == 128 ? launch_d<128, false>(p, q_map, kv_map, stream)
                            : launch_d<64, false>(p, q_map, kv_map, stream);
+}
+
+bool prefill_rows_join(const AttnParams& p) {
+  const int QP = 2 * (kBM / (p.num_heads / p.num_kv_heads));
+  const int64_t units = (int64_t)p.num_tokens / QP + p.num_seqs;  // at most
+  return units * p.num_kv_heads * 4 <= kMaxCtas;
+}
+
+cudaError_t launch_prefill_rows_join(const AttnParams& p, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)kMaxCtas, 2, (unsigned)(p.head_dim / 32));
+  cfg.blockDim = dim3(kBM);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, p.head_dim == 128 ? join_pieces_kernel<128> : join_pieces_kernel<64>,
+                            p);
 }
 
 }  // namespace pkv

@@ -16,7 +16,6 @@ using pkv::AttnParams;
 // Contexts of up to this many 16-key chunks are not divided: the grid that joins
 // the pieces would cost more.
 constexpr int32_t kWholeChunks = 16;
-constexpr size_t kSchedBytes = 256;
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -26,7 +25,7 @@ struct Plan {
   int32_t max_q;  // queries of the requests that the decode grid takes
   int32_t rows;   // (query, head) rows of one KV head that they have at most
   bool whole;     // no context is divided
-  size_t cuts_off, sched_off, total;
+  size_t cuts_off, sched_off, parts_off, total;
 };
 
 Plan plan_calls(int32_t max_query_len, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
@@ -47,7 +46,12 @@ Plan plan_calls(int32_t max_query_len, int32_t num_heads, int32_t num_kv_heads, 
     const size_t n = pkv::decode_rows_workspace(num_kv_heads, s.rows, head_dim, eight, &s.cuts_off);
     s.sched_off = round_up(n, 256);
   }
-  s.total = s.sched_off + kSchedBytes;
+  s.parts_off = s.total = s.sched_off;
+  if (max_query_len > s.max_q) {
+    s.parts_off += round_up(pkv::prefill_rows_sched(), 256);
+    s.total = s.parts_off + pkv::prefill_rows_workspace(head_dim);
+  }
+  if (s.total == 0) s.total = 256;  // (never none, so that a caller's pointer is not null)
   return s;
 }
 
@@ -123,6 +127,7 @@ pkv_status attention(void* out, int32_t out_f32, float* out_lse, const void* q, 
   p.ws_out = reinterpret_cast<float*>(ws);
   p.ws_lse = reinterpret_cast<float*>(ws + sp.cuts_off);
   p.sched = reinterpret_cast<int32_t*>(ws + sp.sched_off);
+  p.prefill_parts = reinterpret_cast<float*>(ws + sp.parts_off);
   p.status = dev_status;
   p.decode_max_q = sp.max_q;
   p.decode_max_rows = sp.rows;
@@ -147,9 +152,10 @@ pkv_status attention(void* out, int32_t out_f32, float* out_lse, const void* q, 
   if (!prefill) return decode(p);
   // the prefill grid, then (unless no request can be short) the decode grid on
   // the SMs that it leaves, as in api.cpp; the work tickets start at zero
-  if (cudaMemsetAsync(p.sched, 0, kSchedBytes, st) != cudaSuccess) return PKV_ERR_CUDA;
+  if (cudaMemsetAsync(p.sched, 0, pkv::prefill_rows_sched(), st) != cudaSuccess) return PKV_ERR_CUDA;
   const bool any_short = (int64_t)num_seqs * max_query_len - num_tokens >=
                          (int64_t)max_query_len - sp.max_q;
+  p.prefill_join = pkv::prefill_rows_join(p);
   AttnParams pp = p;
   if (any_short) {
     int dev = 0, sms = 0;
@@ -161,9 +167,12 @@ pkv_status attention(void* out, int32_t out_f32, float* out_lse, const void* q, 
     pp.no_decode = 1;
   }
   if (pkv::launch_prefill_rows(pp, q_map, eight ? rows : boxes, st) != cudaSuccess) return PKV_ERR_CUDA;
-  if (!any_short) return PKV_OK;
-  p.after_prefill = 1;
-  return decode(p);
+  if (any_short) {
+    p.after_prefill = 1;
+    if (pkv_status e = decode(p); e != PKV_OK) return e;
+  }
+  if (!p.prefill_join) return PKV_OK;
+  return pkv::launch_prefill_rows_join(p, st) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 }  // namespace
