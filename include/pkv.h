@@ -559,16 +559,19 @@ pkv_status pkv_qk_norm_rope_kv_cache_append_fp8(
  *                are rounded to fp16 in requests of more than 32 / G queries and
  *                over the 8-bit cache, to 16 bits of fraction elsewhere)
  *   workspace    at least pkv_window_attention_workspace_size(...) bytes, 256-byte
- *                aligned (13 MB at most). It needs no clearing. One for each concurrent call, and
- *                for each captured graph that may run beside another
+ *                aligned (13 MB at most where no request has more than 32 / G queries,
+ *                54 MB otherwise). It needs no clearing. One for each concurrent call,
+ *                and for each captured graph that may run beside another
  * There is no partition_size: the work of the requests of up to 32 / G queries is
- * cut into equal shares of the keys that they see, whatever their lengths, and the
- * pieces are joined by log-sum-exp. The cuts follow the whole batch's lengths, so a
- * request's result may differ in its last bits from one batch to another; the same
- * call gives the same bits.
+ * cut into equal shares of the keys that they see, whatever their lengths, that of
+ * longer requests where there are too few of them for the GPU, and the pieces are
+ * joined by log-sum-exp. The cuts follow the whole batch's lengths, so a request's
+ * result may differ in its last bits from one batch to another; the same call gives
+ * the same bits.
  * Other arguments, streams and errors as pkv_paged_attention_varlen; num_heads /
  * num_kv_heads may be any number up to 128 (any at all for requests of one query).
- * max_seq_len below 2^30.
+ * max_seq_len below 2^30; num_seqs up to 4415 at head_dim 128 and 30000 at 64 where
+ * max_query_len is above 32 / G (PKV_ERR_UNSUPPORTED past these).
  */
 size_t pkv_window_attention_workspace_size(int32_t max_query_len, int32_t num_heads,
                                            int32_t num_kv_heads, int32_t head_dim,
@@ -821,6 +824,16 @@ pkv_status pkv_copy_blocks(void *kv_pool, const int32_t *copy_src, const int32_t
                            int32_t num_copies, int32_t num_blocks, int32_t block_size,
                            int32_t num_kv_heads, int32_t head_dim, int32_t *dev_status,
                            void *stream);
+
+/*
+ * pkv_copy_blocks_fp8 -- pkv_copy_blocks in an 8-bit pool: blocks and their scales,
+ * bit for bit. kv_pool, kv_scales as pkv_kv_cache_append_fp8 (any sizes whose blocks
+ * are a multiple of 16 bytes).
+ */
+pkv_status pkv_copy_blocks_fp8(void *kv_pool, float *kv_scales, const int32_t *copy_src,
+                               const int32_t *copy_dst, int32_t num_copies, int32_t num_blocks,
+                               int32_t block_size, int32_t num_kv_heads, int32_t head_dim,
+                               int32_t *dev_status, void *stream);
 
 /* Human-readable name of a pkv_status value (static storage). */
 const char *pkv_status_string(pkv_status status);

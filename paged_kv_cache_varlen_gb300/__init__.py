@@ -10,6 +10,7 @@ from .binding import (  # noqa: F401
     PkvError,
     attention_key_weights,
     attention_workspace_size,
+    copy_blocks_fp8,
     evict_compact,
     evict_select,
     kv_cache_append_fp8,
@@ -33,6 +34,7 @@ __all__ = [
     "PkvError",
     "attention_key_weights",
     "attention_workspace_size",
+    "copy_blocks_fp8",
     "evict_compact",
     "evict_select",
     "kv_cache_append_fp8",

@@ -49,6 +49,7 @@ _SIGNATURES = {
         _i32, [_vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _i32, _vp, _i32]
         + [_i32] * 6 + [ctypes.c_float, _vp, ctypes.c_size_t, _vp, _vp]),
     "pkv_copy_blocks": (_i32, [_vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp]),
+    "pkv_copy_blocks_fp8": (_i32, [_vp] * 4 + [_i32] * 5 + [_vp, _vp]),
     "pkv_rope_frequencies": (
         _i32, [_vp, _vp, _i32, ctypes.c_double, _i32] + [ctypes.c_double] * 4),
     "pkv_rope_kv_cache_write": (
@@ -452,6 +453,28 @@ def copy_blocks(kv_pool: torch.Tensor, copy_src: torch.Tensor, copy_dst: torch.T
         _ptr(kv_pool), _ptr(copy_src), _ptr(copy_dst), copy_src.shape[0], nb, bs, hkv, d,
         _ptr(dev_status), _stream(stream, kv_pool.device))
     _check(st, "copy_blocks")
+
+
+def copy_blocks_fp8(kv_pool: torch.Tensor, kv_scales: torch.Tensor, copy_src: torch.Tensor,
+                    copy_dst: torch.Tensor, *, dev_status: torch.Tensor | None = None,
+                    stream=None) -> None:
+    """:func:`copy_blocks` in the 8-bit pool of :func:`kv_cache_append_fp8`: the blocks
+    and their scales, bit for bit."""
+    _need(kv_pool, torch.float8_e4m3fn, 5, "kv_pool")
+    _need(kv_scales, torch.float32, 3, "kv_scales")
+    _need(copy_src, torch.int32, 1, "copy_src")
+    _need(copy_dst, torch.int32, 1, "copy_dst")
+    two, nb, bs, hkv, d = kv_pool.shape
+    if two != 2 or tuple(kv_scales.shape) != (2, nb, hkv):
+        raise ValueError("kv_pool must be [2, NB, BS, Hkv, D] and kv_scales [2, NB, Hkv]")
+    if copy_src.shape != copy_dst.shape:
+        raise ValueError("copy_src and copy_dst differ in length")
+    if dev_status is not None:
+        _need(dev_status, torch.int32, 1, "dev_status")
+    st = load_library().pkv_copy_blocks_fp8(
+        _ptr(kv_pool), _ptr(kv_scales), _ptr(copy_src), _ptr(copy_dst), copy_src.shape[0], nb, bs,
+        hkv, d, _ptr(dev_status), _stream(stream, kv_pool.device))
+    _check(st, "copy_blocks_fp8")
 
 
 class BlockManager:

@@ -565,7 +565,7 @@ pkv_status pkv_copy_blocks(void* kv_pool, const int32_t* copy_src, const int32_t
   if (block_bytes % 16 != 0) return PKV_ERR_UNSUPPORTED;
   if (num_copies > 65535 || block_bytes / 16 / 1024 > 65535) return PKV_ERR_UNSUPPORTED;
   return pkv::launch_copy_blocks(kv_pool, copy_src, copy_dst, num_copies, num_blocks,
-                                 block_bytes / 16, dev_status,
+                                 block_bytes / 16, nullptr, num_kv_heads, dev_status,
                                  static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? PKV_OK
              : PKV_ERR_CUDA;

@@ -211,4 +211,22 @@ pkv_status pkv_qk_norm_rope_kv_cache_append_fp8(
   return append(p, stream);
 }
 
+pkv_status pkv_copy_blocks_fp8(void* kv_pool, float* kv_scales, const int32_t* copy_src,
+                               const int32_t* copy_dst, int32_t num_copies, int32_t num_blocks,
+                               int32_t block_size, int32_t num_kv_heads, int32_t head_dim,
+                               int32_t* dev_status, void* stream) {
+  if (num_copies < 0 || num_blocks <= 0 || block_size <= 0 || num_kv_heads <= 0 || head_dim <= 0)
+    return PKV_ERR_INVALID_ARG;
+  if (num_copies == 0) return PKV_OK;
+  if (!kv_pool || !kv_scales || !copy_src || !copy_dst || !aligned(kv_pool, 16) ||
+      !aligned(kv_scales, 4))
+    return PKV_ERR_INVALID_ARG;
+  const int64_t block_bytes = (int64_t)block_size * num_kv_heads * head_dim;
+  if (block_bytes % 16 != 0) return PKV_ERR_UNSUPPORTED;
+  if (num_copies > 65535 || block_bytes / 16 / 1024 > 65535) return PKV_ERR_UNSUPPORTED;
+  return launched(pkv::launch_copy_blocks(kv_pool, copy_src, copy_dst, num_copies, num_blocks,
+                                          block_bytes / 16, kv_scales, num_kv_heads, dev_status,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

@@ -7,7 +7,8 @@
 // block_size * num_kv_heads * head_dim bf16 values of that half are
 // contiguous in the pool, so the copy is a straight 16-byte vector stream.
 // Copies of one call must be independent (no block both a source and a
-// destination), which the block manager's steps guarantee.
+// destination), which the block manager's steps guarantee. Of an 8-bit pool the
+// blocks' scales go with them.
 #include "common.cuh"
 #include "launch.h"
 
@@ -19,7 +20,7 @@ constexpr int kVecPerThread = 4;  // 16-byte vectors per thread per CTA
 
 __global__ void __launch_bounds__(kThreads)
     copy_blocks_kernel(uint4* pool, const int32_t* src, const int32_t* dst, int32_t num_blocks,
-                       int64_t block_vecs, int32_t* status) {
+                       int64_t block_vecs, float* scales, int32_t num_kv_heads, int32_t* status) {
   griddep_wait();
   griddep_launch_dependents();
   const int c = blockIdx.x;
@@ -44,13 +45,19 @@ __global__ void __launch_bounds__(kThreads)
     const int64_t i = base + (int64_t)k * kThreads;
     if (i < block_vecs) to[i] = v[k];
   }
+  if (scales && blockIdx.z == 0) {
+    float* of_half = scales + (int64_t)blockIdx.y * num_blocks * num_kv_heads;
+    for (int h = threadIdx.x; h < num_kv_heads; h += kThreads)
+      of_half[(int64_t)d * num_kv_heads + h] = of_half[(int64_t)s * num_kv_heads + h];
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_copy_blocks(void* pool, const int32_t* src, const int32_t* dst,
                                int32_t num_copies, int32_t num_blocks, int64_t block_vecs,
-                               int32_t* status, cudaStream_t stream) {
+                               float* scales, int32_t num_kv_heads, int32_t* status,
+                               cudaStream_t stream) {
   const int64_t per_cta = (int64_t)kThreads * kVecPerThread;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)num_copies, 2u, (unsigned)((block_vecs + per_cta - 1) / per_cta));
@@ -62,7 +69,7 @@ cudaError_t launch_copy_blocks(void* pool, const int32_t* src, const int32_t* ds
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, copy_blocks_kernel, static_cast<uint4*>(pool), src, dst,
-                            num_blocks, block_vecs, status);
+                            num_blocks, block_vecs, scales, num_kv_heads, status);
 }
 
 }  // namespace pkv

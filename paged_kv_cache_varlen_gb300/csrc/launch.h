@@ -241,10 +241,11 @@ cudaError_t launch_cascade_merge(float* out, float* out_lse, const float* part_o
                                  cudaStream_t stream);
 
 // Whole-block copies in the pool; block_vecs = 16-byte vectors in one
-// block of one half (K or V).
+// block of one half (K or V); scales: of an 8-bit pool, else null.
 cudaError_t launch_copy_blocks(void* pool, const int32_t* src, const int32_t* dst,
                                int32_t num_copies, int32_t num_blocks, int64_t block_vecs,
-                               int32_t* status, cudaStream_t stream);
+                               float* scales, int32_t num_kv_heads, int32_t* status,
+                               cudaStream_t stream);
 
 // Public dense merge: part_out [P][T*H][D], part_lse [P][T*H].
 cudaError_t launch_lse_merge(float* out, float* out_lse, const float* part_out,
