@@ -30,7 +30,7 @@ SOURCES = ["kv_write.cu", "decode_mma.cu", "decode_rows.cu", "merge.cu", "prefil
            "window_api.cpp", "api_noalloc.cu", "block_manager.cpp"]
 HEADERS = [os.path.join(CSRC, "common.cuh"), os.path.join(CSRC, "launch.h"),
            os.path.join(CSRC, "key_weights.cuh"), os.path.join(CSRC, "rope.cuh"),
-           os.path.join(CSRC, "wait.cuh"),
+           os.path.join(CSRC, "wait.cuh"), os.path.join(CSRC, "e4m3.cuh"),
            os.path.join(ROOT, "include", "pkv.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",

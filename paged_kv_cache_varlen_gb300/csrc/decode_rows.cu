@@ -46,14 +46,8 @@
 #include <math.h>
 
 #include "common.cuh"
+#include "e4m3.cuh"
 #include "launch.h"
-
-#ifndef PKV_ROWS_CTAS
-#define PKV_ROWS_CTAS 3
-#endif
-#ifndef PKV_ROWS_SPW
-#define PKV_ROWS_SPW 2
-#endif
 
 namespace pkv {
 namespace {
@@ -69,10 +63,7 @@ constexpr int kMinShare = 16;
 // What going over to another request costs a CTA, in units of a chunk's time: shares
 // of equal chunks alone ended 4.5 us apart for each request in them (64 contexts of
 // 512 to 4096 keys), about 12 chunks' time with 608 CTAs.
-#ifndef PKV_ROWS_COST
-#define PKV_ROWS_COST 18
-#endif
-constexpr int kStartCost = PKV_ROWS_COST;
+constexpr int kStartCost = 18;
 
 template <bool EIGHT>
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -91,27 +82,6 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Two e4m3 values (the low or the high half of w) as fp16x2, exactly.
-__device__ __forceinline__ uint32_t e4m3_lo(uint32_t w) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
-      : "=r"(r)
-      : "r"(w));
-  return r;
-}
-__device__ __forceinline__ uint32_t e4m3_hi(uint32_t w) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}"
-      : "=r"(r)
-      : "r"(w));
-  return r;
-}
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
@@ -199,11 +169,11 @@ struct Form {
   static constexpr int COLS = 8 * NT;
   static constexpr int ROW = EIGHT ? D : 2 * D;  // bytes of a key's K or V
   static constexpr int SLOT = 2 * kChunk * ROW;
-  static constexpr int SPW = (EIGHT ? (NT == 1 ? PKV_ROWS_SPW : 3) : 2) * (D == 128 ? 1 : 2);
+  static constexpr int SPW = (EIGHT && NT == 2 ? 3 : 2) * (D == 128 ? 1 : 2);
   static constexpr int SLOTS = kWarps * SPW * SLOT;
   static constexpr int RS = D + 4;  // floats of a column in the reduction, padded
   // at most so many CTAs an SM (their registers), fewer where shared memory ends first
-  static constexpr int CTAS = EIGHT && NT == 1 ? PKV_ROWS_CTAS : 3;
+  static constexpr int CTAS = 3;
   static constexpr size_t smem(int rows) {
     return 1024 + SLOTS + kWarps * SPW * sizeof(uint64_t) +
            (size_t)kWarps * (rows < COLS ? rows : COLS) * (RS + 2) * sizeof(float);

@@ -24,6 +24,7 @@
 #include <math.h>
 
 #include "common.cuh"
+#include "e4m3.cuh"
 #include "launch.h"
 #include "wait.cuh"
 
@@ -492,11 +493,6 @@ __device__ __noinline__ void plan_work(const AttnParams& p, int QP, int* ints, S
   sh.in = sums->start[2];
 }
 
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -524,21 +520,6 @@ __device__ __forceinline__ uint32_t bits_below(int n) {
   return ~r;
 }
 
-// Two e4m3 values (the low or the high half of w) as fp16x2, exactly.
-__device__ __forceinline__ uint32_t e4m3_lo(uint32_t w) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
-      : "=r"(r)
-      : "r"(w));
-  return r;
-}
-__device__ __forceinline__ uint32_t e4m3_hi(uint32_t w) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}"
-      : "=r"(r)
-      : "r"(w));
-  return r;
-}
 __device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t h) {
   float a, b;
   asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
