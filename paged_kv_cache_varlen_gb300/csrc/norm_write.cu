@@ -6,7 +6,7 @@
 // position m with the pair's frequency f:
 //   y = x (mean(x^2) + eps)^(-1/2) (w + offset),   t = m f,
 //   (a, b) -> factor * (a cos t - b sin t, b cos t + a sin t),
-// all in fp32, rounded once. The angle is formed as in rope_write.cu.
+// all in fp32, rounded once. The angle is formed modulo a turn as in rope_write.cu.
 //
 // 8 bits: a block's scale for one KV head is the power of two
 //   s = 2^ceil(log2(max |y| / 448)), 448 the largest e4m3 value,
@@ -99,7 +99,9 @@ __device__ __forceinline__ float norm_factor(const float (&y)[16], int GS, float
   for (int i = 0; i < 16; ++i) ss = fmaf(y[i], y[i], ss);
 #pragma unroll
   for (int o = 1; o < GS; o <<= 1) ss += __shfl_xor_sync(kFull, ss, o);
-  return rsqrtf(fmaf(ss, inv_dim, eps));
+  // (a Newton step takes the root's 2 ulp to less than one; not where it is 0 or no number)
+  const float v = fmaf(ss, inv_dim, eps), r = rsqrtf(v), e = fmaf(-v * r, r, 1.f);
+  return fabsf(e) < 1e-3f ? fmaf(0.5f * r, e, r) : r;
 }
 
 // A lane's 16 values turned; c, s: the cosines and sines of its 8 pairs (kHalves,
@@ -398,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, kRowCtas) norm_rope_kernel(const Nor
       if (i + passes - pass < n) next = look(t);
       __syncwarp();  // the last row's angles have been read
       for (int e = lane; e < half; e += 32) {
-        const float2 a = rope_angle(frac[e], (uint32_t)now.pos, p.factor);
+        const float2 a = near_angle(frac[e], (uint32_t)now.pos, p.factor);
         cs[e] = a.x;
         sn[e] = a.y;
       }
@@ -637,7 +639,7 @@ __global__ void __launch_bounds__(kBlockThreads, 512 / kBlockThreads) append_fp8
       const int row = first + e / half, i = e % half;
       const double f = __ldg(p.inv_freq + i);
       const int32_t pos = __ldg(p.positions + tok0 + row);
-      float2 a = rope_angle(turn_fraction(f), (uint32_t)pos, p.factor);
+      float2 a = near_angle(turn_fraction(f), (uint32_t)pos, p.factor);
       if (no_number(f)) a.x = a.y = __uint_as_float(kNan);
       cs[row * PAD + i] = a.x;
       sn[row * PAD + i] = a.y;
