@@ -1,6 +1,10 @@
 """The 8-bit cache's block copies, long requests that are few (their keys are cut
 into shares), batches of many requests, and what the Python calls refuse, on the
 GPU."""
+import os
+import re
+import textwrap
+
 import numpy as np
 import pytest
 import torch
@@ -146,6 +150,36 @@ def test_many_requests_with_prompts_among_them(eight, b):
     ql[[0, b - 1]] = 40, 70
     lens = ql + r.randint(0, 40, b)
     case(lens.tolist(), ql.tolist(), 8, 2, 64, 16, 50, 3, eight, seed=b)
+
+
+def test_the_readme_step_over_the_8_bit_cache():
+    # the README's blocks, run as they are written there
+    with open(os.path.join(os.path.dirname(__file__), "..", "README.md"), encoding="utf-8") as f:
+        text = f.read()
+    part = text[text.index("over the 8-bit cache and through a window."):]
+    blocks = [textwrap.dedent(b) for b in re.findall(r"(?:^    .*\n(?:^\n(?=    ))?)+", part, re.M)]
+    r = np.random.RandomState(5)
+    s = dict(torch=torch, pkv=pkv, num_blocks=200, num_kv_heads=2, inv_freq=pkv.rope_frequencies(
+        128)[0].cuda(), q_norm=torch.ones(128, device="cuda"), k_norm=torch.ones(128, device="cuda"))
+    exec(blocks[0], s)
+    bm = pkv.BlockManager(200, 16)
+    for i in range(2):
+        bm.add_seq(i)
+    for step in range(3):
+        new = [1100, 30] if step == 0 else [1, 1]
+        table, lens, cu, _, src, dst = bm.build_step([0, 1], new, 80)
+        t = int(cu[-1])
+        s.update(table=i32(table), lens=i32(lens), cu=i32(cu), src=i32(src), dst=i32(dst),
+                 max_q=max(new), max_len=int(max(lens)), positions=i32(np.concatenate(
+                     [np.arange(L - n, L) for L, n in zip(lens, new)])))
+        for name, n in (("q", 8), ("k", 2), ("v", 2)):
+            s[name] = torch.from_numpy(r.standard_normal((t, n, 128)).astype(np.float32)).to(
+                torch.bfloat16).cuda()
+        exec(blocks[1], s)
+        assert s["out"].shape == (t, 8, 128) and bool(torch.isfinite(s["out"]).all())
+        # a request's last row is a mean of its values
+        assert 0 < float(s["out"].float().abs().max()) < 5
+    bm.close()
 
 
 def _inputs():
