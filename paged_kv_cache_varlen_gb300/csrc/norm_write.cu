@@ -113,10 +113,16 @@ __device__ __forceinline__ void turn16(float (&y)[16], const float (&c)[8], cons
   if (MODE == kHalves) {
     if (l.turn) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float a = y[i], b = y[8 + i];
-        y[i] = a * c[i] - b * s[i];
-        y[8 + i] = b * c[i] + a * s[i];
+      for (int i = 0; i < 8; i += 2) {  // two pairs an instruction
+        const float2 a = make_float2(y[i], y[i + 1]), b = make_float2(y[8 + i], y[9 + i]);
+        const float2 cc = make_float2(c[i], c[i + 1]), ss = make_float2(s[i], s[i + 1]);
+        const float2 n = __fmul2_rn(b, ss);
+        const float2 x = __ffma2_rn(a, cc, make_float2(-n.x, -n.y));
+        const float2 z = __ffma2_rn(b, cc, __fmul2_rn(a, ss));
+        y[i] = x.x;
+        y[i + 1] = x.y;
+        y[8 + i] = z.x;
+        y[9 + i] = z.y;
       }
     }
   } else if (MODE == kPairs) {
@@ -564,20 +570,21 @@ __global__ void __launch_bounds__(kBlockThreads, 512 / kBlockThreads) append_fp8
     if (n < kBlockThreads) break;
   }
   const int r = count - 1;
-  if (r < 0) return;
-  const int local = item - (__ldg(p.cu_seqlens + r) / BS + 2 * r);
-  auto bad_lengths = [&](int i) {
-    const int32_t a = __ldg(p.cu_seqlens + i), b = __ldg(p.cu_seqlens + i + 1);
-    if (a < 0 || b < a || b > p.num_tokens) return true;
-    const int32_t len = __ldg(p.seq_lens + i);
-    return b > a && (len < b - a || b - a > p.max_query_len || len > p.max_blocks * BS);
+  // lengths that are no good (the three loads at once)
+  auto read_lengths = [&](int i, int32_t& t0, int32_t& qlen, int32_t& len) {
+    t0 = __ldg(p.cu_seqlens + i);
+    const int32_t t1 = __ldg(p.cu_seqlens + i + 1);
+    len = __ldg(p.seq_lens + i);
+    qlen = t1 - t0;
+    return t0 < 0 || t1 < t0 || t1 > p.num_tokens ||
+           (qlen > 0 && (len < qlen || qlen > p.max_query_len || len > p.max_blocks * BS));
   };
+  int32_t t0, qlen, L;
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < p.num_seqs; i += kBlockThreads)
-      if (bad_lengths(i)) set_status(p.status, PKV_DEV_BAD_LENGTHS);
-  if (bad_lengths(r)) return;
-  const int32_t t0 = __ldg(p.cu_seqlens + r), qlen = __ldg(p.cu_seqlens + r + 1) - t0;
-  const int32_t L = __ldg(p.seq_lens + r);
+      if (read_lengths(i, t0, qlen, L)) set_status(p.status, PKV_DEV_BAD_LENGTHS);
+  if (r < 0 || read_lengths(r, t0, qlen, L)) return;
+  const int local = item - (t0 / BS + 2 * r);
   const int32_t start = L - qlen;  // the position of the first new token
   const int32_t block = start / BS + local;
   if (qlen < 1 || block > (L - 1) / BS) return;
@@ -697,6 +704,9 @@ __global__ void __launch_bounds__(kBlockThreads, 512 / kBlockThreads) append_fp8
     const bool key = job < Hkv;
     const int h = key ? job : job - Hkv;
     const bool normed = key && p.k_weight != nullptr, turned = key && half > 0;
+    // the scale: a block that holds rows already keeps its own where that is larger
+    float* scale_at = p.scales + ((int64_t)(key ? 0 : p.num_blocks) + id) * Hkv + h;
+    const float old = first > 0 ? *scale_at : 0.f;
     float top = 0.f;
     for (int g = g0; g <= g1; ++g) {
       rows_of(normed, wk, turned, g, y, ok);
@@ -708,9 +718,6 @@ __global__ void __launch_bounds__(kBlockThreads, 512 / kBlockThreads) append_fp8
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-    // the scale: a block that holds rows already keeps its own where that is larger
-    float* scale_at = p.scales + ((int64_t)(key ? 0 : p.num_blocks) + id) * Hkv + h;
-    const float old = first > 0 ? *scale_at : 0.f;
     const float scale = fmaxf(old, block_scale(top));
     uint8_t* rows = static_cast<uint8_t*>(p.pool) +
                     (((int64_t)(key ? 0 : p.num_blocks) + id) * BS * Hkv + h) * D;
