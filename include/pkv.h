@@ -568,6 +568,8 @@ pkv_status pkv_qk_norm_rope_kv_cache_append_fp8(
  * joined by log-sum-exp. The cuts follow the whole batch's lengths, so a request's
  * result may differ in its last bits from one batch to another; the same call gives
  * the same bits.
+ * out, out_lse and the workspace overlap neither one another nor q, the pool and its
+ * scales (PKV_ERR_INVALID_ARG).
  * Other arguments, streams and errors as pkv_paged_attention_varlen; num_heads /
  * num_kv_heads may be any number up to 128 (any at all for requests of one query).
  * max_seq_len below 2^30; num_seqs up to 4415 at head_dim 128 and 30000 at 64 where

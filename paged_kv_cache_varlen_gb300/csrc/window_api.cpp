@@ -18,6 +18,13 @@ using pkv::AttnParams;
 constexpr int32_t kWholeChunks = 16;
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Whether the byte ranges [a, a + na) and [b, b + nb) meet.
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  if (na == 0 || nb == 0) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // How a call's short requests (up to 32 / G queries) run.
@@ -96,6 +103,27 @@ pkv_status attention(void* out, int32_t out_f32, float* out_lse, const void* q, 
     return PKV_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < sp.total || !aligned(workspace, 256))
     return PKV_ERR_WORKSPACE;
+  // what is written meets nothing that is read
+  const int64_t out_rows = (int64_t)num_tokens * num_heads;
+  const int64_t pool_values = (int64_t)2 * num_blocks * block_size * num_kv_heads * head_dim;
+  struct Range {
+    const void* at;
+    int64_t bytes;
+  };
+  const Range written[] = {{out, out_rows * head_dim * (out_f32 ? 4 : 2)},
+                           {out_lse, out_lse ? out_rows * 4 : 0},
+                           {workspace, (int64_t)sp.total}};
+  const Range read[] = {{q, out_rows * head_dim * 2},
+                        {kv_pool, pool_values * (eight ? 1 : 2)},
+                        {scales, eight ? (int64_t)2 * num_blocks * num_kv_heads * 4 : 0}};
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < 3; ++j)
+      if (overlap(written[i].at, written[i].bytes, read[j].at, read[j].bytes))
+        return PKV_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlap(written[i].at, written[i].bytes, written[j].at, written[j].bytes))
+        return PKV_ERR_INVALID_ARG;
+  }
 
   AttnParams p{};
   p.out = static_cast<float*>(out);

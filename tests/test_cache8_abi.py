@@ -175,6 +175,12 @@ ATTENTION = [
     ({"max_query_len": 40, "num_heads": 258}, UNSUPPORTED),
     ({"max_query_len": 40, "num_seqs": 4416}, UNSUPPORTED),
     ({"max_query_len": 1, "num_heads": 258, "num_seqs": 4416}, CUDA),
+    # results over inputs, over one another, over the workspace
+    ({"out": 64 * MB}, INVALID), ({"out": 512 * MB + 1024}, INVALID),
+    ({"out_lse": 256 * MB + 64}, INVALID), ({"out_lse": 512 * MB}, INVALID),
+    ({"out_lse": 64 * MB + 4}, INVALID), ({"workspace": 64 * MB}, INVALID),
+    ({"workspace": 256 * MB}, INVALID), ({"workspace": 512 * MB}, INVALID),
+    ({"out_lse": 25 * MB}, CUDA), ({"out": 64 * MB + 20480}, CUDA),
     ({"window": 0}, CUDA), ({"window": INT_MAX, "num_sink": INT_MAX}, CUDA),
     ({"max_query_len": 40}, CUDA), ({}, CUDA),
 ]
@@ -186,7 +192,8 @@ def test_attention(lib, eight, over, status):
     assert _window(lib, eight, **over) == status
 
 
-@pytest.mark.parametrize("over", [{"scales": None}, {"scales": 21 * MB + 2}])
+@pytest.mark.parametrize("over", [{"scales": None}, {"scales": 21 * MB + 2}, {"out": 21 * MB},
+                                  {"workspace": 21 * MB}])
 def test_attention_over_no_scales(lib, over):
     assert _window(lib, True, **over) == INVALID
 
