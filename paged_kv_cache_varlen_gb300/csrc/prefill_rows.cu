@@ -4,23 +4,38 @@
 //
 //   * persistent CTAs, one per SM; a work item is (request, KV head, two query
 //     tiles A and B of 128 rows, 128 / G queries of G heads each), taken in the
-//     order of the heaviest requests from a ticket counter in the workspace;
+//     order of the heaviest requests from a ticket counter in the workspace. Where
+//     there are too few items for the SMs, each CTA has an equal share of all their
+//     tiles instead, and the pieces of an item are joined by log-sum-exp;
 //   * the keys that some query of an item sees, its sinks' 16-key chunks and then
 //     its window's, are numbered through: a tile is consecutive ones of them, wherever
 //     they lie in the context, so that a few sinks cost a quarter of a tile and a
 //     window no more than its ends. In these numbers a row sees the columns
-//     [low, lim] and those before num_sink;
+//     [low, lim] and those before the sinks' end;
 //   * S = Q K^T over 64 keys (bf16), O += P V (fp16 P and V), fp32 accumulators in
 //     tensor memory: two S and one O of both query tiles fill its 512 columns, P
 //     (fp16) lies over the first half of its S;
-//   * one issuing thread a query tile: S(0), S(1), then PV(j), S(j + 2): a softmax
-//     goes from one tile to the next without waiting for products;
+//   * a warp issues a query tile's products by one elected lane: S(0), S(1), then
+//     PV(j), S(j + 2), so that a softmax goes from one tile to the next without
+//     waiting for products. (By a lane of a diverged warp each product takes a loop
+//     over lanes to get its operands: 171 us for the prompt below, 156 so.);
 //   * a softmax thread owns a row: 64 scores in registers, one pass;
-//   * K and V arrive by TMA in 16-key boxes into two-stage rings. V becomes fp16 in
-//     place (four converter warps); at 8 bits K becomes bf16 and V fp16, both
-//     exactly, and a block's two scales act on the scores;
+//   * K and V arrive by TMA in 16-key boxes, K into two stages of 128 keys, V into five
+//     of 64. V becomes fp16 in place (four converter warps); at 8 bits K becomes bf16
+//     and V fp16, both exactly, and a block's two scales act on the scores;
 //   * every wait is bounded; on a timeout the CTA drains its copies and products,
 //     frees its tensor memory and leaves with PKV_DEV_TIMEOUT set.
+//
+// What bounds it (32 + 8 heads of 128): over 8 bits the chain of a softmax warp
+// (barrier, tensor-memory load, maximum, exponentials, store: ~2000 cycles for 64 keys
+// where the products of both query tiles take 1024), two such warps an SM quarter, in
+// phase; over bf16 shared memory's 128 bytes a cycle as well, of which 64 keys take
+// 1536 cycles (Q and K of 64-key products 96 KB, V's products 32, its conversion 32,
+// the copies 32). 8-bit chunks of 1500 to 2048 tokens over 4096 to 8192 keys: 349 us,
+// 51 % of the bf16 peak; a prompt of 8192 tokens through a window of 1024: 154 us, 43 %.
+// Tried: 128-key tiles with one S each (the chain QK, softmax, PV of a tile is longer
+// than two of these: 391 us), the weights formed before the maximum is known (373), a
+// half of the next scores loaded between the halves of a softmax (392).
 #include <math.h>
 
 #include "common.cuh"
@@ -1118,7 +1133,7 @@ __device__ __forceinline__ void work_on(const CUtensorMap& q_map, const CUtensor
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&bars->p_ready[x][gt & 1]));
         l += EIGHT ? sum8 : sum.x + sum.y;
-        // (at the loop's end: 353 us at 8 bits and 2048-token chunks, 359 at its start)
+        // (at the loop's end: 8-bit chunks of 2048 tokens 353 us, 359 at its start)
         if (j + 1 < d.n) ok = load_scores(gt + 1, u);
         if (!ok) break;
       }

@@ -182,6 +182,57 @@ def test_the_readme_step_over_the_8_bit_cache():
     bm.close()
 
 
+@BOTH
+@pytest.mark.parametrize("ql", [[1, 1], [40, 1]])
+def test_blocks_past_4_gb(eight, ql):
+    # the same blocks at the end of a pool of more than 2^32 bytes a half
+    hkv, d, bs, nb = 8, 128, 16, 300_000 if eight else 150_000
+    s = Step([300, 77], ql, 16, hkv, d, bs, 100, 3, eight, seed=6)
+    want, wl = s.call()
+    pool = torch.empty((2, nb, bs, hkv, d), dtype=s.pool.dtype, device="cuda")
+    kind = torch.uint8 if eight else torch.int16
+    pool.view(kind)[:, nb - s.nb:] = s.pool.view(kind)
+    s.pool = pool
+    if eight:
+        scales = torch.empty((2, nb, hkv), device="cuda")
+        scales[:, nb - s.nb:] = s.scales
+        s.scales = scales
+    s.table = np.where(s.table >= 0, s.table + nb - s.nb, -1).astype(np.int32)
+    got, gl = s.call()
+    assert torch.equal(got, want) and torch.equal(gl, wl)
+    # and written there
+    t = sum(ql)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q = torch.randn((t, 16, d), device="cuda", generator=g).to(torch.bfloat16)
+    k, v = (torch.randn((t, hkv, d), device="cuda", generator=g).to(torch.bfloat16) for _ in "kv")
+    w = torch.ones(d, device="cuda")
+    inv = pkv.rope_frequencies(d)[0].cuda()
+    pos = i32(np.arange(t))
+    if not eight:
+        slots = (nb - 1) * bs + np.arange(t) - 40
+        pkv.qk_norm_rope_kv_cache_write(q, s.pool, k, v, pos, i32(slots), inv, w, w)
+        rows = s.pool.view(2, -1, hkv, d)[1, torch.from_numpy(slots).cuda()]
+        assert torch.equal(rows, v)
+        return
+    table = np.full((2, 20), -1)
+    for i, L in enumerate(s.lens):
+        table[i, (L - ql[i]) // bs:(L - 1) // bs + 1] = nb - 1 - 5 * i - np.arange(
+            (L - 1) // bs + 1 - (L - ql[i]) // bs)
+    small = torch.zeros((2, 10, bs, hkv, d), device="cuda").to(torch.float8_e4m3fn)
+    near = torch.zeros((2, 10, hkv), device="cuda")
+    s.pool.view(torch.uint8)[:, nb - 10:] = 0
+    s.scales[:, nb - 10:] = 0
+    for p, sc, tab in ((s.pool, s.scales, table), (small, near, np.where(table < 0, -1, table - (nb - 10)))):
+        pkv.qk_norm_rope_kv_cache_append_fp8(q, p, sc, k, v, pos, i32(tab), i32(s.cu), i32(s.lens),
+                                             max(ql), inv, w, w)
+    assert torch.equal(s.pool.view(torch.uint8)[:, nb - 10:], small.view(torch.uint8))
+    assert torch.equal(s.scales[:, nb - 10:], near) and bool((near > 0).any())
+    # copied there
+    pkv.copy_blocks_fp8(s.pool, s.scales, i32([nb - 1]), i32([nb - 20]))
+    assert torch.equal(s.pool.view(torch.uint8)[:, nb - 20], small.view(torch.uint8)[:, 9])
+    assert torch.equal(s.scales[:, nb - 20], near[:, 9])
+
+
 def _inputs():
     q = torch.zeros((4, 8, 64), dtype=torch.bfloat16, device="cuda")
     k = torch.zeros((4, 2, 64), dtype=torch.bfloat16, device="cuda")
