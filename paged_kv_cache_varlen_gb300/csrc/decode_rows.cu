@@ -58,7 +58,8 @@ constexpr int kThreads = kWarps * 32;
 constexpr float kRescaleThreshold = 8.f;
 constexpr uint32_t kFull = 0xffffffffu;
 // A share is at least this many units, so that short contexts are not cut into pieces
-// that cost more than they save.
+// that cost more than they save (2 contexts of 4096 keys, 8 bits: 14.8 us; 16.4 with
+// shares of 8, 16.0 with 32; one of 2048: 12.4, 12.4, 14.6).
 constexpr int kMinShare = 16;
 // What going over to another request costs a CTA, in units of a chunk's time: shares
 // of equal chunks alone ended 4.5 us apart for each request in them (64 contexts of
