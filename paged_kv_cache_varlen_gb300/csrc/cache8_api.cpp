@@ -63,7 +63,7 @@ pkv_status append(pkv::NormRopeParams& p, void* stream) {
   if (2 * p.num_slots > INT32_MAX) return PKV_ERR_UNSUPPORTED;
   // grid items of every share of the heads, counted in 32 bits
   const int64_t items = (int64_t)p.num_tokens / p.block_size + 2 * (int64_t)p.num_seqs;
-  const int64_t shares = (2 * (int64_t)p.num_kv_heads + p.num_heads) / 8 + 1;
+  const int64_t shares = (2 * (int64_t)p.num_kv_heads + p.num_heads) / 2 + 1;
   if (items * (shares < 152 * 4 ? shares : 152 * 4) > INT32_MAX) return PKV_ERR_UNSUPPORTED;
   if (pkv_status s = check_rows(p, 1); s != PKV_OK) return s;
   const int64_t scale_bytes = (int64_t)2 * p.num_blocks * p.num_kv_heads * 4;

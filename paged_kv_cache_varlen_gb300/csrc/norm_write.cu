@@ -32,10 +32,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-// of the block kernel: smaller CTAs whose setups overlap (8192 tokens: 43 us; 256
-// threads 46, 64 threads 47)
-constexpr int kBlockThreads = 128;
-constexpr int kBlockWarps = kBlockThreads / 32;
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kAhead = 3;  // passes whose copies are under way (5: as fast)
 // CTAs an SM; three of them spill (8192 tokens: 36 us, 40 with three)
@@ -531,14 +527,21 @@ cudaError_t launch_rows(const NormRopeParams& p, cudaStream_t stream) {
 
 // One CTA: the rows that the step adds to one block of one request, a share of
 // the heads. A warp holds a group of rows of one head in registers: their largest
-// magnitude gives the scale, and they are written without being read again. Blocks of
-// several groups read them twice, the second time from L2 (8192 tokens of 32 + 8 heads
-// of 128 in blocks of 16, 32, 64: 43, 61, 75 us; their angles also leave room for fewer
-// CTAs. A warp for each of a block's groups: 47, 58, 70). The next group's rows come
-// into shared memory meanwhile (50 us without, 46 with, at 256 threads).
-template <int D, int MODE, int NP>
-__global__ void __launch_bounds__(kBlockThreads, 512 / kBlockThreads)
+// magnitude gives the scale, and they are written without being read again. The groups
+// of a longer block have a warp each, TEAM of them, who tell one another the largest
+// (blocks of more than four groups read their rows twice, the second time from L2). The
+// next rows come into shared memory meanwhile. 8192 tokens of 32 + 8 heads of 128 in
+// blocks of 16, 32, 64: 43, 54, 60 us; 43, 61, 75 when one warp goes through a block's
+// groups twice; 50 for blocks of 16 when nothing is fetched ahead. CTAs of 4 warps, so
+// that their setups overlap (blocks of 16: 46 us with 8, 47 with 2), 8 for teams of 4,
+// as the angles of their blocks leave room for fewer.
+template <int TEAM>
+constexpr int kBlockWarps = TEAM == 4 ? 8 : 4;
+
+template <int D, int MODE, int NP, int TEAM>
+__global__ void __launch_bounds__(kBlockWarps<TEAM> * 32, 16 / kBlockWarps<TEAM>)
     append_fp8_kernel(const NormRopeParams p, const int parts) {
+  constexpr int W = kBlockWarps<TEAM>, kBlockThreads = 32 * W;
   constexpr int V = D / 8, GS = group_lanes(D);
   constexpr int RP = 32 / GS;   // rows at a time
   constexpr int RG = NP * RP;   // of a group
@@ -551,10 +554,10 @@ __global__ void __launch_bounds__(kBlockThreads, 512 / kBlockThreads)
   float* wk = wq + D;                          // [D]
   float* st = wk + D + warp * 512;             // [512] (kAny)
   // the warp's ring: [2][NP][2][32][16], a lane's vectors of the rows of a head
-  uint8_t* ring = reinterpret_cast<uint8_t*>(wk + D + (MODE == kAny ? kBlockWarps * 512 : 0)) +
+  uint8_t* ring = reinterpret_cast<uint8_t*>(wk + D + (MODE == kAny ? W * 512 : 0)) +
                   warp * 2 * NP * 1024 + lane * 16;
-  uint8_t* good = reinterpret_cast<uint8_t*>(wk + D + (MODE == kAny ? kBlockWarps * 512 : 0)) +
-                  kBlockWarps * 2 * NP * 1024;             // [256]: whether a row's position is good
+  uint8_t* good = reinterpret_cast<uint8_t*>(wk + D + (MODE == kAny ? W * 512 : 0)) +
+                  W * 2 * NP * 1024;             // [256]: whether a row's position is good
   float* cs = reinterpret_cast<float*>(good + 256);   // [BS][PAD], then the sines
   float* sn = cs + BS * PAD;
   griddep_wait();
@@ -603,10 +606,13 @@ __global__ void __launch_bounds__(kBlockThreads, 512 / kBlockThreads)
   // A job is a head: of the keys, the values, the queries. The rows of one come into
   // the ring while those before are worked on.
   const int kv = write ? 2 * Hkv : 0, jobs = kv + (p.q ? H : 0);
-  const int job0 = part * kBlockWarps + warp, stride_jobs = parts * kBlockWarps;
-  // keys and values of more than one group are read twice
-  auto sweeps = [&](int job) { return job < kv && g0 != g1 ? 2 : 1; };
-  int fjob = job0, fg = g0, fsweep = 0, to = 0;
+  const int team = warp / TEAM, member = warp % TEAM;
+  const int job0 = part * (W / TEAM) + team, stride_jobs = parts * (W / TEAM);
+  const int own0 = g0 + member;         // the warp's first group (of none: past g1)
+  const bool again = own0 + TEAM <= g1;  // it has several: keys and values are read twice
+  __shared__ float tops[2][W];
+  auto sweeps = [&](int job) { return job < kv && again ? 2 : 1; };
+  int fjob = own0 <= g1 ? job0 : jobs, fg = own0, fsweep = 0, to = 0;
   auto fetch = [&] {
     if (fjob < jobs) {
       const bool query = fjob >= kv, key = !query && fjob < Hkv;
@@ -622,8 +628,9 @@ __global__ void __launch_bounds__(kBlockThreads, 512 / kBlockThreads)
         cp_async_16(dst, at + l.a * 8, 16);
         cp_async_16(dst + 512, at + l.b * 8, 16);
       }
-      if (++fg > g1) {
-        fg = g0;
+      fg += TEAM;
+      if (fg > g1) {
+        fg = own0;
         if (++fsweep == sweeps(fjob)) {
           fsweep = 0;
           fjob += stride_jobs;
@@ -686,12 +693,13 @@ __global__ void __launch_bounds__(kBlockThreads, 512 / kBlockThreads)
       }
   };
 
+  int turn = 0;
   for (int job = job0; job < jobs; job += stride_jobs) {
     float y[NP][16];
     bool ok[NP];
     if (job >= kv) {  // a query head
       const int h = job - kv;
-      for (int g = g0; g <= g1; ++g) {
+      for (int g = own0; g <= g1; g += TEAM) {
         rows_of(p.q_weight != nullptr, wq, half > 0, g, y, ok);
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
@@ -710,7 +718,7 @@ __global__ void __launch_bounds__(kBlockThreads, 512 / kBlockThreads)
     float* scale_at = p.scales + ((int64_t)(key ? 0 : p.num_blocks) + id) * Hkv + h;
     const float old = first > 0 ? *scale_at : 0.f;
     float top = 0.f;
-    for (int g = g0; g <= g1; ++g) {
+    for (int g = own0; g <= g1; g += TEAM) {
       rows_of(normed, wk, turned, g, y, ok);
 #pragma unroll
       for (int i = 0; i < NP; ++i)
@@ -720,21 +728,28 @@ __global__ void __launch_bounds__(kBlockThreads, 512 / kBlockThreads)
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+    if (TEAM > 1) {
+      if (lane == 0) tops[turn][warp] = top;
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(32 * TEAM) : "memory");
+#pragma unroll
+      for (int w = 0; w < TEAM; ++w) top = fmaxf(top, tops[turn][team * TEAM + w]);
+      turn ^= 1;  // (who writes there again has met the others at the next barrier)
+    }
     const float scale = fmaxf(old, block_scale(top));
     uint8_t* rows = static_cast<uint8_t*>(p.pool) +
                     (((int64_t)(key ? 0 : p.num_blocks) + id) * BS * Hkv + h) * D;
     const int64_t step = (int64_t)Hkv * D;
     if (first > 0 && scale != old) {
       const float ratio = old > 0.f ? old / scale : 0.f;
-      for (int e = lane; e < first * (D / 4); e += 32) {
+      for (int e = member * 32 + lane; e < first * (D / 4); e += 32 * TEAM) {
         uint32_t* at = reinterpret_cast<uint32_t*>(rows + (e / (D / 4)) * step) + e % (D / 4);
         *at = rescale4(*at, ratio);
       }
     }
-    __syncwarp();  // every lane has read the old scale
-    if (lane == 0 && scale != old) *scale_at = scale;
-    for (int g = g0; g <= g1; ++g) {
-      if (g0 != g1) rows_of(normed, wk, turned, g, y, ok);
+    __syncwarp();  // every lane (and at the barrier every warp) has read the old scale
+    if (member == 0 && lane == 0 && scale != old) *scale_at = scale;
+    for (int g = own0; g <= g1; g += TEAM) {
+      if (again) rows_of(normed, wk, turned, g, y, ok);
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         uint8_t* out = rows + (g * RG + i * RP + row_slot) * step;
@@ -746,27 +761,28 @@ __global__ void __launch_bounds__(kBlockThreads, 512 / kBlockThreads)
   }
 }
 
-template <int D, int MODE, int NP>
+template <int D, int MODE, int NP, int TEAM>
 cudaError_t launch_append_rows(const NormRopeParams& p, cudaStream_t stream) {
-  size_t smem = 2 * D * sizeof(float) + (MODE == kAny ? kBlockWarps * 512 * sizeof(float) : 0) +
-                kBlockWarps * 2 * NP * 1024 + 256;
+  constexpr int W = kBlockWarps<TEAM>;
+  size_t smem = 2 * D * sizeof(float) + (MODE == kAny ? W * 512 * sizeof(float) : 0) +
+                W * 2 * NP * 1024 + 256;
   if (p.rotary_dim > 0) smem += (size_t)p.block_size * D * sizeof(float);
-  auto kernel = append_fp8_kernel<D, MODE, NP>;
+  auto kernel = append_fp8_kernel<D, MODE, NP, TEAM>;
   if (smem > 48 * 1024) {
     static SmemLimit limit;
-    cudaError_t e = limit.ensure(reinterpret_cast<const void*>(kernel), 216 * 1024);
+    cudaError_t e = limit.ensure(reinterpret_cast<const void*>(kernel), 226 * 1024);
     if (e != cudaSuccess) return e;
   }
   const int64_t items = (int64_t)p.num_tokens / p.block_size + 2 * (int64_t)p.num_seqs;
-  // shares of a block's heads: enough CTAs for the GPU, no more than leave a
-  // warp one head
+  // shares of a block's heads: enough CTAs for the GPU, no more than leave a team of
+  // warps one head
   const int jobs = 2 * p.num_kv_heads + (p.q ? p.num_heads : 0);
   const int64_t blocks = p.num_tokens / p.block_size + p.num_seqs;  // about
   int parts = 1;
-  while (parts * kBlockWarps < jobs && blocks * parts < 152 * 4) ++parts;
+  while (parts * (W / TEAM) < jobs && blocks * parts < 152 * 4) ++parts;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(items * parts));
-  cfg.blockDim = dim3(kBlockThreads);
+  cfg.blockDim = dim3(32 * W);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -782,10 +798,15 @@ cudaError_t launch_append_rows(const NormRopeParams& p, cudaStream_t stream) {
 // by groups of 32; blocks of 32 29 us, 34 by groups of 16).
 template <int D, int MODE>
 cudaError_t launch_append_mode(const NormRopeParams& p, cudaStream_t stream) {
+  constexpr int kRows = D == 64 ? 32 : 16;
   if constexpr (D == 64) {
-    if (p.block_size == 16) return launch_append_rows<D, MODE, 2>(p, stream);
+    if (p.block_size == 16) return launch_append_rows<D, MODE, 2, 1>(p, stream);
   }
-  return launch_append_rows<D, MODE, 4>(p, stream);
+  if constexpr (MODE != kAny) {
+    if (D == 128 && p.block_size > 2 * kRows) return launch_append_rows<128, MODE, 4, 4>(p, stream);
+    if (p.block_size > kRows) return launch_append_rows<D, MODE, 4, 2>(p, stream);
+  }
+  return launch_append_rows<D, MODE, 4, 1>(p, stream);
 }
 
 template <int D>
