@@ -19,7 +19,7 @@
 // sum of squares meets in a few shuffles and the halves of a pair in one lane.
 //
 // What bounds them: bytes, for prompts (8192 tokens of 32 + 8 heads of 128: 201 MB
-// into a bf16 pool, 36 us, 5.6 TB/s; 185 MB into an 8-bit one, 43 us, 4.3 TB/s, where
+// into a bf16 pool, 36 us, 5.6 TB/s; 185 MB into an 8-bit one, 44 us, 4.2 TB/s, where
 // the angles, the magnitudes and the roundings keep the issue slots half busy);
 // latency, for single tokens (3.4 us for one, 5.1 us for 64 of them at 8 bits: a chain
 // of lengths, block, scale, rows).
@@ -559,7 +559,7 @@ cudaError_t launch_rows(const NormRopeParams& p, cudaStream_t stream) {
 // of a longer block have a warp each, TEAM of them, who tell one another the largest
 // (blocks of more than four groups read their rows twice, the second time from L2). The
 // next rows come into shared memory meanwhile. 8192 tokens of 32 + 8 heads of 128 in
-// blocks of 16, 32, 64: 43, 54, 60 us; 43, 61, 75 when one warp goes through a block's
+// blocks of 16, 32, 64: 44, 55, 62 us; 44, 62, 76 when one warp goes through a block's
 // groups twice; 50 for blocks of 16 when nothing is fetched ahead. CTAs of 4 warps, so
 // that their setups overlap (blocks of 16: 46 us with 8, 47 with 2), 8 for teams of 4,
 // as the angles of their blocks leave room for fewer.
@@ -827,7 +827,7 @@ cudaError_t launch_append_rows(const NormRopeParams& p, cudaStream_t stream) {
 
 // A group of rows: 16 at 128 dimensions, and at 64 where the blocks are no longer; 32
 // at 64 dimensions otherwise (8192 tokens of 32 + 8 heads of 64: blocks of 16 26 us, 35
-// by groups of 32; blocks of 32 29 us, 34 by groups of 16).
+// by groups of 32; blocks of 32 31 us, 34 by groups of 16).
 template <int D, int MODE>
 cudaError_t launch_append_mode(const NormRopeParams& p, cudaStream_t stream) {
   constexpr int kRows = D == 64 ? 32 : 16;
