@@ -33,9 +33,9 @@
 // 1536 cycles (Q and K of 64-key products 96 KB, V's products 32, its conversion 32,
 // the copies 32). 8-bit chunks of 1500 to 2048 tokens over 4096 to 8192 keys: 349 us,
 // 51 % of the bf16 peak; a prompt of 8192 tokens through a window of 1024: 154 us, 43 %.
-// Tried: 128-key tiles with one S each (the chain QK, softmax, PV of a tile is longer
-// than two of these: 391 us), the weights formed before the maximum is known (373), a
-// half of the next scores loaded between the halves of a softmax (392).
+// Tried: 128-key tiles with one S each (less of shared memory, a longer chain: 358 and
+// 157 us), the weights formed before the maximum is known (373), a half of the next
+// scores loaded between the halves of a softmax (392), their barrier asked then (351).
 #include <math.h>
 
 #include "common.cuh"
