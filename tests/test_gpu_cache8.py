@@ -10,9 +10,11 @@ import pytest
 import torch
 
 import paged_kv_cache_varlen_gb300 as pkv
+from paged_kv_cache_varlen_gb300 import binding
 
 from . import plain_cache8 as plain
 from .gpu_util import guarded, guards_intact
+from .test_gpu_norm_write import pool8, step, values
 from .test_gpu_window import Step, case, f64, i32
 
 pytestmark = pytest.mark.gpu
@@ -47,6 +49,57 @@ def test_copied_blocks_keep_their_bits(nb, bs, hkv, d):
         pkv.copy_blocks_fp8(pool, scales, i32([0, 1]), i32([1]))
     with pytest.raises(TypeError):
         pkv.copy_blocks_fp8(pool.view(torch.uint8), scales, i32([0]), i32([1]))
+
+
+@pytest.mark.parametrize("bs", [16, 64, 256])
+@pytest.mark.parametrize("hkv,d", [(8, 128), (1, 64), (3, 64)])
+def test_single_tokens_into_blocks(hkv, d, bs):
+    # a token a request at most: rows of their own. Requests without one, first rows of
+    # blocks, rows that make the block's scale grow and that do not, tokens of nobody
+    r = np.random.RandomState(bs + d)
+    ql = r.randint(0, 2, 90)
+    lens = r.randint(1, 400, 90)
+    lens[:6] = bs + 1, bs, 1, 2 * bs, 17, 16
+    table, cu, nb = step(lens.tolist(), ql.tolist(), bs, d)
+    t = int(cu[-1])
+    g = torch.Generator(device="cuda").manual_seed(bs)
+    size = torch.exp2(torch.randint(-6, 6, (t + 3, 1, 1), generator=g, device="cuda").float())
+    k, v = ((torch.randn((t + 3, hkv, d), generator=g, device="cuda") * size).to(torch.bfloat16)
+            for _ in "kv")
+    pool, scales = pool8(nb, bs, hkv, d, bs)
+    want, ws, _ = plain.append(values(pool), f64(scales), f64(k), f64(v), table, cu, lens)
+    assert 0 < np.mean(ws != f64(scales)) < 0.5
+    pkv.kv_cache_append_fp8(pool, scales, k, v, i32(table), i32(cu), i32(lens), 1)
+    assert np.array_equal(f64(scales), ws) and np.array_equal(values(pool), want)
+
+
+def test_single_tokens_that_are_flagged():
+    hkv, d, bs = 2, 64, 16
+    lens, ql = [20, 18, 5, 33, 9], [1, 1, 1, 1, 1]
+    table, cu, nb = step(lens, ql, bs, 5)
+    q, k, v = (torch.randn((5, n, d), device="cuda").to(torch.bfloat16) for n in (4, hkv, hkv))
+    pool, scales = pool8(nb, bs, hkv, d, 7)
+    before, sb = values(pool), f64(scales)
+    bad = table.copy()
+    bad[1, 1] = nb                                   # a block outside the pool
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.full((5, 4, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    pkv.qk_norm_rope_kv_cache_append_fp8(q, pool, scales, k, v, i32([-1, 1, 2, 3, 4]), i32(bad),
+                                         i32(cu), i32([20, 18, 0, 33, 200]), 1, None, q_out=out,
+                                         dev_status=st)
+    # (200: past the table)
+    assert st.item() == (binding.DEV_BAD_BLOCK | binding.DEV_BAD_LENGTHS
+                         | binding.DEV_BAD_POSITION)
+    skipped = [0, 2, 4]
+    assert torch.all(out[skipped] == 7.0) and torch.equal(out[[1, 3]], q[[1, 3]])
+    rest = [b for b in range(nb) if b not in (table[0, 1], table[3, 2])]
+    assert np.array_equal(values(pool)[:, rest], before[:, rest])
+    assert np.array_equal(f64(scales)[:, rest], sb[:, rest])
+    # the bad position's block keeps its rows
+    assert np.array_equal(values(pool)[:, table[0, 1]], before[:, table[0, 1]])
+    # the good token is there
+    want, ws, _ = plain.append(before, sb, f64(k[3:4]), f64(v[3:4]), table[3:4], [0, 1], [33])
+    assert np.array_equal(values(pool)[:, table[3, 2]], want[:, table[3, 2]])
 
 
 def test_a_fork_writes_into_copies():
