@@ -26,12 +26,13 @@
 //   * every wait is bounded; on a timeout the CTA drains its copies and products,
 //     frees its tensor memory and leaves with PKV_DEV_TIMEOUT set.
 //
-// What bounds it (32 + 8 heads of 128): over 8 bits the chain of a softmax warp
-// (barrier, tensor-memory load, maximum, exponentials, store: ~2000 cycles for 64 keys
-// where the products of both query tiles take 1024), two such warps an SM quarter, in
-// phase; over bf16 shared memory's 128 bytes a cycle as well, of which 64 keys take
-// 1536 cycles (Q and K of 64-key products 96 KB, V's products 32, its conversion 32,
-// the copies 32). 8-bit chunks of 1500 to 2048 tokens over 4096 to 8192 keys: 349 us,
+// What bounds it (32 + 8 heads of 128): 64 keys take ~1880 cycles over 8 bits and ~1800
+// over bf16, where the products of both query tiles take 1024 and shared memory, at 128
+// bytes a cycle, 1536 (Q and K of 64-key products 96 KB, V's products 32, the
+// conversions 32, the copies 32). With half of the score products left out 8 and 12 %
+// of the time go, without the conversions 6 and 3 %, without the exponentials none: over
+// bf16 it is shared memory most of all, over 8 bits the waiting of softmax, products and
+// conversions for one another, at 57 % of the issue slots. 8-bit chunks of 1500 to 2048 tokens over 4096 to 8192 keys: 349 us,
 // 51 % of the bf16 peak; a prompt of 8192 tokens through a window of 1024: 154 us, 43 %.
 // Tried: 128-key tiles with one S each (less of shared memory, a longer chain: 358 and
 // 157 us), the weights formed before the maximum is known (373), a half of the next
