@@ -590,206 +590,234 @@ __global__ void __launch_bounds__(kBlockWarps<TEAM> * 32, 16 / kBlockWarps<TEAM>
   float* sn = cs + BS * PAD;
   griddep_wait();
   griddep_launch_dependents();
-  const int item = blockIdx.x / parts, part = blockIdx.x - item * parts;
 
-  // Item x of the grid belongs to the request r with f(r) <= x < f(r + 1), where
-  // f(r) = cu[r] / BS + 2 r leaves each request room for every block it touches.
-  int count = 0;
-  for (int base = 0; base < p.num_seqs; base += kBlockThreads) {
-    const int i = base + threadIdx.x;
-    const bool at = i < p.num_seqs && __ldg(p.cu_seqlens + i) / BS + 2 * i <= item;
-    const int n = __syncthreads_count(at);
-    count += n;
-    if (n < kBlockThreads) break;
-  }
-  const int r = count - 1;
-  // lengths that are no good (the three loads at once)
-  auto read_lengths = [&](int i, int32_t& t0, int32_t& qlen, int32_t& len) {
+  // The items, the blocks that the requests' new tokens reach, stand in a row, request
+  // after request. Each request is looked at by itself: one whose lengths are no good
+  // (cu_seqlens that falls, say) has none and moves no other's.
+  // Request i: its first token, the position of it, its length; its items, -1 where the
+  // lengths are no good.
+  auto items_of = [&](int i, int32_t& t0, int32_t& start, int32_t& len) -> int {
     t0 = __ldg(p.cu_seqlens + i);
     const int32_t t1 = __ldg(p.cu_seqlens + i + 1);
     len = __ldg(p.seq_lens + i);
-    qlen = t1 - t0;
-    return t0 < 0 || t1 < t0 || t1 > p.num_tokens ||
-           (qlen > 0 && (len < qlen || qlen > p.max_query_len || len > p.max_blocks * BS));
+    if (t0 < 0 || t1 < t0 || t1 > p.num_tokens) return -1;
+    if (t1 == t0) return 0;
+    if (len < t1 - t0 || t1 - t0 > p.max_query_len || len > p.max_blocks * BS) return -1;
+    start = len - (t1 - t0);
+    return (len - 1) / BS - start / BS + 1;
   };
-  int32_t t0, qlen, L;
-  if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < p.num_seqs; i += kBlockThreads)
-      if (read_lengths(i, t0, qlen, L)) set_status(p.status, PKV_DEV_BAD_LENGTHS);
-  if (r < 0 || read_lengths(r, t0, qlen, L)) return;
-  const int local = item - (t0 / BS + 2 * r);
-  const int32_t start = L - qlen;  // the position of the first new token
-  const int32_t block = start / BS + local;
-  if (qlen < 1 || block > (L - 1) / BS) return;
-  const int first = max(0, start - block * BS), last = min(BS, L - block * BS);  // its new rows
-  const int32_t tok0 = t0 + block * BS - start;  // the token of row 0 (of row r: tok0 + r)
-  const int32_t id = __ldg(p.block_table + (int64_t)r * p.max_blocks + block);
-  const bool write = id >= 0 && id < p.num_blocks;
-  if (!write && threadIdx.x == 0) set_status(p.status, PKV_DEV_BAD_BLOCK);
-
+  // (every warp for itself, a run of requests a lane: no barrier until the angles)
+  const int per = (p.num_seqs + 31) / 32;
+  const int r0 = min(p.num_seqs, lane * per), r1 = min(p.num_seqs, r0 + per);
+  int32_t t0 = 0, start = 0, len = 0;
+  constexpr uint32_t kMost = INT32_MAX;  // (sums stop here; the grid has fewer items)
+  uint32_t behind = 0;                   // items before the lane's last, it among them
+#pragma unroll 4
+  for (int i = r0; i < r1; ++i) {
+    const int n = items_of(i, t0, start, len);
+    if (n < 0 && blockIdx.x == 0 && warp == 0) set_status(p.status, PKV_DEV_BAD_LENGTHS);
+    behind = min(behind + max(n, 0), kMost);
+  }
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t x = __shfl_up_sync(kFull, behind, o);
+    if (lane >= o) behind = min(behind + x, kMost);
+  }
+  const uint32_t total = __shfl_sync(kFull, behind, 31);
+  uint32_t before = __shfl_up_sync(kFull, behind, 1);
+  if (lane == 0) before = 0;
   const int u = lane % GS, row_slot = lane / GS;
   const LaneVecs l = lane_vecs<MODE>(u, V, half);
   constexpr float inv_dim = 1.f / (float)D;
-  const int g0 = first / RG, g1 = (last - 1) / RG;  // groups of rows
-  // A job is a head: of the keys, the values, the queries. The rows of one come into
-  // the ring while those before are worked on.
-  const int kv = write ? 2 * Hkv : 0, jobs = kv + (p.q ? H : 0);
   const int team = warp / TEAM, member = warp % TEAM;
-  const int job0 = part * (W / TEAM) + team, stride_jobs = parts * (W / TEAM);
-  const int own0 = g0 + member;         // the warp's first group (of none: past g1)
-  const bool again = own0 + TEAM <= g1;  // it has several: keys and values are read twice
   __shared__ float tops[2][W];
-  auto sweeps = [&](int job) { return job < kv && again ? 2 : 1; };
-  int fjob = own0 <= g1 ? job0 : jobs, fg = own0, fsweep = 0, to = 0;
-  auto fetch = [&] {
-    if (fjob < jobs) {
-      const bool query = fjob >= kv, key = !query && fjob < Hkv;
-      const int h = query ? fjob - kv : key ? fjob : fjob - Hkv;
-      const int64_t stride = query ? p.q_stride : key ? p.k_stride : p.v_stride;
-      const uint16_t* x = (query ? p.q : key ? p.k : p.v) + h * D;
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const int row = fg * RG + i * RP + row_slot;
-        if (row < first || row >= last) continue;
-        const uint16_t* at = x + (tok0 + row) * stride;
-        const uint32_t dst = smem_addr(ring + (to * NP + i) * 1024);
-        cp_async_16(dst, at + l.a * 8, 16);
-        cp_async_16(dst + 512, at + l.b * 8, 16);
+  int from = 0, to = 0, turn = 0;
+  bool loaded = false;  // the weights
+  // (one item a CTA, but where requests count the same tokens)
+  const int part = blockIdx.x % parts;
+  const uint32_t step_items = gridDim.x / parts;
+  for (uint32_t item = blockIdx.x / parts; item < total; item += step_items) {
+    int r = r0;
+    uint32_t rest = item - before;
+    const bool holds = item >= before && item < behind;  // one lane: it has the item's request
+    if (per > 1 && holds)
+      for (;; ++r) {
+        const uint32_t n = max(0, items_of(r, t0, start, len));
+        if (rest < n) break;
+        rest -= n;
       }
-      fg += TEAM;
-      if (fg > g1) {
-        fg = own0;
-        if (++fsweep == sweeps(fjob)) {
-          fsweep = 0;
-          fjob += stride_jobs;
-        }
-      }
-      to ^= 1;
-    }
-  };
-  fetch();
+    const int from_lane = __ffs(__ballot_sync(kFull, holds)) - 1;
+    r = __shfl_sync(kFull, r, from_lane);
+    const int32_t pos0 = __shfl_sync(kFull, start, from_lane);  // of its first new token
+    const int32_t block = __shfl_sync(kFull, start / BS + (int)rest, from_lane);
+    const int32_t end = __shfl_sync(kFull, len, from_lane);
+    // its new rows
+    const int first = max(0, pos0 - block * BS), last = min(BS, end - block * BS);
+    // the token of row 0 (of row r: tok0 + r)
+    const int32_t tok0 = __shfl_sync(kFull, t0, from_lane) + block * BS - pos0;
+    const int32_t id = __ldg(p.block_table + (int64_t)r * p.max_blocks + block);
+    const bool write = id >= 0 && id < p.num_blocks;
+    if (!write && threadIdx.x == 0) set_status(p.status, PKV_DEV_BAD_BLOCK);
 
-  for (int i = threadIdx.x; i < D; i += kBlockThreads) {
-    wq[i] = weight_at(p.q_weight, p.weight_f32, p.weight_offset, i);
-    wk[i] = weight_at(p.k_weight, p.weight_f32, p.weight_offset, i);
-  }
-  for (int row = first + threadIdx.x; row < last; row += kBlockThreads) {
-    const bool ok = !p.positions || __ldg(p.positions + tok0 + row) >= 0;
-    good[row] = ok;
-    if (!ok && part == 0) set_status(p.status, PKV_DEV_BAD_POSITION);
-  }
-  if (half > 0)
-    for (int e = threadIdx.x; e < (last - first) * half; e += kBlockThreads) {
-      const int row = first + e / half, i = e % half;
-      const double f = __ldg(p.inv_freq + i);
-      const int32_t pos = __ldg(p.positions + tok0 + row);
-      float2 a = near_angle(turn_fraction(f), (uint32_t)pos, p.factor);
-      if (no_number(f)) a.x = a.y = __uint_as_float(kNan);
-      cs[row * PAD + i] = a.x;
-      sn[row * PAD + i] = a.y;
-    }
-  __syncthreads();
-
-  // the next rows of the ring, group g of one head, normed and turned
-  int from = 0;
-  auto rows_of = [&](bool normed, bool key, bool turned, int g, float (&y)[NP][16],
-                     bool (&ok)[NP]) {
-    cp_async_wait_all();
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      const int row = g * RG + i * RP + row_slot;
-      ok[i] = row >= first && row < last && good[row];
-      const uint8_t* at = ring + (from * NP + i) * 1024;
-      const Vec8 none = Vec8{{0u, 0u, 0u, 0u}};
-      unpack8(ok[i] ? load8(reinterpret_cast<const uint16_t*>(at)) : none, y[i]);
-      unpack8(ok[i] ? load8(reinterpret_cast<const uint16_t*>(at + 512)) : none, y[i] + 8);
-    }
-    from ^= 1;
-    fetch();  // (into the stage read before this one)
-    if (normed)
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        if (key)
-          norm16_near(y[i], wk, l, GS, inv_dim, p.eps);
-        else
-          scale16(y[i], norm_factor(y[i], GS, inv_dim, p.eps), wq, l);
-      }
-    if (turned)
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const int row = min(max(g * RG + i * RP + row_slot, first), last - 1);
-        float c[8], s[8];
-        if (MODE != kAny) load_cs(c, s, cs + row * PAD, sn + row * PAD, u);
-        turn16<MODE>(y[i], c, s, l, u, half, cs + row * PAD, sn + row * PAD,
-                     st + row_slot * (GS * 16));
-      }
-  };
-
-  int turn = 0;
-  for (int job = job0; job < jobs; job += stride_jobs) {
-    float y[NP][16];
-    bool ok[NP];
-    if (job >= kv) {  // a query head
-      const int h = job - kv;
-      for (int g = own0; g <= g1; g += TEAM) {
-        rows_of(p.q_weight != nullptr, false, half > 0, g, y, ok);
+    const int g0 = first / RG, g1 = (last - 1) / RG;  // groups of rows
+    // A job is a head: of the keys, the values, the queries. The rows of one come into
+    // the ring while those before are worked on.
+    const int kv = write ? 2 * Hkv : 0, jobs = kv + (p.q ? H : 0);
+    const int job0 = part * (W / TEAM) + team, stride_jobs = parts * (W / TEAM);
+    const int own0 = g0 + member;         // the warp's first group (of none: past g1)
+    const bool again = own0 + TEAM <= g1;  // it has several: keys and values are read twice
+    auto sweeps = [&](int job) { return job < kv && again ? 2 : 1; };
+    int fjob = own0 <= g1 ? job0 : jobs, fg = own0, fsweep = 0;
+    auto fetch = [&] {
+      if (fjob < jobs) {
+        const bool query = fjob >= kv, key = !query && fjob < Hkv;
+        const int h = query ? fjob - kv : key ? fjob : fjob - Hkv;
+        const int64_t stride = query ? p.q_stride : key ? p.k_stride : p.v_stride;
+        const uint16_t* x = (query ? p.q : key ? p.k : p.v) + h * D;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-          const int row = g * RG + i * RP + row_slot;
-          uint16_t* out = p.q_out + ((int64_t)(tok0 + row) * H + h) * D;
-          if (ok[i]) store8(out + l.a * 8, pack8(y[i]));
-          if (ok[i]) store8(out + l.b * 8, pack8(y[i] + 8));
+          const int row = fg * RG + i * RP + row_slot;
+          if (row < first || row >= last) continue;
+          const uint16_t* at = x + (tok0 + row) * stride;
+          const uint32_t dst = smem_addr(ring + (to * NP + i) * 1024);
+          cp_async_16(dst, at + l.a * 8, 16);
+          cp_async_16(dst + 512, at + l.b * 8, 16);
         }
+        fg += TEAM;
+        if (fg > g1) {
+          fg = own0;
+          if (++fsweep == sweeps(fjob)) {
+            fsweep = 0;
+            fjob += stride_jobs;
+          }
+        }
+        to ^= 1;
       }
-      continue;
+    };
+    fetch();
+
+    for (int i = loaded ? D : threadIdx.x; i < D; i += kBlockThreads) {
+      wq[i] = weight_at(p.q_weight, p.weight_f32, p.weight_offset, i);
+      wk[i] = weight_at(p.k_weight, p.weight_f32, p.weight_offset, i);
     }
-    const bool key = job < Hkv;
-    const int h = key ? job : job - Hkv;
-    const bool normed = key && p.k_weight != nullptr, turned = key && half > 0;
-    // the scale: a block that holds rows already keeps its own where that is larger
-    float* scale_at = p.scales + ((int64_t)(key ? 0 : p.num_blocks) + id) * Hkv + h;
-    const float old = first > 0 ? *scale_at : 0.f;
-    float top = 0.f;
-    for (int g = own0; g <= g1; g += TEAM) {
-      rows_of(normed, true, turned, g, y, ok);
-#pragma unroll
-      for (int i = 0; i < NP; ++i)
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if (ok[i]) top = fmaxf(top, finite_magnitude(y[i][j]));
+    loaded = true;
+    for (int row = first + threadIdx.x; row < last; row += kBlockThreads) {
+      const bool ok = !p.positions || __ldg(p.positions + tok0 + row) >= 0;
+      good[row] = ok;
+      if (!ok && part == 0) set_status(p.status, PKV_DEV_BAD_POSITION);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-    if (TEAM > 1) {
-      if (lane == 0) tops[turn][warp] = top;
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(32 * TEAM) : "memory");
-#pragma unroll
-      for (int w = 0; w < TEAM; ++w) top = fmaxf(top, tops[turn][team * TEAM + w]);
-      turn ^= 1;  // (who writes there again has met the others at the next barrier)
-    }
-    const float scale = fmaxf(old, block_scale(top));
-    uint8_t* rows = static_cast<uint8_t*>(p.pool) +
-                    (((int64_t)(key ? 0 : p.num_blocks) + id) * BS * Hkv + h) * D;
-    const int64_t step = (int64_t)Hkv * D;
-    if (first > 0 && scale != old) {
-      const float ratio = old > 0.f ? old / scale : 0.f;
-      for (int e = member * 32 + lane; e < first * (D / 4); e += 32 * TEAM) {
-        uint32_t* at = reinterpret_cast<uint32_t*>(rows + (e / (D / 4)) * step) + e % (D / 4);
-        *at = rescale4(*at, ratio);
+    if (half > 0)
+      for (int e = threadIdx.x; e < (last - first) * half; e += kBlockThreads) {
+        const int row = first + e / half, i = e % half;
+        const double f = __ldg(p.inv_freq + i);
+        const int32_t pos = __ldg(p.positions + tok0 + row);
+        float2 a = near_angle(turn_fraction(f), (uint32_t)pos, p.factor);
+        if (no_number(f)) a.x = a.y = __uint_as_float(kNan);
+        cs[row * PAD + i] = a.x;
+        sn[row * PAD + i] = a.y;
       }
-    }
-    __syncwarp();  // every lane (and at the barrier every warp) has read the old scale
-    if (member == 0 && lane == 0 && scale != old) *scale_at = scale;
-    for (int g = own0; g <= g1; g += TEAM) {
-      if (again) rows_of(normed, true, turned, g, y, ok);
+    __syncthreads();
+
+    // the next rows of the ring, group g of one head, normed and turned
+    auto rows_of = [&](bool normed, bool key, bool turned, int g, float (&y)[NP][16],
+                       bool (&ok)[NP]) {
+      cp_async_wait_all();
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        uint8_t* out = rows + (g * RG + i * RP + row_slot) * step;
-        if (ok[i]) *reinterpret_cast<uint2*>(out + l.a * 8) = quantise8(y[i], scale);
-        if (ok[i])
-          *reinterpret_cast<uint2*>(out + l.b * 8) = quantise8(y[i] + 8, scale);
+        const int row = g * RG + i * RP + row_slot;
+        ok[i] = row >= first && row < last && good[row];
+        const uint8_t* at = ring + (from * NP + i) * 1024;
+        const Vec8 none = Vec8{{0u, 0u, 0u, 0u}};
+        unpack8(ok[i] ? load8(reinterpret_cast<const uint16_t*>(at)) : none, y[i]);
+        unpack8(ok[i] ? load8(reinterpret_cast<const uint16_t*>(at + 512)) : none, y[i] + 8);
+      }
+      from ^= 1;
+      fetch();  // (into the stage read before this one)
+      if (normed)
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          if (key)
+            norm16_near(y[i], wk, l, GS, inv_dim, p.eps);
+          else
+            scale16(y[i], norm_factor(y[i], GS, inv_dim, p.eps), wq, l);
+        }
+      if (turned)
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          const int row = min(max(g * RG + i * RP + row_slot, first), last - 1);
+          float c[8], s[8];
+          if (MODE != kAny) load_cs(c, s, cs + row * PAD, sn + row * PAD, u);
+          turn16<MODE>(y[i], c, s, l, u, half, cs + row * PAD, sn + row * PAD,
+                       st + row_slot * (GS * 16));
+        }
+    };
+
+    for (int job = job0; job < jobs; job += stride_jobs) {
+      float y[NP][16];
+      bool ok[NP];
+      if (job >= kv) {  // a query head
+        const int h = job - kv;
+        for (int g = own0; g <= g1; g += TEAM) {
+          rows_of(p.q_weight != nullptr, false, half > 0, g, y, ok);
+#pragma unroll
+          for (int i = 0; i < NP; ++i) {
+            const int row = g * RG + i * RP + row_slot;
+            uint16_t* out = p.q_out + ((int64_t)(tok0 + row) * H + h) * D;
+            if (ok[i]) store8(out + l.a * 8, pack8(y[i]));
+            if (ok[i]) store8(out + l.b * 8, pack8(y[i] + 8));
+          }
+        }
+        continue;
+      }
+      const bool key = job < Hkv;
+      const int h = key ? job : job - Hkv;
+      const bool normed = key && p.k_weight != nullptr, turned = key && half > 0;
+      // the scale: a block that holds rows already keeps its own where that is larger
+      float* scale_at = p.scales + ((int64_t)(key ? 0 : p.num_blocks) + id) * Hkv + h;
+      const float old = first > 0 ? *scale_at : 0.f;
+      float top = 0.f;
+      for (int g = own0; g <= g1; g += TEAM) {
+        rows_of(normed, true, turned, g, y, ok);
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (ok[i]) top = fmaxf(top, finite_magnitude(y[i][j]));
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+      if (TEAM > 1) {
+        if (lane == 0) tops[turn][warp] = top;
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(32 * TEAM) : "memory");
+#pragma unroll
+        for (int w = 0; w < TEAM; ++w) top = fmaxf(top, tops[turn][team * TEAM + w]);
+        turn ^= 1;  // (who writes there again has met the others at the next barrier)
+      }
+      const float scale = fmaxf(old, block_scale(top));
+      uint8_t* rows = static_cast<uint8_t*>(p.pool) +
+                      (((int64_t)(key ? 0 : p.num_blocks) + id) * BS * Hkv + h) * D;
+      const int64_t step = (int64_t)Hkv * D;
+      if (first > 0 && scale != old) {
+        const float ratio = old > 0.f ? old / scale : 0.f;
+        for (int e = member * 32 + lane; e < first * (D / 4); e += 32 * TEAM) {
+          uint32_t* at = reinterpret_cast<uint32_t*>(rows + (e / (D / 4)) * step) + e % (D / 4);
+          *at = rescale4(*at, ratio);
+        }
+      }
+      __syncwarp();  // every lane (and at the barrier every warp) has read the old scale
+      if (member == 0 && lane == 0 && scale != old) *scale_at = scale;
+      for (int g = own0; g <= g1; g += TEAM) {
+        if (again) rows_of(normed, true, turned, g, y, ok);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          uint8_t* out = rows + (g * RG + i * RP + row_slot) * step;
+          if (ok[i]) *reinterpret_cast<uint2*>(out + l.a * 8) = quantise8(y[i], scale);
+          if (ok[i])
+            *reinterpret_cast<uint2*>(out + l.b * 8) = quantise8(y[i] + 8, scale);
+        }
       }
     }
+    if (item + step_items < total) __syncthreads();  // the angles have been read
   }
 }
 
