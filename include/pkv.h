@@ -70,9 +70,10 @@ typedef int32_t pkv_status;
                                        max_blocks_per_seq * block_size */
 #define PKV_DEV_TIMEOUT 8           /* an internal pipeline wait gave up; outputs of the
                                        affected tile are unspecified */
-#define PKV_DEV_V_RANGE 16          /* the chunked-prefill kernel met a V value of magnitude
-                                       >= 65536 (or inf / NaN), beyond the fp16 range its
-                                       P.V product uses; that request's outputs are
+#define PKV_DEV_V_RANGE 16          /* a chunked-prefill kernel met a V value that is inf or
+                                       NaN, or (except in pkv_paged_attention_varlen_window)
+                                       of magnitude >= 65536, beyond the fp16 range its P.V
+                                       product uses; that request's outputs are
                                        unspecified */
 #define PKV_DEV_BAD_POSITION 32     /* a negative rotary position */
 #define PKV_DEV_BAD_ROW 64          /* weight_rows entry outside [0, num_rows) */
@@ -165,7 +166,8 @@ size_t pkv_attention_workspace_size(int32_t num_seqs, int32_t num_tokens, int32_
  * (HBM-bound, warp-level tensor-core products; query_len == 1 requests split
  * into partitions merged by log-sum-exp, several-query requests one
  * partition); longer requests run on the chunked-prefill kernel (tcgen05
- * tensor cores).
+ * tensor cores), which holds V in fp16: values below 2^-17 lose bits there, and
+ * those up to 2^-25 count as 0 (pkv_paged_attention_varlen_window keeps them).
  * The kernels use programmatic dependent launch: each waits for the grid
  * before it in the stream to finish before touching memory, so ordinary
  * stream order holds. A batch with requests for both kernels runs them side
@@ -557,7 +559,10 @@ pkv_status pkv_qk_norm_rope_kv_cache_append_fp8(
  *   out          [num_tokens][num_heads][head_dim] bf16, or fp32 when out_f32 is
  *                set, 16-byte aligned; rounded once from fp32 (the softmax weights
  *                are rounded to fp16 in requests of more than 32 / G queries and
- *                over the 8-bit cache, to 16 bits of fraction elsewhere)
+ *                over the 8-bit cache, to 16 bits of fraction elsewhere; bf16 values
+ *                are taken as they are in requests of up to 32 / G queries; in longer
+ *                ones the values of 64 keys and a KV head are held together, exact down
+ *                to 2^-31 of the largest of them or 2^-81, whichever is larger)
  *   workspace    at least pkv_window_attention_workspace_size(...) bytes, 256-byte
  *                aligned (13 MB at most where no request has more than 32 / G queries,
  *                54 MB otherwise). It needs no clearing. One for each concurrent call,

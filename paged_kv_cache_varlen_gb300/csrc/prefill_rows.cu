@@ -23,6 +23,10 @@
 //   * K and V arrive by TMA in 16-key boxes, K into two stages of 128 keys, V into five
 //     of 64. V becomes fp16 in place (four converter warps); at 8 bits K becomes bf16
 //     and V fp16, both exactly, and a block's two scales act on the scores;
+//   * bf16 values have a wider range than fp16: the 64 of a stage are multiplied by one
+//     power of two, which its weights take up as they do an 8-bit block's scale (the
+//     prompt below 157 us, 153 without, which lost values below 2^-17 and refused those
+//     from 2^16 on; 160 with a power for every 16 keys: a longer softmax);
 //   * every wait is bounded; on a timeout the CTA drains its copies and products,
 //     frees its tensor memory and leaves with PKV_DEV_TIMEOUT set.
 //
@@ -139,11 +143,15 @@ struct Bars {
   uint64_t o_done[2][2];   // PV(j) is done
   uint64_t o_free[2];      // the item's O has been read
   uint64_t mma_done;
+  uint64_t v_sized;        // bf16: every converter warp has said how large its rows are
   uint64_t item_full[kRing], item_empty[kRing];
   Piece item[kRing];
   uint32_t tmem_base;
   int32_t abort;
   uint32_t k_mask[kNS], v_mask[kVS];  // boxes of a stage that were loaded
+  uint32_t v_top[2][kConverters / 32];
+  float2 v_scale[kVS];  // bf16: what undoes the power that a stage's values were scaled by:
+                        // its log2, and the power
   Sums sums;
 };
 static_assert(sizeof(Bars) <= 768, "the barriers fit below the work list");
@@ -552,38 +560,55 @@ __device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t h) {
 // rows that the products read; 128 threads. Rows not loaded, behind the needed keys or
 // hidden from every query ([h0, h1)) become zeros. CH: from one 128-byte chunk of the
 // rows to the next.
-// bf16 to fp16 in place (exact below 2^16; `most` gathers the largest magnitudes, per
-// half of a word, NaN above all).
+// bf16 to fp16 in place, in two steps. A thread's pieces of the rows; returns the largest
+// magnitude of the warp's, as the bits of a bf16.
+template <int D>
+constexpr int kBf16Pieces = kHalf * (D / 8) / kConverters;  // of 16 bytes, a thread's
 template <int D, int CH>
-__device__ __forceinline__ void convert_bf16(uint32_t base, int ct, uint32_t load, int end, int h0,
-                                             int h1, uint32_t& most) {
-  constexpr int RP = D / 8;                        // 16-byte pieces of a row
-  constexpr int N = kHalf * RP / kConverters;      // pieces of a thread
-  constexpr int STEP = kConverters / RP;           // their rows are so far apart
+__device__ __forceinline__ uint32_t bf16_at(uint32_t base, int ct, int e) {
+  constexpr int RP = D / 8;  // pieces of a row
+  const int pc = ct % RP, k = ct / RP + kConverters / RP * e;
+  return base + (pc >> 3) * CH + k * 128 + (((uint32_t)(pc & 7) ^ (uint32_t)(k & 7)) << 4);
+}
+template <int D, int CH>
+__device__ __forceinline__ uint32_t load_bf16(uint32_t base, int ct, uint32_t load, int end, int h0,
+                                              int h1, uint4 (&v)[kBf16Pieces<D>]) {
   const bool all =
       end >= kHalf && load == (1u << kHalfBoxes) - 1 && (h0 >= kHalf || h1 <= 0 || h0 >= h1);
-  const int pc = ct % RP, k0 = ct / RP;
-  const uint32_t col = base + (pc >> 3) * CH;
-  uint4 v[N];
+  uint32_t top = 0;
 #pragma unroll
-  for (int e = 0; e < N; ++e) {
-    const int k = k0 + STEP * e;
-    v[e] = lds16(col + k * 128 + (((uint32_t)(pc & 7) ^ (uint32_t)(k & 7)) << 4));
-  }
+  for (int e = 0; e < kBf16Pieces<D>; ++e) v[e] = lds16(bf16_at<D, CH>(base, ct, e));
 #pragma unroll
-  for (int e = 0; e < N; ++e) {
-    const int k = k0 + STEP * e;
-    uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
+  for (int e = 0; e < kBf16Pieces<D>; ++e) {
+    const int k = ct / (D / 8) + kConverters / (D / 8) * e;
     if (!all && !(k < end && ((load >> (k / kSub)) & 1u) && (k < h0 || k >= h1)))
-      w[0] = w[1] = w[2] = w[3] = 0u;
+      v[e] = make_uint4(0u, 0u, 0u, 0u);
+    const uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      asm("max.u16x2 %0, %0, %1;" : "+r"(top) : "r"(w[j] & 0x7fff7fffu));
+  }
+  return __reduce_max_sync(kFull, max(top & 0xffffu, top >> 16));
+}
+// The power of two that the rows are multiplied by, its exponent + 127: brings their
+// largest magnitude into [2^14, 2^15) (within [2^-113, 2^64]; rows of zeros: 2^64), which
+// leaves values exact down to 2^-17, 2^-31 of the largest.
+__device__ __forceinline__ uint32_t bf16_power(uint32_t top) {
+  return min(max(14 + 127 + 127 - (int)(top >> 7), 127 - 113), 127 + 64);
+}
+template <int D, int CH>
+__device__ __forceinline__ void store_bf16(uint32_t base, int ct, uint32_t power,
+                                           const uint4 (&v)[kBf16Pieces<D>]) {
+  const uint32_t times = power << 7 | power << 23;  // as bf16, twice
+#pragma unroll
+  for (int e = 0; e < kBf16Pieces<D>; ++e) {
+    uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
+      asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(w[j]) : "r"(times));
       w[j] = pack_f16x2(bf16_lo(w[j]), bf16_hi(w[j]));
-      asm("{\n\t.reg .b32 a;\n\tabs.f16x2 a, %1;\n\tmax.NaN.f16x2 %0, %0, a;\n\t}"
-          : "+r"(most)
-          : "r"(w[j]));
     }
-    sts16(col + k * 128 + (((uint32_t)(pc & 7) ^ (uint32_t)(k & 7)) << 4), w[0], w[1], w[2], w[3]);
+    sts16(bf16_at<D, CH>(base, ct, e), w[0], w[1], w[2], w[3]);
   }
 }
 // e4m3 in place: box b landed at 2048 b bytes, its rows D bytes apart, swizzled by
@@ -835,8 +860,8 @@ __device__ __forceinline__ void work_on(const CUtensorMap& q_map, const CUtensor
     } else if (warp < kMmaWarp) {
       // ===== converters =====
       const int ct = threadIdx.x - kConvWarp0 * 32;
-      uint32_t most = 0;  // of V, as fp16
-      int gt = 0, vst = 0;
+      uint32_t most = 0;  // of V
+      int gt = 0, vt = 0, vst = 0;
       uint32_t vparity = 0;
       bool ok = true;
       for (int k = 0; ok; ++k) {
@@ -867,18 +892,36 @@ __device__ __forceinline__ void work_on(const CUtensorMap& q_map, const CUtensor
           if (EIGHT)
             convert_e4m3<D, false, Lay::VCH_BYTES>(base, ct, load, d.end - c0, d.sink - c0,
                                                    d.lo_any - c0);
-          else
-            convert_bf16<D, Lay::VCH_BYTES>(base, ct, load, d.end - c0, d.sink - c0,
-                                            d.lo_any - c0, most);
+          else {
+            uint4 v[kBf16Pieces<D>];
+            uint32_t top = load_bf16<D, Lay::VCH_BYTES>(base, ct, load, d.end - c0, d.sink - c0,
+                                                        d.lo_any - c0, v);
+            volatile uint32_t* tops = bars->v_top[vt & 1];
+            if (lane == 0) {
+              tops[ct >> 5] = top;
+              mbar_arrive(smem_addr(&bars->v_sized));
+            }
+            ok = all_wait(&bars->v_sized, vt & 1);
+            if (!ok) break;
+            ++vt;
+#pragma unroll
+            for (int w = 0; w < kConverters / 32; ++w) top = max(top, tops[w]);
+            most = max(most, top);
+            const uint32_t power = bf16_power(top);
+            store_bf16<D, Lay::VCH_BYTES>(base, ct, power, v);
+            if (ct == 0) {
+              volatile float2* scale = &bars->v_scale[vst];
+              scale->x = 127.f - (float)power;
+              scale->y = __uint_as_float(power << 23);
+            }
+          }
           fence_proxy_async_smem();
           mbar_arrive(smem_addr(&bars->v_full[vst]));
           vst = vst + 1 == kVS ? 0 : vst + 1;
           vparity ^= vst == 0 ? 1u : 0u;
         }
       }
-      // infinities and NaN of fp16: magnitudes that round past 65504, or were those
-      if ((most & 0xffffu) >= 0x7c00u || (most >> 16) >= 0x7c00u)
-        set_status(p.status, PKV_DEV_V_RANGE);
+      if (most >= 0x7f80u && ct == 0) set_status(p.status, PKV_DEV_V_RANGE);  // inf, NaN
     } else {
       // ===== the products of query tile x: the warp waits, one lane issues =====
       const int x = warp - kMmaWarp;
@@ -964,14 +1007,24 @@ __device__ __forceinline__ void work_on(const CUtensorMap& q_map, const CUtensor
     const uint32_t sa0 = tmem + lanes + Lay::s_col(x), oa = tmem + lanes + Lay::o_col(x);
     const float sl2 = p.scale_log2;
     bool ok = true;
-    int gt = 0;
+    int gt = 0, vst = 0;
+    uint32_t vparity = 0;
+    float2 vs = make_float2(0.f, 1.f);  // bf16: the V stage's scale, which the weights take up
     auto score_col = [&](int g) { return sa0 + (uint32_t)((g & 1) * kHalf); };
     auto load_scores = [&](int g, uint32_t (&u)[kHalf]) {
-      const bool there = all_wait(&bars->s_full[x][g & 1], (g >> 1) & 1);
+      bool there = all_wait(&bars->s_full[x][g & 1], (g >> 1) & 1);
       tc_fence_after();
       if (there) {
         PKV_TMEM_LD32(score_col(g), u);
         PKV_TMEM_LD32(score_col(g) + 32, (u + 32));
+        if (!EIGHT) {
+          there = all_wait(&bars->v_full[vst], vparity);
+          const volatile float2* scale = &bars->v_scale[vst];
+          vs.x = scale->x;
+          vs.y = scale->y;
+          vst = vst + 1 == kVS ? 0 : vst + 1;
+          vparity ^= vst == 0 ? 1u : 0u;
+        }
         tmem_wait_ld();
       }
       return there;
@@ -1066,7 +1119,7 @@ __device__ __forceinline__ void work_on(const CUtensorMap& q_map, const CUtensor
             a = max3(a, __uint_as_float(u[c]), __uint_as_float(u[c + 1]));
             b = max3(b, __uint_as_float(u[c + 2]), __uint_as_float(u[c + 3]));
           }
-          mx = fmaxf(a, b) * sl2;
+          mx = fmaf(fmaxf(a, b), sl2, vs.x);
         }
         const float mnew = fmaxf(m, mx);
         const bool grow = mnew > m + kRescaleThreshold;
@@ -1093,6 +1146,7 @@ __device__ __forceinline__ void work_on(const CUtensorMap& q_map, const CUtensor
         // weights: the sum takes them before they are rounded to fp16
         float2 sum = make_float2(0.f, 0.f);
         float sum8 = 0.f;
+        const float voff = vs.x - mu;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           uint32_t pk[16];
@@ -1121,7 +1175,7 @@ __device__ __forceinline__ void work_on(const CUtensorMap& q_map, const CUtensor
               const int e = 32 * b + 2 * c;
               const float2 y = __ffma2_rn(
                   make_float2(__uint_as_float(u[e]), __uint_as_float(u[e + 1])),
-                  make_float2(sl2, sl2), make_float2(-mu, -mu));
+                  make_float2(sl2, sl2), make_float2(voff, voff));
               const float2 w = make_float2(fast_exp2(y.x), fast_exp2(y.y));
               pk[c] = pack_f16x2(w.x, w.y);
               sum = __fadd2_rn(sum, w);
@@ -1133,7 +1187,7 @@ __device__ __forceinline__ void work_on(const CUtensorMap& q_map, const CUtensor
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&bars->p_ready[x][gt & 1]));
-        l += EIGHT ? sum8 : sum.x + sum.y;
+        l = EIGHT ? l + sum8 : fmaf(sum.x + sum.y, vs.y, l);
         // (at the loop's end: 8-bit chunks of 2048 tokens 353 us, 359 at its start)
         if (j + 1 < d.n) ok = load_scores(gt + 1, u);
         if (!ok) break;
@@ -1232,6 +1286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_addr(&bars->v_empty[s]), 2);
     }
     mbar_init(smem_addr(&bars->mma_done), 2);
+    mbar_init(smem_addr(&bars->v_sized), kConverters / 32);
     for (int k = 0; k < kRing; ++k) {
       mbar_init(smem_addr(&bars->item_full[k]), 1);
       mbar_init(smem_addr(&bars->item_empty[k]), kItemReaders);

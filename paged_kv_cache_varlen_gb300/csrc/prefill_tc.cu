@@ -504,9 +504,9 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 // One 16-byte piece of a V tile (8 bf16 values) converted in place to fp16
-// (exact for |v| < 65536: fp16 keeps bf16's 8 significant bits); the
-// exponent fields seen are folded into emax (per 16-bit half) for the range
-// check.
+// (exact for 2^-17 <= |v| < 2^16: fp16 keeps bf16's 8 significant bits; smaller
+// ones in steps of 2^-24); the exponent fields seen are folded into emax (per
+// 16-bit half) for the range check.
 __device__ __forceinline__ void v_piece_to_f16(uint32_t addr, uint32_t& emax) {
   uint32_t w[4];
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
