@@ -510,7 +510,8 @@ pkv_status pkv_qk_norm_rope_kv_cache_write(
  *           values that fall below 2^-6 of the new scale);
  *   rows behind the request's last token stay as they were.
  * The blocks written belong to one request of the call (copy shared ones first:
- * pkv_copy_blocks_fp8), each of its rows once.
+ * pkv_copy_blocks_fp8), each of its rows once. num_tokens may be more than
+ * cu_seqlens_q[num_seqs] (a padded batch): rows behind the last request's are left out.
  * Errors: PKV_DEV_BAD_LENGTHS (the request is skipped), PKV_DEV_BAD_BLOCK (that
  * block's rows are not written).
  */
@@ -575,6 +576,8 @@ pkv_status pkv_qk_norm_rope_kv_cache_append_fp8(
  * the same bits.
  * out, out_lse and the workspace overlap neither one another nor q, the pool and its
  * scales (PKV_ERR_INVALID_ARG).
+ * num_tokens may be more than cu_seqlens_q[num_seqs] (a padded batch): rows behind the
+ * last request's stay as they were.
  * Other arguments, streams and errors as pkv_paged_attention_varlen; num_heads /
  * num_kv_heads may be any number up to 128 (any at all for requests of one query).
  * max_seq_len below 2^30; num_seqs up to 4415 at head_dim 128 and 30000 at 64 where

@@ -875,7 +875,7 @@ def _window_attention(q, kv_pool, kv_scales, block_table, cu_seqlens, seq_lens, 
             cu_seqlens, seq_lens, block_table, num_tokens=q.shape[0],
             max_query_len=int(max_query_len), max_seq_len=int(max_seq_len),
             num_blocks=kv_pool.shape[1], block_size=kv_pool.shape[2], window=int(window),
-            num_sink=int(num_sink))
+            num_sink=int(num_sink), padded=True)
     if stream is not None and (out is None or workspace is None):
         # what is made here belongs to the call's stream
         with _on_stream(stream, q.device):

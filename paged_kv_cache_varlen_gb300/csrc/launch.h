@@ -113,7 +113,8 @@ struct AttnParams {
   //     decode grid completes only after the prefill grid has.
   //   no_decode: the host has shown that no request is short enough for the
   //     decode kernel (no decode grid is launched); the prefill kernel flags
-  //     one that is as PKV_DEV_BAD_LENGTHS.
+  //     one that is as PKV_DEV_BAD_LENGTHS (in the calls with a window or an
+  //     8-bit pool, whose batches may be padded, it computes that one too).
   int32_t shared_sms;
   int32_t after_prefill;
   int32_t no_decode;

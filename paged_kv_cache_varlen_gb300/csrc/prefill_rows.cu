@@ -346,10 +346,11 @@ struct Work {
   Share share;
 };
 
-// The call's work: the requests with more than decode_max_q queries, those with the
-// most tiles in a unit first (batches of more than kSortMax requests: as they come;
-// bad lengths flagged by one CTA), the CTAs that work on them, and whether their items
-// are cut. All threads of every CTA come to the same result.
+// The call's work: the requests with more than decode_max_q queries (any queries, where
+// no decode grid runs beside), those with the most tiles in a unit first (batches of more
+// than kSortMax requests: as they come; bad lengths flagged by one CTA), the CTAs that
+// work on them, and whether their items are cut. All threads of every CTA come to the
+// same result.
 template <bool EIGHT, bool CUT>
 __device__ __noinline__ void plan_work(const AttnParams& p, int QP, int* ints, Sums* sums,
                                        Work* out) {
@@ -366,10 +367,10 @@ __device__ __noinline__ void plan_work(const AttnParams& p, int QP, int* ints, S
     const int32_t n = t1 - t0;
     weight = chunks = 0;
     bool bad = t0 < 0 || t1 < t0 || t1 > p.num_tokens;
-    const bool short_one = !bad && n <= p.decode_max_q;
+    // (a batch padded behind its last request may look as if no request were short)
+    const bool short_one = !bad && n <= (p.no_decode ? 0 : p.decode_max_q);
     const bool len_ok = L >= n && L <= p.max_seq_len && L <= p.max_blocks * p.block_size;
     if (short_one) {
-      if (flag && p.no_decode && n > 0) set_status(p.status, PKV_DEV_BAD_LENGTHS);
       if (n > 0 && len_ok) chunks = visible_units(p.window, p.num_sink, L - n, L, kSub).count;
       return 0;
     }

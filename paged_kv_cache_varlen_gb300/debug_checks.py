@@ -41,9 +41,10 @@ def _host(t) -> np.ndarray:
 def check_attention_tables(cu_seqlens, seq_lens, block_table, *, num_tokens: int,
                            max_query_len: int, max_seq_len: int, num_blocks: int,
                            block_size: int, key_start=None, query_start=None, window: int = 0,
-                           num_sink: int = 0) -> None:
+                           num_sink: int = 0, padded: bool = False) -> None:
     """Raise ValueError on the first entry the attention kernels would reject.
-    Blocks that a window hides from every query of a request may be anything."""
+    Blocks that a window hides from every query of a request may be anything.
+    padded: there may be rows behind the last request's."""
     cu = _host(cu_seqlens).astype(np.int64)
     lens = _host(seq_lens).astype(np.int64)
     table = _host(block_table).astype(np.int64)
@@ -53,7 +54,7 @@ def check_attention_tables(cu_seqlens, seq_lens, block_table, *, num_tokens: int
                          f"block_table {table.shape}")
     if cu[0] != 0:
         raise ValueError(f"cu_seqlens_q[0] = {cu[0]}, not 0")
-    if cu[b] != num_tokens:
+    if cu[b] != num_tokens and not (padded and cu[b] < num_tokens):
         raise ValueError(f"cu_seqlens_q[{b}] = {cu[b]}, not num_tokens = {num_tokens}")
     qlen = np.diff(cu)
     bad = np.nonzero(qlen < 0)[0]
@@ -113,7 +114,7 @@ def check_append_tables(cu_seqlens, seq_lens, block_table, *, num_tokens: int,
     # that sees the new tokens alone
     check_attention_tables(cu, lens, table, num_tokens=num_tokens, max_query_len=max_query_len,
                            max_seq_len=most, num_blocks=num_blocks, block_size=block_size,
-                           window=1)
+                           window=1, padded=True)
     taken: dict[int, int] = {}
     for i in range(lens.shape[0]):
         n = int(cu[i + 1] - cu[i])
