@@ -41,6 +41,7 @@
 // Tried: 128-key tiles with one S each (less of shared memory, a longer chain: 358 and
 // 157 us), the weights formed before the maximum is known (373), a half of the next
 // scores loaded between the halves of a softmax (392), their barrier asked then (351).
+#include <float.h>
 #include <math.h>
 
 #include "common.cuh"
@@ -1056,11 +1057,12 @@ __device__ __forceinline__ void work_on(const CUtensorMap& q_map, const CUtensor
         nx_a = nx_i = 1.f;
         nx_l = 0.f;
         if (id >= 0) {
-          // (at least 2^-100 both: a hidden score's -inf times 0 would be NaN)
-          constexpr float kLeast = 7.888609e-31f;
-          nx_a = fmaxf(__ldg(p.scales + (int64_t)id * p.num_kv_heads + d.kvh), kLeast) * sl2;
+          // (never 0: a hidden score's -inf times it would be NaN)
+          nx_a = fmaxf(__ldg(p.scales + (int64_t)id * p.num_kv_heads + d.kvh) * sl2, FLT_MIN);
+          // (a scale below 2^-100 as that: its values are nothing beside any other)
           const float v = fmaxf(
-              __ldg(p.scales + ((int64_t)p.num_blocks + id) * p.num_kv_heads + d.kvh), kLeast);
+              __ldg(p.scales + ((int64_t)p.num_blocks + id) * p.num_kv_heads + d.kvh),
+              7.888609e-31f);
           nx_l = fast_log2(v);
           nx_i = 1.f / v;
         }

@@ -31,3 +31,15 @@ def test_padded_batches(eight, rows, ql, window, sink):
     s.q = s.q[:t].contiguous()
     s.check(out[:t], lse[:t])
     assert guards_intact(buf, out.numel()) and guards_intact(lbuf, lse.numel())
+
+
+@pytest.mark.parametrize("ql", [[1, 3], [70, 40]])
+@pytest.mark.parametrize("scale", [1e-20, 1e-38])
+def test_factors_that_vanish(ql, scale):
+    # blocks of next to no keys (the smallest scale that the writes leave) and a small
+    # score scale: their product is 0 in fp32, and every key counts the same
+    s = Step([100, 90], ql, 4, 2, 128, 16, 40, 3, True, seed=7)
+    s.scales[0] *= 2.0 ** -90
+    for k in s.k:
+        k *= 2.0 ** -90
+    s.check(*s.call(scale=scale), scale=scale)
