@@ -94,6 +94,7 @@ constexpr int kMaxCtas = 152;  // shares at most: their pieces have room in the 
 constexpr float kRescaleThreshold = 14.f;
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr uint32_t kMinusInf = 0xff800000u;
+constexpr int32_t kBadRow = -2;  // of a box in a block that is not there (-1: of none)
 
 constexpr size_t list_ints(int num_seqs) {
   return (num_seqs <= kSortMax ? 5 : 1) * ((size_t)num_seqs + 1);
@@ -651,6 +652,19 @@ __device__ __forceinline__ void convert_e4m3(uint32_t base, int ct, uint32_t loa
   }
 }
 
+// Zeros into the boxes of a K stage (a bit of `boxes` each), by a warp.
+template <int NCH, int CH>
+__device__ __noinline__ void clear_boxes(uint32_t stage, uint32_t boxes) {
+#pragma unroll 1
+  for (int b = 0; b < kBoxes; ++b)
+    if ((boxes >> b) & 1u)
+#pragma unroll 1
+      for (int e = threadIdx.x & 31; e < NCH * kSub * 8; e += 32)
+        st_shared_zero16(stage + b * kSub * 128 + e / (kSub * 8) * CH + e % (kSub * 8) * 16);
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
 // A warp's part of a piece: O, 4 dimensions of its 32 rows after the other, then m and l.
 template <int D>
 constexpr int kWarpFloats = 32 * (D + 2);
@@ -814,14 +828,20 @@ __device__ __forceinline__ void work_on(const CUtensorMap& q_map, const CUtensor
             if (box < d.count) {
               const int key = d.key(box * kSub);
               const int32_t id = __ldg(bt + key / p.block_size);
-              if (id >= 0 && id < p.num_blocks)
+              if (id >= 0 && id < p.num_blocks) {
                 row = first_row + id * p.block_size + key % p.block_size;
-              else
+              } else {
+                row = kBadRow;
                 bad_block = true;
+              }
             }
           }
           if (filled >= stages) ok = warp_wait(&empty[st], parity);
           if (!ok) break;
+          // keys of a bad block count as zeros (the converters see to the other rows)
+          if (!EIGHT && !vrole && __any_sync(kFull, bad_block))
+            clear_boxes<Lay::NCH, Lay::CH_BYTES>(
+                ring + st * stage_bytes, __ballot_sync(kFull, row == kBadRow) >> (box0 & 31));
           const uint32_t load =
               (__ballot_sync(kFull, row >= 0) >> (box0 & 31)) & ((1u << boxes) - 1);
           if (lane == 0) {

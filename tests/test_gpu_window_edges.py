@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import paged_kv_cache_varlen_gb300 as pkv
+from paged_kv_cache_varlen_gb300 import binding
 
 from .gpu_util import guarded, guards_intact
 from .test_gpu_window import BOTH, Step, f64, i32
@@ -43,3 +44,36 @@ def test_factors_that_vanish(ql, scale):
     for k in s.k:
         k *= 2.0 ** -90
     s.check(*s.call(scale=scale), scale=scale)
+
+
+@BOTH
+@pytest.mark.parametrize("window,sink", [(0, 0), (60, 40)])
+def test_prompts_over_blocks_that_are_not_there(eight, window, sink):
+    # flagged; a key of a bad block counts as zeros, whatever the SMs held before
+    s = Step([300, 200], [90, 200], 4, 2, 128, 16, window, sink, eight, seed=8)
+    args = (i32(s.cu), i32(s.lens), 200, 300)
+
+    def call(table, pool):
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        a = (s.q, pool) + ((s.scales,) if eight else ()) + (i32(table),) + args
+        f = pkv.paged_attention_varlen_fp8 if eight else pkv.paged_attention_varlen_window
+        out, _ = f(*a, window=window, num_sink=sink, dev_status=st,
+                   out=torch.empty(s.q.shape, device="cuda"))
+        return out, st.item()
+
+    table = s.table.copy()
+    table[0, [0, 15]], table[1, 3] = s.nb, -1
+    zeros = s.pool.clone()
+    for blk in (s.table[0, 0], s.table[0, 15], s.table[1, 3]):
+        zeros.view(torch.uint8 if eight else torch.int16)[:, int(blk)] = 0
+    want, st = call(s.table, zeros)
+    assert st == 0
+    nan = torch.full_like(s.pool.float(), float("nan")).to(s.pool.dtype)
+    for dirty in (s.pool, nan):
+        call(s.table, dirty)
+        got, st = call(table, s.pool)
+        assert st == binding.DEV_BAD_BLOCK
+        # (8 bits: a bad block has no scales, so that the weights' roundings differ: half a
+        # step of fp16 in either call, of at most the largest value)
+        most = max(np.abs(v).max() for v in s.v)
+        assert torch.allclose(got, want, rtol=0, atol=(2.0 ** -10 + 2.0 ** -13) * most)
