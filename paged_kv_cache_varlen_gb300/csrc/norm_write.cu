@@ -102,10 +102,11 @@ __device__ __forceinline__ float norm_factor(const float (&y)[16], int GS, float
 
 // The same to about half an ulp, for keys that are rounded to 8 bits (of 168M, 104 fall
 // to the other side of a rounding boundary, 133 by the form above; 8192 tokens 44.2 us,
-// 43.3): the factor as r + lo, its products with the weights with their remainders, one
-// rounding a value.
-__device__ __forceinline__ void norm16_near(float (&y)[16], const float* ws, const LaneVecs& l,
-                                            int GS, float inv_dim, float eps) {
+// 43.3): the factor as r + lo (float2), its products with the weights with their
+// remainders, one rounding a value. Both kernels that write 8 bits norm keys so: a key's
+// bits do not depend on what else is in its step.
+__device__ __forceinline__ float2 near_factor(const float (&y)[16], int GS, float inv_dim,
+                                              float eps) {
   float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < 16; ++i) s4[i & 3] = fmaf(y[i], y[i], s4[i & 3]);
@@ -113,7 +114,10 @@ __device__ __forceinline__ void norm16_near(float (&y)[16], const float* ws, con
 #pragma unroll
   for (int o = 1; o < GS; o <<= 1) ss += __shfl_xor_sync(kFull, ss, o);
   const float v = fmaf(ss, inv_dim, eps), r = rsqrtf(v), e = fmaf(-v * r, r, 1.f);
-  const float lo = fabsf(e) < 1e-3f ? 0.5f * r * e : 0.f;
+  return make_float2(r, fabsf(e) < 1e-3f ? 0.5f * r * e : 0.f);
+}
+__device__ __forceinline__ void near_scale16(float (&y)[16], float2 f, const float* ws,
+                                             const LaneVecs& l) {
   const float* wa = ws + max(l.a, 0) * 8;
   const float* wb = ws + max(l.b, 0) * 8;
 #pragma unroll
@@ -122,7 +126,7 @@ __device__ __forceinline__ void norm16_near(float (&y)[16], const float* ws, con
     const float w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float q = r * w[j], rest = fmaf(lo, w[j], fmaf(r, w[j], -q));
+      const float q = f.x * w[j], rest = fmaf(f.y, w[j], fmaf(f.x, w[j], -q));
       y[i + j] = fmaf(y[i + j], q, y[i + j] * rest);
     }
   }
@@ -155,8 +159,8 @@ __device__ __forceinline__ void turn16(float (&y)[16], const float (&c)[8], cons
     for (int i = 0; i < 8; ++i) {
       const float a = y[2 * i], b = y[2 * i + 1];
       if (i < pairs) {
-        y[2 * i] = a * c[i] - b * s[i];
-        y[2 * i + 1] = b * c[i] + a * s[i];
+        y[2 * i] = fmaf(a, c[i], -(b * s[i]));  // (in every kernel the same bits)
+        y[2 * i + 1] = fmaf(b, c[i], a * s[i]);
       }
     }
   } else {
@@ -169,9 +173,9 @@ __device__ __forceinline__ void turn16(float (&y)[16], const float (&c)[8], cons
     for (int i = 0; i < 16; ++i) {
       const int d = u * 16 + i;
       if (d < half)
-        y[i] = y[i] * cs[d] - st[d + half] * sn[d];
+        y[i] = fmaf(y[i], cs[d], -(st[d + half] * sn[d]));
       else if (d < 2 * half)
-        y[i] = y[i] * cs[d - half] + st[d - half] * sn[d - half];
+        y[i] = fmaf(y[i], cs[d - half], st[d - half] * sn[d - half]);
     }
     __syncwarp();
   }
@@ -456,7 +460,12 @@ __global__ void __launch_bounds__(kThreads, kRowCtas) norm_rope_kernel(const Nor
       unpack8(xb, y + 8);
       if (pass * slots < H + Hkv) {
         const float f = norm_factor(y, GS, inv_dim, p.eps);
-        if (normed) scale16(y, f, query ? wq : wk, l);
+        float2 near = make_float2(0.f, 0.f);
+        if (EIGHT && (pass + 1) * slots > H) near = near_factor(y, GS, inv_dim, p.eps);
+        if (normed && EIGHT && key)
+          near_scale16(y, near, wk, l);
+        else if (normed)
+          scale16(y, f, query ? wq : wk, l);
         turn16<MODE>(y, c, s, l, u, half, cs, sn, st + head_slot * (GS * 16));
         if (EIGHT && !query && !key) {  // a value beside keys
           unpack8(xa, y);
@@ -737,7 +746,7 @@ __global__ void __launch_bounds__(kBlockWarps<TEAM> * 32, 16 / kBlockWarps<TEAM>
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
           if (key)
-            norm16_near(y[i], wk, l, GS, inv_dim, p.eps);
+            near_scale16(y[i], near_factor(y[i], GS, inv_dim, p.eps), wk, l);
           else
             scale16(y[i], norm_factor(y[i], GS, inv_dim, p.eps), wq, l);
         }
