@@ -160,7 +160,7 @@ __device__ __forceinline__ void turn16(float (&y)[16], const float (&c)[8], cons
       const float a = y[2 * i], b = y[2 * i + 1];
       if (i < pairs) {
         y[2 * i] = fmaf(a, c[i], -(b * s[i]));  // (in every kernel the same bits)
-        y[2 * i + 1] = fmaf(b, c[i], a * s[i]);
+        y[2 * i + 1] = fmaf(a, s[i], b * c[i]);
       }
     }
   } else {
