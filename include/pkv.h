@@ -464,8 +464,9 @@ pkv_status pkv_rope_kv_cache_write(void *q_out, void *kv_pool, const void *q, co
  *   y = x * (mean over the head of x^2 + eps)^(-1/2) * (weight + weight_offset),
  * then the rotation of y, in fp32, rounded once to bf16. Dimensions >=
  * rotary_dim are normed only. rotary_dim may be 0 (nothing is rotated, inv_freq
- * unused). v_new is a bit copy. A head whose sum of squares passes the fp32
- * range becomes 0.
+ * unused). v_new is a bit copy. Squares are summed in fp32: a head whose sum
+ * passes its range becomes 0; with eps 0, one of values below 2^-63 loses bits of
+ * its norm, and below 2^-75 becomes infinite or NaN.
  * Errors: as pkv_rope_kv_cache_write; PKV_ERR_INVALID_ARG for eps < 0 or a
  * value that is not finite.
  */
@@ -555,7 +556,8 @@ pkv_status pkv_qk_norm_rope_kv_cache_append_fp8(
  * Blocks that hold no key that any query of the request sees are not read: their
  * table entries may hold anything (blocks given back), and so may hidden keys in
  * blocks that are read (NaN included), as long as they lie before the window of
- * the request's first query.
+ * the request's first query. (A value that is NaN or infinite and seen by a later
+ * query of the step may make the request's earlier queries NaN as well.)
  *
  *   out          [num_tokens][num_heads][head_dim] bf16, or fp32 when out_f32 is
  *                set, 16-byte aligned; rounded once from fp32 (the softmax weights
@@ -565,8 +567,8 @@ pkv_status pkv_qk_norm_rope_kv_cache_append_fp8(
  *                ones the values of 64 keys and a KV head are held together, exact down
  *                to 2^-31 of the largest of them or 2^-81, whichever is larger)
  *   workspace    at least pkv_window_attention_workspace_size(...) bytes, 256-byte
- *                aligned (13 MB at most where no request has more than 32 / G queries,
- *                54 MB otherwise). It needs no clearing. One for each concurrent call,
+ *                aligned (8 MB at most where no request has more than 32 / G queries,
+ *                46 MB otherwise). It needs no clearing. One for each concurrent call,
  *                and for each captured graph that may run beside another
  * There is no partition_size: the work of the requests of up to 32 / G queries is
  * cut into equal shares of the keys that they see, whatever their lengths, that of
