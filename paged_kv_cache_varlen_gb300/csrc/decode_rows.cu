@@ -61,9 +61,9 @@ constexpr uint32_t kFull = 0xffffffffu;
 // that cost more than they save (2 contexts of 4096 keys, 8 bits: 14.8 us; 16.4 with
 // shares of 8, 16.0 with 32; one of 2048: 12.4, 12.4, 14.6).
 constexpr int kMinShare = 16;
-// What going over to another request costs a CTA, in units of a chunk's time: shares
-// of equal chunks alone ended 4.5 us apart for each request in them (64 contexts of
-// 512 to 4096 keys), about 12 chunks' time with 608 CTAs.
+// What going over to another request costs a CTA, in units of a chunk's time (64 contexts
+// of 512 to 4096 keys, 8 bits: 62.7 us by equal chunks alone, 59.4 with a cost of 9, 56.7
+// with 18, 57.8 with 36; contexts of 32K to 128K 204.2, 202.9, 202.4, 202.6).
 constexpr int kStartCost = 18;
 
 template <bool EIGHT>

@@ -223,9 +223,9 @@ cudaError_t launch_prefill_rows(const AttnParams& p, const CUtensorMap& q_map,
 bool prefill_rows_fits(int32_t num_seqs, int32_t head_dim);
 // Behind that grid (and the decode grid's), where p.prefill_join is set: joins the items
 // that were cut. That is faster where each is cut into many pieces, in calls of few
-// items (64 queries of 32 heads over 65536 keys, 8 items, 8 bits: 103 us; 121 when the
+// items (64 queries of 32 heads over 65536 keys, 8 items, 8 bits: 102 us; 109 when the
 // CTA that comes last joins its item's pieces); the launch costs more than it saves
-// where there are two of each (a mixed batch: 47 us, 40).
+// where there are two of each (a mixed batch in a graph: 42.7 us, 38.2).
 bool prefill_rows_join(const AttnParams& p);
 cudaError_t launch_prefill_rows_join(const AttnParams& p, cudaStream_t stream);
 

@@ -34,7 +34,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kAhead = 3;  // passes whose copies are under way (5: as fast)
-// CTAs an SM; three of them spill (8192 tokens: 36 us, 40 with three)
+// CTAs an SM; three of them spill (8192 tokens: 36 us, 41 with three)
 constexpr int kRowCtas = 2;
 
 // Where a pair's two dimensions are: kHalves p and p + r / 2, with r / 2 a

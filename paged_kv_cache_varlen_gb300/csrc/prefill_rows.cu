@@ -30,17 +30,18 @@
 //   * every wait is bounded; on a timeout the CTA drains its copies and products,
 //     frees its tensor memory and leaves with PKV_DEV_TIMEOUT set.
 //
-// What bounds it (32 + 8 heads of 128): 64 keys take ~1880 cycles over 8 bits and ~1800
+// What bounds it (32 + 8 heads of 128): 64 keys take ~1880 cycles over 8 bits and ~1840
 // over bf16, where the products of both query tiles take 1024 and shared memory, at 128
 // bytes a cycle, 1536 (Q and K of 64-key products 96 KB, V's products 32, the
 // conversions 32, the copies 32). With half of the score products left out 8 and 12 %
 // of the time go, without the conversions 6 and 3 %, without the exponentials none: over
 // bf16 it is shared memory most of all, over 8 bits the waiting of softmax, products and
-// conversions for one another, at 57 % of the issue slots. 8-bit chunks of 1500 to 2048 tokens over 4096 to 8192 keys: 349 us,
-// 51 % of the bf16 peak; a prompt of 8192 tokens through a window of 1024: 154 us, 43 %.
-// Tried: 128-key tiles with one S each (less of shared memory, a longer chain: 358 and
-// 157 us), the weights formed before the maximum is known (373), a half of the next
-// scores loaded between the halves of a softmax (392), their barrier asked then (351).
+// conversions for one another, at 57 % of the issue slots. 8-bit chunks of 1500 to 2048
+// tokens over 4096 to 8192 keys: 349 us, 51 % of the bf16 peak; a prompt of 8192 tokens
+// through a window of 1024: 159 us, 42 %. Tried (at 349 and 154 us): 128-key tiles with
+// one S each (less of shared memory, a longer chain: 358 and 157), the weights formed
+// before the maximum is known (373), a half of the next scores loaded between the halves
+// of a softmax (392), their barrier asked then (351).
 #include <float.h>
 #include <math.h>
 
@@ -490,8 +491,8 @@ __device__ __noinline__ void plan_work(const AttnParams& p, int QP, int* ints, S
   }
   // Cut, where the last round of tickets, of which some CTAs get none, costs more than
   // to hand over pieces, about kPieceTiles. (Items that differ fill the rounds better,
-  // the light ones last.) 13 requests, 513-key window, 156 items: 42 us by tickets, 38
-  // cut.
+  // the light ones last.) 13 requests, 513-key window, 156 items, in a graph: 40.1 us by
+  // tickets, 38.2 cut.
   if (!may_cut || units == 0 || (int64_t)all * Hkv >= 1 << 30) return;
   const uint32_t total = (uint32_t)all * Hkv;
   const uint32_t ctas = max(1u, min((uint32_t)min(active, kMaxCtas),

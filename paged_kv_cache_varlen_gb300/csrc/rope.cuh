@@ -44,10 +44,12 @@ __device__ __forceinline__ float2 rope_angle(uint64_t frac, uint32_t pos, float 
   return make_float2(c * factor, s * factor);
 }
 
-// The same from the nearest quarter turn on: the rest, 30 bits of a turn, loses at most
-// 2^-28 of one to fp32 (2^-26 above), which keeps the cosine and the sine within an ulp
-// of theirs. (Keys rounded to 8 bits: of 33.6M, 35 fell to the other side of a rounding
-// boundary with the angle above, 24 with this one.)
+// The same from the nearest quarter turn on: the rest, 30 bits of a turn, loses a
+// relative 2^-24 to fp32 (of up to half a turn above). Beside that rounding and the
+// function's own the angle is off by the bits of a turn that are left out, less than
+// 2^-31 of one, 3e-9 rad: far below an ulp of a value near 1, more than one of a sine or
+// cosine below 2^-5. (Keys rounded to 8 bits: of 33.6M, 35 fell to the other side of a
+// rounding boundary with the angle above, 24 with this one.)
 __device__ __forceinline__ float2 near_angle(uint64_t frac, uint32_t pos, float factor) {
   const uint32_t turn = (uint32_t)((frac * pos) >> 32);
   const uint32_t quarter = (turn + (1u << 29)) >> 30;

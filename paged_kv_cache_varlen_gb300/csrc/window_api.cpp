@@ -78,7 +78,7 @@ pkv_status attention(void* out, int32_t out_f32, float* out_lse, const void* q, 
   if (num_seqs < 0 || num_tokens < 0) return PKV_ERR_INVALID_ARG;
   if (num_tokens == 0) return PKV_OK;
   if (num_seqs == 0) return PKV_ERR_INVALID_ARG;
-  if (num_seqs > 65534) return PKV_ERR_UNSUPPORTED;  // grid z: requests + one
+  if (num_seqs > 65534) return PKV_ERR_UNSUPPORTED;  // (as pkv_paged_attention_varlen)
   if (!out || !q || !kv_pool || (eight && !scales) || !block_table || !cu_seqlens_q || !seq_lens)
     return PKV_ERR_INVALID_ARG;
   if (num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads != 0)
