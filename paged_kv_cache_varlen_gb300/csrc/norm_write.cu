@@ -21,7 +21,7 @@
 // What bounds them: bytes, for prompts (8192 tokens of 32 + 8 heads of 128: 201 MB
 // into a bf16 pool, 36 us, 5.6 TB/s; 185 MB into an 8-bit one, 44 us, 4.2 TB/s, where
 // the angles, the magnitudes and the roundings keep the issue slots half busy);
-// latency, for single tokens (3.4 us for one, 5.1 us for 64 of them at 8 bits: a chain
+// latency, for single tokens (3.4 us for one, 5.3 us for 64 of them at 8 bits: a chain
 // of lengths, block, scale, rows).
 #include "common.cuh"
 #include "launch.h"
@@ -888,7 +888,7 @@ cudaError_t launch_append_d(const NormRopeParams& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_append_fp8(const NormRopeParams& p, cudaStream_t stream) {
-  // a token a request: by rows (64 requests of 32 + 8 heads: 5.1 us; 10.0 by blocks,
+  // a token a request: by rows (64 requests of 32 + 8 heads: 5.3 us; 10.0 by blocks,
   // most of whose lanes hold rows that there are not)
   if (p.max_query_len == 1) return launch_rows<true>(p, stream);
   if (p.head_dim == 128) return launch_append_d<128>(p, stream);

@@ -25,8 +25,8 @@
 //     and V fp16, both exactly, and a block's two scales act on the scores;
 //   * bf16 values have a wider range than fp16: the 64 of a stage are multiplied by one
 //     power of two, which its weights take up as they do an 8-bit block's scale (the
-//     prompt below 157 us, 153 without, which lost values below 2^-17 and refused those
-//     from 2^16 on; 160 with a power for every 16 keys: a longer softmax);
+//     prompt below, in a graph, 157 us; 153 without, which lost values below 2^-17 and
+//     refused those from 2^16 on; 160 with a power for every 16 keys: a longer softmax);
 //   * every wait is bounded; on a timeout the CTA drains its copies and products,
 //     frees its tensor memory and leaves with PKV_DEV_TIMEOUT set.
 //
@@ -38,7 +38,7 @@
 // bf16 it is shared memory most of all, over 8 bits the waiting of softmax, products and
 // conversions for one another, at 57 % of the issue slots. 8-bit chunks of 1500 to 2048
 // tokens over 4096 to 8192 keys: 349 us, 51 % of the bf16 peak; a prompt of 8192 tokens
-// through a window of 1024: 159 us, 42 %. Tried (at 349 and 154 us): 128-key tiles with
+// through a window of 1024: 158 us, 42 %. Tried (at 349 and 154 us): 128-key tiles with
 // one S each (less of shared memory, a longer chain: 358 and 157), the weights formed
 // before the maximum is known (373), a half of the next scores loaded between the halves
 // of a softmax (392), their barrier asked then (351).
