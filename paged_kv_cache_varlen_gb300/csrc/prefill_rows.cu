@@ -25,7 +25,7 @@
 //     and V fp16, both exactly, and a block's two scales act on the scores;
 //   * bf16 values have a wider range than fp16: the 64 of a stage are multiplied by one
 //     power of two, which its weights take up as they do an 8-bit block's scale (the
-//     prompt below, in a graph, 157 us; 153 without, which lost values below 2^-17 and
+//     prompt below, in a graph, 156 us; 153 without, which lost values below 2^-17 and
 //     refused those from 2^16 on; 160 with a power for every 16 keys: a longer softmax);
 //   * every wait is bounded; on a timeout the CTA drains its copies and products,
 //     frees its tensor memory and leaves with PKV_DEV_TIMEOUT set.
@@ -1035,19 +1035,20 @@ __device__ __forceinline__ void work_on(const CUtensorMap& q_map, const CUtensor
     float2 vs = make_float2(0.f, 1.f);  // bf16: the V stage's scale, which the weights take up
     auto score_col = [&](int g) { return sa0 + (uint32_t)((g & 1) * kHalf); };
     auto load_scores = [&](int g, uint32_t (&u)[kHalf]) {
-      bool there = all_wait(&bars->s_full[x][g & 1], (g >> 1) & 1);
+      bool there = wait(&bars->s_full[x][g & 1], (g >> 1) & 1);
+      if (!EIGHT) {
+        there = there && wait(&bars->v_full[vst], vparity);
+        const volatile float2* scale = &bars->v_scale[vst];
+        vs.x = scale->x;
+        vs.y = scale->y;
+        vst = vst + 1 == kVS ? 0 : vst + 1;
+        vparity ^= vst == 0 ? 1u : 0u;
+      }
+      there = __all_sync(kFull, there) != 0;  // (all waits before the loads are under way)
       tc_fence_after();
       if (there) {
         PKV_TMEM_LD32(score_col(g), u);
         PKV_TMEM_LD32(score_col(g) + 32, (u + 32));
-        if (!EIGHT) {
-          there = all_wait(&bars->v_full[vst], vparity);
-          const volatile float2* scale = &bars->v_scale[vst];
-          vs.x = scale->x;
-          vs.y = scale->y;
-          vst = vst + 1 == kVS ? 0 : vst + 1;
-          vparity ^= vst == 0 ? 1u : 0u;
-        }
         tmem_wait_ld();
       }
       return there;
