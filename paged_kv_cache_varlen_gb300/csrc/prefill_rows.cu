@@ -564,8 +564,7 @@ __device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t h) {
 // rows that the products read; 128 threads. Rows not loaded, behind the needed keys or
 // hidden from every query ([h0, h1)) become zeros. CH: from one 128-byte chunk of the
 // rows to the next.
-// bf16 to fp16 in place, in two steps. A thread's pieces of the rows; returns the largest
-// magnitude of the warp's, as the bits of a bf16.
+// bf16 to fp16 in place, in two steps.
 template <int D>
 constexpr int kBf16Pieces = kHalf * (D / 8) / kConverters;  // of 16 bytes, a thread's
 template <int D, int CH>
@@ -574,6 +573,8 @@ __device__ __forceinline__ uint32_t bf16_at(uint32_t base, int ct, int e) {
   const int pc = ct % RP, k = ct / RP + kConverters / RP * e;
   return base + (pc >> 3) * CH + k * 128 + (((uint32_t)(pc & 7) ^ (uint32_t)(k & 7)) << 4);
 }
+// First: a thread's pieces of the rows, and the largest magnitude of its warp's, as the
+// bits of a bf16.
 template <int D, int CH>
 __device__ __forceinline__ uint32_t load_bf16(uint32_t base, int ct, uint32_t load, int end, int h0,
                                               int h1, uint4 (&v)[kBf16Pieces<D>]) {
@@ -600,6 +601,7 @@ __device__ __forceinline__ uint32_t load_bf16(uint32_t base, int ct, uint32_t lo
 __device__ __forceinline__ uint32_t bf16_power(uint32_t top) {
   return min(max(14 + 127 + 127 - (int)(top >> 7), 127 - 113), 127 + 64);
 }
+// Second: the pieces times that power, as fp16.
 template <int D, int CH>
 __device__ __forceinline__ void store_bf16(uint32_t base, int ct, uint32_t power,
                                            const uint4 (&v)[kBf16Pieces<D>]) {
